@@ -281,6 +281,139 @@ fo_status_t fo_lion_step(const fo_tensor_t *table, int32_t ntensors,
 #define FO_VERIFY_COUNTS 6
 fo_status_t fo_verify_fast_arithmetic(uint64_t *counts, fo_stream_t stream);
 
+/* --- losses on the logits of a language model ---------------------------------
+ *
+ * The step above consumes gradients; these calls stand at the other end of the
+ * backward pass. Both work on rows of logits x[vocab] at a temperature T:
+ * s = x / T, m = max s, Z = sum exp(s - m), p = exp(s - m) / Z.
+ *   - fo_token_logprobs: log p of given tokens, the entropy, the top
+ *     alternatives (what a distillation teacher writes down), and
+ *     fo_token_logprobs_grad, their gradient;
+ *   - fo_distill: KL(q || p) for a teacher distribution q known by its top
+ *     logits, optionally with its gradient in the same pass, and
+ *     fo_distill_grad, the gradient alone.
+ * Accuracy: statistics and sums are FP32 (one exponential is within 3 ulp, a
+ * sum of a row within a few ulp of its own size); a gradient is rounded once,
+ * to the logits' type. Every result is the same bit for bit on every run: no
+ * atomics join partial sums.
+ * Rules for masked and special values, in every call:
+ *   - a logit of -inf has probability 0, as has one of the type's lowest value
+ *     beside ordinary ones; a row whose every logit is -inf has no
+ *     distribution: log probabilities -inf, entropy 0, gradient 0 (its KL is
+ *     +inf where the teacher's is not 0);
+ *   - NaN, or a logit of +inf, makes the row's results NaN (top_ids are still
+ *     valid: NaN counts as the largest value);
+ *   - a negative token or teacher id is no entry: it adds nothing, and a
+ *     negative token's log probability is 0; an id of vocab or more makes the
+ *     row's results NaN;
+ *   - a row whose incoming gradients (or row weight) are all 0 is not read and
+ *     gets an exactly zero gradient, whatever it holds.
+ */
+
+/* Element type of logits, of their gradient and of a teacher's logits. */
+typedef enum fo_logit_dtype {
+    FO_LOGITS_BF16 = 0,
+    FO_LOGITS_F32 = 1,
+    FO_LOGITS_F16 = 2
+} fo_logit_dtype_t;
+
+#define FO_MAX_TOP_K 128              /* top alternatives and teacher ids by row        */
+#define FO_MAX_ROW_BYTES (1600 * 1024) /* vocab * element size                           */
+#define FO_MAX_LOGIT_ROWS (1 << 27)
+#define FO_LOSS_STATS 4               /* floats of saved statistics by row              */
+
+/*
+ * Logits: `rows` rows of `vocab` contiguous elements. Row r = o * inner_rows + i
+ * starts at element o * outer_stride + i * row_stride (a plain matrix has
+ * inner_rows = rows; logits[:, :-1] of a [batch, time, vocab] tensor has
+ * inner_rows = time - 1 and outer_stride = time * vocab). `data` needs the
+ * alignment of its element type only. Strides are not negative.
+ */
+typedef struct fo_logits {
+    const void *data;
+    int64_t rows, vocab;
+    int64_t row_stride;     /* elements                                   */
+    int64_t inner_rows;     /* >= 1; rows is a multiple of it             */
+    int64_t outer_stride;   /* elements; ignored where inner_rows == rows */
+    double temperature;     /* T, in [2^-20, 2^20]                        */
+    int32_t dtype;          /* fo_logit_dtype_t                           */
+    int32_t reserved;       /* 0                                          */
+} fo_logits_t;
+
+/* A gradient of the logits: same rows, vocab, inner_rows and element type.
+ * Its rows may not overlap one another. `data` and the strides may be those of
+ * the logits themselves (the gradient then replaces them); any other overlap
+ * of the two address ranges is refused. */
+typedef struct fo_logits_grad {
+    void *data;
+    int64_t row_stride, outer_stride;
+} fo_logits_grad_t;
+
+/* A teacher's top logits: k ids and logits by row, [rows, k] contiguous. q is
+ * softmax(logits / temperature) over the row's ids; with tail = 1 it is
+ * q_k = exp(logits_k / temperature - lse) and the rest of the mass,
+ * max(0, 1 - sum q), is one more outcome, compared with the student's
+ * probability of all tokens that are not listed. An id listed twice counts
+ * twice in q. */
+typedef struct fo_teacher {
+    const int32_t *ids;
+    const void *logits;
+    const float *lse;       /* [rows], tail only: log-sum-exp of the teacher's logits / temperature
+                             * over its whole vocabulary; NULL: 0 (logits are log probabilities) */
+    double temperature;     /* in [2^-20, 2^20]          */
+    int32_t k;              /* 1 .. FO_MAX_TOP_K         */
+    int32_t dtype;          /* fo_logit_dtype_t          */
+    int32_t tail;           /* 0 or 1                    */
+    int32_t reserved;       /* 0                         */
+} fo_teacher_t;
+
+/*
+ * fo_token_logprobs -- by row: logp[rows] = log p[token], entropy[rows] =
+ * -sum p log p, and the top_k largest logits, top_ids[rows, top_k] and
+ * top_logp[rows, top_k], in descending order, equal ones by ascending id.
+ * Outputs that are NULL are not computed (tokens may be NULL where logp is;
+ * top_ids and top_logp are both given where top_k > 0). stats[rows,
+ * FO_LOSS_STATS], optional, is what fo_token_logprobs_grad needs.
+ * Errors: FO_ERR_NULL, FO_ERR_MISALIGNED (an array not aligned to its element
+ * type, stats not to 16 bytes), FO_ERR_SIZE (a count is negative or above its
+ * limit, vocab < 1, top_k > vocab), FO_ERR_BAD_ARG (temperature, dtype,
+ * strides, reserved), FO_ERR_ALIAS, FO_ERR_CUDA. rows = 0 is a no-op.
+ */
+fo_status_t fo_token_logprobs(const fo_logits_t *logits, const int64_t *tokens, int32_t top_k, float *logp,
+                              float *entropy, int32_t *top_ids, float *top_logp, float *stats,
+                              fo_stream_t stream);
+
+/*
+ * fo_token_logprobs_grad -- the gradient of
+ *   sum_r g_logp[r] logp[r] + g_entropy[r] entropy[r] + sum_k g_top[r, k] top_logp[r, k]
+ * with respect to the logits, from the stats that fo_token_logprobs wrote for
+ * them (the top ids count as constants). A NULL g_* is 0; tokens are needed
+ * with g_logp, top_ids with g_top. Errors as fo_token_logprobs.
+ */
+fo_status_t fo_token_logprobs_grad(const fo_logits_t *logits, const int64_t *tokens, int32_t top_k,
+                                   const int32_t *top_ids, const float *stats, const float *g_logp,
+                                   const float *g_entropy, const float *g_top, const fo_logits_grad_t *grad,
+                                   fo_stream_t stream);
+
+/*
+ * fo_distill -- loss[r] = w[r] KL(q_r || p_r), w = row_weight or 1 where that
+ * is NULL. With `grad`, also the gradient of sum_r loss[r] with respect to the
+ * logits, in one pass: the logits are read once from device memory. stats
+ * [rows, FO_LOSS_STATS], optional, is what fo_distill_grad needs (of rows with
+ * weight 0 it is not written). `loss` and `grad` may each be NULL.
+ * Errors as fo_token_logprobs.
+ */
+fo_status_t fo_distill(const fo_logits_t *logits, const fo_teacher_t *teacher, const float *row_weight,
+                       float *loss, float *stats, const fo_logits_grad_t *grad, fo_stream_t stream);
+
+/*
+ * fo_distill_grad -- the gradient of sum_r g_loss[r] KL(q_r || p_r) with
+ * respect to the logits, from the stats that fo_distill wrote for them with
+ * the same teacher. Errors as fo_token_logprobs.
+ */
+fo_status_t fo_distill_grad(const fo_logits_t *logits, const fo_teacher_t *teacher, const float *stats,
+                            const float *g_loss, const fo_logits_grad_t *grad, fo_stream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *fo_status_string(fo_status_t status);
 

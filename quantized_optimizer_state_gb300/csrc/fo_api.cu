@@ -40,19 +40,28 @@ int sm_count()
     return n;
 }
 
-}  // namespace fo
-
-namespace {
-
-using fo::Opt;
-
 fo_status_t cuda_status(cudaError_t e)
 {
     if (e == cudaSuccess)
         return FO_OK;
-    fo::t_last_cuda_error = (int)e;
+    t_last_cuda_error = (int)e;
     return FO_ERR_CUDA;
 }
+
+// A CUDA error left pending by earlier work (a non-sticky launch error that
+// nobody has read yet) would be reported by the first cudaGetLastError after
+// this call's own launch, and the call would look failed after part of its
+// work was enqueued. So it is read (and cleared) before anything is launched,
+// and reported as this call's FO_ERR_CUDA, with nothing launched.
+fo_status_t pending_error() { return cuda_status(cudaGetLastError()); }
+
+}  // namespace fo
+
+namespace {
+
+using fo::cuda_status;
+using fo::Opt;
+using fo::pending_error;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -139,20 +148,6 @@ fo_status_t check_disjoint(const fo_tensor_t *table, int32_t ntensors, bool with
             end_written = std::max(end_written, sp.hi);
     }
     return FO_OK;
-}
-
-// A CUDA error left pending by earlier work (a non-sticky launch error that
-// nobody has read yet) would be reported by the first cudaGetLastError after
-// this call's own launch, and the call would look failed after part of its
-// work was enqueued. So it is read (and cleared) before anything is launched,
-// and reported as this call's FO_ERR_CUDA, with nothing launched.
-fo_status_t pending_error()
-{
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
-        return FO_OK;
-    fo::t_last_cuda_error = (int)e;
-    return FO_ERR_CUDA;
 }
 
 // Per-row scalar: decay (AdamW, Lion) or weight decay (SGD), rounded once to FP32.

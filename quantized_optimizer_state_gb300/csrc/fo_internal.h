@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "fo.h"
+
 namespace fo {
 
 constexpr int kGroup = 32;           // quantization group (page: G = 32)
@@ -128,6 +130,10 @@ cudaError_t launch_dequant(const void *q, const uint16_t *scales, float *x, int6
 constexpr int kVerifyCounts = 6;
 cudaError_t launch_verify(unsigned long long *counts, cudaStream_t stream);
 
+// FO_OK, or FO_ERR_CUDA with the error kept for fo_last_cuda_error.
+fo_status_t cuda_status(cudaError_t e);
+// The status of a CUDA error that earlier work left pending (read and cleared).
+fo_status_t pending_error();
 // Number of SMs of the current device (cached per device).
 int sm_count();
 // Kernel launches issued by this library so far.

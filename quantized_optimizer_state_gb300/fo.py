@@ -65,7 +65,34 @@ class LionHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double)]
 
 
+FO_LOGITS_BF16, FO_LOGITS_F32, FO_LOGITS_F16 = 0, 1, 2   # fo_logit_dtype_t
+FO_MAX_TOP_K = 128
+FO_MAX_ROW_BYTES = 1600 * 1024
+FO_MAX_LOGIT_ROWS = 1 << 27
+FO_LOSS_STATS = 4
+
+
+class FoLogits(ctypes.Structure):
+    """Mirror of ``fo_logits_t``."""
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("inner_rows", ctypes.c_int64), ("outer_stride", ctypes.c_int64),
+                ("temperature", ctypes.c_double), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class FoLogitsGrad(ctypes.Structure):
+    """Mirror of ``fo_logits_grad_t``."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("outer_stride", ctypes.c_int64)]
+
+
+class FoTeacher(ctypes.Structure):
+    """Mirror of ``fo_teacher_t``."""
+    _fields_ = [("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("temperature", ctypes.c_double), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("tail", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 assert ctypes.sizeof(FoTensor) == 80
+assert ctypes.sizeof(FoLogits) == 64 and ctypes.sizeof(FoLogitsGrad) == 24 and ctypes.sizeof(FoTeacher) == 48
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -82,6 +109,10 @@ SIGNATURES = {
     "fo_sgd_step": (ctypes.c_int, [_VP, _I32, _VP, _VP]),
     "fo_lion_step": (ctypes.c_int, [_VP, _I32, _VP, _VP]),
     "fo_verify_fast_arithmetic": (ctypes.c_int, [_VP, _VP]),
+    "fo_token_logprobs": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_token_logprobs_grad": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_distill": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_distill_grad": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP]),
     "fo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fo_last_cuda_error": (ctypes.c_int, []),
     "fo_kernel_launch_count": (ctypes.c_uint64, []),
@@ -196,6 +227,8 @@ class _Dtypes:
                 "rho8": (torch.int8,),
                 "rho16": (torch.int16,),
                 "m_q": (torch.int8,),
+                "i32": (torch.int32,),
+                "i64": (torch.int64,),
                 "v_q": (torch.uint8,),
             }
         return cls._cache
@@ -345,6 +378,152 @@ def fo_status_string(status: int) -> str:
 
 def fo_kernel_launch_count() -> int:
     return int(lib().fo_kernel_launch_count())
+
+
+# --- losses on logits --------------------------------------------------------
+
+_LOGIT_DTYPES: dict = {}
+
+
+def _logit_dtype(dtype, name: str) -> int:
+    if not _LOGIT_DTYPES:
+        import torch
+        _LOGIT_DTYPES.update({torch.bfloat16: FO_LOGITS_BF16, torch.float32: FO_LOGITS_F32,
+                              torch.float16: FO_LOGITS_F16})
+    try:
+        return _LOGIT_DTYPES[dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, not "
+                        f"{str(dtype).replace('torch.', '')}") from None
+
+
+def _row_strides(x, name: str):
+    """(rows, inner_rows, row_stride, outer_stride) of the leading dimensions of
+    a tensor whose last dimension is contiguous: one stride, or two of which
+    the first counts rows of the second (logits[:, :-1])."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) < 1:
+        raise ValueError(f"{name} needs a last dimension (the vocabulary)")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension (the vocabulary) must be contiguous")
+    if len(shape) == 2:
+        return shape[0], max(1, shape[0]), stride[0], 0
+    dims = []                        # (size, stride), merged where one stride covers two dimensions
+    for n, s in zip(shape[:-1], stride[:-1]):
+        if n == 1:
+            continue
+        if dims and dims[-1][1] == s * n:
+            dims[-1] = (dims[-1][0] * n, s)
+        else:
+            dims.append((n, s))
+    if len(dims) > 2:
+        raise ValueError(f"{name}: the leading dimensions must be covered by two strides (make it contiguous)")
+    if not dims:
+        return 1, 1, shape[-1], 0
+    if len(dims) == 1:
+        return dims[0][0], max(1, dims[0][0]), dims[0][1], 0
+    return dims[0][0] * dims[1][0], max(1, dims[1][0]), dims[1][1], dims[0][1]
+
+
+def _device_ptr(x, name: str) -> int:
+    if not x.is_cuda:
+        raise ValueError(f"{name}: the library reads and writes device memory: pass CUDA tensors")
+    cur = _current_device()
+    if x.device.index != cur:
+        raise ValueError(f"{name} is on cuda:{x.device.index} but the current device is cuda:{cur}; "
+                         "the library launches on the current device (use torch.cuda.device)")
+    return x.data_ptr()
+
+
+def logits_rows(x, temperature: float = 1.0, name: str = "logits") -> FoLogits:
+    """The ``fo_logits_t`` of a tensor [..., vocab] of bfloat16, float16 or
+    float32: any leading dimensions that two strides cover, the last contiguous."""
+    dt = _logit_dtype(x.dtype, name)
+    ptr = _device_ptr(x, name)
+    rows, inner, rs, os_ = _row_strides(x, name)
+    return FoLogits(ptr, rows, x.shape[-1], rs, inner, os_, float(temperature), dt, 0)
+
+
+def _logits_grad(logits: FoLogits, like, grad, name: str = "grad"):
+    """The ``fo_logits_grad_t`` of ``grad``, a tensor of the logits' shape and type."""
+    if grad is None:
+        return None
+    if grad.dtype != like.dtype:
+        raise TypeError(f"{name} must be {_dtype_names((like.dtype,))}, as the logits are, not "
+                        f"{str(grad.dtype).replace('torch.', '')}")
+    if grad.shape != like.shape:
+        raise ValueError(f"{name} must have the logits' shape {tuple(like.shape)}, not {tuple(grad.shape)}")
+    ptr = _device_ptr(grad, name)
+    rows, inner, rs, os_ = _row_strides(grad, name)
+    want = logits.inner_rows
+    if inner != want:               # one of the two needs a single stride where the other has two
+        if inner == rows:           # grad's rows r = o * want + i are one stride apart
+            os_ = rs * want
+        elif want == logits.rows:   # the logits take the grad's split
+            logits.inner_rows, logits.outer_stride = inner, logits.row_stride * inner
+        else:
+            raise ValueError(f"{name}: its leading dimensions are laid out unlike the logits'")
+    return FoLogitsGrad(ptr, rs, os_)
+
+
+def _teacher(ids, logits, lse, rows: int, temperature: float, tail: bool) -> FoTeacher:
+    d = _Dtypes.get()
+    if logits.shape != ids.shape or len(ids.shape) < 1:
+        raise ValueError(f"teacher_ids and teacher_logits must have one shape [..., k], not {tuple(ids.shape)} "
+                         f"and {tuple(logits.shape)}")
+    k = ids.shape[-1]
+    if ids.numel() != rows * k:
+        raise ValueError(f"teacher_ids holds {ids.numel()} entries; {rows} rows of logits need {rows * k}")
+    dt = _logit_dtype(logits.dtype, "teacher_logits")
+    if lse is not None and not tail:
+        raise ValueError("teacher_lse is read with tail=True only")
+    return FoTeacher(_ptr(ids, "teacher_ids", d["i32"]), _ptr(logits, "teacher_logits"),
+                     _ptr(lse, "teacher_lse", d["f32"], rows), float(temperature), k, dt, 1 if tail else 0, 0)
+
+
+def fo_token_logprobs(logits, tokens=None, top_k: int = 0, logp=None, entropy=None, top_ids=None, top_logp=None,
+                      stats=None, temperature: float = 1.0, stream=None):
+    x = logits_rows(logits, temperature)
+    n, d = x.rows, _Dtypes.get()
+    _check("fo_token_logprobs", lib().fo_token_logprobs(
+        ctypes.byref(x), _ptr(tokens, "tokens", d["i64"], n), int(top_k), _ptr(logp, "logp", d["f32"], n),
+        _ptr(entropy, "entropy", d["f32"], n), _ptr(top_ids, "top_ids", d["i32"], n * top_k),
+        _ptr(top_logp, "top_logp", d["f32"], n * top_k), _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS),
+        _stream(stream)))
+
+
+def fo_token_logprobs_grad(logits, stats, grad, tokens=None, g_logp=None, g_entropy=None, top_ids=None, g_top=None,
+                           top_k: int = 0, temperature: float = 1.0, stream=None):
+    x = logits_rows(logits, temperature)
+    g = _logits_grad(x, logits, grad)
+    n, d = x.rows, _Dtypes.get()
+    _check("fo_token_logprobs_grad", lib().fo_token_logprobs_grad(
+        ctypes.byref(x), _ptr(tokens, "tokens", d["i64"], n), int(top_k),
+        _ptr(top_ids, "top_ids", d["i32"], n * top_k), _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS),
+        _ptr(g_logp, "g_logp", d["f32"], n), _ptr(g_entropy, "g_entropy", d["f32"], n),
+        _ptr(g_top, "g_top", d["f32"], n * top_k), None if g is None else ctypes.byref(g), _stream(stream)))
+
+
+def fo_distill(logits, teacher_ids, teacher_logits, teacher_lse=None, row_weight=None, loss=None, stats=None,
+               grad=None, temperature: float = 1.0, teacher_temperature: float = 1.0, tail: bool = False, stream=None):
+    x = logits_rows(logits, temperature)
+    g = _logits_grad(x, logits, grad)
+    n, d = x.rows, _Dtypes.get()
+    t = _teacher(teacher_ids, teacher_logits, teacher_lse, n, teacher_temperature, tail)
+    _check("fo_distill", lib().fo_distill(
+        ctypes.byref(x), ctypes.byref(t), _ptr(row_weight, "row_weight", d["f32"], n), _ptr(loss, "loss", d["f32"], n),
+        _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS), None if g is None else ctypes.byref(g), _stream(stream)))
+
+
+def fo_distill_grad(logits, teacher_ids, teacher_logits, stats, g_loss, grad, teacher_lse=None,
+                    temperature: float = 1.0, teacher_temperature: float = 1.0, tail: bool = False, stream=None):
+    x = logits_rows(logits, temperature)
+    g = _logits_grad(x, logits, grad)
+    n, d = x.rows, _Dtypes.get()
+    t = _teacher(teacher_ids, teacher_logits, teacher_lse, n, teacher_temperature, tail)
+    _check("fo_distill_grad", lib().fo_distill_grad(
+        ctypes.byref(x), ctypes.byref(t), _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS),
+        _ptr(g_loss, "g_loss", d["f32"], n), None if g is None else ctypes.byref(g), _stream(stream)))
 
 
 FO_VERIFY_COUNTS = 6
