@@ -306,8 +306,8 @@ fo_status_t fo_verify_fast_arithmetic(uint64_t *counts, fo_stream_t stream);
  *   - a negative token or teacher id is no entry: it adds nothing, and a
  *     negative token's log probability is 0; an id of vocab or more makes the
  *     row's results NaN;
- *   - a row whose incoming gradients (or row weight) are all 0 is not read and
- *     gets an exactly zero gradient, whatever it holds.
+ *   - a row whose incoming gradients (or row weight) are all 0 gets an exactly
+ *     zero gradient (and loss), whatever it holds.
  */
 
 /* Element type of logits, of their gradient and of a teacher's logits. */

@@ -1,172 +1,408 @@
 // fo_logprobs.cu -- log probabilities of given tokens with entropy and top
 // alternatives, and their gradient.
-#include "fo_internal.h"
 #include "fo_loss.cuh"
 
 namespace fo {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCandidates = 1024;
 
-// Running statistics: m, Z = sum 2^((x-m)c), W = sum 2^t t with t = (x-m)c.
-struct Stat {
-    float m, z, w;
+struct Shared {
+    uint64_t bar;
+    Stat part[kWarps];
+    Stat mine;                      // this CTA's part, read by the others of the cluster
+    int count;                      // candidates found
+    int sums[kWarps];
+    uint64_t list[kCandidates];     // candidates in any order; later the lists of the other CTAs
+    uint64_t sorted[FO_MAX_TOP_K];  // this CTA's largest, descending
+    int sorted_n;
 };
 
-__device__ __forceinline__ Stat join(Stat a, Stat b, float c)
+__device__ __forceinline__ int block_sum(int v, Shared &sh)
 {
-    Stat r;
-    r.m = fmaxf(a.m, b.m);
-    const float mm = safe_max(r.m);
-    // the floor keeps W finite where one part's values are the type's lowest
-    const float da = a.z == 0.0f ? 0.0f : fmaxf((a.m - mm) * c, -1e30f);
-    const float db = b.z == 0.0f ? 0.0f : fmaxf((b.m - mm) * c, -1e30f);
-    const float ea = exp2_approx(da), eb = exp2_approx(db);
-    r.z = a.z * ea + b.z * eb;
-    r.w = (a.w + da * a.z) * ea + (b.w + db * b.z) * eb;
-    return r;
+    const int s = __reduce_add_sync(~0u, v);
+    if ((threadIdx.x & 31) == 0)
+        sh.sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    int t = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+        t += sh.sums[i];
+    __syncthreads();
+    return t;
 }
 
+// f(key, id) for every element of vector i of the row, held in `v`.
+template <class T, class F>
+__device__ __forceinline__ void each(const Row<T> &row, int i, const uint4 &v, F f)
+{
+    const typename T::raw *e = reinterpret_cast<const typename T::raw *>(&v);
+#pragma unroll
+    for (int k = 0; k < T::kPerVec; ++k) {
+        const int id = row.id(i, k);
+        if (id >= 0 && id < row.vocab)
+            f(order_key(T::widen(e[k])), id);
+    }
+}
+
+// The exact way for a part with very many candidates (most of it tied, or its
+// largest elements in few threads' hands): bisects the order keys for the
+// k-th largest value, then takes everything above it and, of the elements
+// equal to it, those with the lowest ids, in the order of ids. At most 32
+// passes over the part in shared memory, whatever it holds.
+template <class T>
+__device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, const uint4 *buf, int k, Shared &sh)
+{
+    uint32_t kth = 0;
+    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+        if (!(bit & T::kKeyBits))
+            break;
+        const uint32_t at = kth | bit;
+        int n = 0;
+        for (int i = threadIdx.x; i < p.n; i += kThreads)
+            each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int) { n += key >= at; });
+        if (block_sum(n, sh) >= k)
+            kth = at;
+    }
+    constexpr uint32_t mask = T::kKeyBits;   // below it a key is all 0 or all 1
+    if (threadIdx.x == 0)
+        sh.count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n; i += kThreads)
+        each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int id) {
+            if ((key & mask) > kth)
+                sh.list[atomicAdd(&sh.count, 1)] = ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id);
+        });
+    __syncthreads();
+    int have = sh.count;   // below k
+    for (int i0 = 0; i0 < p.n && have < k; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        int n = 0;
+        if (i < p.n)
+            each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int) { n += (key & mask) == kth; });
+        // ties before this thread's
+        int before = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int q = __shfl_up_sync(~0u, before, o);
+            before += (threadIdx.x & 31) >= o ? q : 0;
+        }
+        if ((threadIdx.x & 31) == 31)
+            sh.sums[threadIdx.x >> 5] = before;
+        __syncthreads();
+        int all = 0;
+        before -= n;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            before += w < (threadIdx.x >> 5) ? sh.sums[w] : 0;
+            all += sh.sums[w];
+        }
+        if (n)
+            each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int id) {
+                if ((key & mask) == kth && have + before < k)
+                    sh.list[have + before++] = ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id);
+            });
+        have = min(k, have + all);
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        sh.count = have;
+    __syncthreads();
+}
+
+// The part's largest elements (k, or all where it has fewer), descending, into
+// sh.sorted. `top` is the largest element of the vectors that this thread
+// holds (vectors threadIdx.x, threadIdx.x + kThreads, ...): the k-th largest of
+// the threads' maxima bounds the k-th largest element from below, and for
+// spread-out values few elements besides the top k reach it.
+template <class T>
+__device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const uint4 *buf, float top, int k, Shared &sh)
+{
+    const uint32_t mine = (int)threadIdx.x < p.n ? order_key(top) : 0;
+    uint32_t bound = 0;
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
+        if (__syncthreads_count(mine >= (bound | bit)) >= k)
+            bound |= bit;
+    if (mine >= bound)
+        for (int i = threadIdx.x; i < p.n; i += kThreads) {
+            const uint4 v = buf[i];
+            if (order_key(vec_max<T>(v)) < bound)
+                continue;
+            if (*(volatile int *)&sh.count > kCandidates)
+                break;
+            each<T>(row, p.v0 + i, v, [&](uint32_t key, int id) {
+                if (key >= bound) {
+                    const int at = atomicAdd(&sh.count, 1);
+                    if (at < kCandidates)
+                        sh.list[at] = ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id);
+                }
+            });
+        }
+    __syncthreads();
+    if (sh.count > kCandidates)
+        collect_exact<T>(row, p, buf, k, sh);
+    const int n = sh.count;
+    for (int i = threadIdx.x; i < n; i += kThreads) {   // no two keys are equal
+        const uint64_t key = sh.list[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j)
+            rank += sh.list[j] > key;
+        if (rank < k)
+            sh.sorted[rank] = key;
+    }
+    if (threadIdx.x == 0)
+        sh.sorted_n = min(n, k);
+    __syncthreads();
+}
+
+__device__ __forceinline__ float key_value(uint64_t key)
+{
+    const uint32_t o = (uint32_t)(key >> 32);
+    return __uint_as_float(o == 0xffffffffu ? 0x7fffffffu : o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
+// One row by a cluster of CTAs, each holding a part of it in shared memory:
+// the logits are read from device memory once, by bulk copies, and the
+// statistics and the parts' top lists are joined through distributed shared
+// memory.
 template <class T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
 {
-    __shared__ Stat part[kThreads / 32];
-    __shared__ unsigned long long best[kThreads / 32];
-    const int64_t r = blockIdx.x;
-    const typename T::raw *x = static_cast<const typename T::raw *>(a.in.data) + row_offset(a.in, r, a.in.row_stride, a.in.outer_stride);
-    const int64_t v = a.in.vocab;
-    const float c = a.in.c;
-    Stat s = {-kInf, 0.0f, 0.0f};
-    // sums of 16 first: a chain of roundings of equal terms does not average out
-    for (int64_t j = threadIdx.x; j < v; j += 16 * kThreads) {
-        Stat b = {-kInf, 0.0f, 0.0f};
-        for (int64_t i = j; i < v && i < j + 16 * kThreads; i += kThreads) {
-            const float xv = T::widen(x[i]);
-            if (xv != -kInf)
-                b = join(b, Stat{xv != xv ? b.m : xv, xv - xv == 0.0f ? 1.0f : xv - xv, 0.0f}, c);
-        }
-        s = join(s, b, c);
-    }
-    for (int o = 16; o; o >>= 1)
-        s = join(s, Stat{__shfl_xor_sync(~0u, s.m, o), __shfl_xor_sync(~0u, s.z, o), __shfl_xor_sync(~0u, s.w, o)}, c);
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = part[0];
-    for (int i = 1; i < kThreads / 32; ++i)
-        s = join(s, part[i], c);
-    const float ln_z = logf(s.z);
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    uint4 *buf = reinterpret_cast<uint4 *>(dynamic);
+    __shared__ Shared sh;
+    const uint32_t size = cluster_size(), rank = cluster_rank();
+    const int64_t r = blockIdx.x / size;
+    const Row<T> row(a.in, r);
+    const Part p = part_of(row, rank, size);
     if (threadIdx.x == 0) {
-        const float h = s.z == 0.0f ? 0.0f : ln_z - kLn2 * (s.w / s.z);
-        if (a.logp) {
-            const int64_t t = a.tokens[r];
-            a.logp[r] = t < 0 ? 0.0f : t >= v ? __int_as_float(0x7fffffff) : (float)log_prob(T::widen(x[t]), s.m, s.z, ln_z, a.in.inv_t);
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&sh.bar)) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.count = 0;
+    }
+    __syncthreads();
+    start_part<T>(row, p, buf, &sh.bar);
+    int64_t token = -1;
+    float token_x = 0.0f;
+    if (rank == 0 && threadIdx.x == 0 && a.logp) {
+        token = a.tokens[r];
+        if (token >= 0 && token < row.vocab)
+            token_x = T::widen(row.x[token]);
+    }
+    __syncthreads();
+    const bool arrived = wait_part(&sh.bar);
+
+    Stat s = {-kInf, 0.0f, 0.0f};
+    float top = -kInf;
+    for (int i = threadIdx.x; i < p.n; i += kThreads)
+        absorb<T, true>(s, top, buf[i], a.in);
+    if (!arrived)
+        s.z = __int_as_float(0x7fffffff);
+    s = warp_join<true>(s, a.in);
+    if ((threadIdx.x & 31) == 0)
+        sh.part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = sh.part[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i)
+        s = join<true>(s, sh.part[i], a.in);
+    if (a.k)
+        find_top<T>(row, p, buf, top, a.k, sh);
+    if (size > 1) {
+        if (threadIdx.x == 0)
+            sh.mine = s;
+        cluster_arrive();
+        cluster_wait();
+        Stat all = {-kInf, 0.0f, 0.0f};
+        for (uint32_t i = 0; i < size; ++i) {
+            const uint32_t at = map_shared(&sh.mine, i);
+            all = join<true>(all, Stat{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)}, a.in);
         }
+        s = all;
+    }
+    const float ln_z = logf(s.z);
+    if (rank == 0 && threadIdx.x == 0) {
+        const float h = s.z == 0.0f ? 0.0f : ln_z - kLn2 * (s.w / s.z);
+        if (a.logp)
+            a.logp[r] = token < 0 ? 0.0f : token >= row.vocab ? __int_as_float(0x7fffffff) : (float)log_prob(token_x, s.m, s.z, ln_z, a.in.inv_t);
         if (a.entropy)
             a.entropy[r] = h;
         if (a.stats)
             a.stats[r] = make_float4(s.m, s.z, h, 0.0f);
     }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < a.k; ++k) {
-        unsigned long long b = 0;
-        for (int64_t j = threadIdx.x; j < v; j += kThreads) {
-            const unsigned long long key = entry_key(T::widen(x[j]), (uint32_t)j);
-            if (key < last && key > b)
-                b = key;
+    if (a.k) {
+        // an element's place among all parts' lists: its own place and, for
+        // each other list, how many of that are larger
+        const int k = a.k;
+        if (size > 1) {
+            for (uint32_t i = threadIdx.x; i < size * k; i += kThreads) {
+                const uint32_t from = i / k, j = i % k;
+                sh.list[i] = ld_cluster_u64(map_shared(&sh.sorted[j], from));
+            }
+            if (threadIdx.x < size)
+                sh.sums[threadIdx.x] = (int)__float_as_int(ld_cluster_f32(map_shared(&sh.sorted_n, threadIdx.x)));
+            __syncthreads();
         }
-        for (int o = 16; o; o >>= 1) {
-            const unsigned long long q = __shfl_xor_sync(~0u, b, o);
-            b = q > b ? q : b;
+        if ((int)threadIdx.x < sh.sorted_n) {
+            const uint64_t key = sh.sorted[threadIdx.x];
+            int place = threadIdx.x;
+            for (uint32_t i = 0; i < size && size > 1; ++i) {
+                if (i == rank)
+                    continue;
+                int lo = 0, hi = sh.sums[i];   // the first place whose key is smaller
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.list[i * k + mid] > key)
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                place += lo;
+            }
+            if (place < k) {
+                a.top_ids[r * k + place] = (int32_t)entry_id(key);
+                a.top_logp[r * k + place] = (float)log_prob(key_value(key), s.m, s.z, ln_z, a.in.inv_t);
+            }
         }
-        if ((threadIdx.x & 31) == 0)
-            best[threadIdx.x >> 5] = b;
-        __syncthreads();
-        last = best[0];
-        for (int i = 1; i < kThreads / 32; ++i)
-            last = best[i] > last ? best[i] : last;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const uint32_t id = entry_id(last);
-            a.top_ids[r * a.k + k] = (int32_t)id;
-            a.top_logp[r * a.k + k] = (float)log_prob(T::widen(x[id]), s.m, s.z, ln_z, a.in.inv_t);
-        }
+    }
+    if (!arrived)
+        wait_part(&sh.bar);   // its copies are not left behind
+    if (size > 1) {   // no CTA leaves while another reads its shared memory
+        cluster_arrive();
+        cluster_wait();
     }
 }
 
 // dx_j = (1/T) [ sum of the weights of entries at j - p_j (G + h (ln p_j + H)) ],
-// G the sum of all entries' weights, the entries being the token and the top ids.
-template <class T>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a)
+// G the sum of all entries' weights, the entries being the token and the top
+// ids. With t = (x_j - m) c: dx_j = 2^t (alpha + beta t), plus the weights.
+template <class T, int kVecs>
+__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a, int chunks)
 {
+    typedef typename T::raw raw;
     __shared__ int64_t ids[FO_MAX_TOP_K + 1];
     __shared__ float weight[FO_MAX_TOP_K + 1];
-    const int64_t r = blockIdx.x;
-    const typename T::raw *x = static_cast<const typename T::raw *>(a.in.data) + row_offset(a.in, r, a.in.row_stride, a.in.outer_stride);
-    typename T::raw *g = static_cast<typename T::raw *>(a.out.data) + row_offset(a.in, r, a.out.row_stride, a.out.outer_stride);
-    const int64_t v = a.in.vocab;
+    const int64_t r = blockIdx.x / (unsigned)chunks;
+    const int v0 = (int)(blockIdx.x % (unsigned)chunks) * (kVecs * kThreads);
+    const Row<T> row(a.in, r);
+    raw *g = static_cast<raw *>(a.out.data) + row_offset(a.in, r, a.out.row_stride, a.out.outer_stride);
+    const int tid = threadIdx.x;
+    uint4 v[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int at = v0 + i * kThreads + tid;
+        if (at >= row.full0 && at < row.full1)
+            v[i] = __ldcs(row.vec(at));
+        else if (at < row.vecs) {
+            raw *e = reinterpret_cast<raw *>(&v[i]);
+#pragma unroll
+            for (int k = 0; k < T::kPerVec; ++k) {
+                const int id = row.id(at, k);
+                e[k] = id >= 0 && id < row.vocab ? row.x[id] : T::narrow(-kInf);
+            }
+        }
+    }
     const float4 st = a.stats[r];
     const float m = safe_max(st.x), inv_z = st.y == 0.0f ? 0.0f : 1.0f / st.y, ln_z = logf(st.y);
     const float h = a.g_entropy ? a.g_entropy[r] : 0.0f;
-    if (threadIdx.x <= a.k) {
-        const int i = (int)threadIdx.x - 1;
-        ids[threadIdx.x] = i < 0 ? (a.g_logp ? a.tokens[r] : -1) : a.top_ids[r * a.k + i];
-        weight[threadIdx.x] = i < 0 ? (a.g_logp ? a.g_logp[r] : 0.0f) : a.g_top[r * a.k + i];
+    if (tid <= a.k) {
+        const int i = tid - 1;
+        ids[tid] = i < 0 ? (a.g_logp ? a.tokens[r] : -1) : a.top_ids[r * a.k + i];
+        weight[tid] = i < 0 ? (a.g_logp ? a.g_logp[r] : 0.0f) : a.g_top[r * a.k + i];
     }
     __syncthreads();
     float sum = 0.0f;
     bool any = h != 0.0f;
     for (int i = 0; i <= a.k; ++i) {
-        if (ids[i] >= 0) {
-            any = any || weight[i] != 0.0f;
-            sum += weight[i];
-        }
-        if (ids[i] >= v && weight[i] != 0.0f)
-            sum = __int_as_float(0x7fffffff);
+        if (ids[i] < 0 || weight[i] == 0.0f)
+            continue;
+        any = true;
+        sum += ids[i] >= row.vocab ? __int_as_float(0x7fffffff) : weight[i];
     }
     const bool zero = !any || st.y == 0.0f;
-    for (int64_t j = threadIdx.x; j < v; j += kThreads) {
-        float d = 0.0f;
-        if (!zero) {
-            float w = 0.0f;
-            for (int i = 0; i <= a.k; ++i)
-                if (ids[i] == j)
-                    w += weight[i];
-            float t;
-            const float e = grad_exp<T>(distance(T::widen(x[j]), m, a.in), a.in, t);
-            const float b = h == 0.0f ? 0.0f : h * (__fmaf_rn(t, kLn2, -ln_z) + st.z);
-            d = (w - e * (inv_z / T::kShift * (sum + b))) * a.in.inv_t;
-        }
-        g[j] = T::narrow(d);
+    const float p_scale = inv_z * (a.in.inv_t / T::kShift);
+    const float alpha = h == 0.0f ? -p_scale * sum : -p_scale * (sum + h * (st.z - ln_z));
+    const float beta = h == 0.0f ? 0.0f : -p_scale * h * kLn2;
+
+    // the entries of this chunk; the first of equal ids takes the weight of all
+    const int end = row.id(v0 + kVecs * kThreads, 0);
+    bool entry = false;
+    float entry_value = 0.0f;
+    if (!zero && tid <= a.k && ids[tid] >= 0 && ids[tid] >= row.id(v0, 0) && ids[tid] < end && ids[tid] < row.vocab) {
+        float w = 0.0f;
+        int first = tid;
+        for (int i = a.k; i >= 0; --i)
+            if (ids[i] == ids[tid]) {
+                w += weight[i];
+                first = i;
+            }
+        entry = first == tid;
+        float t;
+        const float e = grad_exp<T>(distance(T::widen(row.x[ids[tid]]), m, a.in), a.in, t);
+        entry_value = __fmaf_rn(w, a.in.inv_t, e * __fmaf_rn(beta, t, alpha));
     }
+    __syncthreads();   // the entries' logits are read before a gradient in their place is written
+    const bool aligned = same_phase(row, g);
+    const f2 nm = splat(-m), al = splat(alpha), be = splat(beta);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int at = v0 + i * kThreads + tid;
+        if (at >= row.vecs)
+            break;
+        f2 x[T::kPerVec / 2];
+        widen_vec<T>(v[i], x);
+#pragma unroll
+        for (int k = 0; k < T::kPerVec / 2; ++k) {
+            float p, q;
+            unpk(add2(x[k], nm), p, q);
+            f2 t;
+            const f2 e = grad_exp2<T>(pk(max_nan(p, a.in.d_min), max_nan(q, a.in.d_min)), a.in, t);
+            x[k] = mul2(e, fma2(be, t, al));
+        }
+        const uint4 d = zero ? make_uint4(0, 0, 0, 0) : narrow_vec<T>(x);
+        if (aligned && at >= row.full0 && at < row.full1)
+            store_stream(g + row.id(at, 0), d);
+        else
+            store_edge<T>(g, row, at, d);
+    }
+    __syncthreads();
+    if (entry)
+        g[ids[tid]] = T::narrow(entry_value);
+}
+
+template <class T>
+cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
+{
+    return launch_cluster(logprobs_kernel<T>, a, a.in.rows, a.in.vocab * sizeof(typename T::raw), kThreads, stream);
+}
+
+template <class T>
+cudaError_t launch(const LogprobGradArgs &a, cudaStream_t stream)
+{
+    const int64_t vecs = a.in.vocab / T::kPerVec + 2;
+    if (vecs * a.in.rows >= (int64_t)sm_count() * 8 * kThreads * 8) {
+        const int64_t chunks = (vecs + 8 * kThreads - 1) / (8 * kThreads);
+        logprobs_grad_kernel<T, 8><<<(unsigned)(chunks * a.in.rows), kThreads, 0, stream>>>(a, (int)chunks);
+    } else {
+        const int64_t chunks = (vecs + kThreads - 1) / kThreads;
+        logprobs_grad_kernel<T, 1><<<(unsigned)(chunks * a.in.rows), kThreads, 0, stream>>>(a, (int)chunks);
+    }
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <class A>
+cudaError_t by_type(int dtype, const A &a, cudaStream_t stream)
+{
+    return dtype == 0 ? launch<Bf16>(a, stream) : dtype == 1 ? launch<F32>(a, stream) : launch<F16>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_token_logprobs(int dtype, const LogprobArgs &a, cudaStream_t stream)
-{
-    const unsigned grid = (unsigned)a.in.rows;
-    if (dtype == 0)
-        logprobs_kernel<Bf16><<<grid, kThreads, 0, stream>>>(a);
-    else if (dtype == 1)
-        logprobs_kernel<F32><<<grid, kThreads, 0, stream>>>(a);
-    else
-        logprobs_kernel<F16><<<grid, kThreads, 0, stream>>>(a);
-    count_launch();
-    return cudaGetLastError();
-}
-
-cudaError_t launch_token_logprobs_grad(int dtype, const LogprobGradArgs &a, cudaStream_t stream)
-{
-    const unsigned grid = (unsigned)a.in.rows;
-    if (dtype == 0)
-        logprobs_grad_kernel<Bf16><<<grid, kThreads, 0, stream>>>(a);
-    else if (dtype == 1)
-        logprobs_grad_kernel<F32><<<grid, kThreads, 0, stream>>>(a);
-    else
-        logprobs_grad_kernel<F16><<<grid, kThreads, 0, stream>>>(a);
-    count_launch();
-    return cudaGetLastError();
-}
+cudaError_t launch_token_logprobs(int dtype, const LogprobArgs &a, cudaStream_t stream) { return by_type(dtype, a, stream); }
+cudaError_t launch_token_logprobs_grad(int dtype, const LogprobGradArgs &a, cudaStream_t stream) { return by_type(dtype, a, stream); }
 
 }  // namespace fo

@@ -6,26 +6,64 @@
 
 #include <cstdint>
 
+#include "fo_internal.h"
 #include "fo_loss.h"
+#include "fo_pair.cuh"
 
 namespace fo {
 
-// Element types by fo_logit_dtype_t.
+// Element types by fo_logit_dtype_t. A vector is 16 bytes, kPerVec elements.
 struct Bf16 {
     typedef uint16_t raw;
-    static constexpr float kShift = 0x1p24f;   // see grad_exp
+    static constexpr int kPerVec = 8;
+    static constexpr float kShift = 0x1p24f;              // see grad_exp
+    static constexpr uint32_t kKeyBits = 0xffff0000u;     // the part of an order key that differs between values
     static __device__ __forceinline__ float widen(raw v) { return __uint_as_float((uint32_t)v << 16); }
     static __device__ __forceinline__ raw narrow(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+    static __device__ __forceinline__ f2 widen2(uint32_t w) { return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+    static __device__ __forceinline__ uint32_t narrow2(f2 v)
+    {
+        float lo, hi;
+        unpk(v, lo, hi);
+        uint32_t d;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
 };
 struct F16 {
     typedef uint16_t raw;
+    static constexpr int kPerVec = 8;
     static constexpr float kShift = 0x1p24f;
+    static constexpr uint32_t kKeyBits = 0xffffe000u;
     static __device__ __forceinline__ float widen(raw v) { return __half2float(__ushort_as_half(v)); }
     static __device__ __forceinline__ raw narrow(float f) { return __half_as_ushort(__float2half_rn(f)); }
+    static __device__ __forceinline__ f2 widen2(uint32_t w) { return pk(widen((raw)w), widen((raw)(w >> 16))); }
+    static __device__ __forceinline__ uint32_t narrow2(f2 v)
+    {
+        float lo, hi;
+        unpk(v, lo, hi);
+        uint32_t d;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
 };
 struct F32 {
     typedef float raw;
+    static constexpr int kPerVec = 4;
     static constexpr float kShift = 1.0f;
+    static constexpr uint32_t kKeyBits = 0xffffffffu;
     static __device__ __forceinline__ float widen(raw v) { return v; }
     static __device__ __forceinline__ raw narrow(float f) { return f; }
 };
@@ -108,6 +146,346 @@ __device__ __forceinline__ float load_dtype(const void *p, int64_t i, int dtype)
         return static_cast<const float *>(p)[i];
     const uint16_t v = static_cast<const uint16_t *>(p)[i];
     return dtype == 0 ? Bf16::widen(v) : F16::widen(v);
+}
+
+// --- a row, in 16-byte vectors -------------------------------------------------
+
+// The pairs of FP32 values of a vector, and back.
+template <class T>
+__device__ __forceinline__ void widen_vec(const uint4 &v, f2 (&x)[T::kPerVec / 2])
+{
+    x[0] = T::widen2(v.x);
+    x[1] = T::widen2(v.y);
+    x[2] = T::widen2(v.z);
+    x[3] = T::widen2(v.w);
+}
+template <>
+__device__ __forceinline__ void widen_vec<F32>(const uint4 &v, f2 (&x)[2])
+{
+    x[0] = pk(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = pk(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <class T>
+__device__ __forceinline__ uint4 narrow_vec(const f2 (&x)[T::kPerVec / 2])
+{
+    return make_uint4(T::narrow2(x[0]), T::narrow2(x[1]), T::narrow2(x[2]), T::narrow2(x[3]));
+}
+template <>
+__device__ __forceinline__ uint4 narrow_vec<F32>(const f2 (&x)[2])
+{
+    float a, b, c, d;
+    unpk(x[0], a, b);
+    unpk(x[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+}
+
+// The largest element of a vector; NaN where it holds one.
+template <class T>
+__device__ __forceinline__ float vec_max(const uint4 &v)
+{
+    const uint32_t w = T::max2(T::max2(v.x, v.y), T::max2(v.z, v.w));
+    return max_nan(T::widen((typename T::raw)w), T::widen((typename T::raw)(w >> 16)));
+}
+template <>
+__device__ __forceinline__ float vec_max<F32>(const uint4 &v)
+{
+    return max_nan(max3_nan(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)), __uint_as_float(v.w));
+}
+
+// A row lies in vectors counted from the 16-byte boundary at or before its
+// first element, which is element `phase` of vector 0. The first and the last
+// vector may reach beyond the row.
+template <class T>
+struct Row {
+    typedef typename T::raw raw;
+    const raw *x;      // the row
+    int phase, vocab;
+    int vecs;          // vectors that hold elements of the row
+    int full0, full1;  // those wholly inside it: [full0, full1)
+
+    __device__ __forceinline__ Row(const LogitRows &in, int64_t r)
+        : x(static_cast<const raw *>(in.data) + row_offset(in, r, in.row_stride, in.outer_stride)), vocab((int)in.vocab)
+    {
+        phase = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(raw));
+        vecs = (phase + vocab + T::kPerVec - 1) / T::kPerVec;
+        full0 = phase ? 1 : 0;
+        full1 = (phase + vocab) / T::kPerVec;
+    }
+    // The element that vector i holds at place e, as an id (outside [0, vocab) beyond the row's ends).
+    __device__ __forceinline__ int id(int i, int e) const { return i * T::kPerVec + e - phase; }
+    __device__ __forceinline__ const uint4 *vec(int i) const { return reinterpret_cast<const uint4 *>(x - phase) + i; }
+};
+
+// Running statistics of a set of logits: m their maximum, z = sum 2^((x-m)c).
+// w is the same sum of other elements (distillation), or sum 2^t t, t = (x-m)c
+// (entropy). An empty set: {-inf, 0, 0}.
+struct Stat {
+    float m, z, w;
+};
+
+template <bool kEntropy>
+__device__ __forceinline__ void rescale(Stat &s, float m, const LogitRows &in)
+{
+    const float t = __fmul_rn(max_nan(__fsub_rn(s.m, m), in.d_min), in.c);   // s.m = -inf: 2^-160, which is 0
+    const float f = exp2_approx(t);
+    s.w = __fmul_rn(kEntropy ? __fmaf_rn(t, s.z, s.w) : s.w, f);
+    s.z = __fmul_rn(s.z, f);
+    s.m = m;
+}
+
+template <bool kEntropy>
+__device__ __forceinline__ Stat join(Stat a, Stat b, const LogitRows &in)
+{
+    const float m = fmaxf(a.m, b.m);
+    if (m != -kInf) {   // else both are empty, or all -inf: nothing to scale
+        rescale<kEntropy>(a, m, in);
+        rescale<kEntropy>(b, m, in);
+    }
+    return Stat{m, a.z + b.z, a.w + b.w};
+}
+
+template <bool kEntropy>
+__device__ __forceinline__ Stat warp_join(Stat s, const LogitRows &in)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        s = join<kEntropy>(s, Stat{__shfl_xor_sync(~0u, s.m, o), __shfl_xor_sync(~0u, s.z, o), __shfl_xor_sync(~0u, s.w, o)}, in);
+    return s;
+}
+
+// Adds a vector to the statistics, and its maximum to `top` (NaN stays).
+// The sum of the vector is formed first: chains of additions stay short.
+template <class T, bool kEntropy>
+__device__ __forceinline__ void absorb(Stat &s, float &top, const uint4 &v, const LogitRows &in)
+{
+    const float vm = vec_max<T>(v);
+    top = max_nan(top, vm);
+    if (vm > s.m)
+        rescale<kEntropy>(s, vm, in);
+    const f2 nm = splat(-safe_max(s.m)), c = splat(in.c);
+    f2 x[T::kPerVec / 2];
+    widen_vec<T>(v, x);
+    f2 z[T::kPerVec / 2], w = 0;
+#pragma unroll
+    for (int i = 0; i < T::kPerVec / 2; ++i) {
+        f2 d = add2(x[i], nm);
+        float a, b;
+        if (kEntropy) {   // t stays finite: 0 times it is 0
+            unpk(d, a, b);
+            d = pk(max_nan(a, in.d_min), max_nan(b, in.d_min));
+        }
+        const f2 t = mul2(d, c);
+        unpk(t, a, b);
+        z[i] = pk(exp2_approx(a), exp2_approx(b));
+        if (kEntropy)
+            w = i ? fma2(z[i], t, w) : mul2(z[i], t);
+    }
+#pragma unroll
+    for (int n = T::kPerVec / 4; n; n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            z[i] = add2(z[i], z[i + n]);
+    float a, b;
+    unpk(z[0], a, b);
+    s.z = __fadd_rn(s.z, __fadd_rn(a, b));
+    if (kEntropy) {
+        unpk(w, a, b);
+        s.w = __fadd_rn(s.w, __fadd_rn(a, b));
+    }
+}
+
+// --- rows held in the shared memory of a cluster -----------------------------------
+
+__device__ __forceinline__ uint32_t shared_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The address of `p`, of this CTA's shared memory, in that of another CTA of the cluster.
+__device__ __forceinline__ uint32_t map_shared(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ double ld_cluster_f64(uint32_t a)
+{
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a)
+{
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// This CTA's vectors of a row: [v0, v0 + n), at `buf` in shared memory.
+struct Part {
+    int v0, n;
+};
+template <class T>
+__device__ __forceinline__ Part part_of(const Row<T> &row, uint32_t rank, uint32_t size)
+{
+    const int per = (row.vecs + (int)size - 1) / (int)size;
+    const int v0 = min((int)rank * per, row.vecs);
+    return Part{v0, min(per, row.vecs - v0)};
+}
+
+constexpr int kCopyBytes = 16384;   // of one bulk copy
+
+// Starts the copies of a part into shared memory. The vectors wholly inside
+// the row come by bulk copies that `bar` counts; those that reach beyond its
+// ends element by element (no byte outside the row is read), filled up with
+// -inf. Thread 0 has initialised `bar` for one arrival; all threads call this,
+// and a barrier of the CTA has to follow before the others' elements are read.
+template <class T>
+__device__ __forceinline__ void start_part(const Row<T> &row, const Part &p, uint4 *buf, uint64_t *bar)
+{
+    typedef typename T::raw raw;
+    const int lo = max(p.v0, row.full0), hi = min(p.v0 + p.n, row.full1);
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(bar)), "r"(bytes) : "memory");
+        for (uint32_t at = 0; at < bytes; at += kCopyBytes) {
+            const uint32_t size = min((uint32_t)kCopyBytes, bytes - at);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             shared_address(buf + (lo - p.v0)) + at),
+                         "l"(reinterpret_cast<const char *>(row.vec(lo)) + at), "r"(size), "r"(shared_address(bar))
+                         : "memory");
+        }
+    }
+    const int side = threadIdx.x / T::kPerVec, e = threadIdx.x % T::kPerVec;
+    const int i = side == 0 ? 0 : row.vecs - 1;
+    if (side < 2 && (i < row.full0 || i >= row.full1) && i >= p.v0 && i < p.v0 + p.n) {
+        const int id = row.id(i, e);
+        raw v = T::narrow(-kInf);
+        if (id >= 0 && id < row.vocab)
+            v = row.x[id];
+        reinterpret_cast<raw *>(buf + (i - p.v0))[e] = v;
+    }
+}
+
+// Waits for the copies. The number of tries is bounded (each one sleeps in the
+// hardware for a while): a copy that never ends gives false, not a hang.
+__device__ __forceinline__ bool wait_part(uint64_t *bar)
+{
+    for (int i = 0; i < 1 << 20; ++i) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n"
+                     " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n"
+                     " selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done)
+                     : "r"(shared_address(bar))
+                     : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
+
+// --- gradients -----------------------------------------------------------------
+
+// Element e of a stored vector goes to its place in the gradient's row.
+template <class T>
+__device__ __forceinline__ void store_edge(typename T::raw *g, const Row<T> &row, int i, const uint4 &v)
+{
+    const typename T::raw *e = reinterpret_cast<const typename T::raw *>(&v);
+#pragma unroll
+    for (int k = 0; k < T::kPerVec; ++k) {
+        const int id = row.id(i, k);
+        if (id >= 0 && id < row.vocab)
+            g[id] = e[k];
+    }
+}
+
+__device__ __forceinline__ void store_stream(void *p, const uint4 &v) { __stcs(static_cast<uint4 *>(p), v); }
+
+// Whether vectors of the logits' row are vectors of the gradient's too.
+template <class T>
+__device__ __forceinline__ bool same_phase(const Row<T> &row, const typename T::raw *g)
+{
+    return ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(row.x)) & 15) == 0;
+}
+
+// grad_exp for a pair, d not held at d_min (e is 0 there; t may be -inf).
+template <class T>
+__device__ __forceinline__ f2 grad_exp2(f2 d, const LogitRows &in, f2 &t)
+{
+    const f2 c = splat(in.c);
+    float a, b;
+    t = mul2(d, c);
+    if (sizeof(typename T::raw) == 2) {
+        unpk(fma2(d, c, splat(24.0f)), a, b);
+        return pk(exp2_approx(a), exp2_approx(b));
+    }
+    unpk(t, a, b);
+    asm("ex2.approx.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.f32 %0, %0;" : "+f"(b));
+    const f2 e = pk(a, b), minus_one = splat(-1.0f);
+    const f2 r = fma2(d, splat(in.c_lo), fma2(d, c, mul2(t, minus_one)));
+    return fma2(e, mul2(r, splat(kLn2)), e);
+}
+
+// --- launches ------------------------------------------------------------------
+
+constexpr int kMaxCluster = 8;
+
+// A row by a cluster: the smallest power of two of CTAs whose parts are at
+// most kPartBytes (three such CTAs share an SM, so that one computes while the
+// others load); more while the grid would leave SMs without a CTA and parts
+// stay above kSmallPart.
+constexpr int64_t kPartBytes = 64 * 1024;
+constexpr int64_t kSmallPart = 8 * 1024;
+
+template <class Args>
+cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, int64_t row_bytes, int threads, cudaStream_t stream)
+{
+    int size = 1;
+    while (size < kMaxCluster && (row_bytes > size * kPartBytes ||
+                                  (rows * size < 2 * sm_count() && row_bytes > size * kSmallPart)))
+        size *= 2;
+    const int64_t vecs = (row_bytes + 30) / 16;   // at any alignment
+    const size_t bytes = (size_t)((vecs + size - 1) / size) * 16;
+    cudaError_t e = cudaSuccess;
+    if (bytes > 32 * 1024)   // with the static part, beyond what a kernel gets unasked
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * size));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = size > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    count_launch();
+    const cudaError_t last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
 }
 
 }  // namespace fo

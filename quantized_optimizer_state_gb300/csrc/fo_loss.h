@@ -26,8 +26,8 @@ struct GradRows {
 
 // Statistics by row, saved for the gradients:
 //   log probabilities: {m, Z, H, unused}
-//   distillation:      {m, Z, A, B}: dKL/ds_j = A p_j - q_j for a listed token,
-//                      (A - B) p_j for another, B = q_rest / p_rest (0 without tail)
+//   distillation:      {m, Z, m_r, F}: m_r the largest logit that is not listed,
+//                      F 2^((x_j - m_r) c) the gradient of KL by s_j at such a j
 struct LogprobArgs {
     LogitRows in;
     const int64_t *tokens;   // may be null (then logp is)

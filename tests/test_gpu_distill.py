@@ -154,6 +154,22 @@ def test_rest_of_the_student_is_summed_not_subtracted(mass):
     assert ((got - rest).abs() <= 2.0 ** -17 * rest.abs()).all()
 
 
+@pytest.mark.parametrize("gap", [60.0, 100.0, 300.0])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_rest_far_below_the_listed_logits(gap, dtype):
+    """A rest whose probability FP32 cannot hold still has a finite loss and its own share of the gradient."""
+    v = 3001
+    x = make(2, v, dtype, seed=3, scale=1.0)
+    x.sub_(gap / 2)
+    ids = torch.tensor([[0, 10, 100, 3000], [1, 2, 3, 4]], dtype=torch.int32, device="cuda")
+    x.scatter_(1, ids.long(), gap / 2)
+    y = torch.log(torch.tensor([[0.4, 0.3, 0.1, 0.1]] * 2, device="cuda"))
+    loss, grad = check(x, ids, y, tail=True)
+    assert torch.isfinite(loss).all() and (loss > 0.05 * gap).all()
+    rest = grad.double().scatter_(1, ids.long(), 0.0).sum(1)     # minus what the teacher leaves for the rest
+    assert (rest + 0.1).abs().max() < 0.1 * (2.0 ** -8 if dtype != F32 else 2.0 ** -17)
+
+
 def test_gradient_against_differences():
     n, v, k, eps = 3, 41, 6, 2.0 ** -6
     x = make(n, v, F32, seed=21, scale=1.5)
