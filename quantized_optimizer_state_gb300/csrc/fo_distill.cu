@@ -7,6 +7,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int64_t kPartBytes = 64 * 1024;
 constexpr int kEntryWarps = FO_MAX_TOP_K / 32;   // warps that hold an entry a thread
 
 // The teacher's row: ids (-1: none), q and ln q.
@@ -114,7 +115,7 @@ struct PartSums {
 struct Shared {
     uint64_t bar;
     Entries t;
-    Stat part[kWarps];
+    Stat part[kWarps + 1];
     Stat listed[kEntryWarps];
     double dot[kEntryWarps];
     float q[kEntryWarps];
@@ -222,20 +223,14 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(DistillArgs a)
     }
     __syncthreads();
 
-    Stat rest = {-kInf, 0.0f, 0.0f};
-    float top = -kInf;
+    Running<T, false> run;
+#pragma unroll 2
     for (int i = tid; i < p.n; i += kThreads)
-        absorb<T, false>(rest, top, buf[i], a.in);
+        run.add(buf[i], a.in);
+    Stat rest = run.stat(a.in);
     if (!arrived)
         rest.z = __int_as_float(0x7fffffff);
-    rest = warp_join<false>(rest, a.in);
-    if ((tid & 31) == 0)
-        sh.part[tid >> 5] = rest;
-    __syncthreads();
-    rest = sh.part[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i)
-        rest = join<false>(rest, sh.part[i], a.in);
+    rest = block_join<false, kWarps>(rest, sh.part, a.in);
     float qs = (sh.q[0] + sh.q[1]) + (sh.q[2] + sh.q[3]);
     double dot = (sh.dot[0] + sh.dot[1]) + (sh.dot[2] + sh.dot[3]);
     if (size > 1) {
@@ -243,11 +238,9 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(DistillArgs a)
             sh.mine = PartSums{rest, listed, qs, dot};
         cluster_arrive();
         cluster_wait();
-        rest = listed = Stat{-kInf, 0.0f, 0.0f};
-        for (uint32_t i = 0; i < size; ++i) {
-            rest = join<false>(rest, ld_cluster_stat(map_shared(&sh.mine.rest, i)), a.in);
-            listed = join<false>(listed, ld_cluster_stat(map_shared(&sh.mine.listed, i)), a.in);
-        }
+        const uint32_t from = (tid & 7) % size;
+        rest = warp_join<false>(ld_cluster_stat(map_shared(&sh.mine.rest, from)), a.in, size);
+        listed = warp_join<false>(ld_cluster_stat(map_shared(&sh.mine.listed, from)), a.in, size);
         if (rank == 0 && tid < 32) {
             qs = 0.0f;
             dot = 0.0;
@@ -331,16 +324,8 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(DistillGradArgs 
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int at = v0 + i * kThreads + tid;
-        if (at >= row.full0 && at < row.full1)
-            v[i] = __ldcs(row.vec(at));
-        else if (at < row.vecs) {
-            raw *e = reinterpret_cast<raw *>(&v[i]);
-#pragma unroll
-            for (int k = 0; k < T::kPerVec; ++k) {
-                const int id = row.id(at, k);
-                e[k] = id >= 0 && id < row.vocab ? row.x[id] : T::narrow(-kInf);
-            }
-        }
+        if (at < row.vecs)
+            v[i] = load_vec(row, at);
     }
     if (tid < 32)
         read_teacher(t, a.teacher, r, row.vocab);
@@ -380,7 +365,14 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(DistillGradArgs 
 template <class T>
 cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
 {
-    return launch_cluster(distill_kernel<T>, a, a.in.rows, a.in.vocab * sizeof(typename T::raw), kThreads, stream);
+    // the smallest cluster whose parts are at most kPartBytes (three such CTAs
+    // share an SM, so that one computes while the others load); larger while
+    // the grid would leave SMs without a CTA and parts stay above 8 KB
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw);
+    int size = 1;
+    while (size < kMaxCluster && (bytes > size * kPartBytes || (a.in.rows * size < 2 * sm_count() && bytes > size * 8192)))
+        size *= 2;
+    return launch_cluster(distill_kernel<T>, a, a.in.rows, size, part_vecs(bytes, size) * 16, kThreads, stream);
 }
 
 template <class T>

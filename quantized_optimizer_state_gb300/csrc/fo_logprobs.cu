@@ -8,13 +8,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCandidates = 1024;
+constexpr int kGroup = 4;          // vectors that a thread loads at once; one maximum is kept for them
+constexpr int kGroupStep = kGroup * kThreads;
+constexpr int kGroups = 512;       // candidate groups
 
 struct Shared {
-    uint64_t bar;
-    Stat part[kWarps];
+    Stat part[kWarps + 1];
     Stat mine;                      // this CTA's part, read by the others of the cluster
-    int count;                      // candidates found
+    int count, groups;              // candidates found
     int sums[kWarps];
+    int group[kGroups];
     uint64_t list[kCandidates];     // candidates in any order; later the lists of the other CTAs
     uint64_t sorted[FO_MAX_TOP_K];  // this CTA's largest, descending
     int sorted_n;
@@ -34,10 +37,11 @@ __device__ __forceinline__ int block_sum(int v, Shared &sh)
     return t;
 }
 
-// f(key, id) for every element of vector i of the row, held in `v`.
+// f(key, id) for every element of vector i of the row.
 template <class T, class F>
-__device__ __forceinline__ void each(const Row<T> &row, int i, const uint4 &v, F f)
+__device__ __forceinline__ void each(const Row<T> &row, int i, F f)
 {
+    const uint4 v = load_vec(row, i);
     const typename T::raw *e = reinterpret_cast<const typename T::raw *>(&v);
 #pragma unroll
     for (int k = 0; k < T::kPerVec; ++k) {
@@ -47,33 +51,40 @@ __device__ __forceinline__ void each(const Row<T> &row, int i, const uint4 &v, F
     }
 }
 
-// The exact way for a part with very many candidates (most of it tied, or its
-// largest elements in few threads' hands): bisects the order keys for the
-// k-th largest value, then takes everything above it and, of the elements
-// equal to it, those with the lowest ids, in the order of ids. At most 32
-// passes over the part in shared memory, whatever it holds.
+__device__ __forceinline__ uint64_t list_key(uint32_t key, int id) { return ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id); }
+
+// The exact way for a part with very many candidates: most of it tied, as
+// where a mask leaves fewer than k tokens, or its largest elements in few
+// threads' hands. Finds the k-th largest value, then takes everything above it
+// and, of the elements equal to it, those with the lowest ids, in the order of
+// ids. `kth`: a value that at least k elements reach; if fewer than k are
+// above it, as with ties, it is the k-th largest, else it is bisected for
+// (a pass over the part, by now in the L2 cache, for each bit that values
+// differ in, whatever the part holds).
 template <class T>
-__device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, const uint4 *buf, int k, Shared &sh)
+__device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, uint32_t kth, int k, Shared &sh)
 {
-    uint32_t kth = 0;
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-        if (!(bit & T::kKeyBits))
-            break;
-        const uint32_t at = kth | bit;
+    constexpr uint32_t mask = T::kKeyBits;   // below it a key is all 0 or all 1
+    const auto count = [&](uint32_t at) {
         int n = 0;
         for (int i = threadIdx.x; i < p.n; i += kThreads)
-            each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int) { n += key >= at; });
-        if (block_sum(n, sh) >= k)
-            kth = at;
+            each<T>(row, p.v0 + i, [&](uint32_t key, int) { n += (key & mask) >= at; });
+        return block_sum(n, sh);
+    };
+    constexpr uint32_t unit = mask & (0u - mask);
+    if (kth != (0xffffffffu & mask) && count(kth + unit) >= k) {
+        kth = 0;
+        for (uint32_t bit = 0x80000000u; bit & mask; bit >>= 1)
+            if (count(kth | bit) >= k)
+                kth |= bit;
     }
-    constexpr uint32_t mask = T::kKeyBits;   // below it a key is all 0 or all 1
     if (threadIdx.x == 0)
         sh.count = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.n; i += kThreads)
-        each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int id) {
+        each<T>(row, p.v0 + i, [&](uint32_t key, int id) {
             if ((key & mask) > kth)
-                sh.list[atomicAdd(&sh.count, 1)] = ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id);
+                sh.list[atomicAdd(&sh.count, 1)] = list_key(key, id);
         });
     __syncthreads();
     int have = sh.count;   // below k
@@ -81,7 +92,7 @@ __device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, con
         const int i = i0 + threadIdx.x;
         int n = 0;
         if (i < p.n)
-            each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int) { n += (key & mask) == kth; });
+            each<T>(row, p.v0 + i, [&](uint32_t key, int) { n += (key & mask) == kth; });
         // ties before this thread's
         int before = n;
 #pragma unroll
@@ -100,9 +111,9 @@ __device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, con
             all += sh.sums[w];
         }
         if (n)
-            each<T>(row, p.v0 + i, buf[i], [&](uint32_t key, int id) {
+            each<T>(row, p.v0 + i, [&](uint32_t key, int id) {
                 if ((key & mask) == kth && have + before < k)
-                    sh.list[have + before++] = ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id);
+                    sh.list[have + before++] = list_key(key, id);
             });
         have = min(k, have + all);
         __syncthreads();
@@ -112,42 +123,62 @@ __device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, con
     __syncthreads();
 }
 
-// The part's largest elements (k, or all where it has fewer), descending, into
-// sh.sorted. `top` is the largest element of the vectors that this thread
-// holds (vectors threadIdx.x, threadIdx.x + kThreads, ...): the k-th largest of
-// the threads' maxima bounds the k-th largest element from below, and for
-// spread-out values few elements besides the top k reach it.
 template <class T>
-__device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const uint4 *buf, float top, int k, Shared &sh)
+__device__ __forceinline__ uint32_t largest_key(const Largest<T> &l) { return order_key(l.value_nan()); }
+
+// The part's largest elements (k, or all where it has fewer), descending, into
+// sh.sorted. `mine` is the key of the largest element of this thread (0
+// without elements): the k-th largest of the threads' maxima bounds the k-th
+// largest element from below, and for spread-out values few elements besides
+// the top k reach it. `maxima` holds a maximum for each kGroup vectors of a
+// thread, so that only those groups are read again that reach the bound.
+template <class T>
+__device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const Largest<T> *maxima, uint32_t mine, int k, Shared &sh)
 {
-    const uint32_t mine = (int)threadIdx.x < p.n ? order_key(top) : 0;
     uint32_t bound = 0;
 #pragma unroll 1
     for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
         if (__syncthreads_count(mine >= (bound | bit)) >= k)
             bound |= bit;
     if (mine >= bound)
-        for (int i = threadIdx.x; i < p.n; i += kThreads) {
-            const uint4 v = buf[i];
-            if (order_key(vec_max<T>(v)) < bound)
+        for (int i = threadIdx.x; i < p.n; i += kGroupStep) {
+            const int at = i / kGroupStep * kThreads + (int)threadIdx.x;
+            if (largest_key(maxima[at]) >= bound) {
+                const int n = atomicAdd(&sh.groups, 1);
+                if (n < kGroups)
+                    sh.group[n] = at;
+            }
+        }
+    __syncthreads();
+    const int groups = sh.groups;
+    if (groups <= kGroups)
+        for (int j = threadIdx.x; j < groups * kGroup; j += kThreads) {
+            const int at = sh.group[j / kGroup];
+            const int i = at / kThreads * kGroupStep + j % kGroup * kThreads + at % kThreads;
+            if (i >= p.n || *(volatile int *)&sh.count > kCandidates)
                 continue;
-            if (*(volatile int *)&sh.count > kCandidates)
-                break;
-            each<T>(row, p.v0 + i, v, [&](uint32_t key, int id) {
+            each<T>(row, p.v0 + i, [&](uint32_t key, int id) {
                 if (key >= bound) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kCandidates)
-                        sh.list[at] = ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)id);
+                    const int n = atomicAdd(&sh.count, 1);
+                    if (n < kCandidates)
+                        sh.list[n] = list_key(key, id);
                 }
             });
         }
     __syncthreads();
-    if (sh.count > kCandidates)
-        collect_exact<T>(row, p, buf, k, sh);
+    if (groups > kGroups || sh.count > kCandidates) {
+        __syncthreads();
+        // the bound to the last bit that values differ in
+        for (uint32_t bit = 0x8000u; bit & T::kKeyBits; bit >>= 1)
+            if (__syncthreads_count(mine >= (bound | bit)) >= k)
+                bound |= bit;
+        collect_exact<T>(row, p, bound, k, sh);
+    }
     const int n = sh.count;
     for (int i = threadIdx.x; i < n; i += kThreads) {   // no two keys are equal
         const uint64_t key = sh.list[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j)
             rank += sh.list[j] > key;
         if (rank < k)
@@ -164,27 +195,21 @@ __device__ __forceinline__ float key_value(uint64_t key)
     return __uint_as_float(o == 0xffffffffu ? 0x7fffffffu : o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
-// One row by a cluster of CTAs, each holding a part of it in shared memory:
-// the logits are read from device memory once, by bulk copies, and the
-// statistics and the parts' top lists are joined through distributed shared
-// memory.
+// One row by a cluster of CTAs (one CTA where there are many rows): one pass
+// over the row by plain loads, statistics in registers, joined through the
+// (distributed) shared memory.
 template <class T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char dynamic[];
-    uint4 *buf = reinterpret_cast<uint4 *>(dynamic);
+    Largest<T> *maxima = reinterpret_cast<Largest<T> *>(dynamic);
     __shared__ Shared sh;
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const int64_t r = blockIdx.x / size;
     const Row<T> row(a.in, r);
     const Part p = part_of(row, rank, size);
-    if (threadIdx.x == 0) {
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&sh.bar)) : "memory");
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        sh.count = 0;
-    }
-    __syncthreads();
-    start_part<T>(row, p, buf, &sh.bar);
+    if (threadIdx.x == 0)
+        sh.count = sh.groups = 0;
     int64_t token = -1;
     float token_x = 0.0f;
     if (rank == 0 && threadIdx.x == 0 && a.logp) {
@@ -192,36 +217,40 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
         if (token >= 0 && token < row.vocab)
             token_x = T::widen(row.x[token]);
     }
-    __syncthreads();
-    const bool arrived = wait_part(&sh.bar);
 
-    Stat s = {-kInf, 0.0f, 0.0f};
-    float top = -kInf;
-    for (int i = threadIdx.x; i < p.n; i += kThreads)
-        absorb<T, true>(s, top, buf[i], a.in);
-    if (!arrived)
-        s.z = __int_as_float(0x7fffffff);
-    s = warp_join<true>(s, a.in);
-    if ((threadIdx.x & 31) == 0)
-        sh.part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = sh.part[0];
+    Running<T, true> run;
+    for (int i0 = 0; i0 < p.n; i0 += kGroupStep) {
+        const int i = p.v0 + i0 + (int)threadIdx.x;
+        uint4 v[kGroup];
+        const Largest<T> before = run.top;
+        run.top = Largest<T>::none();
+        if (p.v0 + i0 >= row.full0 && i0 + kGroupStep <= p.n && p.v0 + i0 + kGroupStep <= row.full1) {
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i)
-        s = join<true>(s, sh.part[i], a.in);
+            for (int j = 0; j < kGroup; ++j)
+                v[j] = __ldcs(row.vec(i + j * kThreads));
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                run.add(v[j], a.in);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kGroup; ++j)
+                if (i0 + (int)threadIdx.x + j * kThreads < p.n)
+                    run.add(load_vec(row, i + j * kThreads), a.in);
+        }
+        if (a.k && i0 + (int)threadIdx.x < p.n)
+            maxima[i0 / kGroupStep * kThreads + threadIdx.x] = run.top;
+        run.top = run.top.with(before);
+    }
+    Stat s = block_join<true, kWarps>(run.stat(a.in), sh.part, a.in);
     if (a.k)
-        find_top<T>(row, p, buf, top, a.k, sh);
+        find_top<T>(row, p, maxima, (int)threadIdx.x < p.n ? largest_key(run.top) : 0, a.k, sh);
     if (size > 1) {
         if (threadIdx.x == 0)
             sh.mine = s;
         cluster_arrive();
         cluster_wait();
-        Stat all = {-kInf, 0.0f, 0.0f};
-        for (uint32_t i = 0; i < size; ++i) {
-            const uint32_t at = map_shared(&sh.mine, i);
-            all = join<true>(all, Stat{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)}, a.in);
-        }
-        s = all;
+        const uint32_t at = map_shared(&sh.mine, (threadIdx.x & 7) % size);
+        s = warp_join<true>(Stat{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)}, a.in, size);
     }
     const float ln_z = logf(s.z);
     if (rank == 0 && threadIdx.x == 0) {
@@ -268,8 +297,6 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
             }
         }
     }
-    if (!arrived)
-        wait_part(&sh.bar);   // its copies are not left behind
     if (size > 1) {   // no CTA leaves while another reads its shared memory
         cluster_arrive();
         cluster_wait();
@@ -294,16 +321,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int at = v0 + i * kThreads + tid;
-        if (at >= row.full0 && at < row.full1)
-            v[i] = __ldcs(row.vec(at));
-        else if (at < row.vecs) {
-            raw *e = reinterpret_cast<raw *>(&v[i]);
-#pragma unroll
-            for (int k = 0; k < T::kPerVec; ++k) {
-                const int id = row.id(at, k);
-                e[k] = id >= 0 && id < row.vocab ? row.x[id] : T::narrow(-kInf);
-            }
-        }
+        if (at < row.vecs)
+            v[i] = load_vec(row, at);
     }
     const float4 st = a.stats[r];
     const float m = safe_max(st.x), inv_z = st.y == 0.0f ? 0.0f : 1.0f / st.y, ln_z = logf(st.y);
@@ -376,7 +395,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
 template <class T>
 cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
 {
-    return launch_cluster(logprobs_kernel<T>, a, a.in.rows, a.in.vocab * sizeof(typename T::raw), kThreads, stream);
+    // one CTA a row, or a cluster that shares it while the grid would leave SMs short of CTAs
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw);
+    int size = 1;
+    while (size < kMaxCluster && a.in.rows * size < 4 * sm_count() && bytes > size * 8192)
+        size *= 2;
+    const int64_t groups = (part_vecs(bytes, size) + kGroupStep - 1) / kGroupStep;
+    return launch_cluster(logprobs_kernel<T>, a, a.in.rows, size, a.k ? groups * kThreads * 4 : 0, kThreads, stream);
 }
 
 template <class T>

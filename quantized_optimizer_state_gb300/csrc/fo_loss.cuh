@@ -35,6 +35,15 @@ struct Bf16 {
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
+    // whether either element of a is greater than b's
+    static __device__ __forceinline__ bool any_gt2(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        asm("{\n .reg .pred p, q;\n setp.gt.bf16x2 p|q, %1, %2;\n or.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(d) : "r"(a), "r"(b));
+        return d != 0;
+    }
+    static __device__ __forceinline__ uint32_t twice(float f) { return (uint32_t)narrow(f) * 0x10001u; }
+    static __device__ __forceinline__ bool finite(float f) { return fabsf(f) < 0x1p126f; }
 };
 struct F16 {
     typedef uint16_t raw;
@@ -58,6 +67,14 @@ struct F16 {
         asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
+    static __device__ __forceinline__ bool any_gt2(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        asm("{\n .reg .pred p, q;\n setp.gt.f16x2 p|q, %1, %2;\n or.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(d) : "r"(a), "r"(b));
+        return d != 0;
+    }
+    static __device__ __forceinline__ uint32_t twice(float f) { return (uint32_t)narrow(f) * 0x10001u; }
+    static __device__ __forceinline__ bool finite(float f) { return fabsf(f) < 65000.0f; }
 };
 struct F32 {
     typedef float raw;
@@ -66,6 +83,7 @@ struct F32 {
     static constexpr uint32_t kKeyBits = 0xffffffffu;
     static __device__ __forceinline__ float widen(raw v) { return v; }
     static __device__ __forceinline__ raw narrow(float f) { return f; }
+    static __device__ __forceinline__ bool finite(float f) { return fabsf(f) < 0x1p126f; }
 };
 
 constexpr float kLn2 = 0.693147180559945309f;
@@ -179,17 +197,17 @@ __device__ __forceinline__ uint4 narrow_vec<F32>(const f2 (&x)[2])
     return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
 
-// The largest element of a vector; NaN where it holds one.
+// The vector's elements raised to `floor_` where they are below it. NaN stays.
 template <class T>
-__device__ __forceinline__ float vec_max(const uint4 &v)
+__device__ __forceinline__ uint4 raise(const uint4 &v, uint32_t floor_)
 {
-    const uint32_t w = T::max2(T::max2(v.x, v.y), T::max2(v.z, v.w));
-    return max_nan(T::widen((typename T::raw)w), T::widen((typename T::raw)(w >> 16)));
+    return make_uint4(T::max2(v.x, floor_), T::max2(v.y, floor_), T::max2(v.z, floor_), T::max2(v.w, floor_));
 }
-template <>
-__device__ __forceinline__ float vec_max<F32>(const uint4 &v)
+template <class T>
+__device__ __forceinline__ uint4 raise(const uint4 &v, float floor_)
 {
-    return max_nan(max3_nan(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)), __uint_as_float(v.w));
+    return make_uint4(__float_as_uint(max_nan(__uint_as_float(v.x), floor_)), __float_as_uint(max_nan(__uint_as_float(v.y), floor_)),
+                      __float_as_uint(max_nan(__uint_as_float(v.z), floor_)), __float_as_uint(max_nan(__uint_as_float(v.w), floor_)));
 }
 
 // A row lies in vectors counted from the 16-byte boundary at or before its
@@ -216,9 +234,56 @@ struct Row {
     __device__ __forceinline__ const uint4 *vec(int i) const { return reinterpret_cast<const uint4 *>(x - phase) + i; }
 };
 
-// Running statistics of a set of logits: m their maximum, z = sum 2^((x-m)c).
-// w is the same sum of other elements (distillation), or sum 2^t t, t = (x-m)c
-// (entropy). An empty set: {-inf, 0, 0}.
+// Vector i of a row; where it reaches beyond the row's ends, the row's elements
+// one by one (no byte outside the row is read) and -inf beside them.
+template <class T>
+__device__ __forceinline__ uint4 load_vec(const Row<T> &row, int i)
+{
+    if (i >= row.full0 && i < row.full1)
+        return __ldcs(row.vec(i));
+    uint4 v;
+    typename T::raw *e = reinterpret_cast<typename T::raw *>(&v);
+#pragma unroll
+    for (int k = 0; k < T::kPerVec; ++k) {
+        const int id = row.id(i, k);
+        e[k] = id >= 0 && id < row.vocab ? row.x[id] : T::narrow(-kInf);
+    }
+    return v;
+}
+
+// The elementwise largest of a vector's packed words (one word for the 16-bit
+// types, whose two halves are kept apart; the value itself for FP32). NaN stays.
+template <class T>
+struct Largest {
+    uint32_t w;
+    static __device__ __forceinline__ Largest none() { return Largest{T::twice(-kInf)}; }
+    static __device__ __forceinline__ Largest of(const uint4 &v) { return Largest{T::max2(T::max2(v.x, v.y), T::max2(v.z, v.w))}; }
+    __device__ __forceinline__ Largest with(Largest o) const { return Largest{T::max2(w, o.w)}; }
+    __device__ __forceinline__ bool above(uint32_t bound) const { return T::any_gt2(w, bound); }
+    __device__ __forceinline__ float lo() const { return T::widen((typename T::raw)w); }
+    __device__ __forceinline__ float hi() const { return T::widen((typename T::raw)(w >> 16)); }
+    __device__ __forceinline__ float value() const { return fmaxf(lo(), hi()); }         // of what is not NaN
+    __device__ __forceinline__ float value_nan() const { return max_nan(lo(), hi()); }   // NaN where there is one
+    static __device__ __forceinline__ uint32_t bound(float f) { return T::twice(f); }
+};
+template <>
+struct Largest<F32> {
+    float w;
+    static __device__ __forceinline__ Largest none() { return Largest{-kInf}; }
+    static __device__ __forceinline__ Largest of(const uint4 &v)
+    {
+        return Largest{max_nan(max3_nan(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)), __uint_as_float(v.w))};
+    }
+    __device__ __forceinline__ Largest with(Largest o) const { return Largest{max_nan(w, o.w)}; }
+    __device__ __forceinline__ bool above(float bound) const { return w > bound; }
+    __device__ __forceinline__ float value() const { return w; }
+    __device__ __forceinline__ float value_nan() const { return w; }
+    static __device__ __forceinline__ float bound(float f) { return f; }
+};
+
+// Statistics of a set of logits: m a reference near their maximum (at most
+// 2^32 below it in 2^((x-m)c)), z = sum 2^((x-m)c), w = sum 2^t t with
+// t = (x-m)c (entropy; else unused). An empty set: {-inf, 0, 0}.
 struct Stat {
     float m, z, w;
 };
@@ -228,7 +293,8 @@ __device__ __forceinline__ void rescale(Stat &s, float m, const LogitRows &in)
 {
     const float t = __fmul_rn(max_nan(__fsub_rn(s.m, m), in.d_min), in.c);   // s.m = -inf: 2^-160, which is 0
     const float f = exp2_approx(t);
-    s.w = __fmul_rn(kEntropy ? __fmaf_rn(t, s.z, s.w) : s.w, f);
+    if (kEntropy)
+        s.w = __fmul_rn(__fmaf_rn(t, s.z, s.w), f);
     s.z = __fmul_rn(s.z, f);
     s.m = m;
 }
@@ -241,58 +307,148 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, const LogitRows &in)
         rescale<kEntropy>(a, m, in);
         rescale<kEntropy>(b, m, in);
     }
-    return Stat{m, a.z + b.z, a.w + b.w};
+    return Stat{m, a.z + b.z, kEntropy ? a.w + b.w : 0.0f};
 }
 
+// Over the first `n` lanes of a warp (a power of two), in every lane of them.
 template <bool kEntropy>
-__device__ __forceinline__ Stat warp_join(Stat s, const LogitRows &in)
+__device__ __forceinline__ Stat warp_join(Stat s, const LogitRows &in, int n = 32)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        s = join<kEntropy>(s, Stat{__shfl_xor_sync(~0u, s.m, o), __shfl_xor_sync(~0u, s.z, o), __shfl_xor_sync(~0u, s.w, o)}, in);
+    float m = s.m;
+    for (int o = n / 2; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (m != -kInf)
+        rescale<kEntropy>(s, m, in);
+    for (int o = n / 2; o; o >>= 1) {
+        s.z += __shfl_xor_sync(~0u, s.z, o);
+        if (kEntropy)
+            s.w += __shfl_xor_sync(~0u, s.w, o);
+    }
     return s;
 }
 
-// Adds a vector to the statistics, and its maximum to `top` (NaN stays).
-// The sum of the vector is formed first: chains of additions stay short.
-template <class T, bool kEntropy>
-__device__ __forceinline__ void absorb(Stat &s, float &top, const uint4 &v, const LogitRows &in)
+// Over a CTA of kWarps warps: the result in every thread. `part` is shared
+// memory of kWarps + 1 entries.
+template <bool kEntropy, int kWarps>
+__device__ __forceinline__ Stat block_join(Stat s, Stat *part, const LogitRows &in)
 {
-    const float vm = vec_max<T>(v);
-    top = max_nan(top, vm);
-    if (vm > s.m)
-        rescale<kEntropy>(s, vm, in);
-    const f2 nm = splat(-safe_max(s.m)), c = splat(in.c);
-    f2 x[T::kPerVec / 2];
-    widen_vec<T>(v, x);
-    f2 z[T::kPerVec / 2], w = 0;
-#pragma unroll
-    for (int i = 0; i < T::kPerVec / 2; ++i) {
-        f2 d = add2(x[i], nm);
-        float a, b;
-        if (kEntropy) {   // t stays finite: 0 times it is 0
-            unpk(d, a, b);
-            d = pk(max_nan(a, in.d_min), max_nan(b, in.d_min));
-        }
-        const f2 t = mul2(d, c);
-        unpk(t, a, b);
-        z[i] = pk(exp2_approx(a), exp2_approx(b));
-        if (kEntropy)
-            w = i ? fma2(z[i], t, w) : mul2(z[i], t);
+    s = warp_join<kEntropy>(s, in);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        s = part[threadIdx.x % kWarps];
+        s = warp_join<kEntropy>(s, in, kWarps);
+        if (threadIdx.x == 0)
+            part[kWarps] = s;
     }
-#pragma unroll
-    for (int n = T::kPerVec / 4; n; n >>= 1)
-#pragma unroll
-        for (int i = 0; i < n; ++i)
-            z[i] = add2(z[i], z[i + n]);
-    float a, b;
-    unpk(z[0], a, b);
-    s.z = __fadd_rn(s.z, __fadd_rn(a, b));
-    if (kEntropy) {
-        unpk(w, a, b);
-        s.w = __fadd_rn(s.w, __fadd_rn(a, b));
-    }
+    __syncthreads();
+    return part[kWarps];
 }
+
+// One thread's statistics while it walks over its vectors. An exponential
+// costs one fused multiply-add, 2^(x c - M): M is the reference m times c,
+// rounded, and the rounding is undone at the end. m follows the maximum
+// loosely: it is moved where a vector reaches 16 powers of two above it, which
+// after the first vector is rare, and saves the rescaling of most vectors.
+// `careful` marks references beside which x c - M does not do: of 2^60 and
+// more (x c may overflow, and the difference of two unequal logits is beyond
+// any exponent there), and, for the entropy, those next to the type's lowest
+// value; vectors are then taken element by element through x - m.
+template <class T, bool kEntropy>
+struct Running {
+    float m, ref;                       // the reference and RN(m c)
+    f2 z, w;
+    Largest<T> top;                     // the largest seen; NaN stays
+    decltype(Largest<T>::bound(0.0f)) limit, floor_;
+    bool careful;
+
+    __device__ __forceinline__ Running()
+        : m(-kInf), ref(0.0f), z(0), w(0), top(Largest<T>::none()), limit(Largest<T>::bound(-kInf)), floor_(limit), careful(kEntropy)
+    {
+    }
+
+    // Moves the reference up to the largest seen.
+    __device__ __forceinline__ void move(const LogitRows &in)
+    {
+        const float to = top.value(), reach = __fmul_rn(-in.d_min, 1.02f);
+        const float low = to - fmaxf(reach, fabsf(to) * 0x1p-6f);   // where 2^t is 0, at the type's precision
+        const bool c = !(fabsf(to) < 0x1p60f) || (kEntropy && !T::finite(low));
+        const float r = __fmul_rn(to, in.c);
+        float t = c || careful ? __fmul_rn(to == m ? 0.0f : __fsub_rn(m, to), in.c) : __fsub_rn(ref, r);
+        t = max_nan(t, -160.0f);
+        const float f = m == -kInf ? 0.0f : exp2_approx(t);
+        if (kEntropy)
+            w = mul2(fma2(splat(t), z, w), splat(f));
+        z = mul2(z, splat(f));
+        m = to;
+        ref = r;
+        careful = c;
+        limit = Largest<T>::bound(c ? to : __fmaf_rn(-in.d_min, 0.1f, to));   // -d_min c = 160
+        floor_ = Largest<T>::bound(low);
+    }
+
+    __device__ __forceinline__ void add(const uint4 &v, const LogitRows &in)
+    {
+        const Largest<T> vt = Largest<T>::of(v);
+        top = top.with(vt);
+        if (vt.above(limit))
+            move(in);
+        f2 x[T::kPerVec / 2], e[T::kPerVec / 2];
+        float a, b;
+        if (!careful) {
+            const f2 c = splat(in.c), r = splat(-ref);
+            if (kEntropy)
+                widen_vec<T>(raise<T>(v, floor_), x);
+            else
+                widen_vec<T>(v, x);
+#pragma unroll
+            for (int i = 0; i < T::kPerVec / 2; ++i) {
+                const f2 t = fma2(x[i], c, r);
+                unpk(t, a, b);
+                e[i] = pk(exp2_approx(a), exp2_approx(b));
+                if (kEntropy)
+                    w = fma2(e[i], t, w);
+            }
+        } else {
+            const float at = safe_max(m);
+            widen_vec<T>(v, x);
+#pragma unroll
+            for (int i = 0; i < T::kPerVec / 2; ++i) {
+                unpk(x[i], a, b);
+                const f2 t = pk(__fmul_rn(distance(a, at, in), in.c), __fmul_rn(distance(b, at, in), in.c));
+                unpk(t, a, b);
+                e[i] = pk(exp2_approx(a), exp2_approx(b));
+                if (kEntropy)
+                    w = fma2(e[i], t, w);
+            }
+        }
+        // the vector's sum first: chains of additions stay short
+#pragma unroll
+        for (int n = T::kPerVec / 4; n; n >>= 1)
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                e[i] = add2(e[i], e[i + n]);
+        z = add2(z, e[0]);
+    }
+
+    __device__ __forceinline__ Stat stat(const LogitRows &in) const
+    {
+        float a, b;
+        unpk(z, a, b);
+        Stat s = {m, __fadd_rn(a, b), 0.0f};
+        unpk(w, a, b);
+        if (kEntropy)
+            s.w = __fadd_rn(a, b);
+        if (!careful && m != -kInf) {   // from 2^ref to 2^(m c)
+            const float d = __fmaf_rn(m, in.c, -ref), f = exp2_approx(-d);
+            if (kEntropy)
+                s.w = __fmul_rn(__fmaf_rn(-d, s.z, s.w), f);
+            s.z = __fmul_rn(s.z, f);
+        }
+        return s;
+    }
+};
 
 // --- rows held in the shared memory of a cluster -----------------------------------
 
@@ -448,25 +604,14 @@ __device__ __forceinline__ f2 grad_exp2(f2 d, const LogitRows &in, f2 &t)
 
 constexpr int kMaxCluster = 8;
 
-// A row by a cluster: the smallest power of two of CTAs whose parts are at
-// most kPartBytes (three such CTAs share an SM, so that one computes while the
-// others load); more while the grid would leave SMs without a CTA and parts
-// stay above kSmallPart.
-constexpr int64_t kPartBytes = 64 * 1024;
-constexpr int64_t kSmallPart = 8 * 1024;
-
+// A row by a cluster of `size` CTAs.
 template <class Args>
-cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, int64_t row_bytes, int threads, cudaStream_t stream)
+cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, int size, size_t shared_bytes, int threads,
+                           cudaStream_t stream)
 {
-    int size = 1;
-    while (size < kMaxCluster && (row_bytes > size * kPartBytes ||
-                                  (rows * size < 2 * sm_count() && row_bytes > size * kSmallPart)))
-        size *= 2;
-    const int64_t vecs = (row_bytes + 30) / 16;   // at any alignment
-    const size_t bytes = (size_t)((vecs + size - 1) / size) * 16;
     cudaError_t e = cudaSuccess;
-    if (bytes > 32 * 1024)   // with the static part, beyond what a kernel gets unasked
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (shared_bytes > 32 * 1024)   // with the static part, beyond what a kernel gets unasked
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_bytes);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return e;
@@ -474,7 +619,7 @@ cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, in
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * size));
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = shared_bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -487,5 +632,9 @@ cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, in
     const cudaError_t last = cudaGetLastError();
     return e != cudaSuccess ? e : last;
 }
+
+// Vectors of a row of `row_bytes` bytes at any alignment, and of one CTA's part of it.
+inline int64_t row_vecs(int64_t row_bytes) { return (row_bytes + 30) / 16; }
+inline int64_t part_vecs(int64_t row_bytes, int size) { return (row_vecs(row_bytes) + size - 1) / size; }
 
 }  // namespace fo
