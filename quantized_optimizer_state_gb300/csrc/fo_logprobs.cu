@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
     if (rank == 0 && threadIdx.x == 0) {
         const float h = s.z == 0.0f ? 0.0f : ln_z - kLn2 * (s.w / s.z);
         if (a.logp)
-            a.logp[r] = token < 0 ? 0.0f : token >= row.vocab ? __int_as_float(0x7fffffff) : (float)log_prob(token_x, s.m, s.z, ln_z, a.in.inv_t);
+            a.logp[r] = token < 0 ? 0.0f : token >= row.vocab ? __int_as_float(0x7fffffff) : log_prob(token_x, s.m, s.z, ln_z, a.in.inv_t);
         if (a.entropy)
             a.entropy[r] = h;
         if (a.stats)
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
             }
             if (place < k) {
                 a.top_ids[r * k + place] = (int32_t)entry_id(key);
-                a.top_logp[r * k + place] = (float)log_prob(key_value(key), s.m, s.z, ln_z, a.in.inv_t);
+                a.top_logp[r * k + place] = log_prob(key_value(key), s.m, s.z, ln_z, a.in.inv_t);
             }
         }
     }

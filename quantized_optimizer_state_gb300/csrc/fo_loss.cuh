@@ -149,13 +149,15 @@ __device__ __forceinline__ uint32_t entry_id(uint64_t key) { return 0xffffffffu 
 // -inf and not NaN.
 __device__ __forceinline__ float safe_max(float m) { return m == -kInf ? 0.0f : m; }
 
+// (x - m) / 4, finite for any two finite logits: beside one of the type's
+// lowest value the difference itself may lie outside FP32, although what it is
+// weighted or divided by brings it back.
+__device__ __forceinline__ float quarter_distance(float x, float m) { return __fsub_rn(0.25f * x, 0.25f * safe_max(m)); }
+
 // log p of a logit, given m, Z and ln Z; -inf in a row without a distribution.
-// In double, for the few entries of a row that need it: beside a logit of the
-// type's lowest value the difference may lie outside FP32 although what it is
-// weighted with brings it back.
-__device__ __forceinline__ double log_prob(float x, float m, float z, float ln_z, float inv_t)
+__device__ __forceinline__ float log_prob(float x, float m, float z, float ln_z, float inv_t)
 {
-    return z == 0.0f ? -(double)kInf : ((double)x - (double)safe_max(m)) * (double)inv_t - (double)ln_z;
+    return z == 0.0f ? -kInf : __fmaf_rn(quarter_distance(x, m), 4.0f * inv_t, -ln_z);
 }
 
 __device__ __forceinline__ float load_dtype(const void *p, int64_t i, int dtype)
@@ -480,12 +482,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t a)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ double ld_cluster_f64(uint32_t a)
-{
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a)
 {
     uint64_t v;
@@ -493,7 +489,7 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a)
     return v;
 }
 
-// This CTA's vectors of a row: [v0, v0 + n), at `buf` in shared memory.
+// This CTA's vectors of a row: [v0, v0 + n).
 struct Part {
     int v0, n;
 };
@@ -505,30 +501,63 @@ __device__ __forceinline__ Part part_of(const Row<T> &row, uint32_t rank, uint32
     return Part{v0, min(per, row.vecs - v0)};
 }
 
+// mbarriers. A wait is bounded (each try sleeps in the hardware for a while):
+// something that never comes gives false, not a hang.
+__device__ __forceinline__ void barrier_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_address(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_address(bar)) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity)
+{
+    for (int i = 0; i < 1 << 20; ++i) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n"
+                     " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                     " selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done)
+                     : "r"(shared_address(bar)), "r"(parity)
+                     : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
+
+// The same by all lanes of a warp, which agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) { return __all_sync(~0u, barrier_wait(bar, parity)); }
+
 constexpr int kCopyBytes = 16384;   // of one bulk copy
 
-// Starts the copies of a part into shared memory. The vectors wholly inside
-// the row come by bulk copies that `bar` counts; those that reach beyond its
-// ends element by element (no byte outside the row is read), filled up with
-// -inf. Thread 0 has initialised `bar` for one arrival; all threads call this,
-// and a barrier of the CTA has to follow before the others' elements are read.
+// Starts the copies of a part into shared memory, by one warp. The vectors
+// wholly inside the row come by bulk copies that `full` counts; those that
+// reach beyond its ends element by element (no byte outside the row is read),
+// filled up with -inf.
 template <class T>
-__device__ __forceinline__ void start_part(const Row<T> &row, const Part &p, uint4 *buf, uint64_t *bar)
+__device__ __forceinline__ void load_part(const Row<T> &row, const Part &p, uint4 *buf, uint64_t *full)
 {
     typedef typename T::raw raw;
+    const int lane = threadIdx.x & 31;
     const int lo = max(p.v0, row.full0), hi = min(p.v0 + p.n, row.full1);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
         const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(bar)), "r"(bytes) : "memory");
+        barrier_expect(full, bytes);
         for (uint32_t at = 0; at < bytes; at += kCopyBytes) {
             const uint32_t size = min((uint32_t)kCopyBytes, bytes - at);
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                              shared_address(buf + (lo - p.v0)) + at),
-                         "l"(reinterpret_cast<const char *>(row.vec(lo)) + at), "r"(size), "r"(shared_address(bar))
+                         "l"(reinterpret_cast<const char *>(row.vec(lo)) + at), "r"(size), "r"(shared_address(full))
                          : "memory");
         }
     }
-    const int side = threadIdx.x / T::kPerVec, e = threadIdx.x % T::kPerVec;
+    const int side = lane / T::kPerVec, e = lane % T::kPerVec;
     const int i = side == 0 ? 0 : row.vecs - 1;
     if (side < 2 && (i < row.full0 || i >= row.full1) && i >= p.v0 && i < p.v0 + p.n) {
         const int id = row.id(i, e);
@@ -539,22 +568,16 @@ __device__ __forceinline__ void start_part(const Row<T> &row, const Part &p, uin
     }
 }
 
-// Waits for the copies. The number of tries is bounded (each one sleeps in the
-// hardware for a while): a copy that never ends gives false, not a hang.
-__device__ __forceinline__ bool wait_part(uint64_t *bar)
+// Stores into another CTA's shared memory of the cluster (launched as one), and
+// an arrival at a barrier there that the stores before it precede.
+__device__ __forceinline__ void st_cluster(uint32_t at, float a, float b)
 {
-    for (int i = 0; i < 1 << 20; ++i) {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n"
-                     " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n"
-                     " selp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done)
-                     : "r"(shared_address(bar))
-                     : "memory");
-        if (done)
-            return true;
-    }
-    return false;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // --- gradients -----------------------------------------------------------------
