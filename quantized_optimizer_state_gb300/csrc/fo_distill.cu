@@ -7,16 +7,14 @@
 namespace fo {
 namespace {
 
-constexpr int kConsumers = 256;                   // threads that sum and write the gradient
-constexpr int kWarps = kConsumers / 32;
-constexpr int kFetcher = kWarps, kJoiner = kWarps + 1;   // two warps more: see distill_kernel
-constexpr int kThreads = kConsumers + 64;
-constexpr int kMaxBuffers = 3;
-constexpr int kTurns = 4;                         // rows whose sums may be on their way
+constexpr int kStream = 256;                      // threads that walk over a row
+constexpr int kWarps = kStream / 32;
+constexpr int kThreads = kStream + 32;            // and a warp for the teacher's entries
+constexpr int kGroup = 4;                         // vectors that a thread loads at once
+constexpr int kGroupStep = kGroup * kStream;
 constexpr int kGradThreads = 256;
-constexpr int64_t kPartBytes = 36 * 1024;
-constexpr int64_t kSharedBytes = 212 * 1024;      // for parts, in one CTA
-constexpr int kMaxRowsEach = 16;
+constexpr int kCtasPerSm = 4;
+constexpr int64_t kCacheBytes = 80 << 20;         // of the 129 MB L2 cache, for rows between their passes
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -126,415 +124,276 @@ struct Listed {
     float q, dot;   // sum of q over the entries, sum of q (x - m) / 4
 };
 
-// What the fetching warp hands over with a part.
-struct Entries {
-    int32_t id[FO_MAX_TOP_K];   // a listed token of the part, each once; -1: none
-    float x[FO_MAX_TOP_K];      // its logit
-    float q[FO_MAX_TOP_K];      // the weight of all entries that list it
-    float part_q[FO_MAX_TOP_K]; // the weight of this entry, 0 outside the part
-    float weight, sum, rest, qlogq;
-};
-
-// What the joining warp hands to those that write the gradient.
-struct Coefficients {
-    float m_rest, f;            // an unlisted token: f 2^((x - m_rest) c)
-    float m, inv_z;             // a listed one: p = 2^((x - m) c) inv_z
-};
-
 struct Shared {
-    uint64_t full[kMaxBuffers], ready[kMaxBuffers], empty[kMaxBuffers];
-    uint64_t stats[kTurns], joined[kTurns], written;
-    Listed listed[kTurns][kMaxCluster];               // of all CTAs of the cluster,
-    float2 rest[kTurns][kMaxCluster * kWarps];        // m, z of their warps: written by each CTA into all
-    Coefficients co[kTurns];
-    Entries entries[kMaxBuffers];
-    int32_t ids[FO_MAX_TOP_K];                        // for rows that list an id twice
+    Listed listed;
+    Stat part[kWarps];
+    Stat mine;                  // this CTA's sums, read by the others of the cluster
+    float sum, rest, qlogq;     // of the teacher's row
+    int32_t ids[FO_MAX_TOP_K];
     float q[FO_MAX_TOP_K];
 };
 
-// A buffer of a ring and how often it has been used, modulo 2.
-struct Cursor {
-    int at = 0;
-    uint32_t turn = 0;
-    __device__ __forceinline__ void next(int n)
-    {
-        if (++at == n) {
-            at = 0;
-            turn ^= 1;
-        }
-    }
-};
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
 
-// The listed tokens of a part that has arrived: their logits are replaced by
-// -inf, so that what is summed after is the rest alone. By one warp.
+// m, z pairs joined over a warp: the largest m, and z at that.
+__device__ __forceinline__ float2 join_pairs(float m, float z, const LogitRows &in)
+{
+    float top = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    return make_float2(top, warp_sum(z * exp2_approx(distance(m, safe_max(top), in) * in.c)));
+}
+
+// The elements that `mask` has a bit for become -inf.
 template <class T>
-__device__ __forceinline__ void take_entries(const Row<T> &row, const Part &p, uint4 *buf, const TeacherRow &t, int k, Shared &sh, Entries &out)
+__device__ __forceinline__ uint4 without(uint4 v, uint32_t mask)
+{
+    typename T::raw *e = reinterpret_cast<typename T::raw *>(&v);
+#pragma unroll
+    for (int k = 0; k < T::kPerVec; ++k)
+        if (mask >> k & 1)
+            e[k] = T::narrow(-kInf);
+    return v;
+}
+
+// All threads of the CTA, from different places in the code.
+__device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+// One row by a cluster of CTAs (one CTA for short rows). A first pass sums the
+// exponentials, a second writes the gradient; it reads the row again, but from
+// the L2 cache: the launch keeps the rows at work at once well below its size.
+// With kTail the rest of the student's mass is summed over the tokens that are
+// not listed, which a byte for each vector in shared memory marks: 1 - sum p
+// would lose a small rest. That sum also keeps a reference of its own: it may
+// lie further below the listed logits than FP32's exponents reach.
+template <class T, bool kTail>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillArgs a)
 {
     typedef typename T::raw raw;
-    raw *e = reinterpret_cast<raw *>(buf);
-    const int lane = threadIdx.x & 31;
-    int place[kSlots];
-    float x[kSlots], q[kSlots];
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        place[i] = -1;
-        x[i] = 0.0f;
-        q[i] = t.q[i];
-        if (t.id[i] < 0 || t.id[i] >= row.vocab)
-            continue;
-        const int at = t.id[i] + row.phase - p.v0 * T::kPerVec;
-        if (at >= 0 && at < p.n * T::kPerVec) {
-            place[i] = at;
-            x[i] = T::widen(e[at]);
+    extern __shared__ __align__(16) unsigned char marks[];
+    __shared__ __align__(16) Shared sh;
+    const uint32_t size = cluster_size(), rank = cluster_rank();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t r = blockIdx.x / size;
+    const Row<T> row(a.in, r);
+    const Part p = part_of(row, rank, size);
+    const float weight = a.weight ? a.weight[r] : 1.0f;
+    raw *g = static_cast<raw *>(a.grad.data);
+    int lo = row.vecs, hi = 0;   // vectors that are stored whole
+    if (g) {
+        g += row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
+        if (same_phase(row, g)) {
+            lo = row.full0;
+            hi = row.full1;
         }
     }
-    __syncwarp();
-    // one entry of each token: whoever's number stands in the token's place
-    constexpr bool k16 = sizeof(raw) == 2;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-        if (place[i] >= 0) {
-            if (k16)
-                reinterpret_cast<uint16_t *>(e)[place[i]] = (uint16_t)(lane + 32 * i);
+    if (weight == 0.0f) {   // the same in all CTAs of the cluster
+        if (rank == 0 && tid == 0 && a.loss)
+            a.loss[r] = 0.0f;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int i = p.v0 + tid; g && i < p.v0 + p.n; i += kThreads) {
+            if (i >= lo && i < hi)
+                store_stream(g + row.id(i, 0), zero);
             else
-                reinterpret_cast<uint32_t *>(e)[place[i]] = (uint32_t)(lane + 32 * i);
+                store_edge<T>(g, row, i, zero);
         }
-    __syncwarp();
-    bool mine[kSlots], twice = false;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        mine[i] = place[i] >= 0 && (k16 ? reinterpret_cast<uint16_t *>(e)[place[i]] : reinterpret_cast<uint32_t *>(e)[place[i]]) ==
-                                       (uint32_t)(lane + 32 * i);
-        twice = twice || (place[i] >= 0 && !mine[i]);
+        return;
     }
-    if (__any_sync(~0u, twice)) {   // q of equal ids is added up in their order
+    if (kTail) {
+        for (int i = tid; i < (p.n + 15) / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(marks)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+    const int end = p.v0 + p.n;
+    int32_t mine[kSlots];   // entry warp: listed tokens in the part
+    float x[kSlots];
+    Stat s = {-kInf, 0.0f, 0.0f};
+    if (tid >= kStream) {
+        const TeacherRaw w = load_teacher(a.teacher, r);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            mine[i] = -1;
+            x[i] = -kInf;
+            if (w.id[i] < max(0, row.id(p.v0, 0)) || w.id[i] >= min(row.vocab, row.id(end, 0)))
+                continue;
+            mine[i] = w.id[i];
+            x[i] = T::widen(row.x[w.id[i]]);
+        }
+        if (kTail) {
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i)
+                if (mine[i] >= 0) {
+                    const int at = mine[i] + row.phase - p.v0 * T::kPerVec, byte = at / T::kPerVec;
+                    atomicOr(reinterpret_cast<uint32_t *>(marks) + byte / 4, 1u << (byte % 4 * 8 + at % T::kPerVec));
+                }
+            block_barrier();
+        }
+        const TeacherRow t = make_teacher(a.teacher, w, row.vocab);
+        float ql = 0.0f, m = -kInf;
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             sh.ids[lane + 32 * i] = t.id[i];
             sh.q[lane + 32 * i] = t.q[i];
+            ql += t.q[i] > 0.0f ? t.q[i] * t.logq[i] : 0.0f;
+            m = fmaxf(m, x[i]);
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            if (mine[i]) {
-                q[i] = 0.0f;
-                for (int j = 0; j < k; ++j)
-                    if (sh.ids[j] == t.id[i])
-                        q[i] += sh.q[j];
+        for (int o = 16; o; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        Listed l = {m, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            if (mine[i] < 0)
+                continue;
+            if (t.q[i] > 0.0f) {
+                l.q += t.q[i];
+                l.dot = __fmaf_rn(t.q[i], quarter_distance(x[i], m), l.dot);
             }
-    }
-    __syncwarp();
-    float ql = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        if (mine[i])
-            e[place[i]] = T::narrow(-kInf);
-        out.id[lane + 32 * i] = mine[i] ? t.id[i] : -1;
-        out.x[lane + 32 * i] = x[i];
-        out.q[lane + 32 * i] = q[i];
-        out.part_q[lane + 32 * i] = place[i] >= 0 ? t.q[i] : 0.0f;
-        ql += t.q[i] > 0.0f ? t.q[i] * t.logq[i] : 0.0f;
-    }
-    ql = warp_sum(ql);
-    if (lane == 0) {
-        out.sum = t.sum;
-        out.rest = t.rest;
-        out.qlogq = ql;
-    }
-}
-
-// The sums over the entries in a part, in every lane of a warp.
-__device__ __forceinline__ Listed sum_entries(const Entries &en, const LogitRows &in)
-{
-    const int lane = threadIdx.x & 31;
-    float x[kSlots], m = -kInf;
-    bool mine[kSlots];
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        x[i] = en.x[lane + 32 * i];
-        mine[i] = en.id[lane + 32 * i] >= 0;
-        if (mine[i])
-            m = fmaxf(m, x[i]);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    Listed l = {m, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        const float q = en.part_q[lane + 32 * i];
-        if (mine[i])   // NaN for NaN and +inf
-            l.z += x[i] - x[i] == 0.0f || x[i] == -kInf ? exp2_approx(distance(x[i], safe_max(m), in) * in.c) : x[i] - x[i];
-        if (q > 0.0f) {
-            l.q += q;
-            l.dot = __fmaf_rn(q, quarter_distance(x[i], m), l.dot);
+            if (kTail) {   // each token once
+                bool first = true;
+                for (int j = 0; j < lane + 32 * i; ++j)
+                    first = first && sh.ids[j] != mine[i];
+                if (first)   // NaN for NaN and +inf
+                    l.z += x[i] - x[i] == 0.0f || x[i] == -kInf ? exp2_approx(distance(x[i], safe_max(m), a.in) * a.in.c) : x[i] - x[i];
+            }
         }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        l.z += __shfl_xor_sync(~0u, l.z, o);
-        l.q += __shfl_xor_sync(~0u, l.q, o);
-        l.dot += __shfl_xor_sync(~0u, l.dot, o);
-    }
-    return l;
-}
-
-// Rows by a cluster of CTAs, each holding a part of a row in shared memory:
-// logits are read from device memory once, for the loss and the gradient. In
-// each CTA
-//   - a warp fetches parts, by bulk copies, ahead of the others, and takes the
-//     listed tokens out of them;
-//   - eight warps sum the rest and send their sums to all CTAs of the cluster;
-//     then they write the gradient of the row before from shared memory, whose
-//     sums have been joined meanwhile;
-//   - a warp sends the listed tokens' sums, joins all, and writes the loss.
-// The rest is summed, not taken as 1 - sum p, which would lose a small one;
-// and it keeps a reference of its own: it may lie further below the listed
-// logits than FP32's exponents reach.
-template <class T>
-__global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a)
-{
-    typedef typename T::raw raw;
-    extern __shared__ __align__(16) unsigned char dynamic[];
-    __shared__ Shared sh;
-    const uint32_t size = cluster_size(), rank = cluster_rank();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t first = (int64_t)(blockIdx.x / size) * a.rows_each, last = min(a.in.rows, first + a.rows_each);
-    uint4 *const parts = reinterpret_cast<uint4 *>(dynamic);
-    if (tid == 0) {
-        for (int i = 0; i < kMaxBuffers; ++i) {
-            barrier_init(&sh.full[i], 1);
-            barrier_init(&sh.ready[i], 1);
-            barrier_init(&sh.empty[i], kWarps + 1);
-        }
-        for (int i = 0; i < kTurns; ++i) {
-            barrier_init(&sh.stats[i], size * (kWarps + 1));
-            barrier_init(&sh.joined[i], 1);
-        }
-        barrier_init(&sh.written, kWarps);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (size > 1) {   // the barriers are there before another CTA's sums come
-        cluster_arrive();
-        cluster_wait();
-    } else
-        __syncthreads();
-
-    bool ok = true;   // false: a wait ran out
-    if (warp == kFetcher) {
-        Cursor c;
-        uint32_t full_turn = 0;   // a bit for each buffer
-        float weight = a.weight ? a.weight[first] : 1.0f;
-        TeacherRaw raw_teacher = load_teacher(a.teacher, first);
-        for (int64_t r = first; r < last && ok; ++r, c.next(a.buffers)) {
-            uint4 *const buf = parts + c.at * a.buffer_vecs;
-            const Row<T> row(a.in, r);
-            const Part p = part_of(row, rank, size);
-            ok = warp_wait(&sh.empty[c.at], c.turn ^ 1);
-            const bool use = weight != 0.0f && ok;
-            if (use) {
-                // the last row's stores to this buffer come before the copies of this one
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                load_part<T>(row, p, buf, &sh.full[c.at]);
-            }
-            const float this_weight = weight;
-            const TeacherRaw w = raw_teacher;
-            if (r + 1 < last) {   // on their way while this row's logits come
-                weight = a.weight ? a.weight[r + 1] : 1.0f;
-                raw_teacher = load_teacher(a.teacher, r + 1);
-            }
-            if (use) {
-                const TeacherRow t = make_teacher(a.teacher, w, row.vocab);
-                ok = warp_wait(&sh.full[c.at], (full_turn >> c.at) & 1);
-                full_turn ^= 1u << c.at;
-                __syncwarp();
-                take_entries<T>(row, p, buf, t, a.teacher.k, sh, sh.entries[c.at]);
-            }
-            if (lane == 0)
-                sh.entries[c.at].weight = this_weight;
-            __syncwarp();
-            if (lane == 0 && ok)
-                barrier_arrive(&sh.ready[c.at]);
-        }
-        if (!ok)   // copies that are still on their way are not left behind
-            for (int i = 0; i < a.buffers; ++i)
-                barrier_wait(&sh.full[i], (full_turn >> i) & 1);
-    } else if (warp == kJoiner) {
-        Cursor c;
-        uint32_t active = 0;   // rows whose sums have been exchanged
-        for (int64_t r = first; r < last; ++r, c.next(a.buffers)) {
-            const Entries &en = sh.entries[c.at];
-            ok = ok && warp_wait(&sh.ready[c.at], c.turn);
-            const float weight = en.weight;
-            const bool writes = (uint32_t)r % size == rank && lane == 0;   // the loss, in turn
-            if (!ok || weight == 0.0f) {   // the same in all CTAs of the cluster
-                if (writes && a.loss)
-                    a.loss[r] = ok ? 0.0f : __int_as_float(0x7fffffff);
-            } else {
-                const int turn = active % kTurns;
-                const Listed own = sum_entries(en, a.in);
-                if (size == 1) {
-                    if (lane == 0) {
-                        sh.listed[turn][0] = own;
-                        barrier_arrive(&sh.stats[turn]);
-                    }
-                } else if (lane < (int)size) {
-                    const uint32_t at = map_shared(&sh.listed[turn][rank], lane);
-                    st_cluster(at, own.m, own.z);
-                    st_cluster(at + 8, own.q, own.dot);
-                    fence_cluster();
-                    arrive_cluster(map_shared(&sh.stats[turn], lane));
-                }
-                ok = warp_wait(&sh.stats[turn], (active / kTurns) & 1);
-                if (size > 1)
-                    fence_cluster();
-                ++active;
-                // the rest: two of the warps' sums a lane, of one reference first
-                float2 u = make_float2(-kInf, 0.0f), v = u;
-                if (lane < (int)size * kWarps)
-                    u = sh.rest[turn][lane];
-                if (lane + 32 < (int)size * kWarps)
-                    v = sh.rest[turn][lane + 32];
-                const Listed l = lane < (int)size ? sh.listed[turn][lane] : Listed{-kInf, 0.0f, 0.0f, 0.0f};
-                float mr = fmaxf(u.x, v.x), ml = l.m;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    mr = fmaxf(mr, __shfl_xor_sync(~0u, mr, o));
-                    ml = fmaxf(ml, __shfl_xor_sync(~0u, ml, o));
-                }
-                const float m = fmaxf(mr, ml), mm = safe_max(m), mrr = safe_max(mr);
-                // exponentials of -160 powers of two and less are 0
-                float zr = u.y * exp2_approx(distance(u.x, mrr, a.in) * a.in.c) + v.y * exp2_approx(distance(v.x, mrr, a.in) * a.in.c);
-                float zl = l.z * exp2_approx(distance(l.m, mm, a.in) * a.in.c);
-                float qs = l.q, dot = l.q != 0.0f ? __fmaf_rn(l.q, quarter_distance(l.m == -kInf ? 0.0f : l.m, m), l.dot) : 0.0f;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    zr += __shfl_xor_sync(~0u, zr, o);
-                    zl += __shfl_xor_sync(~0u, zl, o);
-                    qs += __shfl_xor_sync(~0u, qs, o);
-                    dot += __shfl_xor_sync(~0u, dot, o);
-                }
-                const float down = exp2_approx(distance(mr, mm, a.in) * a.in.c);
-                const float z = __fmaf_rn(zr, down, zl), inv_z = z == 0.0f ? 0.0f : 1.0f / z;
-                const float sum = ok ? en.sum : __int_as_float(0x7fffffff), q_rest = en.rest;
-                // an unlisted token: p - q_rest p / p_rest, by 2^((x - m_rest) c)
-                const float f = __fsub_rn(down * (sum * inv_z), zr == 0.0f ? 0.0f : q_rest / zr);
-                if (lane == 0) {
-                    sh.co[turn] = Coefficients{mrr, f, mm, inv_z};
-                    barrier_arrive(&sh.joined[turn]);
-                }
-                if (writes) {
-                    // KL = sum q ln q - sum q s + (sum q) ln Z, and the rest's term
-                    const float ln_z = logf(z);
-                    float kl = en.qlogq;
-                    if (qs != 0.0f)
-                        kl = __fmaf_rn(dot, -4.0f * a.in.inv_t, __fmaf_rn(qs, ln_z, kl));
-                    if (z == 0.0f && sum != 0.0f)
-                        kl = kInf;
-                    if (q_rest > 0.0f)
-                        kl = zr == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - (__fmaf_rn(quarter_distance(mr, m), 4.0f * a.in.inv_t, logf(zr)) - ln_z));
-                    if (sum != sum || z != z)
-                        kl = __int_as_float(0x7fffffff);
-                    if (a.loss)
-                        a.loss[r] = kl * weight;
-                    if (a.stats)
-                        a.stats[r] = make_float4(m, z, mr, f);
-                }
-            }
-            __syncwarp();
-            if (lane == 0)
-                barrier_arrive(&sh.empty[c.at]);
+        l.z = warp_sum(l.z);
+        l.q = warp_sum(l.q);
+        l.dot = warp_sum(l.dot);
+        ql = warp_sum(ql);
+        if (lane == 0) {
+            sh.listed = l;
+            sh.sum = t.sum;
+            sh.rest = t.rest;
+            sh.qlogq = ql;
         }
     } else {
-        Cursor c, d;                            // of the row that is summed, of the one whose gradient is written
-        uint32_t summed = 0, done = 0, full_turn = 0;
-        const bool has_grad = a.grad.data != nullptr;
-        const int lag = a.buffers > 1 && has_grad ? 1 : 0;
-        for (int64_t r = first; r < last + lag; ++r) {
-            if (r < last) {
-                const uint4 *const buf = parts + c.at * a.buffer_vecs;
-                const Part p = part_of(Row<T>(a.in, r), rank, size);
-                ok = ok && warp_wait(&sh.ready[c.at], c.turn);
-                if (ok && sh.entries[c.at].weight != 0.0f) {
-                    ok = warp_wait(&sh.full[c.at], (full_turn >> c.at) & 1);
-                    full_turn ^= 1u << c.at;
-                    Running<T, false> run;
-#pragma unroll 2
-                    for (int i = tid; i < p.n; i += kConsumers)
-                        run.add(buf[i], a.in);
-                    const Stat part = warp_join<false>(run.stat(a.in), a.in);
-                    const int turn = summed++ % kTurns, slot = rank * kWarps + warp;
-                    if (size == 1) {
-                        if (lane == 0) {
-                            sh.rest[turn][slot] = make_float2(part.m, part.z);
-                            barrier_arrive(&sh.stats[turn]);
-                        }
-                    } else if (lane < (int)size) {
-                        st_cluster(map_shared(&sh.rest[turn][slot], lane), part.m, part.z);
-                        fence_cluster();
-                        arrive_cluster(map_shared(&sh.stats[turn], lane));
+        if (kTail)
+            block_barrier();
+        Running<T, false> run;
+        for (int i0 = p.v0; i0 < end; i0 += kGroupStep) {
+            const int i = i0 + tid;
+            if (i0 >= row.full0 && i0 + kGroupStep <= min(end, row.full1)) {
+                uint4 v[kGroup];
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    v[j] = *row.vec(i + j * kStream);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) {
+                    if (kTail) {
+                        const uint32_t mask = marks[i - p.v0 + j * kStream];
+                        if (mask)
+                            v[j] = without<T>(v[j], mask);
                     }
+                    run.add(v[j], a.in);
                 }
-                if (!has_grad) {
-                    __syncwarp();
-                    if (lane == 0)
-                        barrier_arrive(&sh.empty[c.at]);
-                }
-                c.next(a.buffers);
+            } else {
+#pragma unroll 1
+                for (int j = i; j < min(end, i0 + kGroupStep); j += kStream)
+                    run.add(without<T>(load_vec(row, j), kTail ? marks[j - p.v0] : 0u), a.in);
             }
-            if (!has_grad || r < first + lag)
-                continue;
-            const uint4 *const buf = parts + d.at * a.buffer_vecs;
-            const Entries &en = sh.entries[d.at];
-            const Row<T> row(a.in, r - lag);
-            const Part p = part_of(row, rank, size);
-            raw *const g = static_cast<raw *>(a.grad.data) + row_offset(a.in, r - lag, a.grad.row_stride, a.grad.outer_stride);
-            const bool aligned = same_phase(row, g);
-            if (ok && en.weight == 0.0f) {
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                for (int i = tid; i < p.n; i += kConsumers) {
-                    const int at = p.v0 + i;
-                    if (aligned && at >= row.full0 && at < row.full1)
-                        store_stream(g + row.id(at, 0), zero);
-                    else
-                        store_edge<T>(g, row, at, zero);
-                }
-            } else if (ok) {
-                const int turn = done % kTurns;
-                ok = warp_wait(&sh.joined[turn], (done / kTurns) & 1);
-                const Coefficients co = sh.co[turn];
-                const float scale = en.weight * a.in.inv_t;
-                const f2 nm = splat(-co.m_rest), f = splat(co.f * (scale / T::kShift));
-#pragma unroll 2
-                for (int i = tid; i < p.n; i += kConsumers) {
-                    const int at = p.v0 + i;
-                    const uint4 v = grad_vec<T>(buf[i], nm, f, a.in);
-                    if (aligned && at >= row.full0 && at < row.full1)
-                        store_stream(g + row.id(at, 0), v);
-                    else
-                        store_edge<T>(g, row, at, v);
-                }
-                // the listed tokens' places once more, after the vectors
-                __syncwarp();
-                if (lane == 0)
-                    barrier_arrive(&sh.written);
-                if (warp < kSlots)
-                    ok = warp_wait(&sh.written, done & 1) && ok;
-                ++done;
-                if (tid < FO_MAX_TOP_K && en.id[tid] >= 0)
-                    g[en.id[tid]] = T::narrow(co.inv_z == 0.0f ? 0.0f : grad_listed<T>(en.x[tid], co.m, en.q[tid], en.sum, co.inv_z, scale, a.in));
-            }
-            __syncwarp();
-            if (lane == 0)
-                barrier_arrive(&sh.empty[d.at]);
-            d.next(a.buffers);
         }
+        s = warp_join<false>(run.stat(a.in), a.in);
+        if (lane == 0)
+            sh.part[tid >> 5] = s;
     }
-    if (size > 1) {   // no CTA leaves while another may write to it
+    block_barrier();
+    s = warp_join<false>(sh.part[lane % kWarps], a.in, kWarps);
+    Listed l = sh.listed;
+    if (size > 1) {
+        if (tid == 0)
+            sh.mine = s;
         cluster_arrive();
         cluster_wait();
+        const uint32_t at = map_shared(&sh.mine, lane % size), from = map_shared(&sh.listed, lane % size);
+        const bool once = lane < (int)size;
+        const float2 v = join_pairs(ld_cluster_f32(at), once ? ld_cluster_f32(at + 4) : 0.0f, a.in);
+        s = Stat{v.x, v.y, 0.0f};
+        const float4 u = ld_cluster_f4(from);
+        const float2 lz = join_pairs(u.x, once ? u.y : 0.0f, a.in);
+        l.m = lz.x;
+        l.z = lz.y;
+        l.q = warp_sum(once ? u.z : 0.0f);
+        l.dot = warp_sum(once && u.z != 0.0f ? __fmaf_rn(u.z, quarter_distance(u.x == -kInf ? 0.0f : u.x, l.m), u.w) : 0.0f);
+        cluster_arrive();   // what was read here is free to go; the wait is at the end
     }
+    // of all tokens (without tail the listed ones are in s already); m_rest and z_rest of those that are not listed
+    const float m = kTail ? fmaxf(s.m, l.m) : s.m, mm = safe_max(m), m_rest = safe_max(s.m);
+    const float down = exp2_approx(distance(s.m, mm, a.in) * a.in.c);
+    const float z = kTail ? __fmaf_rn(s.z, down, l.z * exp2_approx(distance(l.m, mm, a.in) * a.in.c)) : s.z;
+    const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = sh.sum, q_rest = sh.rest;
+    // an unlisted token: p - q_rest p / p_rest, by 2^((x - m_rest) c)
+    const float f = __fsub_rn(down * (sum * inv_z), !kTail || s.z == 0.0f ? 0.0f : q_rest / s.z);
+    if (g) {
+        const float scale = weight * a.in.inv_t;
+        const f2 nm = splat(-m_rest), ff = splat(f * (scale / T::kShift));
+        if (tid < kStream) {
+            for (int i0 = p.v0; i0 < end; i0 += kGroupStep) {
+                const int i = i0 + tid;
+                if (i0 >= max(lo, row.full0) && i0 + kGroupStep <= min(end, hi)) {
+                    uint4 v[kGroup];
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        v[j] = __ldcs(row.vec(i + j * kStream));
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        store_stream(g + row.id(i + j * kStream, 0), grad_vec<T>(v[j], nm, ff, a.in));
+                } else {
+#pragma unroll 1
+                    for (int j = i; j < min(end, i0 + kGroupStep); j += kStream) {
+                        const uint4 v = grad_vec<T>(load_vec(row, j), nm, ff, a.in);
+                        if (j >= lo && j < hi)
+                            store_stream(g + row.id(j, 0), v);
+                        else
+                            store_edge<T>(g, row, j, v);
+                    }
+                }
+            }
+        }
+        block_barrier();
+        if (tid >= kStream) {   // the listed tokens' places once more; the first of equal ids takes the weight of all
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                if (mine[i] < 0)
+                    continue;
+                float q = 0.0f;
+                bool first = true;
+                for (int j = 0; j < a.teacher.k; ++j)
+                    if (sh.ids[j] == mine[i]) {
+                        q += sh.q[j];
+                        first = first && j >= lane + 32 * i;
+                    }
+                if (first)
+                    g[mine[i]] = T::narrow(z == 0.0f ? 0.0f : grad_listed<T>(x[i], mm, q, sum, inv_z, scale, a.in));
+            }
+        }
+    }
+    if (rank == 0 && tid == 0) {
+        // KL = sum q ln q - sum q s + (sum q) ln Z, and the rest's term
+        const float ln_z = logf(z), four = 4.0f * a.in.inv_t;
+        float kl = sh.qlogq;
+        if (l.q != 0.0f)
+            kl = __fmaf_rn(-four, __fmaf_rn(l.q, quarter_distance(l.m == -kInf ? 0.0f : l.m, m), l.dot), __fmaf_rn(l.q, ln_z, kl));
+        if (z == 0.0f && sum != 0.0f)
+            kl = kInf;
+        if (kTail && q_rest > 0.0f)
+            kl = s.z == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - (__fmaf_rn(quarter_distance(s.m, m), four, logf(s.z)) - ln_z));
+        if (sum != sum || z != z)
+            kl = __int_as_float(0x7fffffff);
+        if (a.loss)
+            a.loss[r] = kl * weight;
+        if (a.stats)
+            a.stats[r] = make_float4(m, z, s.m, f);
+    }
+    if (size > 1)
+        cluster_wait();   // no CTA leaves while another reads its shared memory
 }
 
 // The gradient from saved statistics.
@@ -606,26 +465,18 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillGradA
 }
 
 template <class T>
-cudaError_t launch(const DistillArgs &args, cudaStream_t stream)
+cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
 {
-    DistillArgs a = args;
-    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), sms = sm_count();
-    // the smallest cluster whose parts are at most kPartBytes (three buffers of
-    // which leave room for two CTAs on an SM); larger while the grid would
-    // leave SMs without a CTA and parts stay above 8 KB
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * kCtasPerSm;
+    // one CTA a row, or a cluster that shares it: while the rows at work at
+    // once would not stay in the L2 cache between the passes, and while the
+    // grid would leave SMs short of CTAs
     int size = 1;
-    while (size < kMaxCluster && (bytes > size * kPartBytes || (a.in.rows * size < 2 * sms && bytes > size * 8192)))
+    while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (a.in.rows * size < ctas && bytes > size * 8192)))
         size *= 2;
-    a.buffer_vecs = (int)part_vecs(bytes, size);
-    const int64_t part = a.buffer_vecs * 16;
-    a.buffers = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBuffers, kSharedBytes / part));
-    // rows in turn by one cluster, so that fetching runs ahead, as far as the
-    // clusters that fit on the GPU at once still get several such groups each
-    const int64_t resident = std::max<int64_t>(1, sms * std::min<int64_t>(3, (kSharedBytes + sizeof(Shared)) / (a.buffers * part + sizeof(Shared))) / size);
-    a.rows_each = (int)std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows / (4 * resident)));
-    a.buffers = std::min(a.buffers, a.rows_each);
-    const int64_t clusters = (a.in.rows + a.rows_each - 1) / a.rows_each;
-    return launch_cluster(distill_kernel<T>, a, clusters, size, a.buffers * part, kThreads, stream);
+    if (a.teacher.tail)
+        return launch_cluster(distill_kernel<T, true>, a, a.in.rows, size, (part_vecs(bytes, size) + 15) / 16 * 16, kThreads, stream);
+    return launch_cluster(distill_kernel<T, false>, a, a.in.rows, size, 0, kThreads, stream);
 }
 
 template <class T>

@@ -63,9 +63,6 @@ struct DistillArgs {
     float *loss;             // may be null
     float4 *stats;           // may be null
     GradRows grad;           // data may be null
-    // set by the launch: rows that a cluster takes one after the other, parts
-    // that its CTAs hold at once (1 or 2) and the vectors of each
-    int32_t rows_each, buffers, buffer_vecs;
 };
 
 struct DistillGradArgs {
