@@ -181,12 +181,20 @@ def _ptr(x, name: str = "tensor", dtypes=None, min_numel: Optional[int] = None) 
     return x.data_ptr()
 
 
+_raw_stream = None   # torch's current stream of a device, as an address
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
         import torch
-        if not torch.cuda.is_available():
-            return None
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            if not torch.cuda.is_available():
+                return None
+            # without a Stream object (4 us on the host) where torch has the call
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+                (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     dev = getattr(stream, "device", None)
@@ -227,8 +235,6 @@ class _Dtypes:
                 "rho8": (torch.int8,),
                 "rho16": (torch.int16,),
                 "m_q": (torch.int8,),
-                "i32": (torch.int32,),
-                "i64": (torch.int64,),
                 "v_q": (torch.uint8,),
             }
         return cls._cache
@@ -425,13 +431,21 @@ def _row_strides(x, name: str):
     return dims[0][0] * dims[1][0], max(1, dims[1][0]), dims[1][1], dims[0][1]
 
 
-def _device_ptr(x, name: str) -> int:
+def _device_ptr(x, name: str, cur: int) -> int:
     if not x.is_cuda:
         raise ValueError(f"{name}: the library reads and writes device memory: pass CUDA tensors")
-    cur = _current_device()
     if x.device.index != cur:
         raise ValueError(f"{name} is on cuda:{x.device.index} but the current device is cuda:{cur}; "
                          "the library launches on the current device (use torch.cuda.device)")
+    return x.data_ptr()
+
+
+def _array(x, name: str, dtype, numel: int, cur: int) -> Optional[int]:
+    """``_ptr`` for one element type, with the current device known."""
+    if x is None:
+        return None
+    if x.dtype is not dtype or not x.is_cuda or x.device.index != cur or not x.is_contiguous() or x.numel() < numel:
+        return _ptr(x, name, (dtype,), numel)     # says what is wrong
     return x.data_ptr()
 
 
@@ -439,7 +453,7 @@ def logits_rows(x, temperature: float = 1.0, name: str = "logits") -> FoLogits:
     """The ``fo_logits_t`` of a tensor [..., vocab] of bfloat16, float16 or
     float32: any leading dimensions that two strides cover, the last contiguous."""
     dt = _logit_dtype(x.dtype, name)
-    ptr = _device_ptr(x, name)
+    ptr = _device_ptr(x, name, _current_device())
     rows, inner, rs, os_ = _row_strides(x, name)
     return FoLogits(ptr, rows, x.shape[-1], rs, inner, os_, float(temperature), dt, 0)
 
@@ -453,7 +467,7 @@ def _logits_grad(logits: FoLogits, like, grad, name: str = "grad"):
                         f"{str(grad.dtype).replace('torch.', '')}")
     if grad.shape != like.shape:
         raise ValueError(f"{name} must have the logits' shape {tuple(like.shape)}, not {tuple(grad.shape)}")
-    ptr = _device_ptr(grad, name)
+    ptr = _device_ptr(grad, name, _current_device())
     rows, inner, rs, os_ = _row_strides(grad, name)
     want = logits.inner_rows
     if inner != want:               # one of the two needs a single stride where the other has two
@@ -466,8 +480,8 @@ def _logits_grad(logits: FoLogits, like, grad, name: str = "grad"):
     return FoLogitsGrad(ptr, rs, os_)
 
 
-def _teacher(ids, logits, lse, rows: int, temperature: float, tail: bool) -> FoTeacher:
-    d = _Dtypes.get()
+def _teacher(ids, logits, lse, rows: int, temperature: float, tail: bool, cur: int) -> FoTeacher:
+    import torch
     if logits.shape != ids.shape or len(ids.shape) < 1:
         raise ValueError(f"teacher_ids and teacher_logits must have one shape [..., k], not {tuple(ids.shape)} "
                          f"and {tuple(logits.shape)}")
@@ -477,53 +491,65 @@ def _teacher(ids, logits, lse, rows: int, temperature: float, tail: bool) -> FoT
     dt = _logit_dtype(logits.dtype, "teacher_logits")
     if lse is not None and not tail:
         raise ValueError("teacher_lse is read with tail=True only")
-    return FoTeacher(_ptr(ids, "teacher_ids", d["i32"]), _ptr(logits, "teacher_logits"),
-                     _ptr(lse, "teacher_lse", d["f32"], rows), float(temperature), k, dt, 1 if tail else 0, 0)
+    return FoTeacher(_array(ids, "teacher_ids", torch.int32, 0, cur), _array(logits, "teacher_logits", logits.dtype, 0, cur),
+                     _array(lse, "teacher_lse", torch.float32, rows, cur), temperature, k, dt, 1 if tail else 0, 0)
 
 
 def fo_token_logprobs(logits, tokens=None, top_k: int = 0, logp=None, entropy=None, top_ids=None, top_logp=None,
                       stats=None, temperature: float = 1.0, stream=None):
+    import torch
     x = logits_rows(logits, temperature)
-    n, d = x.rows, _Dtypes.get()
-    _check("fo_token_logprobs", lib().fo_token_logprobs(
-        ctypes.byref(x), _ptr(tokens, "tokens", d["i64"], n), int(top_k), _ptr(logp, "logp", d["f32"], n),
-        _ptr(entropy, "entropy", d["f32"], n), _ptr(top_ids, "top_ids", d["i32"], n * top_k),
-        _ptr(top_logp, "top_logp", d["f32"], n * top_k), _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS),
-        _stream(stream)))
+    n, f32, cur = x.rows, torch.float32, _current_device()
+    status = lib().fo_token_logprobs(
+        ctypes.byref(x), _array(tokens, "tokens", torch.int64, n, cur), int(top_k), _array(logp, "logp", f32, n, cur),
+        _array(entropy, "entropy", f32, n, cur), _array(top_ids, "top_ids", torch.int32, n * top_k, cur),
+        _array(top_logp, "top_logp", f32, n * top_k, cur), _array(stats, "stats", f32, n * FO_LOSS_STATS, cur),
+        _stream(stream))
+    if status:
+        _check("fo_token_logprobs", status)
 
 
 def fo_token_logprobs_grad(logits, stats, grad, tokens=None, g_logp=None, g_entropy=None, top_ids=None, g_top=None,
                            top_k: int = 0, temperature: float = 1.0, stream=None):
+    import torch
     x = logits_rows(logits, temperature)
     g = _logits_grad(x, logits, grad)
-    n, d = x.rows, _Dtypes.get()
-    _check("fo_token_logprobs_grad", lib().fo_token_logprobs_grad(
-        ctypes.byref(x), _ptr(tokens, "tokens", d["i64"], n), int(top_k),
-        _ptr(top_ids, "top_ids", d["i32"], n * top_k), _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS),
-        _ptr(g_logp, "g_logp", d["f32"], n), _ptr(g_entropy, "g_entropy", d["f32"], n),
-        _ptr(g_top, "g_top", d["f32"], n * top_k), None if g is None else ctypes.byref(g), _stream(stream)))
+    n, f32, cur = x.rows, torch.float32, _current_device()
+    status = lib().fo_token_logprobs_grad(
+        ctypes.byref(x), _array(tokens, "tokens", torch.int64, n, cur), int(top_k),
+        _array(top_ids, "top_ids", torch.int32, n * top_k, cur), _array(stats, "stats", f32, n * FO_LOSS_STATS, cur),
+        _array(g_logp, "g_logp", f32, n, cur), _array(g_entropy, "g_entropy", f32, n, cur),
+        _array(g_top, "g_top", f32, n * top_k, cur), None if g is None else ctypes.byref(g), _stream(stream))
+    if status:
+        _check("fo_token_logprobs_grad", status)
 
 
 def fo_distill(logits, teacher_ids, teacher_logits, teacher_lse=None, row_weight=None, loss=None, stats=None,
                grad=None, temperature: float = 1.0, teacher_temperature: float = 1.0, tail: bool = False, stream=None):
+    import torch
     x = logits_rows(logits, temperature)
     g = _logits_grad(x, logits, grad)
-    n, d = x.rows, _Dtypes.get()
-    t = _teacher(teacher_ids, teacher_logits, teacher_lse, n, teacher_temperature, tail)
-    _check("fo_distill", lib().fo_distill(
-        ctypes.byref(x), ctypes.byref(t), _ptr(row_weight, "row_weight", d["f32"], n), _ptr(loss, "loss", d["f32"], n),
-        _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS), None if g is None else ctypes.byref(g), _stream(stream)))
+    n, f32, cur = x.rows, torch.float32, _current_device()
+    t = _teacher(teacher_ids, teacher_logits, teacher_lse, n, teacher_temperature, tail, cur)
+    status = lib().fo_distill(
+        ctypes.byref(x), ctypes.byref(t), _array(row_weight, "row_weight", f32, n, cur), _array(loss, "loss", f32, n, cur),
+        _array(stats, "stats", f32, n * FO_LOSS_STATS, cur), None if g is None else ctypes.byref(g), _stream(stream))
+    if status:
+        _check("fo_distill", status)
 
 
 def fo_distill_grad(logits, teacher_ids, teacher_logits, stats, g_loss, grad, teacher_lse=None,
                     temperature: float = 1.0, teacher_temperature: float = 1.0, tail: bool = False, stream=None):
+    import torch
     x = logits_rows(logits, temperature)
     g = _logits_grad(x, logits, grad)
-    n, d = x.rows, _Dtypes.get()
-    t = _teacher(teacher_ids, teacher_logits, teacher_lse, n, teacher_temperature, tail)
-    _check("fo_distill_grad", lib().fo_distill_grad(
-        ctypes.byref(x), ctypes.byref(t), _ptr(stats, "stats", d["f32"], n * FO_LOSS_STATS),
-        _ptr(g_loss, "g_loss", d["f32"], n), None if g is None else ctypes.byref(g), _stream(stream)))
+    n, f32, cur = x.rows, torch.float32, _current_device()
+    t = _teacher(teacher_ids, teacher_logits, teacher_lse, n, teacher_temperature, tail, cur)
+    status = lib().fo_distill_grad(
+        ctypes.byref(x), ctypes.byref(t), _array(stats, "stats", f32, n * FO_LOSS_STATS, cur),
+        _array(g_loss, "g_loss", f32, n, cur), None if g is None else ctypes.byref(g), _stream(stream))
+    if status:
+        _check("fo_distill_grad", status)
 
 
 FO_VERIFY_COUNTS = 6

@@ -19,6 +19,7 @@ lies. The rules for masked, infinite and invalid entries stand in
 """
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -43,7 +44,7 @@ def _aligned_like(logits: torch.Tensor) -> torch.Tensor:
     alignment (modulo 16 bytes), so that the kernels' vectors of both line up:
     rows of an odd vocabulary in a padded matrix would otherwise not. At most
     7 elements are added to a row."""
-    if logits.dim() == 2 and logits.shape[0] > 1 and logits.stride(0) >= logits.shape[1]:
+    if logits.dim() == 2 and logits.shape[0] > 1 and logits.stride(0) > logits.shape[1]:
         per_16 = 16 // logits.element_size()
         pitch = logits.shape[1] + (logits.stride(0) - logits.shape[1]) % per_16
         return torch.empty((logits.shape[0], pitch), dtype=logits.dtype,
@@ -51,35 +52,46 @@ def _aligned_like(logits: torch.Tensor) -> torch.Tensor:
     return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
 
 
+def _on_device_of(x: torch.Tensor):
+    """Backward passes run on autograd's threads: the library's calls launch on the current device."""
+    return contextlib.nullcontext() if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)
+
+
+def _logprobs(logits, tokens, top_k, temperature, entropy, stats):
+    rows, dev, f32 = logits.shape[:-1], logits.device, torch.float32
+    logp = torch.empty(rows, dtype=f32, device=dev) if tokens is not None else None
+    ent = torch.empty(rows, dtype=f32, device=dev) if entropy else None
+    top_ids = torch.empty(rows + (top_k,), dtype=torch.int32, device=dev) if top_k else None
+    top_logp = torch.empty(rows + (top_k,), dtype=f32, device=dev) if top_k else None
+    fo.fo_token_logprobs(logits, tokens, top_k, logp, ent, top_ids, top_logp, stats, temperature)
+    return logp, ent, top_ids, top_logp
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, top_k, temperature, entropy):
-        rows = logits.shape[:-1]
-        f32 = dict(dtype=torch.float32, device=logits.device)
-        logp = torch.empty(rows, **f32) if tokens is not None else None
-        ent = torch.empty(rows, **f32) if entropy else None
-        top_ids = torch.empty(rows + (top_k,), dtype=torch.int32, device=logits.device) if top_k else None
-        top_logp = torch.empty(rows + (top_k,), **f32) if top_k else None
-        stats = torch.empty(rows + (fo.FO_LOSS_STATS,), **f32) if ctx.needs_input_grad[0] else None
-        fo.fo_token_logprobs(logits, tokens, top_k, logp, ent, top_ids, top_logp, stats, temperature)
-        if stats is not None:
-            ctx.save_for_backward(logits, tokens, top_ids, stats)
-            ctx.temperature = temperature
-            if top_ids is not None:
-                ctx.mark_non_differentiable(top_ids)
-            ctx.set_materialize_grads(False)
-        return logp, ent, top_ids, top_logp
+        stats = torch.empty(logits.shape[:-1] + (fo.FO_LOSS_STATS,), dtype=torch.float32, device=logits.device)
+        out = _logprobs(logits, tokens, top_k, temperature, entropy, stats)
+        ctx.save_for_backward(logits, tokens, out[2], stats)
+        ctx.temperature = temperature
+        if top_k:
+            ctx.mark_non_differentiable(out[2])
+        ctx.set_materialize_grads(False)
+        return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_logp, g_entropy, _, g_top):
         logits, tokens, top_ids, stats = ctx.saved_tensors
-        c = lambda g: None if g is None else g.contiguous()
         grad = _aligned_like(logits)
-        with torch.cuda.device(logits.device):
-            fo.fo_token_logprobs_grad(logits, stats, grad, tokens, c(g_logp), c(g_entropy), top_ids, c(g_top),
-                                      0 if top_ids is None else top_ids.shape[-1], ctx.temperature)
+        with _on_device_of(logits):
+            fo.fo_token_logprobs_grad(logits, stats, grad, tokens, _dense(g_logp), _dense(g_entropy), top_ids,
+                                      _dense(g_top), 0 if top_ids is None else top_ids.shape[-1], ctx.temperature)
         return grad, None, None, None, None
+
+
+def _dense(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if g is None else g.contiguous()
 
 
 def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top_k: int = 0,
@@ -92,26 +104,25 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     ascending id. Differentiable in the logits through ``logp``, ``entropy``
     and ``top_logp``.
     """
-    top_k = int(top_k)
     if tokens is not None:
         _check_rows("tokens", tokens, logits.shape[:-1])
         tokens = tokens.contiguous()
-    if not 0 <= top_k <= fo.FO_MAX_TOP_K or (top_k > logits.shape[-1] and logits.numel()):
+    if top_k and (not 0 < top_k <= fo.FO_MAX_TOP_K or (top_k > logits.shape[-1] and logits.numel())):
         raise ValueError(f"top_k must be in 0..{min(fo.FO_MAX_TOP_K, logits.shape[-1])}, not {top_k}")
-    return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, top_k, float(temperature), bool(entropy)))
+    if logits.requires_grad and torch.is_grad_enabled():
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, top_k, float(temperature), bool(entropy)))
+    return TokenLogprobs(*_logprobs(logits, tokens, top_k, float(temperature), entropy, None))
 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, teacher, lse, temperature, teacher_temperature, tail):
-        rows = logits.shape[:-1]
-        loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        stats = None
-        if ctx.needs_input_grad[0]:
-            stats = torch.empty(rows + (fo.FO_LOSS_STATS,), dtype=torch.float32, device=logits.device)
-            ctx.save_for_backward(logits, ids, teacher, lse, stats)
-            ctx.how = (temperature, teacher_temperature, tail)
+        rows, dev = logits.shape[:-1], logits.device
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        stats = torch.empty(rows + (fo.FO_LOSS_STATS,), dtype=torch.float32, device=dev)
         fo.fo_distill(logits, ids, teacher, lse, None, loss, stats, None, temperature, teacher_temperature, tail)
+        ctx.save_for_backward(logits, ids, teacher, lse, stats)
+        ctx.how = (temperature, teacher_temperature, tail)
         return loss
 
     @staticmethod
@@ -119,7 +130,7 @@ class _Distill(torch.autograd.Function):
     def backward(ctx, g_loss):
         logits, ids, teacher, lse, stats = ctx.saved_tensors
         grad = _aligned_like(logits)
-        with torch.cuda.device(logits.device):
+        with _on_device_of(logits):
             fo.fo_distill_grad(logits, ids, teacher, stats, g_loss.contiguous(), grad, lse, *ctx.how)
         return grad, None, None, None, None, None, None
 
@@ -148,12 +159,16 @@ def distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     one more outcome. Differentiable in ``logits``; no factor T^2 is applied.
     """
     _check_teacher(logits, teacher_ids, teacher_logits, teacher_lse)
-    return _Distill.apply(logits, teacher_ids.contiguous(), teacher_logits.detach().contiguous(),
-                          None if teacher_lse is None else teacher_lse.detach().contiguous(), float(temperature),
-                          float(teacher_temperature), bool(tail))
+    ids, teacher = teacher_ids.contiguous(), teacher_logits.detach().contiguous()
+    lse = None if teacher_lse is None else teacher_lse.detach().contiguous()
+    how = (float(temperature), float(teacher_temperature), bool(tail))
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _Distill.apply(logits, ids, teacher, lse, *how)
+    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
+    fo.fo_distill(logits, ids, teacher, lse, None, loss, None, None, *how)
+    return loss
 
 
-@torch.no_grad()
 def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, *,
                       row_weight: Optional[torch.Tensor] = None, temperature: float = 1.0,
                       teacher_temperature: float = 1.0, tail: bool = False,
@@ -169,8 +184,6 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
     _check_rows("row_weight", row_weight, logits.shape[:-1])
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
     grad = _aligned_like(logits) if out is None else out
-    fo.fo_distill(logits, teacher_ids.contiguous(), teacher_logits.contiguous(),
-                  None if teacher_lse is None else teacher_lse.contiguous(),
-                  None if row_weight is None else row_weight.contiguous(), loss, None, grad, temperature,
-                  teacher_temperature, tail)
+    fo.fo_distill(logits, teacher_ids.contiguous(), teacher_logits.contiguous(), _dense(teacher_lse), _dense(row_weight),
+                  loss, None, grad, float(temperature), float(teacher_temperature), bool(tail))
     return loss, grad
