@@ -7,14 +7,16 @@
 namespace fo {
 namespace {
 
-constexpr int kStream = 256;                      // threads that walk over a row
-constexpr int kWarps = kStream / 32;
-constexpr int kThreads = kStream + 32;            // and a warp for the teacher's entries
-constexpr int kGroup = 4;                         // vectors that a thread loads at once
-constexpr int kGroupStep = kGroup * kStream;
+constexpr int kWarps = 8;                         // that walk over a row
+constexpr int kStream = kWarps * 32;
+constexpr int kFetcher = kWarps, kTeacher = kWarps + 1;   // and two more: see distill_kernel
+constexpr int kThreads = kStream + 64;
+constexpr int kStageVecs = 2 * kStream;           // vectors that are copied at once (8 KB)
+constexpr int kStages = 8;                        // such copies in flight or in use
 constexpr int kGradThreads = 256;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 constexpr int64_t kCacheBytes = 80 << 20;         // of the 129 MB L2 cache, for rows between their passes
+constexpr int kMaxRowsEach = 8;
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -125,20 +127,16 @@ struct Listed {
 };
 
 struct Shared {
-    Listed listed;
-    Stat part[kWarps];
-    Stat mine;                  // this CTA's sums, read by the others of the cluster
-    float sum, rest, qlogq;     // of the teacher's row
-    int32_t ids[FO_MAX_TOP_K];
+    uint64_t full[kStages], ready[kStages], empty[kStages];   // of a stage: copied; the listed tokens taken out; used
+    uint64_t summed, joined, written;                         // of a row
+    uint64_t cluster[2];                                      // all CTAs' sums have come
+    float4 sums[2][kMaxCluster];                              // written by each CTA into all: listed m, z, q, dot,
+    float2 rests[2][kMaxCluster];                             // and the streamed m, z
+    float2 part[kWarps];                                      // m, z of the warps
+    float m, f;                                               // the gradient: f 2^((x - m) c)
+    __align__(16) int32_t ids[FO_MAX_TOP_K];
     float q[FO_MAX_TOP_K];
 };
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
-}
 
 // m, z pairs joined over a warp: the largest m, and z at that.
 __device__ __forceinline__ float2 join_pairs(float m, float z, const LogitRows &in)
@@ -150,250 +148,392 @@ __device__ __forceinline__ float2 join_pairs(float m, float z, const LogitRows &
     return make_float2(top, warp_sum(z * exp2_approx(distance(m, safe_max(top), in) * in.c)));
 }
 
-// The elements that `mask` has a bit for become -inf.
+// A place in the ring of stages and how often it has been used, modulo 2.
+struct Cursor {
+    int at = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == kStages) {
+            at = 0;
+            turn ^= 1;
+        }
+    }
+};
+
+// Starts the copy of vectors [i0, i1) of a row into a stage, by one warp. The
+// vectors wholly inside the row come by a bulk copy; those that reach beyond
+// its ends element by element (no byte outside the row is read), filled up
+// with -inf. `full` counts the copy's bytes and two arrivals.
 template <class T>
-__device__ __forceinline__ uint4 without(uint4 v, uint32_t mask)
+__device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, uint4 *stage, uint64_t *full)
 {
-    typename T::raw *e = reinterpret_cast<typename T::raw *>(&v);
-#pragma unroll
-    for (int k = 0; k < T::kPerVec; ++k)
-        if (mask >> k & 1)
-            e[k] = T::narrow(-kInf);
-    return v;
+    typedef typename T::raw raw;
+    const int lane = threadIdx.x & 31;
+    const int lo = max(i0, row.full0), hi = min(i1, row.full1);
+    if (lane == 0) {
+        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
+        barrier_expect(full, bytes);
+        if (bytes)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             shared_address(stage + (lo - i0))),
+                         "l"(row.vec(lo)), "r"(bytes), "r"(shared_address(full))
+                         : "memory");
+    }
+    if (lo > i0 || hi < i1) {
+        const int side = lane / T::kPerVec, e = lane % T::kPerVec;
+        const int i = side == 0 ? 0 : row.vecs - 1;
+        if (side < 2 && (i < row.full0 || i >= row.full1) && i >= i0 && i < i1) {
+            const int id = row.id(i, e);
+            raw v = T::narrow(-kInf);
+            if (id >= 0 && id < row.vocab)
+                v = row.x[id];
+            reinterpret_cast<raw *>(stage + (i - i0))[e] = v;
+        }
+        __syncwarp();
+    }
+    if (lane == 0)
+        barrier_arrive(full);
 }
 
-// All threads of the CTA, from different places in the code.
-__device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-
-// One row by a cluster of CTAs (one CTA for short rows). A first pass sums the
-// exponentials, a second writes the gradient; it reads the row again, but from
-// the L2 cache: the launch keeps the rows at work at once well below its size.
+// Rows by a cluster of CTAs (one CTA a row for short rows). A first pass over
+// a row sums the exponentials, a second writes the gradient; it reads the row
+// again, but from the L2 cache: the launch keeps the rows at work at once well
+// below its size. In each CTA
+//   - a warp keeps bulk copies in flight into a ring of stages, running ahead
+//     over the passes and rows, so that the memory is not idle while sums are
+//     joined;
+//   - kWarps warps take the stages, sum, and write the gradient;
+//   - a warp reads the teacher's row, joins the sums, in the CTA and over the
+//     cluster, and writes the loss and, last, the gradient of the listed
+//     tokens.
 // With kTail the rest of the student's mass is summed over the tokens that are
-// not listed, which a byte for each vector in shared memory marks: 1 - sum p
-// would lose a small rest. That sum also keeps a reference of its own: it may
-// lie further below the listed logits than FP32's exponents reach.
+// not listed (they are replaced by -inf in their stage): 1 - sum p would lose
+// a small rest. That sum also keeps a reference of its own: it may lie further
+// below the listed logits than FP32's exponents reach.
 template <class T, bool kTail>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillArgs a)
 {
     typedef typename T::raw raw;
-    extern __shared__ __align__(16) unsigned char marks[];
+    extern __shared__ __align__(16) unsigned char dynamic[];
     __shared__ __align__(16) Shared sh;
     const uint32_t size = cluster_size(), rank = cluster_rank();
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t r = blockIdx.x / size;
-    const Row<T> row(a.in, r);
-    const Part p = part_of(row, rank, size);
-    const float weight = a.weight ? a.weight[r] : 1.0f;
-    raw *g = static_cast<raw *>(a.grad.data);
-    int lo = row.vecs, hi = 0;   // vectors that are stored whole
-    if (g) {
-        g += row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
-        if (same_phase(row, g)) {
-            lo = row.full0;
-            hi = row.full1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t first = (int64_t)(blockIdx.x / size) * a.rows_each, last = min(a.in.rows, first + a.rows_each);
+    uint4 *const stages = reinterpret_cast<uint4 *>(dynamic);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            barrier_init(&sh.full[i], 2);
+            barrier_init(&sh.ready[i], 1);
+            barrier_init(&sh.empty[i], kWarps);
         }
+        barrier_init(&sh.summed, kWarps);
+        barrier_init(&sh.joined, 1);
+        barrier_init(&sh.written, kWarps);
+        for (int i = 0; i < 2; ++i)
+            barrier_init(&sh.cluster[i], size);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (weight == 0.0f) {   // the same in all CTAs of the cluster
-        if (rank == 0 && tid == 0 && a.loss)
-            a.loss[r] = 0.0f;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int i = p.v0 + tid; g && i < p.v0 + p.n; i += kThreads) {
-            if (i >= lo && i < hi)
-                store_stream(g + row.id(i, 0), zero);
-            else
-                store_edge<T>(g, row, i, zero);
-        }
-        return;
-    }
-    if (kTail) {
-        for (int i = tid; i < (p.n + 15) / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(marks)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
-    const int end = p.v0 + p.n;
-    int32_t mine[kSlots];   // entry warp: listed tokens in the part
-    float x[kSlots];
-    Stat s = {-kInf, 0.0f, 0.0f};
-    if (tid >= kStream) {
-        const TeacherRaw w = load_teacher(a.teacher, r);
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            mine[i] = -1;
-            x[i] = -kInf;
-            if (w.id[i] < max(0, row.id(p.v0, 0)) || w.id[i] >= min(row.vocab, row.id(end, 0)))
-                continue;
-            mine[i] = w.id[i];
-            x[i] = T::widen(row.x[w.id[i]]);
-        }
-        if (kTail) {
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i)
-                if (mine[i] >= 0) {
-                    const int at = mine[i] + row.phase - p.v0 * T::kPerVec, byte = at / T::kPerVec;
-                    atomicOr(reinterpret_cast<uint32_t *>(marks) + byte / 4, 1u << (byte % 4 * 8 + at % T::kPerVec));
-                }
-            block_barrier();
-        }
-        const TeacherRow t = make_teacher(a.teacher, w, row.vocab);
-        float ql = 0.0f, m = -kInf;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            sh.ids[lane + 32 * i] = t.id[i];
-            sh.q[lane + 32 * i] = t.q[i];
-            ql += t.q[i] > 0.0f ? t.q[i] * t.logq[i] : 0.0f;
-            m = fmaxf(m, x[i]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        Listed l = {m, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            if (mine[i] < 0)
-                continue;
-            if (t.q[i] > 0.0f) {
-                l.q += t.q[i];
-                l.dot = __fmaf_rn(t.q[i], quarter_distance(x[i], m), l.dot);
-            }
-            if (kTail) {   // each token once
-                bool first = true;
-                for (int j = 0; j < lane + 32 * i; ++j)
-                    first = first && sh.ids[j] != mine[i];
-                if (first)   // NaN for NaN and +inf
-                    l.z += x[i] - x[i] == 0.0f || x[i] == -kInf ? exp2_approx(distance(x[i], safe_max(m), a.in) * a.in.c) : x[i] - x[i];
-            }
-        }
-        l.z = warp_sum(l.z);
-        l.q = warp_sum(l.q);
-        l.dot = warp_sum(l.dot);
-        ql = warp_sum(ql);
-        if (lane == 0) {
-            sh.listed = l;
-            sh.sum = t.sum;
-            sh.rest = t.rest;
-            sh.qlogq = ql;
-        }
-    } else {
-        if (kTail)
-            block_barrier();
-        Running<T, false> run;
-        for (int i0 = p.v0; i0 < end; i0 += kGroupStep) {
-            const int i = i0 + tid;
-            if (i0 >= row.full0 && i0 + kGroupStep <= min(end, row.full1)) {
-                uint4 v[kGroup];
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    v[j] = *row.vec(i + j * kStream);
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j) {
-                    if (kTail) {
-                        const uint32_t mask = marks[i - p.v0 + j * kStream];
-                        if (mask)
-                            v[j] = without<T>(v[j], mask);
-                    }
-                    run.add(v[j], a.in);
-                }
-            } else {
-#pragma unroll 1
-                for (int j = i; j < min(end, i0 + kGroupStep); j += kStream)
-                    run.add(without<T>(load_vec(row, j), kTail ? marks[j - p.v0] : 0u), a.in);
-            }
-        }
-        s = warp_join<false>(run.stat(a.in), a.in);
-        if (lane == 0)
-            sh.part[tid >> 5] = s;
-    }
-    block_barrier();
-    s = warp_join<false>(sh.part[lane % kWarps], a.in, kWarps);
-    Listed l = sh.listed;
-    if (size > 1) {
-        if (tid == 0)
-            sh.mine = s;
+    if (size > 1) {   // the barriers are there before another CTA's sums come
         cluster_arrive();
         cluster_wait();
-        const uint32_t at = map_shared(&sh.mine, lane % size), from = map_shared(&sh.listed, lane % size);
-        const bool once = lane < (int)size;
-        const float2 v = join_pairs(ld_cluster_f32(at), once ? ld_cluster_f32(at + 4) : 0.0f, a.in);
-        s = Stat{v.x, v.y, 0.0f};
-        const float4 u = ld_cluster_f4(from);
-        const float2 lz = join_pairs(u.x, once ? u.y : 0.0f, a.in);
-        l.m = lz.x;
-        l.z = lz.y;
-        l.q = warp_sum(once ? u.z : 0.0f);
-        l.dot = warp_sum(once && u.z != 0.0f ? __fmaf_rn(u.z, quarter_distance(u.x == -kInf ? 0.0f : u.x, l.m), u.w) : 0.0f);
-        cluster_arrive();   // what was read here is free to go; the wait is at the end
-    }
-    // of all tokens (without tail the listed ones are in s already); m_rest and z_rest of those that are not listed
-    const float m = kTail ? fmaxf(s.m, l.m) : s.m, mm = safe_max(m), m_rest = safe_max(s.m);
-    const float down = exp2_approx(distance(s.m, mm, a.in) * a.in.c);
-    const float z = kTail ? __fmaf_rn(s.z, down, l.z * exp2_approx(distance(l.m, mm, a.in) * a.in.c)) : s.z;
-    const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = sh.sum, q_rest = sh.rest;
-    // an unlisted token: p - q_rest p / p_rest, by 2^((x - m_rest) c)
-    const float f = __fsub_rn(down * (sum * inv_z), !kTail || s.z == 0.0f ? 0.0f : q_rest / s.z);
-    if (g) {
-        const float scale = weight * a.in.inv_t;
-        const f2 nm = splat(-m_rest), ff = splat(f * (scale / T::kShift));
-        if (tid < kStream) {
-            for (int i0 = p.v0; i0 < end; i0 += kGroupStep) {
-                const int i = i0 + tid;
-                if (i0 >= max(lo, row.full0) && i0 + kGroupStep <= min(end, hi)) {
-                    uint4 v[kGroup];
+    } else
+        __syncthreads();
+
+    const int passes = a.grad.data ? 2 : 1;
+    bool ok = true;          // false: a wait ran out
+    uint32_t active = 0;     // rows done with a weight other than 0
+    float next_weight = a.weight ? a.weight[first] : 1.0f;
+    if (warp == kFetcher) {
+        Cursor c;
+        for (int64_t r = first; r < last && ok; ++r) {
+            const float weight = next_weight;
+            if (r + 1 < last && a.weight)
+                next_weight = a.weight[r + 1];
+            if (weight == 0.0f)
+                continue;
+            const Row<T> row(a.in, r);
+            const Part p = part_of(row, rank, size);
+            for (int pass = 0; pass < passes; ++pass)
+                for (int i = 0; i < p.n && ok; i += kStageVecs, c.next()) {
+                    ok = warp_wait(&sh.empty[c.at], c.turn ^ 1);
+                    // what was stored to this stage comes before the copy to it
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (ok)
+                        fill_stage<T>(row, p.v0 + i, p.v0 + min(p.n, i + kStageVecs), stages + c.at * kStageVecs, &sh.full[c.at]);
+                }
+        }
+        // copies that are still on their way are not left behind
+        for (int i = 0; i < kStages && !ok; ++i, c.next())
+            barrier_wait(&sh.full[c.at], c.turn ^ 1);
+    } else if (warp == kTeacher) {
+        Cursor c;
+        TeacherRaw next = load_teacher(a.teacher, first);
+        for (int64_t r = first; r < last; ++r) {
+            const float weight = next_weight;
+            const TeacherRaw w = next;
+            if (r + 1 < last) {
+                next = load_teacher(a.teacher, r + 1);
+                if (a.weight)
+                    next_weight = a.weight[r + 1];
+            }
+            const bool writes = (uint32_t)r % size == rank && lane == 0;   // the loss, in turn
+            if (weight == 0.0f || !ok) {   // the same in all CTAs of the cluster
+                if (writes && a.loss)
+                    a.loss[r] = ok ? 0.0f : __int_as_float(0x7fffffff);
+                continue;
+            }
+            const Row<T> row(a.in, r);
+            const Part p = part_of(row, rank, size);
+            const int id0 = max(0, row.id(p.v0, 0)), id1 = min(row.vocab, row.id(p.v0 + p.n, 0));
+            int32_t mine[kSlots];   // listed tokens in the part; -2: none
+            float x[kSlots];        // their logits
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        v[j] = __ldcs(row.vec(i + j * kStream));
+            for (int i = 0; i < kSlots; ++i) {
+                const bool in = w.id[i] >= id0 && w.id[i] < id1;
+                mine[i] = in ? w.id[i] : -2;
+                x[i] = in ? T::widen(row.x[w.id[i]]) : -kInf;
+            }
+            if (kTail)
+                for (int i = 0; i < p.n; i += kStageVecs, c.next()) {
+                    ok = ok && warp_wait(&sh.full[c.at], c.turn);
+                    raw *const e = reinterpret_cast<raw *>(stages + c.at * kStageVecs);
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        store_stream(g + row.id(i + j * kStream, 0), grad_vec<T>(v[j], nm, ff, a.in));
-                } else {
-#pragma unroll 1
-                    for (int j = i; j < min(end, i0 + kGroupStep); j += kStream) {
-                        const uint4 v = grad_vec<T>(load_vec(row, j), nm, ff, a.in);
-                        if (j >= lo && j < hi)
-                            store_stream(g + row.id(j, 0), v);
-                        else
-                            store_edge<T>(g, row, j, v);
+                    for (int j = 0; j < kSlots; ++j) {
+                        const int at = mine[j] + row.phase - (p.v0 + i) * T::kPerVec;
+                        if (ok && mine[j] >= 0 && at >= 0 && at < min(kStageVecs, p.n - i) * T::kPerVec)
+                            e[at] = T::narrow(-kInf);
                     }
+                    __syncwarp();
+                    if (lane == 0)
+                        barrier_arrive(&sh.ready[c.at]);
+                }
+            const TeacherRow t = make_teacher(a.teacher, w, row.vocab);
+            Listed l = {-kInf, 0.0f, 0.0f, 0.0f};
+            float ql = 0.0f;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                sh.ids[lane + 32 * i] = t.id[i];
+                sh.q[lane + 32 * i] = t.q[i];
+                ql += t.q[i] > 0.0f ? t.q[i] * t.logq[i] : 0.0f;
+                l.m = fmaxf(l.m, x[i]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                l.m = fmaxf(l.m, __shfl_xor_sync(~0u, l.m, o));
+            // an id listed twice is rare, but is one token: the first entry takes the weight of all
+            bool twice = false;
+            for (int j = 0; j < a.teacher.k; j += 4) {
+                const int4 u = *reinterpret_cast<const int4 *>(sh.ids + j);
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+                    const int e = lane + 32 * i;
+                    twice = twice || (u.x == mine[i] && j != e) || (u.y == mine[i] && j + 1 != e) || (u.z == mine[i] && j + 2 != e) ||
+                            (u.w == mine[i] && j + 3 != e);
                 }
             }
-        }
-        block_barrier();
-        if (tid >= kStream) {   // the listed tokens' places once more; the first of equal ids takes the weight of all
+            float q_all[kSlots];
+            uint32_t again = 0;   // a bit for each place whose token an earlier entry has
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i)
+                q_all[i] = t.q[i];
+            if (__any_sync(~0u, twice)) {
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+                    float q = 0.0f;
+                    for (int j = 0; j < a.teacher.k; ++j)
+                        if (sh.ids[j] == mine[i]) {
+                            q += sh.q[j];
+                            again |= j < lane + 32 * i ? 1u << i : 0u;
+                        }
+                    q_all[i] = q;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
                 if (mine[i] < 0)
                     continue;
-                float q = 0.0f;
-                bool first = true;
-                for (int j = 0; j < a.teacher.k; ++j)
-                    if (sh.ids[j] == mine[i]) {
-                        q += sh.q[j];
-                        first = first && j >= lane + 32 * i;
-                    }
-                if (first)
-                    g[mine[i]] = T::narrow(z == 0.0f ? 0.0f : grad_listed<T>(x[i], mm, q, sum, inv_z, scale, a.in));
+                if (t.q[i] > 0.0f) {
+                    l.q += t.q[i];
+                    l.dot = __fmaf_rn(t.q[i], quarter_distance(x[i], l.m), l.dot);
+                }
+                if (kTail && !(again >> i & 1))   // NaN for NaN and +inf
+                    l.z += x[i] - x[i] == 0.0f || x[i] == -kInf ? exp2_approx(distance(x[i], safe_max(l.m), a.in) * a.in.c) : x[i] - x[i];
             }
+            if (kTail)
+                l.z = warp_sum(l.z);
+            l.q = warp_sum(l.q);
+            l.dot = warp_sum(l.dot);
+            ql = warp_sum(ql);
+
+            ok = warp_wait(&sh.summed, active & 1) && ok;
+            float2 s = make_float2(-kInf, 0.0f);
+            if (lane < kWarps)
+                s = sh.part[lane];
+            s = join_pairs(s.x, s.y, a.in);
+            if (size > 1) {
+                const int turn = active & 1;
+                if (lane < (int)size) {
+                    const uint32_t at = map_shared(&sh.sums[turn][rank], lane);
+                    st_cluster(at, l.m, l.z);
+                    st_cluster(at + 8, l.q, l.dot);
+                    st_cluster(map_shared(&sh.rests[turn][rank], lane), s.x, s.y);
+                    fence_cluster();
+                    arrive_cluster(map_shared(&sh.cluster[turn], lane));
+                }
+                ok = warp_wait(&sh.cluster[turn], (active >> 1) & 1) && ok;
+                fence_cluster();
+                float4 v = make_float4(-kInf, 0.0f, 0.0f, 0.0f);
+                s = make_float2(-kInf, 0.0f);
+                if (lane < (int)size) {
+                    v = sh.sums[turn][lane];
+                    s = sh.rests[turn][lane];
+                }
+                s = join_pairs(s.x, s.y, a.in);
+                const float2 lz = join_pairs(v.x, v.y, a.in);
+                l.m = lz.x;
+                l.z = lz.y;
+                l.q = warp_sum(v.z);
+                l.dot = warp_sum(v.z != 0.0f ? __fmaf_rn(v.z, quarter_distance(v.x == -kInf ? 0.0f : v.x, l.m), v.w) : 0.0f);
+            }
+            // s: what was streamed: with kTail the rest alone, else all tokens
+            const float m = kTail ? fmaxf(s.x, l.m) : s.x, mm = safe_max(m), m_rest = safe_max(s.x);
+            const float down = exp2_approx(distance(s.x, mm, a.in) * a.in.c);
+            const float z = kTail ? __fmaf_rn(s.y, down, l.z * exp2_approx(distance(l.m, mm, a.in) * a.in.c)) : s.y;
+            const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = ok ? t.sum : __int_as_float(0x7fffffff), q_rest = t.rest;
+            // an unlisted token: p - q_rest p / p_rest, by 2^((x - m_rest) c)
+            const float f = __fsub_rn(down * (sum * inv_z), !kTail || s.y == 0.0f ? 0.0f : q_rest / s.y);
+            const float scale = weight * a.in.inv_t;
+            if (lane == 0) {
+                sh.m = m_rest;
+                sh.f = f * (scale / T::kShift);
+                barrier_arrive(&sh.joined);
+            }
+            if (writes) {
+                // KL = sum q ln q - sum q s + (sum q) ln Z, and the rest's term
+                const float ln_z = logf(z), four = 4.0f * a.in.inv_t;
+                float kl = ql;
+                if (l.q != 0.0f)
+                    kl = __fmaf_rn(-four, __fmaf_rn(l.q, quarter_distance(l.m == -kInf ? 0.0f : l.m, m), l.dot), __fmaf_rn(l.q, ln_z, kl));
+                if (z == 0.0f && sum != 0.0f)
+                    kl = kInf;
+                if (kTail && q_rest > 0.0f)
+                    kl = s.y == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - (__fmaf_rn(quarter_distance(s.x, m), four, logf(s.y)) - ln_z));
+                if (sum != sum || z != z)
+                    kl = __int_as_float(0x7fffffff);
+                if (a.loss)
+                    a.loss[r] = kl * weight;
+                if (a.stats)
+                    a.stats[r] = make_float4(m, z, s.x, f);
+            }
+            if (passes == 2) {
+                if (kTail)   // the second pass's stages go by
+                    for (int i = 0; i < p.n; i += kStageVecs)
+                        c.next();
+                ok = warp_wait(&sh.written, active & 1) && ok;
+                raw *const g = static_cast<raw *>(a.grad.data) + row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i)   // the listed tokens' places once more, after the vectors
+                    if (ok && mine[i] >= 0 && !(again >> i & 1))
+                        g[mine[i]] = T::narrow(z == 0.0f ? 0.0f : grad_listed<T>(x[i], mm, q_all[i], sum, inv_z, scale, a.in));
+            }
+            ++active;
+        }
+    } else {
+        Cursor c;
+        uint32_t ready_turn = 0;   // a bit for each stage: `ready` is for the first pass alone
+        for (int64_t r = first; r < last; ++r) {
+            const float weight = next_weight;
+            if (r + 1 < last && a.weight)
+                next_weight = a.weight[r + 1];
+            const Row<T> row(a.in, r);
+            const Part p = part_of(row, rank, size);
+            raw *g = static_cast<raw *>(a.grad.data);
+            int lo = row.vecs, hi = 0;   // vectors that are stored whole
+            if (g) {
+                g += row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
+                if (same_phase(row, g)) {
+                    lo = row.full0;
+                    hi = row.full1;
+                }
+            }
+            const auto write = [&](int i, const uint4 &v) {
+                if (i >= lo && i < hi)
+                    store_stream(g + row.id(i, 0), v);
+                else
+                    store_edge<T>(g, row, i, v);
+            };
+            if (weight == 0.0f) {
+                for (int i = p.v0 + tid; g && i < p.v0 + p.n; i += kStream)
+                    write(i, make_uint4(0, 0, 0, 0));
+                continue;
+            }
+            Running<T, false> run;
+            for (int i0 = 0; i0 < p.n && ok; i0 += kStageVecs, c.next()) {
+                ok = warp_wait(&sh.full[c.at], c.turn);
+                if (kTail) {
+                    ok = ok && warp_wait(&sh.ready[c.at], (ready_turn >> c.at) & 1);
+                    ready_turn ^= 1u << c.at;
+                }
+                const uint4 *const stage = stages + c.at * kStageVecs;
+                if (i0 + kStageVecs <= p.n) {
+                    uint4 v[kStageVecs / kStream];
+#pragma unroll
+                    for (int j = 0; j < kStageVecs / kStream; ++j)
+                        v[j] = stage[tid + j * kStream];
+#pragma unroll
+                    for (int j = 0; j < kStageVecs / kStream; ++j)
+                        run.add(v[j], a.in);
+                } else
+                    for (int i = tid; i < p.n - i0; i += kStream)
+                        run.add(stage[i], a.in);
+                __syncwarp();
+                if (lane == 0)
+                    barrier_arrive(&sh.empty[c.at]);
+            }
+            if (passes == 1 && active > 0)   // the last row's sums have been read
+                ok = ok && warp_wait(&sh.joined, (active - 1) & 1);
+            const Stat s = warp_join<false>(run.stat(a.in), a.in);
+            if (lane == 0) {
+                sh.part[warp] = make_float2(s.m, s.z);
+                barrier_arrive(&sh.summed);
+            }
+            if (passes == 2) {
+                ok = warp_wait(&sh.joined, active & 1) && ok;
+                const f2 nm = splat(-sh.m), f = splat(sh.f);
+                for (int i0 = 0; i0 < p.n && ok; i0 += kStageVecs, c.next()) {
+                    ok = warp_wait(&sh.full[c.at], c.turn);
+                    const uint4 *const stage = stages + c.at * kStageVecs;
+                    if (i0 + kStageVecs <= p.n && p.v0 + i0 >= lo && p.v0 + i0 + kStageVecs <= hi) {
+                        uint4 v[kStageVecs / kStream];
+#pragma unroll
+                        for (int j = 0; j < kStageVecs / kStream; ++j)
+                            v[j] = stage[tid + j * kStream];
+                        raw *const to = g + row.id(p.v0 + i0 + tid, 0);
+#pragma unroll
+                        for (int j = 0; j < kStageVecs / kStream; ++j)
+                            store_stream(to + j * kStream * T::kPerVec, grad_vec<T>(v[j], nm, f, a.in));
+                    } else
+                        for (int i = tid; i < min(kStageVecs, p.n - i0); i += kStream)
+                            write(p.v0 + i0 + i, grad_vec<T>(stage[i], nm, f, a.in));
+                    __syncwarp();
+                    if (lane == 0)
+                        barrier_arrive(&sh.empty[c.at]);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    barrier_arrive(&sh.written);
+            }
+            ++active;
         }
     }
-    if (rank == 0 && tid == 0) {
-        // KL = sum q ln q - sum q s + (sum q) ln Z, and the rest's term
-        const float ln_z = logf(z), four = 4.0f * a.in.inv_t;
-        float kl = sh.qlogq;
-        if (l.q != 0.0f)
-            kl = __fmaf_rn(-four, __fmaf_rn(l.q, quarter_distance(l.m == -kInf ? 0.0f : l.m, m), l.dot), __fmaf_rn(l.q, ln_z, kl));
-        if (z == 0.0f && sum != 0.0f)
-            kl = kInf;
-        if (kTail && q_rest > 0.0f)
-            kl = s.z == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - (__fmaf_rn(quarter_distance(s.m, m), four, logf(s.z)) - ln_z));
-        if (sum != sum || z != z)
-            kl = __int_as_float(0x7fffffff);
-        if (a.loss)
-            a.loss[r] = kl * weight;
-        if (a.stats)
-            a.stats[r] = make_float4(m, z, s.m, f);
+    if (size > 1) {   // no CTA leaves while another may write to it
+        cluster_arrive();
+        cluster_wait();
     }
-    if (size > 1)
-        cluster_wait();   // no CTA leaves while another reads its shared memory
 }
 
 // The gradient from saved statistics.
@@ -465,8 +605,9 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillGradA
 }
 
 template <class T>
-cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
+cudaError_t launch(const DistillArgs &args, cudaStream_t stream)
 {
+    DistillArgs a = args;
     const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * kCtasPerSm;
     // one CTA a row, or a cluster that shares it: while the rows at work at
     // once would not stay in the L2 cache between the passes, and while the
@@ -474,9 +615,13 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
     int size = 1;
     while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (a.in.rows * size < ctas && bytes > size * 8192)))
         size *= 2;
+    // a few rows one after the other, where there are many
+    a.rows_each = (int)std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
+    const int64_t clusters = (a.in.rows + a.rows_each - 1) / a.rows_each;
+    const size_t shared = (size_t)kStages * kStageVecs * 16;
     if (a.teacher.tail)
-        return launch_cluster(distill_kernel<T, true>, a, a.in.rows, size, (part_vecs(bytes, size) + 15) / 16 * 16, kThreads, stream);
-    return launch_cluster(distill_kernel<T, false>, a, a.in.rows, size, 0, kThreads, stream);
+        return launch_cluster(distill_kernel<T, true>, a, clusters, size, shared, kThreads, stream);
+    return launch_cluster(distill_kernel<T, false>, a, clusters, size, shared, kThreads, stream);
 }
 
 template <class T>

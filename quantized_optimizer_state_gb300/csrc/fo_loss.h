@@ -63,6 +63,7 @@ struct DistillArgs {
     float *loss;             // may be null
     float4 *stats;           // may be null
     GradRows grad;           // data may be null
+    int32_t rows_each;       // set by the launch: rows that a cluster takes one after the other
 };
 
 struct DistillGradArgs {
