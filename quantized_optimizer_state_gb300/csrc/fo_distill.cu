@@ -11,12 +11,13 @@ constexpr int kWarps = 8;                         // that walk over a row
 constexpr int kStream = kWarps * 32;
 constexpr int kFetcher = kWarps, kTeacher = kWarps + 1;   // and two more: see distill_kernel
 constexpr int kThreads = kStream + 64;
-constexpr int kStageVecs = 2 * kStream;           // vectors that are copied at once (8 KB)
-constexpr int kStages = 8;                        // such copies in flight or in use
+constexpr int kStageVecs = 4 * kStream;           // vectors that are copied at once (8 KB)
+constexpr int kStages = 4;                        // such copies in flight or in use
 constexpr int kGradThreads = 256;
 constexpr int kCtasPerSm = 3;
 constexpr int64_t kCacheBytes = 80 << 20;         // of the 129 MB L2 cache, for rows between their passes
-constexpr int kMaxRowsEach = 8;
+constexpr int kMaxRowsEach = 2;
+constexpr int64_t kMaxPart = 128 * 1024;
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -27,23 +28,41 @@ struct TeacherRow {
     float rest;                  // the mass that is not listed (0 without tail)
 };
 
-// What it is made from, as loaded.
+// What it is made from, as loaded: nothing here waits for a load, so that all
+// of a row's are on their way at once (places beyond k repeat the first).
 struct TeacherRaw {
     int32_t id[kSlots];
-    float logit[kSlots], lse;
+    uint32_t bits[kSlots];   // of the logits
+    float lse;
 };
 
 __device__ __forceinline__ TeacherRaw load_teacher(const Teacher &t, int64_t r)
 {
     TeacherRaw w;
+    int64_t at[kSlots];
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
         const int e = (int)(threadIdx.x & 31) + 32 * i;
-        w.id[i] = e < t.k ? t.ids[r * t.k + e] : -1;
-        w.logit[i] = e < t.k ? load_dtype(t.logits, r * t.k + e, t.dtype) : 0.0f;
+        at[i] = r * t.k + (e < t.k ? e : 0);
+        w.id[i] = t.ids[at[i]];
+    }
+    if (t.dtype == FO_LOGITS_F32) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            w.bits[i] = static_cast<const uint32_t *>(t.logits)[at[i]];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            w.bits[i] = static_cast<const uint16_t *>(t.logits)[at[i]];
     }
     w.lse = t.lse ? t.lse[r] : 0.0f;
     return w;
+}
+
+// The id of place i: -1 for none.
+__device__ __forceinline__ int32_t id_at(const Teacher &t, const TeacherRaw &w, int i)
+{
+    return (int)(threadIdx.x & 31) + 32 * i < t.k ? w.id[i] : -1;
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -61,8 +80,11 @@ __device__ __forceinline__ TeacherRow make_teacher(const Teacher &t, const Teach
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
-        s.id[i] = w.id[i];
-        s.logq[i] = w.id[i] < 0 ? -kInf : w.logit[i] * t.inv_t;
+        s.id[i] = id_at(t, w, i);
+        const float logit = t.dtype == FO_LOGITS_F32    ? __uint_as_float(w.bits[i])
+                            : t.dtype == FO_LOGITS_BF16 ? Bf16::widen((uint16_t)w.bits[i])
+                                                        : F16::widen((uint16_t)w.bits[i]);
+        s.logq[i] = s.id[i] < 0 ? -kInf : logit * t.inv_t;
         m = fmaxf(m, s.logq[i]);
         bad = bad || s.id[i] >= vocab;
     }
@@ -127,8 +149,8 @@ struct Listed {
 };
 
 struct Shared {
-    uint64_t full[kStages], ready[kStages], empty[kStages];   // of a stage: copied; the listed tokens taken out; used
-    uint64_t summed, joined, written;                         // of a row
+    uint64_t full[kStages], empty[kStages];                   // of a stage: copied; used
+    uint64_t marked, summed, joined, written;                 // of a row
     uint64_t cluster[2];                                      // all CTAs' sums have come
     float4 sums[2][kMaxCluster];                              // written by each CTA into all: listed m, z, q, dot,
     float2 rests[2][kMaxCluster];                             // and the streamed m, z
@@ -196,6 +218,54 @@ __device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, ui
         barrier_arrive(full);
 }
 
+// A byte in shared memory for each vector of a part, with a bit for each of
+// its elements that is a listed token.
+template <class T>
+__device__ __forceinline__ uint32_t mark_bit(const Row<T> &row, const Part &p, int32_t id, int &word)
+{
+    const int at = id + row.phase - p.v0 * T::kPerVec, byte = at / T::kPerVec;
+    word = byte / 4;
+    return 1u << (byte % 4 * 8 + at % T::kPerVec);
+}
+
+// The elements that `mask` has a bit for become -inf.
+template <class T>
+__device__ __forceinline__ uint4 without(uint4 v, uint32_t mask)
+{
+    typename T::raw *e = reinterpret_cast<typename T::raw *>(&v);
+#pragma unroll
+    for (int k = 0; k < T::kPerVec; ++k)
+        if (mask >> k & 1)
+            e[k] = T::narrow(-kInf);
+    return v;
+}
+
+// For lists with a token in two entries, which is rare: the first stands for
+// all. q_all: its weight, that of all. By one warp.
+__device__ __forceinline__ uint32_t merge_twice(Shared &sh, const TeacherRow &t, int k, const int32_t (&mine)[kSlots], float (&q_all)[kSlots])
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        sh.ids[lane + 32 * i] = t.id[i];
+        sh.q[lane + 32 * i] = t.q[i];
+    }
+    __syncwarp();
+    uint32_t again = 0;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        float q = 0.0f;
+        for (int j = 0; j < k; ++j)
+            if (sh.ids[j] == mine[i]) {
+                q += sh.q[j];
+                again |= j < lane + 32 * i ? 1u << i : 0u;
+            }
+        q_all[i] = q;
+    }
+    return again;
+}
+
 // Rows by a cluster of CTAs (one CTA a row for short rows). A first pass over
 // a row sums the exponentials, a second writes the gradient; it reads the row
 // again, but from the L2 cache: the launch keeps the rows at work at once well
@@ -208,9 +278,9 @@ __device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, ui
 //     cluster, and writes the loss and, last, the gradient of the listed
 //     tokens.
 // With kTail the rest of the student's mass is summed over the tokens that are
-// not listed (they are replaced by -inf in their stage): 1 - sum p would lose
-// a small rest. That sum also keeps a reference of its own: it may lie further
-// below the listed logits than FP32's exponents reach.
+// not listed: 1 - sum p would lose a small rest. That sum also keeps a
+// reference of its own: it may lie further below the listed logits than FP32's
+// exponents reach.
 template <class T, bool kTail>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillArgs a)
 {
@@ -221,12 +291,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t first = (int64_t)(blockIdx.x / size) * a.rows_each, last = min(a.in.rows, first + a.rows_each);
     uint4 *const stages = reinterpret_cast<uint4 *>(dynamic);
+    unsigned char *const mark_bytes = dynamic + kStages * kStageVecs * 16;
+    uint32_t *const marks = reinterpret_cast<uint32_t *>(mark_bytes);
+    for (int i = tid; i < a.mark_words; i += kThreads)
+        marks[i] = 0;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             barrier_init(&sh.full[i], 2);
-            barrier_init(&sh.ready[i], 1);
             barrier_init(&sh.empty[i], kWarps);
         }
+        barrier_init(&sh.marked, 1);
         barrier_init(&sh.summed, kWarps);
         barrier_init(&sh.joined, 1);
         barrier_init(&sh.written, kWarps);
@@ -268,8 +342,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
         for (int i = 0; i < kStages && !ok; ++i, c.next())
             barrier_wait(&sh.full[c.at], c.turn ^ 1);
     } else if (warp == kTeacher) {
-        Cursor c;
+        int32_t mine[kSlots];   // listed tokens in the part; -2: none
+        raw x[kSlots];          // their logits
+        bool twice = false;     // a token is in two entries
+        const auto start = [&](int64_t r, const TeacherRaw &w) {
+            const Row<T> row(a.in, r);
+            const Part p = part_of(row, rank, size);
+            const int id0 = max(0, row.id(p.v0, 0)), id1 = min(row.vocab, row.id(p.v0 + p.n, 0));
+            twice = false;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                const int32_t id = id_at(a.teacher, w, i);
+                mine[i] = id >= id0 && id < id1 ? id : -2;
+                x[i] = row.x[max(mine[i], 0)];   // used where there is one
+                if (mine[i] >= 0 && a.mark_words) {
+                    int word;
+                    const uint32_t bit = mark_bit(row, p, mine[i], word);
+                    twice = twice || (atomicOr(marks + word, bit) & bit);
+                }
+            }
+            twice = __any_sync(~0u, twice);
+            if (lane == 0)
+                barrier_arrive(&sh.marked);
+        };
         TeacherRaw next = load_teacher(a.teacher, first);
+        if (next_weight != 0.0f)
+            start(first, next);
         for (int64_t r = first; r < last; ++r) {
             const float weight = next_weight;
             const TeacherRaw w = next;
@@ -282,86 +380,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
             if (weight == 0.0f || !ok) {   // the same in all CTAs of the cluster
                 if (writes && a.loss)
                     a.loss[r] = ok ? 0.0f : __int_as_float(0x7fffffff);
+                if (r + 1 < last && next_weight != 0.0f)
+                    start(r + 1, next);
                 continue;
             }
-            const Row<T> row(a.in, r);
-            const Part p = part_of(row, rank, size);
-            const int id0 = max(0, row.id(p.v0, 0)), id1 = min(row.vocab, row.id(p.v0 + p.n, 0));
-            int32_t mine[kSlots];   // listed tokens in the part; -2: none
-            float x[kSlots];        // their logits
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
-                const bool in = w.id[i] >= id0 && w.id[i] < id1;
-                mine[i] = in ? w.id[i] : -2;
-                x[i] = in ? T::widen(row.x[w.id[i]]) : -kInf;
-            }
-            if (kTail)
-                for (int i = 0; i < p.n; i += kStageVecs, c.next()) {
-                    ok = ok && warp_wait(&sh.full[c.at], c.turn);
-                    raw *const e = reinterpret_cast<raw *>(stages + c.at * kStageVecs);
-#pragma unroll
-                    for (int j = 0; j < kSlots; ++j) {
-                        const int at = mine[j] + row.phase - (p.v0 + i) * T::kPerVec;
-                        if (ok && mine[j] >= 0 && at >= 0 && at < min(kStageVecs, p.n - i) * T::kPerVec)
-                            e[at] = T::narrow(-kInf);
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        barrier_arrive(&sh.ready[c.at]);
-                }
-            const TeacherRow t = make_teacher(a.teacher, w, row.vocab);
-            Listed l = {-kInf, 0.0f, 0.0f, 0.0f};
-            float ql = 0.0f;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
-                sh.ids[lane + 32 * i] = t.id[i];
-                sh.q[lane + 32 * i] = t.q[i];
-                ql += t.q[i] > 0.0f ? t.q[i] * t.logq[i] : 0.0f;
-                l.m = fmaxf(l.m, x[i]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                l.m = fmaxf(l.m, __shfl_xor_sync(~0u, l.m, o));
-            // an id listed twice is rare, but is one token: the first entry takes the weight of all
-            bool twice = false;
-            for (int j = 0; j < a.teacher.k; j += 4) {
-                const int4 u = *reinterpret_cast<const int4 *>(sh.ids + j);
-#pragma unroll
-                for (int i = 0; i < kSlots; ++i) {
-                    const int e = lane + 32 * i;
-                    twice = twice || (u.x == mine[i] && j != e) || (u.y == mine[i] && j + 1 != e) || (u.z == mine[i] && j + 2 != e) ||
-                            (u.w == mine[i] && j + 3 != e);
-                }
-            }
+            const TeacherRow t = make_teacher(a.teacher, w, (int)a.in.vocab);
             float q_all[kSlots];
-            uint32_t again = 0;   // a bit for each place whose token an earlier entry has
+            uint32_t again = 0;   // a bit for the entries beside the one that stands for their token
 #pragma unroll
             for (int i = 0; i < kSlots; ++i)
                 q_all[i] = t.q[i];
-            if (__any_sync(~0u, twice)) {
+            if (twice)
+                again = merge_twice(sh, t, a.teacher.k, mine, q_all);
+            Listed l = {-kInf, 0.0f, 0.0f, 0.0f};
+            float ql = 0.0f, xf[kSlots];
 #pragma unroll
-                for (int i = 0; i < kSlots; ++i) {
-                    float q = 0.0f;
-                    for (int j = 0; j < a.teacher.k; ++j)
-                        if (sh.ids[j] == mine[i]) {
-                            q += sh.q[j];
-                            again |= j < lane + 32 * i ? 1u << i : 0u;
-                        }
-                    q_all[i] = q;
-                }
+            for (int i = 0; i < kSlots; ++i) {
+                ql += t.q[i] > 0.0f ? t.q[i] * t.logq[i] : 0.0f;
+                xf[i] = mine[i] < 0 ? -kInf : T::widen(x[i]);
+                l.m = fmaxf(l.m, xf[i]);
             }
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                l.m = fmaxf(l.m, __shfl_xor_sync(~0u, l.m, o));
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
                 if (mine[i] < 0)
                     continue;
                 if (t.q[i] > 0.0f) {
                     l.q += t.q[i];
-                    l.dot = __fmaf_rn(t.q[i], quarter_distance(x[i], l.m), l.dot);
+                    l.dot = __fmaf_rn(t.q[i], quarter_distance(xf[i], l.m), l.dot);
                 }
                 if (kTail && !(again >> i & 1))   // NaN for NaN and +inf
-                    l.z += x[i] - x[i] == 0.0f || x[i] == -kInf ? exp2_approx(distance(x[i], safe_max(l.m), a.in) * a.in.c) : x[i] - x[i];
+                    l.z += xf[i] - xf[i] == 0.0f || xf[i] == -kInf ? exp2_approx(distance(xf[i], safe_max(l.m), a.in) * a.in.c) : xf[i] - xf[i];
             }
             if (kTail)
                 l.z = warp_sum(l.z);
@@ -429,22 +480,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
                 if (a.stats)
                     a.stats[r] = make_float4(m, z, s.x, f);
             }
+            int32_t done[kSlots];   // this row's, while the next is started
+            const Row<T> row(a.in, r);
+            const Part p = part_of(row, rank, size);
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                done[i] = mine[i];
+                if (mine[i] >= 0 && a.mark_words) {   // every warp has summed: the marks go
+                    int word;
+                    mark_bit(row, p, mine[i], word);
+                    marks[word] = 0;
+                }
+            }
+            __syncwarp();
+            if (r + 1 < last && next_weight != 0.0f)
+                start(r + 1, next);
             if (passes == 2) {
-                if (kTail)   // the second pass's stages go by
-                    for (int i = 0; i < p.n; i += kStageVecs)
-                        c.next();
                 ok = warp_wait(&sh.written, active & 1) && ok;
                 raw *const g = static_cast<raw *>(a.grad.data) + row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
 #pragma unroll
                 for (int i = 0; i < kSlots; ++i)   // the listed tokens' places once more, after the vectors
-                    if (ok && mine[i] >= 0 && !(again >> i & 1))
-                        g[mine[i]] = T::narrow(z == 0.0f ? 0.0f : grad_listed<T>(x[i], mm, q_all[i], sum, inv_z, scale, a.in));
+                    if (ok && done[i] >= 0 && !(again >> i & 1))
+                        g[done[i]] = T::narrow(z == 0.0f ? 0.0f : grad_listed<T>(xf[i], mm, q_all[i], sum, inv_z, scale, a.in));
             }
             ++active;
         }
     } else {
         Cursor c;
-        uint32_t ready_turn = 0;   // a bit for each stage: `ready` is for the first pass alone
         for (int64_t r = first; r < last; ++r) {
             const float weight = next_weight;
             if (r + 1 < last && a.weight)
@@ -471,13 +533,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
                     write(i, make_uint4(0, 0, 0, 0));
                 continue;
             }
+            if (kTail)
+                ok = ok && warp_wait(&sh.marked, active & 1);
             Running<T, false> run;
             for (int i0 = 0; i0 < p.n && ok; i0 += kStageVecs, c.next()) {
                 ok = warp_wait(&sh.full[c.at], c.turn);
-                if (kTail) {
-                    ok = ok && warp_wait(&sh.ready[c.at], (ready_turn >> c.at) & 1);
-                    ready_turn ^= 1u << c.at;
-                }
                 const uint4 *const stage = stages + c.at * kStageVecs;
                 if (i0 + kStageVecs <= p.n) {
                     uint4 v[kStageVecs / kStream];
@@ -485,11 +545,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
                     for (int j = 0; j < kStageVecs / kStream; ++j)
                         v[j] = stage[tid + j * kStream];
 #pragma unroll
-                    for (int j = 0; j < kStageVecs / kStream; ++j)
+                    for (int j = 0; j < kStageVecs / kStream; ++j) {
+                        const uint32_t mask = kTail ? mark_bytes[i0 + j * kStream + tid] : 0u;
+                        if (kTail && mask)
+                            v[j] = without<T>(v[j], mask);
                         run.add(v[j], a.in);
+                    }
                 } else
                     for (int i = tid; i < p.n - i0; i += kStream)
-                        run.add(stage[i], a.in);
+                        run.add(without<T>(stage[i], kTail ? mark_bytes[i0 + i] : 0u), a.in);
                 __syncwarp();
                 if (lane == 0)
                     barrier_arrive(&sh.empty[c.at]);
@@ -608,17 +672,21 @@ template <class T>
 cudaError_t launch(const DistillArgs &args, cudaStream_t stream)
 {
     DistillArgs a = args;
+    const bool marks = a.teacher.tail || a.grad.data;
     const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * kCtasPerSm;
     // one CTA a row, or a cluster that shares it: while the rows at work at
-    // once would not stay in the L2 cache between the passes, and while the
-    // grid would leave SMs short of CTAs
+    // once would not stay in the L2 cache between the passes, while a part's
+    // marks would take a CTA's place on the SM, and while the grid would leave
+    // SMs short of CTAs
     int size = 1;
-    while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (a.in.rows * size < ctas && bytes > size * 8192)))
+    while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (marks && bytes > size * kMaxPart) ||
+                                  (a.in.rows * size < ctas && bytes > size * 8192)))
         size *= 2;
     // a few rows one after the other, where there are many
     a.rows_each = (int)std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
     const int64_t clusters = (a.in.rows + a.rows_each - 1) / a.rows_each;
-    const size_t shared = (size_t)kStages * kStageVecs * 16;
+    a.mark_words = marks ? (int)(part_vecs(bytes, size) + 3) / 4 : 0;
+    const size_t shared = (size_t)kStages * kStageVecs * 16 + (size_t)a.mark_words * 4;
     if (a.teacher.tail)
         return launch_cluster(distill_kernel<T, true>, a, clusters, size, shared, kThreads, stream);
     return launch_cluster(distill_kernel<T, false>, a, clusters, size, shared, kThreads, stream);

@@ -63,7 +63,9 @@ struct DistillArgs {
     float *loss;             // may be null
     float4 *stats;           // may be null
     GradRows grad;           // data may be null
-    int32_t rows_each;       // set by the launch: rows that a cluster takes one after the other
+    // set by the launch: rows that a cluster takes one after the other, and
+    // words of shared memory for its marks (fo_distill.cu)
+    int32_t rows_each, mark_words;
 };
 
 struct DistillGradArgs {
