@@ -170,54 +170,6 @@ __device__ __forceinline__ float2 join_pairs(float m, float z, const LogitRows &
     return make_float2(top, warp_sum(z * exp2_approx(distance(m, safe_max(top), in) * in.c)));
 }
 
-// A place in the ring of stages and how often it has been used, modulo 2.
-struct Cursor {
-    int at = 0;
-    uint32_t turn = 0;
-    __device__ __forceinline__ void next()
-    {
-        if (++at == kStages) {
-            at = 0;
-            turn ^= 1;
-        }
-    }
-};
-
-// Starts the copy of vectors [i0, i1) of a row into a stage, by one warp. The
-// vectors wholly inside the row come by a bulk copy; those that reach beyond
-// its ends element by element (no byte outside the row is read), filled up
-// with -inf. `full` counts the copy's bytes and two arrivals.
-template <class T>
-__device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, uint4 *stage, uint64_t *full)
-{
-    typedef typename T::raw raw;
-    const int lane = threadIdx.x & 31;
-    const int lo = max(i0, row.full0), hi = min(i1, row.full1);
-    if (lane == 0) {
-        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
-        barrier_expect(full, bytes);
-        if (bytes)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             shared_address(stage + (lo - i0))),
-                         "l"(row.vec(lo)), "r"(bytes), "r"(shared_address(full))
-                         : "memory");
-    }
-    if (lo > i0 || hi < i1) {
-        const int side = lane / T::kPerVec, e = lane % T::kPerVec;
-        const int i = side == 0 ? 0 : row.vecs - 1;
-        if (side < 2 && (i < row.full0 || i >= row.full1) && i >= i0 && i < i1) {
-            const int id = row.id(i, e);
-            raw v = T::narrow(-kInf);
-            if (id >= 0 && id < row.vocab)
-                v = row.x[id];
-            reinterpret_cast<raw *>(stage + (i - i0))[e] = v;
-        }
-        __syncwarp();
-    }
-    if (lane == 0)
-        barrier_arrive(full);
-}
-
 // A byte in shared memory for each vector of a part, with a bit for each of
 // its elements that is a listed token.
 template <class T>
@@ -319,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
     uint32_t active = 0;     // rows done with a weight other than 0
     float next_weight = a.weight ? a.weight[first] : 1.0f;
     if (warp == kFetcher) {
-        Cursor c;
+        Cursor<kStages> c;
         for (int64_t r = first; r < last && ok; ++r) {
             const float weight = next_weight;
             if (r + 1 < last && a.weight)
@@ -506,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
             ++active;
         }
     } else {
-        Cursor c;
+        Cursor<kStages> c;
         for (int64_t r = first; r < last; ++r) {
             const float weight = next_weight;
             if (r + 1 < last && a.weight)

@@ -5,43 +5,48 @@
 namespace fo {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCandidates = 1024;
-constexpr int kGroup = 4;          // vectors that a thread loads at once; one maximum is kept for them
-constexpr int kGroupStep = kGroup * kThreads;
-constexpr int kGroups = 512;       // candidate groups
+constexpr int kGradThreads = 256;
+constexpr int kWide = 256, kMiddle = 128, kNarrow = 64;   // threads to a row: see launch
+constexpr int kGroup = 4;                      // vectors of a thread that one maximum is kept for
+constexpr int kCtasPerSm = 4;
 
+// What the kN threads of a row share.
+template <int kN>
 struct Shared {
-    Stat part[kWarps + 1];
-    Stat mine;                      // this CTA's part, read by the others of the cluster
-    int count, groups;              // candidates found
-    int sums[kWarps];
+    static constexpr int kCandidates = kN == kWide ? 1024 : 512;
+    static constexpr int kGroups = 2 * kN;
+    Stat part[kN / 32];
+    Stat mine;                                // this CTA's part, read by the others of the cluster
+    int count, groups;                        // candidates found
+    int sums[kN / 32 < kMaxCluster ? kMaxCluster : kN / 32];
+    uint2 range[kN / 32];
+    int counts[2][kN / 32];
     int group[kGroups];
-    uint64_t list[kCandidates];     // candidates in any order; later the lists of the other CTAs
-    uint64_t sorted[FO_MAX_TOP_K];  // this CTA's largest, descending
+    uint64_t list[kCandidates];               // candidates in any order; later the lists of the other CTAs
+    uint64_t sorted[FO_MAX_TOP_K];            // this CTA's largest, descending
     int sorted_n;
 };
+static_assert(Shared<kWide>::kCandidates >= kMaxCluster * FO_MAX_TOP_K, "the lists of a cluster");
 
-__device__ __forceinline__ int block_sum(int v, Shared &sh)
+template <int kN>
+__device__ __forceinline__ int block_sum(int v, Shared<kN> &sh)
 {
     const int s = __reduce_add_sync(~0u, v);
     if ((threadIdx.x & 31) == 0)
         sh.sums[threadIdx.x >> 5] = s;
-    __syncthreads();
+    barrier_among<kN>();
     int t = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i)
+    for (int i = 0; i < kN / 32; ++i)
         t += sh.sums[i];
-    __syncthreads();
+    barrier_among<kN>();
     return t;
 }
 
 // f(key, id) for every element of vector i of the row.
 template <class T, class F>
-__device__ __forceinline__ void each(const Row<T> &row, int i, F f)
+__device__ __forceinline__ void each(const Row<T> &row, int i, const uint4 &v, F f)
 {
-    const uint4 v = load_vec(row, i);
     const typename T::raw *e = reinterpret_cast<const typename T::raw *>(&v);
 #pragma unroll
     for (int k = 0; k < T::kPerVec; ++k) {
@@ -61,14 +66,14 @@ __device__ __forceinline__ uint64_t list_key(uint32_t key, int id) { return ((ui
 // above it, as with ties, it is the k-th largest, else it is bisected for
 // (a pass over the part, by now in the L2 cache, for each bit that values
 // differ in, whatever the part holds).
-template <class T>
-__device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, uint32_t kth, int k, Shared &sh)
+template <class T, int kN>
+__device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, uint32_t kth, int k, Shared<kN> &sh)
 {
     constexpr uint32_t mask = T::kKeyBits;   // below it a key is all 0 or all 1
     const auto count = [&](uint32_t at) {
         int n = 0;
-        for (int i = threadIdx.x; i < p.n; i += kThreads)
-            each<T>(row, p.v0 + i, [&](uint32_t key, int) { n += (key & mask) >= at; });
+        for (int i = threadIdx.x; i < p.n; i += kN)
+            each<T>(row, p.v0 + i, load_vec(row, p.v0 + i), [&](uint32_t key, int) { n += (key & mask) >= at; });
         return block_sum(n, sh);
     };
     constexpr uint32_t unit = mask & (0u - mask);
@@ -80,19 +85,22 @@ __device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, uin
     }
     if (threadIdx.x == 0)
         sh.count = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.n; i += kThreads)
-        each<T>(row, p.v0 + i, [&](uint32_t key, int id) {
+    barrier_among<kN>();
+    for (int i = threadIdx.x; i < p.n; i += kN)
+        each<T>(row, p.v0 + i, load_vec(row, p.v0 + i), [&](uint32_t key, int id) {
             if ((key & mask) > kth)
                 sh.list[atomicAdd(&sh.count, 1)] = list_key(key, id);
         });
-    __syncthreads();
+    barrier_among<kN>();
     int have = sh.count;   // below k
-    for (int i0 = 0; i0 < p.n && have < k; i0 += kThreads) {
+    for (int i0 = 0; i0 < p.n && have < k; i0 += kN) {
         const int i = i0 + threadIdx.x;
+        uint4 v;
         int n = 0;
-        if (i < p.n)
-            each<T>(row, p.v0 + i, [&](uint32_t key, int) { n += (key & mask) == kth; });
+        if (i < p.n) {
+            v = load_vec(row, p.v0 + i);
+            each<T>(row, p.v0 + i, v, [&](uint32_t key, int) { n += (key & mask) == kth; });
+        }
         // ties before this thread's
         int before = n;
 #pragma unroll
@@ -102,80 +110,113 @@ __device__ __noinline__ void collect_exact(const Row<T> &row, const Part &p, uin
         }
         if ((threadIdx.x & 31) == 31)
             sh.sums[threadIdx.x >> 5] = before;
-        __syncthreads();
+        barrier_among<kN>();
         int all = 0;
         before -= n;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            before += w < (threadIdx.x >> 5) ? sh.sums[w] : 0;
+        for (int w = 0; w < kN / 32; ++w) {
+            before += w < (int)(threadIdx.x >> 5) ? sh.sums[w] : 0;
             all += sh.sums[w];
         }
         if (n)
-            each<T>(row, p.v0 + i, [&](uint32_t key, int id) {
+            each<T>(row, p.v0 + i, v, [&](uint32_t key, int id) {
                 if ((key & mask) == kth && have + before < k)
                     sh.list[have + before++] = list_key(key, id);
             });
         have = min(k, have + all);
-        __syncthreads();
+        barrier_among<kN>();
     }
     if (threadIdx.x == 0)
         sh.count = have;
-    __syncthreads();
+    barrier_among<kN>();
 }
 
 template <class T>
 __device__ __forceinline__ uint32_t largest_key(const Largest<T> &l) { return order_key(l.value_nan()); }
+
+// The k-th largest of the threads' keys, cut to its upper 16 bits; 0 where
+// fewer than k are not 0. Two bits a step, from the first that keys differ in.
+template <int kN>
+__device__ __forceinline__ uint32_t kth_key(uint32_t mine, int k, Shared<kN> &sh)
+{
+    constexpr int kWarps = kN / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t hi = __reduce_max_sync(~0u, mine), lo = __reduce_min_sync(~0u, mine);
+    if (lane == 0)
+        sh.range[warp] = make_uint2(lo, hi);
+    barrier_among<kN>();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        lo = min(lo, sh.range[i].x);
+        hi = max(hi, sh.range[i].y);
+    }
+    int bit = 31 - __clz((int)(((lo ^ hi) & 0xffff0000u) | 0x8000u));   // 15: they agree
+    bit |= 1;                                                           // the upper of a pair
+    uint32_t bound = bit >= 31 ? 0u : hi & (0xfffffffeu << bit);
+    for (int step = 0; bit > 16; bit -= 2, ++step) {
+        const uint32_t u = 1u << (bit - 1);
+        const int n = __popc(__ballot_sync(~0u, mine >= bound + u)) | __popc(__ballot_sync(~0u, mine >= bound + 2 * u)) << 10 |
+                      __popc(__ballot_sync(~0u, mine >= bound + 3 * u)) << 20;
+        if (lane == 0)
+            sh.counts[step & 1][warp] = n;
+        barrier_among<kN>();
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i)
+            all += sh.counts[step & 1][i];
+        bound += (all >> 20) >= k ? 3 * u : (all >> 10 & 1023) >= k ? 2 * u : (all & 1023) >= k ? u : 0u;
+    }
+    return bound;
+}
 
 // The part's largest elements (k, or all where it has fewer), descending, into
 // sh.sorted. `mine` is the key of the largest element of this thread (0
 // without elements): the k-th largest of the threads' maxima bounds the k-th
 // largest element from below, and for spread-out values few elements besides
 // the top k reach it. `maxima` holds a maximum for each kGroup vectors of a
-// thread, so that only those groups are read again that reach the bound.
-template <class T>
-__device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const Largest<T> *maxima, uint32_t mine, int k, Shared &sh)
+// thread, so that only those groups are read again, from the L2 cache, that
+// reach the bound.
+template <class T, int kN>
+__device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const Largest<T> *maxima, uint32_t mine, int k, Shared<kN> &sh)
 {
-    uint32_t bound = 0;
-#pragma unroll 1
-    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-        if (__syncthreads_count(mine >= (bound | bit)) >= k)
-            bound |= bit;
+    if (threadIdx.x == 0)
+        sh.count = sh.groups = 0;
+    const uint32_t bound = kth_key<kN>(mine, k, sh);
     if (mine >= bound)
-        for (int i = threadIdx.x; i < p.n; i += kGroupStep) {
-            const int at = i / kGroupStep * kThreads + (int)threadIdx.x;
+        for (int i = threadIdx.x; i < p.n; i += kGroup * kN) {
+            const int at = i / (kGroup * kN) * kN + (int)threadIdx.x;
             if (largest_key(maxima[at]) >= bound) {
                 const int n = atomicAdd(&sh.groups, 1);
-                if (n < kGroups)
+                if (n < Shared<kN>::kGroups)
                     sh.group[n] = at;
             }
         }
-    __syncthreads();
+    barrier_among<kN>();
     const int groups = sh.groups;
-    if (groups <= kGroups)
-        for (int j = threadIdx.x; j < groups * kGroup; j += kThreads) {
+    if (groups <= Shared<kN>::kGroups)
+        for (int j = threadIdx.x; j < groups * kGroup; j += kN) {
             const int at = sh.group[j / kGroup];
-            const int i = at / kThreads * kGroupStep + j % kGroup * kThreads + at % kThreads;
-            if (i >= p.n || *(volatile int *)&sh.count > kCandidates)
+            const int i = at / kN * (kGroup * kN) + j % kGroup * kN + at % kN;
+            if (i >= p.n || *(volatile int *)&sh.count > Shared<kN>::kCandidates)
                 continue;
-            each<T>(row, p.v0 + i, [&](uint32_t key, int id) {
+            const uint4 v = load_vec(row, p.v0 + i);
+            if (largest_key(Largest<T>::of(v)) < bound)
+                continue;
+            each<T>(row, p.v0 + i, v, [&](uint32_t key, int id) {
                 if (key >= bound) {
                     const int n = atomicAdd(&sh.count, 1);
-                    if (n < kCandidates)
+                    if (n < Shared<kN>::kCandidates)
                         sh.list[n] = list_key(key, id);
                 }
             });
         }
-    __syncthreads();
-    if (groups > kGroups || sh.count > kCandidates) {
-        __syncthreads();
-        // the bound to the last bit that values differ in
-        for (uint32_t bit = 0x8000u; bit & T::kKeyBits; bit >>= 1)
-            if (__syncthreads_count(mine >= (bound | bit)) >= k)
-                bound |= bit;
-        collect_exact<T>(row, p, bound, k, sh);
+    barrier_among<kN>();
+    if (groups > Shared<kN>::kGroups || sh.count > Shared<kN>::kCandidates) {
+        barrier_among<kN>();
+        collect_exact<T, kN>(row, p, bound & T::kKeyBits, k, sh);
     }
     const int n = sh.count;
-    for (int i = threadIdx.x; i < n; i += kThreads) {   // no two keys are equal
+    for (int i = threadIdx.x; i < n; i += kN) {   // no two keys are equal
         const uint64_t key = sh.list[i];
         int rank = 0;
 #pragma unroll 4
@@ -186,7 +227,7 @@ __device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const
     }
     if (threadIdx.x == 0)
         sh.sorted_n = min(n, k);
-    __syncthreads();
+    barrier_among<kN>();
 }
 
 __device__ __forceinline__ float key_value(uint64_t key)
@@ -195,55 +236,17 @@ __device__ __forceinline__ float key_value(uint64_t key)
     return __uint_as_float(o == 0xffffffffu ? 0x7fffffffu : o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
-// One row by a cluster of CTAs (one CTA where there are many rows): one pass
-// over the row by plain loads, statistics in registers, joined through the
-// (distributed) shared memory.
-template <class T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
+// What follows the pass over a part: the sums and top lists joined in the CTA
+// and over the cluster, and the row's results. By the first kN threads; the
+// cluster's barriers are passed once.
+template <class T, int kN>
+__device__ __forceinline__ void finish(const LogprobArgs &a, int64_t r, const Row<T> &row, const Part &p, const Running<T, true> &run,
+                                       const Largest<T> *maxima, int64_t token, float token_x, Shared<kN> &sh)
 {
-    extern __shared__ __align__(16) unsigned char dynamic[];
-    Largest<T> *maxima = reinterpret_cast<Largest<T> *>(dynamic);
-    __shared__ Shared sh;
     const uint32_t size = cluster_size(), rank = cluster_rank();
-    const int64_t r = blockIdx.x / size;
-    const Row<T> row(a.in, r);
-    const Part p = part_of(row, rank, size);
-    if (threadIdx.x == 0)
-        sh.count = sh.groups = 0;
-    int64_t token = -1;
-    float token_x = 0.0f;
-    if (rank == 0 && threadIdx.x == 0 && a.logp) {
-        token = a.tokens[r];
-        if (token >= 0 && token < row.vocab)
-            token_x = T::widen(row.x[token]);
-    }
-
-    Running<T, true> run;
-    for (int i0 = 0; i0 < p.n; i0 += kGroupStep) {
-        const int i = p.v0 + i0 + (int)threadIdx.x;
-        uint4 v[kGroup];
-        const Largest<T> before = run.top;
-        run.top = Largest<T>::none();
-        if (p.v0 + i0 >= row.full0 && i0 + kGroupStep <= p.n && p.v0 + i0 + kGroupStep <= row.full1) {
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                v[j] = __ldcs(row.vec(i + j * kThreads));
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                run.add(v[j], a.in);
-        } else {
-#pragma unroll 1
-            for (int j = 0; j < kGroup; ++j)
-                if (i0 + (int)threadIdx.x + j * kThreads < p.n)
-                    run.add(load_vec(row, i + j * kThreads), a.in);
-        }
-        if (a.k && i0 + (int)threadIdx.x < p.n)
-            maxima[i0 / kGroupStep * kThreads + threadIdx.x] = run.top;
-        run.top = run.top.with(before);
-    }
-    Stat s = block_join<true, kWarps>(run.stat(a.in), sh.part, a.in);
+    Stat s = block_join<true, kN>(run.stat(a.in), sh.part, a.in);
     if (a.k)
-        find_top<T>(row, p, maxima, (int)threadIdx.x < p.n ? largest_key(run.top) : 0, a.k, sh);
+        find_top<T, kN>(row, p, maxima, (int)threadIdx.x < p.n ? largest_key(run.top) : 0, a.k, sh);
     if (size > 1) {
         if (threadIdx.x == 0)
             sh.mine = s;
@@ -262,41 +265,96 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
         if (a.stats)
             a.stats[r] = make_float4(s.m, s.z, h, 0.0f);
     }
-    if (a.k) {
-        // an element's place among all parts' lists: its own place and, for
-        // each other list, how many of that are larger
-        const int k = a.k;
-        if (size > 1) {
-            for (uint32_t i = threadIdx.x; i < size * k; i += kThreads) {
-                const uint32_t from = i / k, j = i % k;
-                sh.list[i] = ld_cluster_u64(map_shared(&sh.sorted[j], from));
-            }
-            if (threadIdx.x < size)
-                sh.sums[threadIdx.x] = (int)__float_as_int(ld_cluster_f32(map_shared(&sh.sorted_n, threadIdx.x)));
-            __syncthreads();
+    if (a.k == 0)
+        return;
+    // an element's place among all parts' lists: its own place and, for each
+    // other list, how many of that are larger
+    const int k = a.k;
+    if (size > 1) {
+        for (uint32_t i = threadIdx.x; i < size * k; i += kN) {
+            const uint32_t from = i / k, j = i % k;
+            sh.list[i] = ld_cluster_u64(map_shared(&sh.sorted[j], from));
         }
-        if ((int)threadIdx.x < sh.sorted_n) {
-            const uint64_t key = sh.sorted[threadIdx.x];
-            int place = threadIdx.x;
-            for (uint32_t i = 0; i < size && size > 1; ++i) {
-                if (i == rank)
-                    continue;
-                int lo = 0, hi = sh.sums[i];   // the first place whose key is smaller
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (sh.list[i * k + mid] > key)
-                        lo = mid + 1;
-                    else
-                        hi = mid;
-                }
-                place += lo;
+        if (threadIdx.x < size)
+            sh.sums[threadIdx.x] = (int)__float_as_int(ld_cluster_f32(map_shared(&sh.sorted_n, threadIdx.x)));
+        barrier_among<kN>();
+    }
+    for (int n = threadIdx.x; n < sh.sorted_n; n += kN) {
+        const uint64_t key = sh.sorted[n];
+        int place = n;
+        for (uint32_t i = 0; i < size && size > 1; ++i) {
+            if (i == rank)
+                continue;
+            int lo = 0, hi = sh.sums[i];   // the first place whose key is smaller
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (sh.list[i * k + mid] > key)
+                    lo = mid + 1;
+                else
+                    hi = mid;
             }
-            if (place < k) {
-                a.top_ids[r * k + place] = (int32_t)entry_id(key);
-                a.top_logp[r * k + place] = log_prob(key_value(key), s.m, s.z, ln_z, a.in.inv_t);
-            }
+            place += lo;
+        }
+        if (place < k) {
+            a.top_ids[r * k + place] = (int32_t)entry_id(key);
+            a.top_logp[r * k + place] = log_prob(key_value(key), s.m, s.z, ln_z, a.in.inv_t);
         }
     }
+}
+
+// The given token's logit, on its way while the row is walked over.
+template <class T>
+__device__ __forceinline__ float load_token(const LogprobArgs &a, int64_t r, const Row<T> &row, int64_t &token)
+{
+    token = -1;
+    if (threadIdx.x != 0 || cluster_rank() != 0 || !a.logp)
+        return 0.0f;
+    token = a.tokens[r];
+    return T::widen(row.x[token >= 0 && token < row.vocab ? token : 0]);
+}
+
+// One row by a cluster of CTAs of kN threads (one CTA where there are many
+// rows): one pass over the row by plain loads, sums in registers. Bound by the
+// loads and, for the 16-bit types, nearly as much by the instructions: about
+// 5.5 an element, one of them the exponential.
+template <class T, int kN>
+__global__ void __launch_bounds__(kN, 1280 / kN) logprobs_kernel(LogprobArgs a)
+{
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    Largest<T> *const maxima = reinterpret_cast<Largest<T> *>(dynamic);
+    __shared__ Shared<kN> sh;
+    constexpr int kStep = kGroup * kN;
+    const uint32_t size = cluster_size();
+    const int64_t r = blockIdx.x / size;
+    const Row<T> row(a.in, r);
+    const Part p = part_of(row, cluster_rank(), size);
+    const int tid = threadIdx.x;
+    int64_t token;
+    const float token_x = load_token(a, r, row, token);
+    Running<T, true> run;
+    for (int i0 = 0; i0 < p.n; i0 += kStep) {
+        const int i = p.v0 + i0 + tid;
+        const Largest<T> before = run.top;
+        run.top = Largest<T>::none();
+        if (p.v0 + i0 >= row.full0 && i0 + kStep <= p.n && p.v0 + i0 + kStep <= row.full1) {
+            uint4 v[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                v[j] = __ldcs(row.vec(i + j * kN));
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                run.add(v[j], a.in);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kGroup; ++j)
+                if (i0 + tid + j * kN < p.n)
+                    run.add(load_vec(row, i + j * kN), a.in);
+        }
+        if (a.k && i0 + tid < p.n)
+            maxima[i0 / kGroup + tid] = run.top;
+        run.top = run.top.with(before);
+    }
+    finish<T, kN>(a, r, row, p, run, maxima, token, token_x, sh);
     if (size > 1) {   // no CTA leaves while another reads its shared memory
         cluster_arrive();
         cluster_wait();
@@ -307,20 +365,20 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
 // G the sum of all entries' weights, the entries being the token and the top
 // ids. With t = (x_j - m) c: dx_j = 2^t (alpha + beta t), plus the weights.
 template <class T, int kVecs>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a, int chunks)
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGradArgs a, int chunks)
 {
     typedef typename T::raw raw;
     __shared__ int64_t ids[FO_MAX_TOP_K + 1];
     __shared__ float weight[FO_MAX_TOP_K + 1];
     const int64_t r = blockIdx.x / (unsigned)chunks;
-    const int v0 = (int)(blockIdx.x % (unsigned)chunks) * (kVecs * kThreads);
+    const int v0 = (int)(blockIdx.x % (unsigned)chunks) * (kVecs * kGradThreads);
     const Row<T> row(a.in, r);
     raw *g = static_cast<raw *>(a.out.data) + row_offset(a.in, r, a.out.row_stride, a.out.outer_stride);
     const int tid = threadIdx.x;
     uint4 v[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        const int at = v0 + i * kThreads + tid;
+        const int at = v0 + i * kGradThreads + tid;
         if (at < row.vecs)
             v[i] = load_vec(row, at);
     }
@@ -347,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
     const float beta = h == 0.0f ? 0.0f : -p_scale * h * kLn2;
 
     // the entries of this chunk; the first of equal ids takes the weight of all
-    const int end = row.id(v0 + kVecs * kThreads, 0);
+    const int end = row.id(v0 + kVecs * kGradThreads, 0);
     bool entry = false;
     float entry_value = 0.0f;
     if (!zero && tid <= a.k && ids[tid] >= 0 && ids[tid] >= row.id(v0, 0) && ids[tid] < end && ids[tid] < row.vocab) {
@@ -368,7 +426,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
     const f2 nm = splat(-m), al = splat(alpha), be = splat(beta);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        const int at = v0 + i * kThreads + tid;
+        const int at = v0 + i * kGradThreads + tid;
         if (at >= row.vecs)
             break;
         f2 x[T::kPerVec / 2];
@@ -392,28 +450,48 @@ __global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs
         g[ids[tid]] = T::narrow(entry_value);
 }
 
+template <class T, int kN>
+cudaError_t launch(const LogprobArgs &a, int size, cudaStream_t stream)
+{
+    const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
+    const int64_t groups = (vecs + kGroup * kN - 1) / (kGroup * kN);
+    return launch_cluster(logprobs_kernel<T, kN>, a, a.in.rows, size, a.k ? groups * kN * 4 : 0, kN, stream);
+}
+
 template <class T>
 cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
 {
-    // one CTA a row, or a cluster that shares it while the grid would leave SMs short of CTAs
-    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw);
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * kCtasPerSm;
+    // Many rows: one CTA each, of as few threads as the row and its list of
+    // alternatives leave busy, so that more rows are on an SM at once and their
+    // joins and lists overlap. Measured at 256 / 128 / 64 threads: 16384 x 1000
+    // BF16 54 / - / 18 us, with 20 alternatives 124 / - / 53; 3001 x 50257 with
+    // 64 alternatives 91 / 81 / - us; 4096 x 128256 without any 180 / 169 / -,
+    // with 64 of them 226 / 253 / -.
+    if (a.in.rows >= ctas) {
+        if (bytes <= 16 * 1024 && a.k <= kNarrow)
+            return launch<T, kNarrow>(a, 1, stream);
+        if (a.k == 0 || (a.k <= 64 && bytes <= 128 * 1024))
+            return launch<T, kMiddle>(a, 1, stream);
+        return launch<T, kWide>(a, 1, stream);
+    }
+    // few rows: a cluster shares one while the grid would leave SMs short of CTAs
     int size = 1;
-    while (size < kMaxCluster && a.in.rows * size < 4 * sm_count() && bytes > size * 8192)
+    while (size < kMaxCluster && a.in.rows * size < ctas && bytes > size * 8192)
         size *= 2;
-    const int64_t groups = (part_vecs(bytes, size) + kGroupStep - 1) / kGroupStep;
-    return launch_cluster(logprobs_kernel<T>, a, a.in.rows, size, a.k ? groups * kThreads * 4 : 0, kThreads, stream);
+    return launch<T, kWide>(a, size, stream);
 }
 
 template <class T>
 cudaError_t launch(const LogprobGradArgs &a, cudaStream_t stream)
 {
     const int64_t vecs = a.in.vocab / T::kPerVec + 2;
-    if (vecs * a.in.rows >= (int64_t)sm_count() * 8 * kThreads * 8) {
-        const int64_t chunks = (vecs + 8 * kThreads - 1) / (8 * kThreads);
-        logprobs_grad_kernel<T, 8><<<(unsigned)(chunks * a.in.rows), kThreads, 0, stream>>>(a, (int)chunks);
+    if (vecs * a.in.rows >= (int64_t)sm_count() * 8 * kGradThreads * 8) {
+        const int64_t chunks = (vecs + 8 * kGradThreads - 1) / (8 * kGradThreads);
+        logprobs_grad_kernel<T, 8><<<(unsigned)(chunks * a.in.rows), kGradThreads, 0, stream>>>(a, (int)chunks);
     } else {
-        const int64_t chunks = (vecs + kThreads - 1) / kThreads;
-        logprobs_grad_kernel<T, 1><<<(unsigned)(chunks * a.in.rows), kThreads, 0, stream>>>(a, (int)chunks);
+        const int64_t chunks = (vecs + kGradThreads - 1) / kGradThreads;
+        logprobs_grad_kernel<T, 1><<<(unsigned)(chunks * a.in.rows), kGradThreads, 0, stream>>>(a, (int)chunks);
     }
     count_launch();
     return cudaGetLastError();

@@ -329,23 +329,23 @@ __device__ __forceinline__ Stat warp_join(Stat s, const LogitRows &in, int n = 3
     return s;
 }
 
-// Over a CTA of kWarps warps: the result in every thread. `part` is shared
-// memory of kWarps + 1 entries.
-template <bool kEntropy, int kWarps>
+// Among the first kN threads of a CTA.
+template <int kN>
+__device__ __forceinline__ void barrier_among()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(kN) : "memory");
+}
+
+// Over the first kN threads of a CTA: the result in every one of them. `part`
+// is shared memory of kN / 32 entries.
+template <bool kEntropy, int kN>
 __device__ __forceinline__ Stat block_join(Stat s, Stat *part, const LogitRows &in)
 {
     s = warp_join<kEntropy>(s, in);
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        s = part[threadIdx.x % kWarps];
-        s = warp_join<kEntropy>(s, in, kWarps);
-        if (threadIdx.x == 0)
-            part[kWarps] = s;
-    }
-    __syncthreads();
-    return part[kWarps];
+    barrier_among<kN>();
+    return warp_join<kEntropy>(part[threadIdx.x % (kN / 32)], in, kN / 32);
 }
 
 // One thread's statistics while it walks over its vectors. An exponential
@@ -534,38 +534,53 @@ __device__ __forceinline__ bool barrier_wait(uint64_t *bar, uint32_t parity)
 // The same by all lanes of a warp, which agree on the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) { return __all_sync(~0u, barrier_wait(bar, parity)); }
 
-constexpr int kCopyBytes = 16384;   // of one bulk copy
+// A place in the ring of stages and how often it has been used, modulo 2.
+template <int kStages>
+struct Cursor {
+    int at = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == kStages) {
+            at = 0;
+            turn ^= 1;
+        }
+    }
+};
 
-// Starts the copies of a part into shared memory, by one warp. The vectors
-// wholly inside the row come by bulk copies that `full` counts; those that
-// reach beyond its ends element by element (no byte outside the row is read),
-// filled up with -inf.
+// Starts the copy of vectors [i0, i1) of a row into a stage, by one warp. The
+// vectors wholly inside the row come by a bulk copy; those that reach beyond
+// its ends element by element (no byte outside the row is read), filled up
+// with -inf. `full` counts the copy's bytes and two arrivals.
 template <class T>
-__device__ __forceinline__ void load_part(const Row<T> &row, const Part &p, uint4 *buf, uint64_t *full)
+__device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, uint4 *stage, uint64_t *full)
 {
     typedef typename T::raw raw;
     const int lane = threadIdx.x & 31;
-    const int lo = max(p.v0, row.full0), hi = min(p.v0 + p.n, row.full1);
+    const int lo = max(i0, row.full0), hi = min(i1, row.full1);
     if (lane == 0) {
         const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
         barrier_expect(full, bytes);
-        for (uint32_t at = 0; at < bytes; at += kCopyBytes) {
-            const uint32_t size = min((uint32_t)kCopyBytes, bytes - at);
+        if (bytes)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             shared_address(buf + (lo - p.v0)) + at),
-                         "l"(reinterpret_cast<const char *>(row.vec(lo)) + at), "r"(size), "r"(shared_address(full))
+                             shared_address(stage + (lo - i0))),
+                         "l"(row.vec(lo)), "r"(bytes), "r"(shared_address(full))
                          : "memory");
+    }
+    if (lo > i0 || hi < i1) {
+        const int side = lane / T::kPerVec, e = lane % T::kPerVec;
+        const int i = side == 0 ? 0 : row.vecs - 1;
+        if (side < 2 && (i < row.full0 || i >= row.full1) && i >= i0 && i < i1) {
+            const int id = row.id(i, e);
+            raw v = T::narrow(-kInf);
+            if (id >= 0 && id < row.vocab)
+                v = row.x[id];
+            reinterpret_cast<raw *>(stage + (i - i0))[e] = v;
         }
+        __syncwarp();
     }
-    const int side = lane / T::kPerVec, e = lane % T::kPerVec;
-    const int i = side == 0 ? 0 : row.vecs - 1;
-    if (side < 2 && (i < row.full0 || i >= row.full1) && i >= p.v0 && i < p.v0 + p.n) {
-        const int id = row.id(i, e);
-        raw v = T::narrow(-kInf);
-        if (id >= 0 && id < row.vocab)
-            v = row.x[id];
-        reinterpret_cast<raw *>(buf + (i - p.v0))[e] = v;
-    }
+    if (lane == 0)
+        barrier_arrive(full);
 }
 
 // Stores into another CTA's shared memory of the cluster (launched as one), and
