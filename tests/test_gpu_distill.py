@@ -292,3 +292,41 @@ def test_refusals():
         losses.distill_loss(x, ids, y, teacher_temperature=float("nan"))
     with pytest.raises(fo.FoError, match="BAD_ARG"):       # rows of the gradient on top of one another
         losses.distill_loss_grad(x, ids, y, out=torch.empty(1000, dtype=BF, device="cuda").expand(4, 1000))
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("v,dtype", [(2003, BF), (4100, F32), (33001, F16)])
+def test_rows_that_a_cluster_takes_in_turn(v, dtype, tail):
+    """More rows than CTAs: several by each, rows of weight 0 among them, in place and not."""
+    n = 4000 if v < 10000 else 2500
+    x = make(n, v, dtype, seed=v)
+    ids, y, lse = make_teacher(n, v, 24, seed=5)
+    ids[::7, 20] = ids[::7, 3]                # a token listed twice
+    w = torch.rand(n, generator=gen(5), device="cuda") / n
+    w[torch.rand(n, generator=gen(6), device="cuda") < 0.4] = 0.0
+    x[w == 0] = math.nan
+    how = dict(tail=tail, teacher_lse=lse if tail else None)
+    want, grad, tol, scale = ref.distill(x.nan_to_num(0.0), ids, y, tail=tail, lse=how["teacher_lse"], weight=w)
+    loss, g = losses.distill_loss_grad(x, ids, y, row_weight=w, **how)
+    ref.close(loss, want, tol, "loss")
+    ref.close(g, grad, ref.grad_tolerance(grad, scale, dtype), "gradient")
+    for _ in range(2):
+        z = x.clone()
+        again, gz = losses.distill_loss_grad(z, ids, y, row_weight=w, out=z, **how)
+        assert torch.equal(gz, g) and torch.equal(again, loss)
+    keep = w != 0
+    alone = losses.distill_loss(x[keep], ids[keep], y[keep], tail=tail, teacher_lse=lse[keep] if tail else None)
+    ref.close(alone * w[keep], want[keep], tol[keep] * 1.01 + 2.0 ** -23 * want[keep].abs(), "loss alone")
+
+
+def test_a_teacher_that_is_not_a_number():
+    x = make(4, 1000, F32)
+    ids, y, lse = make_teacher(4, 1000, 8, short=False)
+    y[1, 2] = math.nan
+    y[2, 5] = math.nan
+    ids[2, 5] = -1                            # no entry: what stands beside it does not matter
+    y[3, 0] = INF
+    for tail in (False, True):
+        loss, g = losses.distill_loss_grad(x, ids, y, tail=tail, teacher_lse=lse if tail else None)
+        assert loss.isnan().tolist() == [False, True, False, True]
+        assert g[1].isnan().all() and g[3].isnan().all() and torch.isfinite(g[[0, 2]]).all()

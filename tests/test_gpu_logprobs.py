@@ -371,3 +371,31 @@ def test_refusals():
         losses.token_logprobs(x.cpu(), t.cpu())
     with pytest.raises(ValueError, match="strides"):
         losses.token_logprobs(torch.empty(4, 6, 8, 10, device="cuda")[:3, :5, :7], torch.zeros(3, 5, 7, dtype=torch.long, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("v,k", [(40, 40), (130, 64), (1000, 20), (1000, 65), (1000, 128), (4099, 64), (9001, 3), (33000, 64), (70001, 100)])
+def test_many_rows_of_each_width(v, k, dtype):
+    """Enough rows that each is one CTA's: of 64, 128 and 256 threads by its length and its list."""
+    n = 640 if v > 20000 else 1500
+    x = make(n, v, dtype, seed=v)
+    x[7] = -INF                               # nothing left
+    x[8, 2:] = -INF                           # fewer tokens left than are listed
+    x[9] = 0.5                                # all tied
+    x[10, ::2] = -0.0
+    x[10, 1::2] = 0.0
+    t = torch.randint(0, v, (n,), generator=gen(1), device="cuda")
+    check_forward(x, t, k, 0.8)
+    check_forward(x, t, 0, 1.0)
+
+
+def test_alternatives_of_rows_with_nan():
+    """NaN counts as the largest value, wherever it lies; the ids stay valid and distinct."""
+    for n, v in ((2, 50257), (900, 1000)):
+        x = make(n, v, BF, seed=v)
+        x[0, [3, v // 2, v - 1]] = math.nan
+        x[1, :] = math.nan
+        o = losses.token_logprobs(x, top_k=10)
+        assert o.top_ids[0, :3].tolist() == [3, v // 2, v - 1]
+        assert o.top_ids[1].tolist() == list(range(10))
+        assert o.top_ids[0].unique().numel() == 10 and o.top_logp[:2].isnan().all()
