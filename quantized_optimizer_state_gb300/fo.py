@@ -146,9 +146,17 @@ def _check(fn: str, status: int) -> None:
         raise FoError(fn, status, msg)
 
 
+_get_device = None   # torch's current device, without its checks once CUDA is initialised
+
+
 def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    global _get_device
+    if _get_device is None:
+        import torch
+        device = torch.cuda.current_device()
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        return device
+    return _get_device()
 
 
 def _dtype_names(dtypes) -> str:
@@ -452,10 +460,12 @@ def _array(x, name: str, dtype, numel: int, cur: int) -> Optional[int]:
 def logits_rows(x, temperature: float = 1.0, name: str = "logits") -> FoLogits:
     """The ``fo_logits_t`` of a tensor [..., vocab] of bfloat16, float16 or
     float32: any leading dimensions that two strides cover, the last contiguous."""
-    dt = _logit_dtype(x.dtype, name)
+    dt = _LOGIT_DTYPES.get(x.dtype)
+    if dt is None:
+        dt = _logit_dtype(x.dtype, name)
     ptr = _device_ptr(x, name, _current_device())
     rows, inner, rs, os_ = _row_strides(x, name)
-    return FoLogits(ptr, rows, x.shape[-1], rs, inner, os_, float(temperature), dt, 0)
+    return FoLogits(ptr, rows, x.shape[-1], rs, inner, os_, temperature, dt, 0)
 
 
 def _logits_grad(logits: FoLogits, like, grad, name: str = "grad"):

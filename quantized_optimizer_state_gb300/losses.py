@@ -20,6 +20,7 @@ lies. The rules for masked, infinite and invalid entries stand in
 from __future__ import annotations
 
 import contextlib
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -39,59 +40,87 @@ def _check_rows(name: str, x: Optional[torch.Tensor], shape) -> None:
         raise ValueError(f"{name} must have the logits' leading shape {tuple(shape)}, not {tuple(x.shape)}")
 
 
-def _aligned_like(logits: torch.Tensor) -> torch.Tensor:
-    """An uninitialised gradient for ``logits`` whose rows start at the same
-    alignment (modulo 16 bytes), so that the kernels' vectors of both line up:
-    rows of an odd vocabulary in a padded matrix would otherwise not. At most
-    7 elements are added to a row."""
-    if logits.dim() == 2 and logits.shape[0] > 1 and logits.stride(0) > logits.shape[1]:
-        per_16 = 16 // logits.element_size()
-        pitch = logits.shape[1] + (logits.stride(0) - logits.shape[1]) % per_16
-        return torch.empty((logits.shape[0], pitch), dtype=logits.dtype,
-                           device=logits.device)[:, :logits.shape[1]]
-    return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+# The functions below hand the C calls the addresses of tensors that they have
+# just made themselves; what the caller passes is checked by fo's helpers.
+
+def _empty_grad(logits: torch.Tensor, x: fo.FoLogits):
+    """An uninitialised gradient for ``logits`` and its layout. Its rows start at
+    the same alignment (modulo 16 bytes) as the logits', so that the kernels'
+    vectors of both line up: rows of an odd vocabulary in a padded matrix would
+    otherwise not. At most 7 elements are added to a row."""
+    vocab = x.vocab
+    if x.inner_rows == x.rows and x.rows > 1 and x.row_stride > vocab and logits.dim() == 2:
+        pitch = vocab + (x.row_stride - vocab) % (16 // logits.element_size())
+        grad = torch.empty((x.rows, pitch), dtype=logits.dtype, device=logits.device)[:, :vocab]
+        return grad, fo.FoLogitsGrad(grad.data_ptr(), pitch, 0)
+    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    return grad, fo.FoLogitsGrad(grad.data_ptr(), vocab, x.inner_rows * vocab)
 
 
 def _on_device_of(x: torch.Tensor):
     """Backward passes run on autograd's threads: the library's calls launch on the current device."""
-    return contextlib.nullcontext() if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)
+    return contextlib.nullcontext() if x.device.index == fo._current_device() else torch.cuda.device(x.device)
 
 
-def _logprobs(logits, tokens, top_k, temperature, entropy, stats):
-    rows, dev, f32 = logits.shape[:-1], logits.device, torch.float32
-    logp = torch.empty(rows, dtype=f32, device=dev) if tokens is not None else None
-    ent = torch.empty(rows, dtype=f32, device=dev) if entropy else None
-    top_ids = torch.empty(rows + (top_k,), dtype=torch.int32, device=dev) if top_k else None
-    top_logp = torch.empty(rows + (top_k,), dtype=f32, device=dev) if top_k else None
-    fo.fo_token_logprobs(logits, tokens, top_k, logp, ent, top_ids, top_logp, stats, temperature)
-    return logp, ent, top_ids, top_logp
+def _dense(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if g is None else g.contiguous()
+
+
+def _logprobs(logits, tokens, top_k, temperature, entropy, rows, with_stats):
+    x = fo.logits_rows(logits, temperature)
+    dev, f32, empty = logits.device, torch.float32, torch.empty
+    logp = ent = top_ids = top_logp = stats = None
+    p_tokens = p_logp = p_ent = p_ids = p_top = p_stats = None
+    if tokens is not None:
+        p_tokens = fo._array(tokens, "tokens", torch.int64, x.rows, dev.index)
+        logp = empty(rows, dtype=f32, device=dev)
+        p_logp = logp.data_ptr()
+    if entropy:
+        ent = empty(rows, dtype=f32, device=dev)
+        p_ent = ent.data_ptr()
+    if top_k:
+        top_ids = empty(rows + (top_k,), dtype=torch.int32, device=dev)
+        top_logp = empty(rows + (top_k,), dtype=f32, device=dev)
+        p_ids, p_top = top_ids.data_ptr(), top_logp.data_ptr()
+    if with_stats:
+        stats = empty((x.rows, fo.FO_LOSS_STATS), dtype=f32, device=dev)
+        p_stats = stats.data_ptr()
+    status = fo.lib().fo_token_logprobs(ctypes.byref(x), p_tokens, top_k, p_logp, p_ent, p_ids, p_top, p_stats,
+                                        fo._stream(None))
+    if status:
+        fo._check("fo_token_logprobs", status)
+    return logp, ent, top_ids, top_logp, stats
 
 
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, tokens, top_k, temperature, entropy):
-        stats = torch.empty(logits.shape[:-1] + (fo.FO_LOSS_STATS,), dtype=torch.float32, device=logits.device)
-        out = _logprobs(logits, tokens, top_k, temperature, entropy, stats)
-        ctx.save_for_backward(logits, tokens, out[2], stats)
+    def forward(ctx, logits, tokens, top_k, temperature, entropy, rows):
+        logp, ent, top_ids, top_logp, stats = _logprobs(logits, tokens, top_k, temperature, entropy, rows, True)
+        ctx.save_for_backward(logits, tokens, top_ids, stats)
         ctx.temperature = temperature
         if top_k:
-            ctx.mark_non_differentiable(out[2])
+            ctx.mark_non_differentiable(top_ids)
         ctx.set_materialize_grads(False)
-        return out
+        return logp, ent, top_ids, top_logp
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_logp, g_entropy, _, g_top):
         logits, tokens, top_ids, stats = ctx.saved_tensors
-        grad = _aligned_like(logits)
         with _on_device_of(logits):
-            fo.fo_token_logprobs_grad(logits, stats, grad, tokens, _dense(g_logp), _dense(g_entropy), top_ids,
-                                      _dense(g_top), 0 if top_ids is None else top_ids.shape[-1], ctx.temperature)
-        return grad, None, None, None, None
-
-
-def _dense(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    return None if g is None else g.contiguous()
+            x = fo.logits_rows(logits, ctx.temperature)
+            grad, to = _empty_grad(logits, x)
+            n, cur, f32 = x.rows, logits.device.index, torch.float32
+            k = 0 if top_ids is None else top_ids.shape[-1]
+            g_logp, g_entropy, g_top = _dense(g_logp), _dense(g_entropy), _dense(g_top)
+            status = fo.lib().fo_token_logprobs_grad(
+                ctypes.byref(x), None if tokens is None else tokens.data_ptr(), k,
+                None if top_ids is None else top_ids.data_ptr(), stats.data_ptr(), fo._array(g_logp, "g_logp", f32, n, cur),
+                fo._array(g_entropy, "g_entropy", f32, n, cur), fo._array(g_top, "g_top", f32, n * k, cur),
+                ctypes.byref(to), fo._stream(None))
+            if status:
+                fo._check("fo_token_logprobs_grad", status)
+        return grad, None, None, None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top_k: int = 0,
@@ -104,23 +133,42 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     ascending id. Differentiable in the logits through ``logp``, ``entropy``
     and ``top_logp``.
     """
+    rows = logits.shape[:-1]
     if tokens is not None:
-        _check_rows("tokens", tokens, logits.shape[:-1])
+        _check_rows("tokens", tokens, rows)
         tokens = tokens.contiguous()
     if top_k and (not 0 < top_k <= fo.FO_MAX_TOP_K or (top_k > logits.shape[-1] and logits.numel())):
         raise ValueError(f"top_k must be in 0..{min(fo.FO_MAX_TOP_K, logits.shape[-1])}, not {top_k}")
     if logits.requires_grad and torch.is_grad_enabled():
-        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, top_k, float(temperature), bool(entropy)))
-    return TokenLogprobs(*_logprobs(logits, tokens, top_k, float(temperature), entropy, None))
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, top_k, temperature, entropy, rows))
+    return TokenLogprobs(*_logprobs(logits, tokens, top_k, temperature, entropy, rows, False)[:4])
+
+
+def _distill(logits, ids, teacher, lse, weight, temperature, teacher_temperature, tail, with_stats, with_grad, out=None):
+    x = fo.logits_rows(logits, temperature)
+    dev, n = logits.device, x.rows
+    t = fo._teacher(ids, teacher, lse, n, teacher_temperature, tail, dev.index)
+    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
+    grad = to = stats = p_stats = None
+    if out is not None:
+        grad, to = out, fo._logits_grad(x, logits, out)
+    elif with_grad:
+        grad, to = _empty_grad(logits, x)
+    if with_stats:
+        stats = torch.empty((n, fo.FO_LOSS_STATS), dtype=torch.float32, device=dev)
+        p_stats = stats.data_ptr()
+    status = fo.lib().fo_distill(ctypes.byref(x), ctypes.byref(t),
+                                 fo._array(weight, "row_weight", torch.float32, n, dev.index), loss.data_ptr(), p_stats,
+                                 None if to is None else ctypes.byref(to), fo._stream(None))
+    if status:
+        fo._check("fo_distill", status)
+    return loss, grad, stats
 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, teacher, lse, temperature, teacher_temperature, tail):
-        rows, dev = logits.shape[:-1], logits.device
-        loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        stats = torch.empty(rows + (fo.FO_LOSS_STATS,), dtype=torch.float32, device=dev)
-        fo.fo_distill(logits, ids, teacher, lse, None, loss, stats, None, temperature, teacher_temperature, tail)
+        loss, _, stats = _distill(logits, ids, teacher, lse, None, temperature, teacher_temperature, tail, True, False)
         ctx.save_for_backward(logits, ids, teacher, lse, stats)
         ctx.how = (temperature, teacher_temperature, tail)
         return loss
@@ -129,9 +177,18 @@ class _Distill(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_loss):
         logits, ids, teacher, lse, stats = ctx.saved_tensors
-        grad = _aligned_like(logits)
+        temperature, teacher_temperature, tail = ctx.how
         with _on_device_of(logits):
-            fo.fo_distill_grad(logits, ids, teacher, stats, g_loss.contiguous(), grad, lse, *ctx.how)
+            x = fo.logits_rows(logits, temperature)
+            cur = logits.device.index
+            t = fo._teacher(ids, teacher, lse, x.rows, teacher_temperature, tail, cur)
+            grad, to = _empty_grad(logits, x)
+            g_loss = g_loss.contiguous()
+            status = fo.lib().fo_distill_grad(ctypes.byref(x), ctypes.byref(t), stats.data_ptr(),
+                                              fo._array(g_loss, "g_loss", torch.float32, x.rows, cur), ctypes.byref(to),
+                                              fo._stream(None))
+            if status:
+                fo._check("fo_distill_grad", status)
         return grad, None, None, None, None, None, None
 
 
@@ -159,14 +216,10 @@ def distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     one more outcome. Differentiable in ``logits``; no factor T^2 is applied.
     """
     _check_teacher(logits, teacher_ids, teacher_logits, teacher_lse)
-    ids, teacher = teacher_ids.contiguous(), teacher_logits.detach().contiguous()
-    lse = None if teacher_lse is None else teacher_lse.detach().contiguous()
-    how = (float(temperature), float(teacher_temperature), bool(tail))
+    ids, teacher, lse = teacher_ids.contiguous(), teacher_logits.detach().contiguous(), _dense(teacher_lse)
     if logits.requires_grad and torch.is_grad_enabled():
-        return _Distill.apply(logits, ids, teacher, lse, *how)
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    fo.fo_distill(logits, ids, teacher, lse, None, loss, None, None, *how)
-    return loss
+        return _Distill.apply(logits, ids, teacher, lse, temperature, teacher_temperature, tail)
+    return _distill(logits, ids, teacher, lse, None, temperature, teacher_temperature, tail, False, False)[0]
 
 
 def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, *,
@@ -182,8 +235,5 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
     """
     _check_teacher(logits, teacher_ids, teacher_logits, teacher_lse)
     _check_rows("row_weight", row_weight, logits.shape[:-1])
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    grad = _aligned_like(logits) if out is None else out
-    fo.fo_distill(logits, teacher_ids.contiguous(), teacher_logits.contiguous(), _dense(teacher_lse), _dense(row_weight),
-                  loss, None, grad, float(temperature), float(teacher_temperature), bool(tail))
-    return loss, grad
+    return _distill(logits, teacher_ids.contiguous(), teacher_logits.contiguous(), _dense(teacher_lse), _dense(row_weight),
+                    temperature, teacher_temperature, tail, False, True, out)[:2]
