@@ -554,11 +554,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
 
 // The gradient from saved statistics.
 template <class T, int kVecs>
-__global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillGradArgs a, int chunks)
+__global__ void __launch_bounds__(kGradThreads, 4) distill_grad_kernel(DistillGradArgs a, int chunks)
 {
     typedef typename T::raw raw;
     __shared__ int32_t ids[FO_MAX_TOP_K];
     __shared__ float qs[FO_MAX_TOP_K], sum_q;
+    __shared__ uint32_t taken[kVecs * kGradThreads * T::kPerVec / 32];   // a bit for each element of the chunk
     const int64_t r = blockIdx.x / (unsigned)chunks;
     const int v0 = (int)(blockIdx.x % (unsigned)chunks) * (kVecs * kGradThreads);
     const Row<T> row(a.in, r);
@@ -571,6 +572,8 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillGradA
         if (at < row.vecs)
             v[i] = load_vec(row, at);
     }
+    for (int i = tid; i < kVecs * kGradThreads * T::kPerVec / 32; i += kGradThreads)
+        taken[i] = 0;
     if (tid < 32) {
         const TeacherRow t = make_teacher(a.teacher, load_teacher(a.teacher, r), row.vocab);
 #pragma unroll
@@ -586,22 +589,28 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillGradA
     __syncthreads();
     const float inv_z = st.y == 0.0f ? 0.0f : 1.0f / st.y, scale = gl * a.in.inv_t;
     const bool zero = st.y == 0.0f;
-    bool entry = false;   // the first of equal ids takes the weight of all
-    float entry_value = 0.0f;
+    // this thread's entry, if its token is in the chunk
+    bool entry = false, again = false;
+    float q = 0.0f, x = 0.0f;
     if (!zero && tid < a.teacher.k) {
         const int32_t id = ids[tid];
-        if (id >= max(0, row.id(v0, 0)) && id < min(row.vocab, row.id(v0 + kVecs * kGradThreads, 0))) {
-            float q = 0.0f;
-            entry = true;
-            for (int i = 0; i < a.teacher.k; ++i)
-                if (ids[i] == id) {
-                    q += qs[i];
-                    entry = entry && i >= tid;
-                }
-            entry_value = grad_listed<T>(T::widen(row.x[id]), safe_max(st.x), q, sum_q, inv_z, scale, a.in);
+        entry = id >= max(0, row.id(v0, 0)) && id < min(row.vocab, row.id(v0 + kVecs * kGradThreads, 0));
+        if (entry) {
+            q = qs[tid];
+            x = T::widen(row.x[id]);
+            again = claim(taken, id - row.id(v0, 0));
         }
     }
-    __syncthreads();   // the entries' logits are read before a gradient in their place is written
+    // the entries' logits are read before a gradient in their place is written
+    if (__syncthreads_or(again) && entry) {   // rare: the first of equal ids takes the weight of all
+        q = 0.0f;
+        again = false;
+        for (int i = 0; i < a.teacher.k; ++i)
+            if (ids[i] == ids[tid]) {
+                q += qs[i];
+                again = again || i < tid;
+            }
+    }
     const bool aligned = same_phase(row, g);
     const f2 nm = splat(-safe_max(st.z)), f = splat(st.w * (scale / T::kShift));
 #pragma unroll
@@ -616,8 +625,8 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillGradA
             store_edge<T>(g, row, at, d);
     }
     __syncthreads();
-    if (entry)
-        g[ids[tid]] = T::narrow(entry_value);
+    if (entry && !again)
+        g[ids[tid]] = T::narrow(grad_listed<T>(x, safe_max(st.x), q, sum_q, inv_z, scale, a.in));
 }
 
 template <class T>

@@ -369,7 +369,9 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGrad
 {
     typedef typename T::raw raw;
     __shared__ int64_t ids[FO_MAX_TOP_K + 1];
-    __shared__ float weight[FO_MAX_TOP_K + 1];
+    __shared__ float weight[FO_MAX_TOP_K + 1], sum_weight;
+    __shared__ bool any_weight;
+    __shared__ uint32_t taken[kVecs * kGradThreads * T::kPerVec / 32];   // a bit for each element of the chunk
     const int64_t r = blockIdx.x / (unsigned)chunks;
     const int v0 = (int)(blockIdx.x % (unsigned)chunks) * (kVecs * kGradThreads);
     const Row<T> row(a.in, r);
@@ -390,38 +392,54 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGrad
         ids[tid] = i < 0 ? (a.g_logp ? a.tokens[r] : -1) : a.top_ids[r * a.k + i];
         weight[tid] = i < 0 ? (a.g_logp ? a.g_logp[r] : 0.0f) : a.g_top[r * a.k + i];
     }
+    for (int i = tid; i < kVecs * kGradThreads * T::kPerVec / 32; i += kGradThreads)
+        taken[i] = 0;
     __syncthreads();
-    float sum = 0.0f;
-    bool any = h != 0.0f;
-    for (int i = 0; i <= a.k; ++i) {
-        if (ids[i] < 0 || weight[i] == 0.0f)
-            continue;
-        any = true;
-        sum += ids[i] >= row.vocab ? __int_as_float(0x7fffffff) : weight[i];
+    // the sum of the weights; NaN where an id is out of range
+    if (tid < 32) {
+        float part = 0.0f;
+        bool any = false;
+        for (int i = tid; i <= a.k; i += 32)
+            if (ids[i] >= 0 && weight[i] != 0.0f) {
+                any = true;
+                part += ids[i] >= row.vocab ? __int_as_float(0x7fffffff) : weight[i];
+            }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            part += __shfl_xor_sync(~0u, part, o);
+        any = __any_sync(~0u, any);
+        if (tid == 0) {
+            sum_weight = part;
+            any_weight = any;
+        }
     }
-    const bool zero = !any || st.y == 0.0f;
+    // this thread's entry, if its token is in the chunk
+    bool entry = false, again = false;
+    float w = 0.0f, x_entry = 0.0f;
+    if (tid <= a.k) {
+        const int64_t id = ids[tid];
+        entry = id >= max(0, row.id(v0, 0)) && id < min(row.vocab, row.id(v0 + kVecs * kGradThreads, 0));
+        if (entry) {
+            w = weight[tid];
+            x_entry = T::widen(row.x[id]);
+            again = claim(taken, (int)id - row.id(v0, 0));
+        }
+    }
+    // the entries' logits are read before a gradient in their place is written
+    if (__syncthreads_or(again) && entry) {   // the first of equal ids takes the weight of all
+        w = 0.0f;
+        again = false;
+        for (int i = 0; i <= a.k; ++i)
+            if (ids[i] == ids[tid]) {
+                w += weight[i];
+                again = again || i < tid;
+            }
+    }
+    const float sum = sum_weight;
+    const bool zero = (!any_weight && h == 0.0f) || st.y == 0.0f;
     const float p_scale = inv_z * (a.in.inv_t / T::kShift);
     const float alpha = h == 0.0f ? -p_scale * sum : -p_scale * (sum + h * (st.z - ln_z));
     const float beta = h == 0.0f ? 0.0f : -p_scale * h * kLn2;
-
-    // the entries of this chunk; the first of equal ids takes the weight of all
-    const int end = row.id(v0 + kVecs * kGradThreads, 0);
-    bool entry = false;
-    float entry_value = 0.0f;
-    if (!zero && tid <= a.k && ids[tid] >= 0 && ids[tid] >= row.id(v0, 0) && ids[tid] < end && ids[tid] < row.vocab) {
-        float w = 0.0f;
-        int first = tid;
-        for (int i = a.k; i >= 0; --i)
-            if (ids[i] == ids[tid]) {
-                w += weight[i];
-                first = i;
-            }
-        entry = first == tid;
-        float t;
-        const float e = grad_exp<T>(distance(T::widen(row.x[ids[tid]]), m, a.in), a.in, t);
-        entry_value = __fmaf_rn(w, a.in.inv_t, e * __fmaf_rn(beta, t, alpha));
-    }
-    __syncthreads();   // the entries' logits are read before a gradient in their place is written
     const bool aligned = same_phase(row, g);
     const f2 nm = splat(-m), al = splat(alpha), be = splat(beta);
 #pragma unroll
@@ -446,8 +464,11 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGrad
             store_edge<T>(g, row, at, d);
     }
     __syncthreads();
-    if (entry)
-        g[ids[tid]] = T::narrow(entry_value);
+    if (entry && !again && !zero) {
+        float t;
+        const float e = grad_exp<T>(distance(x_entry, m, a.in), a.in, t);
+        g[ids[tid]] = T::narrow(__fmaf_rn(w, a.in.inv_t, e * __fmaf_rn(beta, t, alpha)));
+    }
 }
 
 template <class T, int kN>

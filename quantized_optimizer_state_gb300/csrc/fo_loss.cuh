@@ -597,6 +597,9 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 
 // --- gradients -----------------------------------------------------------------
 
+// Sets bit `at`; whether it was set before.
+__device__ __forceinline__ bool claim(uint32_t *bits, int at) { return atomicOr(bits + at / 32, 1u << at % 32) >> at % 32 & 1; }
+
 // Element e of a stored vector goes to its place in the gradient's row.
 template <class T>
 __device__ __forceinline__ void store_edge(typename T::raw *g, const Row<T> &row, int i, const uint4 &v)
