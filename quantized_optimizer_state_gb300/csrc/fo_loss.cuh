@@ -141,8 +141,7 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// The same with the id below it: larger keys come first, no two are equal.
-__device__ __forceinline__ uint64_t entry_key(float v, uint32_t id) { return ((uint64_t)order_key(v) << 32) | (0xffffffffu - id); }
+// The id of an entry's key: order_key above, the complement of the id below it.
 __device__ __forceinline__ uint32_t entry_id(uint64_t key) { return 0xffffffffu - (uint32_t)key; }
 
 // The maximum to subtract: 0 for a row that is all -inf, so that x - m is
@@ -158,14 +157,6 @@ __device__ __forceinline__ float quarter_distance(float x, float m) { return __f
 __device__ __forceinline__ float log_prob(float x, float m, float z, float ln_z, float inv_t)
 {
     return z == 0.0f ? -kInf : __fmaf_rn(quarter_distance(x, m), 4.0f * inv_t, -ln_z);
-}
-
-__device__ __forceinline__ float load_dtype(const void *p, int64_t i, int dtype)
-{
-    if (dtype == 1)
-        return static_cast<const float *>(p)[i];
-    const uint16_t v = static_cast<const uint16_t *>(p)[i];
-    return dtype == 0 ? Bf16::widen(v) : F16::widen(v);
 }
 
 // --- a row, in 16-byte vectors -------------------------------------------------
@@ -299,17 +290,6 @@ __device__ __forceinline__ void rescale(Stat &s, float m, const LogitRows &in)
         s.w = __fmul_rn(__fmaf_rn(t, s.z, s.w), f);
     s.z = __fmul_rn(s.z, f);
     s.m = m;
-}
-
-template <bool kEntropy>
-__device__ __forceinline__ Stat join(Stat a, Stat b, const LogitRows &in)
-{
-    const float m = fmaxf(a.m, b.m);
-    if (m != -kInf) {   // else both are empty, or all -inf: nothing to scale
-        rescale<kEntropy>(a, m, in);
-        rescale<kEntropy>(b, m, in);
-    }
-    return Stat{m, a.z + b.z, kEntropy ? a.w + b.w : 0.0f};
 }
 
 // Over the first `n` lanes of a warp (a power of two), in every lane of them.

@@ -330,3 +330,18 @@ def test_a_teacher_that_is_not_a_number():
         loss, g = losses.distill_loss_grad(x, ids, y, tail=tail, teacher_lse=lse if tail else None)
         assert loss.isnan().tolist() == [False, True, False, True]
         assert g[1].isnan().all() and g[3].isnan().all() and torch.isfinite(g[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_lists_with_tokens_listed_twice(dtype):
+    """128 ids, some of them twice or three times, close together and far apart in the list; a row a CTA."""
+    n, v = 600, 5003
+    x = make(n, v, dtype, seed=8)
+    ids, y, _ = make_teacher(n, v, 128, seed=8, short=False)
+    for r, (to, of) in enumerate([(slice(96, 128), slice(0, 32)), (40, 3), (slice(1, 128, 2), slice(0, 128, 2)),
+                                  ([10, 42, 74, 106], [10] * 4), ([32, 64], [0, 0]), (33, 32)]):
+        ids[r::7, to] = ids[r::7, of].clone()
+    x.scatter_(1, ids.clamp(min=0).long(), torch.full_like(y, 16.0).to(dtype))     # a listed token weighs as much as all others
+    lse = torch.logsumexp(y, 1) + 0.2
+    check(x, ids, y)
+    check(x, ids, y, lse, tail=True)
