@@ -13,9 +13,12 @@
  *     elements with one FP16 scale per group;
  *   - the fused step (section "融合优化器步骤", Algorithm 4): dequantize m
  *     and v, rebuild theta, apply the standard AdamW / SGD / Lion update,
- *     requantize m and v and re-split theta, in one pass over memory.
+ *     requantize m and v and re-split theta, in one pass over memory;
  *
- * Exact arithmetic contract (what every entry point computes, bit for bit):
+ * and the losses on a language model's logits whose gradients that step
+ * consumes (last section, with rules of their own on accuracy and alignment).
+ *
+ * Exact arithmetic contract of the step and its codecs (bit for bit):
  *   theta' = BF16(theta), round to nearest even.
  *   h      = half the BF16 gap between theta' and its neighbour on theta's
  *            side (the usual ULP/2, halved again just below a power of two).
@@ -49,8 +52,8 @@
  * of the largest table seen), kept until the thread exits; nothing else
  * persists between calls.
  *
- * Layout: element arrays are contiguous, one element per entry; each array
- * must start on a 16-byte boundary. Scale arrays hold ceil(numel/32) FP16
+ * Layout of the step and its codecs: element arrays are contiguous, one element
+ * per entry; each array must start on a 16-byte boundary. Scale arrays hold ceil(numel/32) FP16
  * values (any 2-byte alignment); group k covers elements [32k, 32k+32) of its
  * tensor and the last group of a tensor may be partial.
  *
@@ -292,10 +295,13 @@ fo_status_t fo_verify_fast_arithmetic(uint64_t *counts, fo_stream_t stream);
  *   - fo_distill: KL(q || p) for a teacher distribution q known by its top
  *     logits, optionally with its gradient in the same pass, and
  *     fo_distill_grad, the gradient alone.
- * Accuracy: statistics and sums are FP32 (one exponential is within 3 ulp, a
- * sum of a row within a few ulp of its own size); a gradient is rounded once,
- * to the logits' type. Every result is the same bit for bit on every run: no
- * atomics join partial sums.
+ * Arrays need the alignment of their element type only, stats that of 16
+ * bytes. Nothing here needs a workspace.
+ * Accuracy: statistics and sums are FP32. An exponential of (x - m) / T is
+ * within 2^-22 plus 3 roundings of its argument, relatively, and a row's sum is
+ * of short chains of them; a gradient is rounded once, to the logits' type.
+ * Every result is the same bit for bit on every run with the same arrays at
+ * the same addresses modulo 16: no atomics join partial sums.
  * Rules for masked and special values, in every call:
  *   - a logit of -inf has probability 0, as has one of the type's lowest value
  *     beside ordinary ones; a row whose every logit is -inf has no
@@ -398,7 +404,8 @@ fo_status_t fo_token_logprobs_grad(const fo_logits_t *logits, const int64_t *tok
 /*
  * fo_distill -- loss[r] = w[r] KL(q_r || p_r), w = row_weight or 1 where that
  * is NULL. With `grad`, also the gradient of sum_r loss[r] with respect to the
- * logits, in one pass: the logits are read once from device memory. stats
+ * logits, in the same call: the logits come from device memory once (a second
+ * time from the L2 cache) and the gradient goes there once. stats
  * [rows, FO_LOSS_STATS], optional, is what fo_distill_grad needs (of rows with
  * weight 0 it is not written). `loss` and `grad` may each be NULL.
  * Errors as fo_token_logprobs.

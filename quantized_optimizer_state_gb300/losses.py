@@ -8,9 +8,10 @@ library's kernels: what stands between a model's head and the optimizers of
 * :func:`distill_loss` -- KL divergence from a teacher known by its top
   logits; differentiable;
 * :func:`distill_loss_grad` -- the same loss with its gradient in one call: the
-  logits are read once and the gradient written once, where loss and backward
-  pass read them twice. For training loops that know the weight of each row
-  beforehand: ``loss, grad = distill_loss_grad(...); logits.backward(grad)``.
+  logits come from device memory once and the gradient goes there once, where
+  loss and backward pass fetch them twice. For training loops that know the
+  weight of each row beforehand:
+  ``loss, grad = distill_loss_grad(...); logits.backward(grad)``.
 
 Logits are bfloat16, float16 or float32 CUDA tensors ``[..., vocab]`` whose
 last dimension is contiguous; a slice like ``logits[:, :-1]`` is read where it
@@ -227,10 +228,10 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
                       teacher_temperature: float = 1.0, tail: bool = False,
                       teacher_lse: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
     """``(loss, grad)``: ``loss = row_weight * distill_loss(...)`` by position and
-    the gradient of its sum with respect to the logits, in one pass.
+    the gradient of its sum with respect to the logits, in one call.
 
     ``row_weight`` (float32, 1 where None): for a mean over n tokens 1 / n, and
-    0 for padding, whose logits are then not read. ``out``: where to write the
+    0 for padding, whatever its logits hold. ``out``: where to write the
     gradient; it may be ``logits`` itself, which the gradient then replaces.
     """
     _check_teacher(logits, teacher_ids, teacher_logits, teacher_lse)
