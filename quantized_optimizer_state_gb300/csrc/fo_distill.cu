@@ -29,6 +29,8 @@ constexpr int kMaxRowsEach = 2;
 constexpr int64_t kCacheBytes = 80 << 20;
 constexpr int64_t kMaxPart = 128 * 1024;          // bytes of a part: its marks are a 16th of that
 constexpr int kGradThreads = 256;
+constexpr float kLn2High = 0x1.62e4p-1f;          // 15 bits of ln 2
+constexpr float kLn2Low = (float)(0.69314718055994531 - 0x1.62e4p-1);
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -435,11 +437,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
                 barrier_arrive(&sh.joined);
             }
             if (writes) {
-                // KL = sum q ln q - sum q s + (sum q) ln Z, and the rest's term
+                // KL = sum q ln q - sum q s + (sum q) ln Z, and the rest's
+                // term. ln Z is taken as its power of two, whose product with
+                // the upper bits of ln 2 is exact, and a part below 0.41: it
+                // cancels most of sum q s, and a rounding of ln Z itself would
+                // show in a small loss.
                 const float ln_z = logf(z), four = 4.0f * a.in.inv_t;
                 float kl = ql;
-                if (l.q != 0.0f)
-                    kl = __fmaf_rn(-four, __fmaf_rn(l.q, quarter_distance(l.m == -kInf ? 0.0f : l.m, m), l.dot), __fmaf_rn(l.q, ln_z, kl));
+                if (l.q != 0.0f) {
+                    const int k = z > 0.0f && z < kInf ? ilogbf(z * 1.41421356f) : 0;
+                    const float low = __fmaf_rn((float)k, kLn2Low, logf(ldexpf(z, -k)));
+                    const float qs = four * __fmaf_rn(l.q, quarter_distance(l.m == -kInf ? 0.0f : l.m, m), l.dot);
+                    kl = __fadd_rn(__fmaf_rn(l.q, (float)k * kLn2High, -qs), __fmaf_rn(l.q, low, kl));
+                }
                 if (z == 0.0f && sum != 0.0f)
                     kl = kInf;
                 if (kTail && q_rest > 0.0f)
@@ -520,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillAr
                         const uint32_t mask = kTail ? mark_bytes[i0 + j * kStream + tid] : 0u;
                         if (kTail && mask)
                             v[j] = without<T>(v[j], mask);
-                        run.add(v[j], a.in);
                     }
+                    run.add(v, a.in);
                 } else
                     for (int i = tid; i < p.n - i0; i += kStream)
                         run.add(without<T>(stage[i], kTail ? mark_bytes[i0 + i] : 0u), a.in);

@@ -346,9 +346,7 @@ __global__ void __launch_bounds__(kN, 1280 / kN) logprobs_kernel(LogprobArgs a)
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
                 v[j] = __ldcs(row.vec(i + j * kN));
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                run.add(v[j], a.in);
+            run.add(v, a.in);
         } else {
 #pragma unroll 1
             for (int j = 0; j < kGroup; ++j)

@@ -370,48 +370,70 @@ struct Running {
         floor_ = Largest<T>::bound(low);
     }
 
+    // Vectors at a time: one look at the reference for all, and their sum is
+    // formed first, so that the chains of additions into z and w stay short.
+    template <int N>
+    __device__ __forceinline__ void add(const uint4 (&v)[N], const LogitRows &in)
+    {
+        Largest<T> most = Largest<T>::of(v[0]);
+#pragma unroll
+        for (int j = 1; j < N; ++j)
+            most = most.with(Largest<T>::of(v[j]));
+        top = top.with(most);
+        if (most.above(limit))
+            move(in);
+        constexpr int kPairs = T::kPerVec / 2;
+        f2 sums[N], weighted = 0;
+        const f2 c = splat(in.c), r = splat(-ref);
+        const float at = safe_max(m);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            f2 x[kPairs], e[kPairs];
+            float a, b;
+            if (!careful) {
+                if (kEntropy)
+                    widen_vec<T>(raise<T>(v[j], floor_), x);
+                else
+                    widen_vec<T>(v[j], x);
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i)
+                    x[i] = fma2(x[i], c, r);
+            } else {
+                widen_vec<T>(v[j], x);
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    unpk(x[i], a, b);
+                    x[i] = pk(__fmul_rn(distance(a, at, in), in.c), __fmul_rn(distance(b, at, in), in.c));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                unpk(x[i], a, b);
+                e[i] = pk(exp2_approx(a), exp2_approx(b));
+                if (kEntropy)
+                    weighted = fma2(e[i], x[i], weighted);
+            }
+#pragma unroll
+            for (int n = kPairs / 2; n; n >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+                    e[i] = add2(e[i], e[i + n]);
+            sums[j] = e[0];
+        }
+#pragma unroll
+        for (int n = N / 2; n; n >>= 1)
+#pragma unroll
+            for (int j = 0; j < n; ++j)
+                sums[j] = add2(sums[j], sums[j + n]);
+        z = add2(z, sums[0]);
+        if (kEntropy)
+            w = add2(w, weighted);
+    }
+
     __device__ __forceinline__ void add(const uint4 &v, const LogitRows &in)
     {
-        const Largest<T> vt = Largest<T>::of(v);
-        top = top.with(vt);
-        if (vt.above(limit))
-            move(in);
-        f2 x[T::kPerVec / 2], e[T::kPerVec / 2];
-        float a, b;
-        if (!careful) {
-            const f2 c = splat(in.c), r = splat(-ref);
-            if (kEntropy)
-                widen_vec<T>(raise<T>(v, floor_), x);
-            else
-                widen_vec<T>(v, x);
-#pragma unroll
-            for (int i = 0; i < T::kPerVec / 2; ++i) {
-                const f2 t = fma2(x[i], c, r);
-                unpk(t, a, b);
-                e[i] = pk(exp2_approx(a), exp2_approx(b));
-                if (kEntropy)
-                    w = fma2(e[i], t, w);
-            }
-        } else {
-            const float at = safe_max(m);
-            widen_vec<T>(v, x);
-#pragma unroll
-            for (int i = 0; i < T::kPerVec / 2; ++i) {
-                unpk(x[i], a, b);
-                const f2 t = pk(__fmul_rn(distance(a, at, in), in.c), __fmul_rn(distance(b, at, in), in.c));
-                unpk(t, a, b);
-                e[i] = pk(exp2_approx(a), exp2_approx(b));
-                if (kEntropy)
-                    w = fma2(e[i], t, w);
-            }
-        }
-        // the vector's sum first: chains of additions stay short
-#pragma unroll
-        for (int n = T::kPerVec / 4; n; n >>= 1)
-#pragma unroll
-            for (int i = 0; i < n; ++i)
-                e[i] = add2(e[i], e[i + n]);
-        z = add2(z, e[0]);
+        const uint4 one[1] = {v};
+        add(one, in);
     }
 
     __device__ __forceinline__ Stat stat(const LogitRows &in) const
