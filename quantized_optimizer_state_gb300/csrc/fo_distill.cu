@@ -16,17 +16,15 @@ namespace {
 // against 1, 4 and 8: 700 / 345 / 203 against 757 / 343 / 204, 709 / 358 / 203
 // and 749 / 358 / 202: the fetching runs on into the second row, and short
 // turns spread the end of the grid. (Listed tokens were dearer then.)
-constexpr int kWarps = 8;                         // that walk over a row
-constexpr int kStream = kWarps * 32;
-constexpr int kFetcher = kWarps, kTeacher = kWarps + 1;   // and two more: see distill_kernel
-constexpr int kThreads = kStream + 64;
-constexpr int kStageVecs = 4 * kStream;           // vectors that are copied at once (16 KB)
-constexpr int kStages = 4;                        // such copies in flight or in use
-constexpr int kCtasPerSm = 3;
+constexpr int kLong = 8, kShort = 2;              // warps that walk over a row: see launch
+constexpr int kStages = 4;                        // copies of four vectors a thread, in flight or in use
+constexpr int kCtasPerSm = 3;                     // of kLong warps; of kShort ones kShortPerSm
+constexpr int kShortPerSm = 8;
 constexpr int kMaxRowsEach = 2;
 // Of the 129 MB L2 cache, for rows between their passes. 116 MB is slower (877
 // against 761 us on the first case above), 60 MB the same.
 constexpr int64_t kCacheBytes = 80 << 20;
+constexpr int64_t kShortRow = 32 * 1024;
 constexpr int64_t kMaxPart = 128 * 1024;          // bytes of a part: its marks are a 16th of that
 constexpr int kGradThreads = 256;
 constexpr float kLn2High = 0x1.62e4p-1f;          // 15 bits of ln 2
@@ -167,7 +165,7 @@ struct Shared {
     uint64_t cluster[2];                                      // all CTAs' sums have come
     float4 sums[2][kMaxCluster];                              // written by each CTA into all: listed m, z, q, dot,
     float2 rests[2][kMaxCluster];                             // and the streamed m, z
-    float2 part[kWarps];                                      // m, z of the warps
+    float2 part[kLong];                                       // m, z of the warps
     float m, f;                                               // the gradient: f 2^((x - m) c)
     __align__(16) int32_t ids[FO_MAX_TOP_K];
     float q[FO_MAX_TOP_K];
@@ -254,10 +252,12 @@ __device__ __forceinline__ uint32_t merge_twice(Shared &sh, const TeacherRow &t,
 // not listed: 1 - sum p would lose a small rest. That sum also keeps a
 // reference of its own: it may lie further below the listed logits than FP32's
 // exponents reach.
-template <class T, bool kTail>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) distill_kernel(DistillArgs a)
+template <class T, bool kTail, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm : kShortPerSm) distill_kernel(DistillArgs a)
 {
     typedef typename T::raw raw;
+    constexpr int kStream = kWarps * 32, kFetcher = kWarps, kTeacher = kWarps + 1, kThreads = kStream + 64;
+    constexpr int kStageVecs = 4 * kStream;   // vectors that are copied at once
     extern __shared__ __align__(16) unsigned char dynamic[];
     __shared__ __align__(16) Shared sh;
     const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -660,28 +660,44 @@ __global__ void __launch_bounds__(kGradThreads, 4) distill_grad_kernel(DistillGr
         g[ids[tid]] = T::narrow(grad_listed<T>(x, safe_max(st.x), q, sum_q, inv_z, scale, a.in));
 }
 
-template <class T>
-cudaError_t launch(const DistillArgs &args, cudaStream_t stream)
+template <class T, int kWarps>
+cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream_t stream)
 {
-    DistillArgs a = args;
+    const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
+    a.mark_words = marks ? (int)(vecs + 3) / 4 : 0;
+    // a few rows one after the other, where there are many
+    a.rows_each = (int)std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
+    const int64_t clusters = (a.in.rows + a.rows_each - 1) / a.rows_each;
+    const size_t shared = (size_t)kStages * 4 * kWarps * 32 * 16 + (size_t)a.mark_words * 4;
+    const int threads = kWarps * 32 + 64;
+    if (a.teacher.tail)
+        return launch_cluster(distill_kernel<T, true, kWarps>, a, clusters, size, shared, threads, stream);
+    return launch_cluster(distill_kernel<T, false, kWarps>, a, clusters, size, shared, threads, stream);
+}
+
+template <class T>
+cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
+{
     const bool marks = a.teacher.tail || a.grad.data;
-    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * kCtasPerSm;
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw);
+    // Many rows too short for eight warps, each by two: the steps between the
+    // passes are what a short row takes its time for, and more of them overlap.
+    // Loss with gradient, BF16, 8 ids, 8 warps against 2 (us): 16384 x 1000
+    // 138 / 56, 4096 x 8192 48 / 35, 8192 x 16000 119 / 105, 8192 x 32000
+    // 174 / 210.
+    int64_t ctas = (int64_t)sm_count() * kShortPerSm;
+    if (bytes <= kShortRow && a.in.rows >= ctas)
+        return launch<T, kShort>(a, 1, marks, ctas, stream);
     // one CTA a row, or a cluster that shares it: while the rows at work at
     // once would not stay in the L2 cache between the passes, while a part's
     // marks would take a CTA's place on the SM, and while the grid would leave
     // SMs short of CTAs
+    ctas = (int64_t)sm_count() * kCtasPerSm;
     int size = 1;
     while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (marks && bytes > size * kMaxPart) ||
                                   (a.in.rows * size < ctas && bytes > size * 8192)))
         size *= 2;
-    // a few rows one after the other, where there are many
-    a.rows_each = (int)std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
-    const int64_t clusters = (a.in.rows + a.rows_each - 1) / a.rows_each;
-    a.mark_words = marks ? (int)(part_vecs(bytes, size) + 3) / 4 : 0;
-    const size_t shared = (size_t)kStages * kStageVecs * 16 + (size_t)a.mark_words * 4;
-    if (a.teacher.tail)
-        return launch_cluster(distill_kernel<T, true>, a, clusters, size, shared, kThreads, stream);
-    return launch_cluster(distill_kernel<T, false>, a, clusters, size, shared, kThreads, stream);
+    return launch<T, kLong>(a, size, marks, ctas, stream);
 }
 
 template <class T>
