@@ -9,6 +9,8 @@ constexpr int kGradThreads = 256;
 constexpr int kWide = 256, kMiddle = 128, kNarrow = 64;   // threads to a row: see launch
 constexpr int kGroup = 4;                      // vectors of a thread that one maximum is kept for
 constexpr int kCtasPerSm = 4;
+constexpr int kThreadsPerSm = 1280;
+constexpr int kAheadBytes = 128;               // for each thread of a row: see logprobs_kernel
 
 // What the kN threads of a row share.
 template <int kN>
@@ -22,7 +24,7 @@ struct Shared {
     uint2 range[kN / 32];
     int counts[2][kN / 32];
     int group[kGroups];
-    uint64_t list[kCandidates];               // candidates in any order; later the lists of the other CTAs
+    __align__(16) uint64_t list[kCandidates]; // candidates in any order; later the lists of the other CTAs
     uint64_t sorted[FO_MAX_TOP_K];            // this CTA's largest, descending
     int sorted_n;
 };
@@ -169,6 +171,37 @@ __device__ __forceinline__ uint32_t kth_key(uint32_t mine, int k, Shared<kN> &sh
     return bound;
 }
 
+// A value that all elements with keys from `bound` on reach, NaN counting as
+// the largest: !(x < floor). Where no number is it, a few more reach it.
+__device__ __forceinline__ float key_floor(uint32_t bound)
+{
+    bound = min(bound, 0xff800000u);   // +inf
+    return bound <= 0x007fffffu ? -kInf : __uint_as_float(bound & 0x80000000u ? bound & 0x7fffffffu : ~bound);
+}
+
+// A bit for each element of vector i that reaches the floor.
+template <class T>
+__device__ __forceinline__ uint32_t reached(const Row<T> &row, int i, const uint4 &v, float floor_)
+{
+    const typename T::raw *e = reinterpret_cast<const typename T::raw *>(&v);
+    uint32_t found = 0;
+#pragma unroll
+    for (int k = 0; k < T::kPerVec; ++k)
+        found |= T::widen(e[k]) < floor_ ? 0u : 1u << k;
+    const int lo = max(0, -row.id(i, 0)), hi = min(T::kPerVec, row.vocab - row.id(i, 0));
+    return found & ((1u << hi) - (1u << lo));
+}
+
+// Element k of a vector, k not known when it is compiled.
+template <class T>
+__device__ __forceinline__ float element(const uint4 &v, int k)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int at = k * 4 / T::kPerVec;
+    const uint32_t word = at == 0 ? w[0] : at == 1 ? w[1] : at == 2 ? w[2] : w[3];
+    return sizeof(typename T::raw) == 4 ? __uint_as_float(word) : T::widen((typename T::raw)(word >> k % 2 * 16));
+}
+
 // The part's largest elements (k, or all where it has fewer), descending, into
 // sh.sorted. `mine` is the key of the largest element of this thread (0
 // without elements): the k-th largest of the threads' maxima bounds the k-th
@@ -182,10 +215,11 @@ __device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const
     if (threadIdx.x == 0)
         sh.count = sh.groups = 0;
     const uint32_t bound = kth_key<kN>(mine, k, sh);
+    const float floor_ = key_floor(bound);
     if (mine >= bound)
         for (int i = threadIdx.x; i < p.n; i += kGroup * kN) {
             const int at = i / (kGroup * kN) * kN + (int)threadIdx.x;
-            if (largest_key(maxima[at]) >= bound) {
+            if (!(maxima[at].value_nan() < floor_)) {
                 const int n = atomicAdd(&sh.groups, 1);
                 if (n < Shared<kN>::kGroups)
                     sh.group[n] = at;
@@ -194,21 +228,28 @@ __device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const
     barrier_among<kN>();
     const int groups = sh.groups;
     if (groups <= Shared<kN>::kGroups)
-        for (int j = threadIdx.x; j < groups * kGroup; j += kN) {
-            const int at = sh.group[j / kGroup];
-            const int i = at / kN * (kGroup * kN) + j % kGroup * kN + at % kN;
-            if (i >= p.n || *(volatile int *)&sh.count > Shared<kN>::kCandidates)
-                continue;
-            const uint4 v = load_vec(row, p.v0 + i);
-            if (largest_key(Largest<T>::of(v)) < bound)
-                continue;
-            each<T>(row, p.v0 + i, v, [&](uint32_t key, int id) {
-                if (key >= bound) {
-                    const int n = atomicAdd(&sh.count, 1);
-                    if (n < Shared<kN>::kCandidates)
-                        sh.list[n] = list_key(key, id);
+        for (int j = threadIdx.x; j < groups; j += kN) {
+            if (*(volatile int *)&sh.count > Shared<kN>::kCandidates)
+                break;
+            const int at = sh.group[j], i = at / kN * (kGroup * kN) + at % kN;
+            uint4 v[kGroup];
+#pragma unroll
+            for (int q = 0; q < kGroup; ++q)
+                if (i + q * kN < p.n)
+                    v[q] = load_vec(row, p.v0 + i + q * kN);
+            uint32_t found = 0;
+#pragma unroll
+            for (int q = 0; q < kGroup; ++q)
+                if (i + q * kN < p.n)
+                    found |= reached<T>(row, p.v0 + i + q * kN, v[q], floor_) << q * T::kPerVec;
+            int n = found ? atomicAdd(&sh.count, __popc(found)) : 0;
+            for (; found; found &= found - 1, ++n) {
+                const int b = __ffs((int)found) - 1, q = b / T::kPerVec;
+                if (n < Shared<kN>::kCandidates) {
+                    const uint4 w = q == 0 ? v[0] : q == 1 ? v[1] : q == 2 ? v[2] : v[3];
+                    sh.list[n] = list_key(order_key(element<T>(w, b % T::kPerVec)), row.id(p.v0 + i + q * kN, b % T::kPerVec));
                 }
-            });
+            }
         }
     barrier_among<kN>();
     if (groups > Shared<kN>::kGroups || sh.count > Shared<kN>::kCandidates) {
@@ -219,9 +260,12 @@ __device__ __forceinline__ void find_top(const Row<T> &row, const Part &p, const
     for (int i = threadIdx.x; i < n; i += kN) {   // no two keys are equal
         const uint64_t key = sh.list[i];
         int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j)
-            rank += sh.list[j] > key;
+#pragma unroll 2
+        for (int j = 0; j + 1 < n; j += 2) {
+            const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&sh.list[j]);
+            rank += (two.x > key) + (two.y > key);
+        }
+        rank += n % 2 && sh.list[n - 1] > key;
         if (rank < k)
             sh.sorted[rank] = key;
     }
@@ -302,6 +346,15 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t r, const Ro
     }
 }
 
+// Starts the way of a row's first bytes into the L2 cache.
+template <class T>
+__device__ __forceinline__ void fetch_ahead(const Row<T> &row, int bytes)
+{
+    const int n = min(row.full1 - row.full0, bytes / 16);
+    if (n > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row.vec(row.full0)), "r"(n * 16) : "memory");
+}
+
 // The given token's logit, on its way while the row is walked over.
 template <class T>
 __device__ __forceinline__ float load_token(const LogprobArgs &a, int64_t r, const Row<T> &row, int64_t &token)
@@ -323,7 +376,7 @@ __device__ __forceinline__ float load_token(const LogprobArgs &a, int64_t r, con
 // ring that run ahead into the next row were slower (206 and 147 us): the same
 // warps finish the row, and fewer of them fit.
 template <class T, int kN>
-__global__ void __launch_bounds__(kN, 1280 / kN) logprobs_kernel(LogprobArgs a)
+__global__ void __launch_bounds__(kN, kThreadsPerSm / kN) logprobs_kernel(LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char dynamic[];
     Largest<T> *const maxima = reinterpret_cast<Largest<T> *>(dynamic);
@@ -357,6 +410,8 @@ __global__ void __launch_bounds__(kN, 1280 / kN) logprobs_kernel(LogprobArgs a)
             maxima[i0 / kGroup + tid] = run.top;
         run.top = run.top.with(before);
     }
+    if (a.ahead && tid == 0 && r + a.ahead < a.in.rows)
+        fetch_ahead(Row<T>(a.in, r + a.ahead), kN * kAheadBytes);
     finish<T, kN>(a, r, row, p, run, maxima, token, token_x, sh);
     if (size > 1) {   // no CTA leaves while another reads its shared memory
         cluster_arrive();
@@ -477,8 +532,9 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGrad
 }
 
 template <class T, int kN>
-cudaError_t launch(const LogprobArgs &a, int size, cudaStream_t stream)
+cudaError_t launch(LogprobArgs a, int size, cudaStream_t stream)
 {
+    a.ahead = a.k && size == 1 ? sm_count() * (kThreadsPerSm / kN) : 0;
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     const int64_t groups = (vecs + kGroup * kN - 1) / (kGroup * kN);
     return launch_cluster(logprobs_kernel<T, kN>, a, a.in.rows, size, a.k ? groups * kN * 4 : 0, kN, stream);

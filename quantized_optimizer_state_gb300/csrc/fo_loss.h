@@ -36,6 +36,7 @@ struct LogprobArgs {
     int32_t *top_ids;        // [rows, k]
     float *top_logp;
     float4 *stats;           // may be null
+    int32_t ahead;           // set by the launch (fo_logprobs.cu)
 };
 
 struct LogprobGradArgs {
