@@ -26,6 +26,7 @@ constexpr int kMaxRowsEach = 2;
 constexpr int64_t kCacheBytes = 80 << 20;
 constexpr int64_t kShortRow = 32 * 1024;
 constexpr int64_t kMaxPart = 128 * 1024;          // bytes of a part: its marks are a 16th of that
+constexpr int64_t kMinPart = 16 * 1024;           // bytes of a row that are worth a CTA of their own
 constexpr int kGradThreads = 256;
 constexpr float kLn2High = 0x1.62e4p-1f;          // 15 bits of ln 2
 constexpr float kLn2Low = (float)(0.69314718055994531 - 0x1.62e4p-1);
@@ -690,12 +691,14 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
         return launch<T, kShort>(a, 1, marks, ctas, stream);
     // one CTA a row, or a cluster that shares it: while the rows at work at
     // once would not stay in the L2 cache between the passes, while a part's
-    // marks would take a CTA's place on the SM, and while the grid would leave
-    // SMs short of CTAs
+    // marks would take a CTA's place on the SM, and until half of the CTAs that
+    // fit are there (all of them measured slower: a second set of clusters
+    // waits for the first; loss with gradient, 64 ids, all / half: 64 x 50257
+    // BF16 14.6 / 9.3 us, 100 x 128256 BF16 19.3 / 13.7)
     ctas = (int64_t)sm_count() * kCtasPerSm;
     int size = 1;
     while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (marks && bytes > size * kMaxPart) ||
-                                  (a.in.rows * size < ctas && bytes > size * 8192)))
+                                  (2 * a.in.rows * size < ctas && bytes > size * kMinPart)))
         size *= 2;
     return launch<T, kLong>(a, size, marks, ctas, stream);
 }

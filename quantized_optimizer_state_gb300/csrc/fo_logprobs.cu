@@ -8,8 +8,8 @@ namespace {
 constexpr int kGradThreads = 256;
 constexpr int kWide = 256, kMiddle = 128, kNarrow = 64;   // threads to a row: see launch
 constexpr int kGroup = 4;                      // vectors of a thread that one maximum is kept for
-constexpr int kCtasPerSm = 4;
-constexpr int kThreadsPerSm = 1280;
+constexpr int kThreadsPerSm = 1280;            // of resident rows
+constexpr int64_t kMinPart = 32 * 1024;        // bytes of a row that are worth a CTA of their own
 constexpr int kAheadBytes = 128;               // for each thread of a row: see logprobs_kernel
 
 // What the kN threads of a row share.
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGrad
 template <class T, int kN>
 cudaError_t launch(LogprobArgs a, int size, cudaStream_t stream)
 {
-    a.ahead = a.k && size == 1 ? sm_count() * (kThreadsPerSm / kN) : 0;
+    a.ahead = size == 1 ? sm_count() * (kThreadsPerSm / kN) : 0;
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     const int64_t groups = (vecs + kGroup * kN - 1) / (kGroup * kN);
     return launch_cluster(logprobs_kernel<T, kN>, a, a.in.rows, size, a.k ? groups * kN * 4 : 0, kN, stream);
@@ -543,23 +543,30 @@ cudaError_t launch(LogprobArgs a, int size, cudaStream_t stream)
 template <class T>
 cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
 {
-    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * kCtasPerSm;
-    // Many rows: one CTA each, of as few threads as the row and its list of
-    // alternatives leave busy, so that more rows are on an SM at once and their
-    // joins and lists overlap. Measured at 256 / 128 / 64 threads: 16384 x 1000
-    // BF16 54 / - / 18 us, with 20 alternatives 124 / - / 53; 3001 x 50257 with
-    // 64 alternatives 91 / 81 / - us; 4096 x 128256 without any 180 / 169 / -,
-    // with 64 of them 226 / 253 / -.
-    if (a.in.rows >= ctas) {
-        if (bytes <= 16 * 1024 && a.k <= kNarrow)
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), ctas = (int64_t)sm_count() * (kThreadsPerSm / kWide);
+    // More rows than CTAs of 256 threads fit: one CTA each, of as few threads as
+    // the row and its list leave busy, so that more rows are on an SM at once and
+    // their joins and lists overlap. A list of k wants 2 k threads: the bound is
+    // the k-th of their maxima, and as the lowest of all it would let in more
+    // candidates than there is room for (4096 x 8192 BF16 with 64 alternatives,
+    // 64 threads: 246 us, found the exact way, against 10). Measured at 256 / 128
+    // / 64 threads: 16384 x 1000 BF16 54 / - / 18 us, with 20 alternatives 124 /
+    // - / 53; 3001 x 50257 with 64 of them 91 / 81 / - us; 4096 x 128256 without
+    // any 180 / 169 / -, with 64 of them 226 / 253 / -; 610 x 128256 30 / 40 / -.
+    if (a.in.rows > ctas) {
+        if (bytes <= 16 * 1024 && a.k <= kNarrow / 2)
             return launch<T, kNarrow>(a, 1, stream);
         if (a.k == 0 || (a.k <= 64 && bytes <= 128 * 1024))
             return launch<T, kMiddle>(a, 1, stream);
         return launch<T, kWide>(a, 1, stream);
     }
-    // few rows: a cluster shares one while the grid would leave SMs short of CTAs
+    // Few rows: a cluster shares one until there are two CTAs to an SM. Up to four
+    // measured slower, where a second set of clusters waits for the first (100 x
+    // 50257 BF16 13.5 / 8.0 us, 300 x 128256 FP32 35 / 26), and so did parts of
+    // 8 KB against 32 KB (1 x 50257 with 64 alternatives 12.1 / 10.9, 64 x 50257
+    // 16.6 / 12.6; without any, 4 x 50257, 5.6 / 6.6).
     int size = 1;
-    while (size < kMaxCluster && a.in.rows * size < ctas && bytes > size * 8192)
+    while (size < kMaxCluster && a.in.rows * size < 2 * sm_count() && bytes > size * kMinPart)
         size *= 2;
     return launch<T, kWide>(a, size, stream);
 }
