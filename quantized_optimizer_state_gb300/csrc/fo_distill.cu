@@ -689,15 +689,21 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
     int64_t ctas = (int64_t)sm_count() * kShortPerSm;
     if (bytes <= kShortRow && a.in.rows >= ctas)
         return launch<T, kShort>(a, 1, marks, ctas, stream);
-    // one CTA a row, or a cluster that shares it: while the rows at work at
-    // once would not stay in the L2 cache between the passes, while a part's
-    // marks would take a CTA's place on the SM, and until half of the CTAs that
-    // fit are there (all of them measured slower: a second set of clusters
-    // waits for the first; loss with gradient, 64 ids, all / half: 64 x 50257
-    // BF16 14.6 / 9.3 us, 100 x 128256 BF16 19.3 / 13.7)
-    ctas = (int64_t)sm_count() * kCtasPerSm;
+    // One CTA a row, or a cluster that shares it:
+    //   - while the rows at work at once would not stay in the L2 cache between
+    //     the passes;
+    //   - while a part's marks would leave room for two CTAs on an SM and there
+    //     are rows for three (in clusters all the same, 300 x 128256 BF16 takes
+    //     44 us against 35);
+    //   - until half of the CTAs that fit are there. All of them measured slower,
+    //     a second set of clusters waiting for the first: 64 x 50257 BF16 14.6 us
+    //     against 9.3, 100 x 128256 BF16 19.3 against 13.7.
+    // (Loss with gradient, 64 ids.)
+    const int64_t sms = sm_count();
+    ctas = sms * kCtasPerSm;
     int size = 1;
-    while (size < kMaxCluster && ((a.grad.data && bytes * (ctas / size) > kCacheBytes) || (marks && bytes > size * kMaxPart) ||
+    while (size < kMaxCluster && ((a.grad.data && bytes * std::min(a.in.rows, ctas / size) > kCacheBytes) ||
+                                  (marks && a.in.rows * size > 2 * sms && bytes > size * kMaxPart) ||
                                   (2 * a.in.rows * size < ctas && bytes > size * kMinPart)))
         size *= 2;
     return launch<T, kLong>(a, size, marks, ctas, stream);
