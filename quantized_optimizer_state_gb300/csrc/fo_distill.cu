@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
     __shared__ __align__(16) Shared sh;
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t first = (int64_t)(blockIdx.x / size) * a.rows_each, last = min(a.in.rows, first + a.rows_each);
+    const int64_t first = blockIdx.x / size, step = gridDim.x / size, rows = a.in.rows;   // this cluster's rows
     uint4 *const stages = reinterpret_cast<uint4 *>(dynamic);
     unsigned char *const mark_bytes = dynamic + kStages * kStageVecs * 16;
     uint32_t *const marks = reinterpret_cast<uint32_t *>(mark_bytes);
@@ -295,10 +295,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
     float next_weight = a.weight ? a.weight[first] : 1.0f;
     if (warp == kFetcher) {
         Cursor<kStages> c;
-        for (int64_t r = first; r < last && ok; ++r) {
+        for (int64_t r = first; r < rows && ok; r += step) {
             const float weight = next_weight;
-            if (r + 1 < last && a.weight)
-                next_weight = a.weight[r + 1];
+            if (r + step < rows && a.weight)
+                next_weight = a.weight[r + step];
             if (weight == 0.0f)
                 continue;
             const Row<T> row(a.in, r);
@@ -343,20 +343,20 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
         TeacherRaw next = load_teacher(a.teacher, first);
         if (next_weight != 0.0f)
             start(first, next);
-        for (int64_t r = first; r < last; ++r) {
+        for (int64_t r = first; r < rows; r += step) {
             const float weight = next_weight;
             const TeacherRaw w = next;
-            if (r + 1 < last) {
-                next = load_teacher(a.teacher, r + 1);
+            if (r + step < rows) {
+                next = load_teacher(a.teacher, r + step);
                 if (a.weight)
-                    next_weight = a.weight[r + 1];
+                    next_weight = a.weight[r + step];
             }
             const bool writes = (uint32_t)r % size == rank && lane == 0;   // the loss, in turn
             if (weight == 0.0f || !ok) {   // the same in all CTAs of the cluster
                 if (writes && a.loss)
                     a.loss[r] = ok ? 0.0f : __int_as_float(0x7fffffff);
-                if (r + 1 < last && next_weight != 0.0f)
-                    start(r + 1, next);
+                if (r + step < rows && next_weight != 0.0f)
+                    start(r + step, next);
                 continue;
             }
             const TeacherRow t = make_teacher(a.teacher, w, (int)a.in.vocab);
@@ -476,8 +476,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                 }
             }
             __syncwarp();
-            if (r + 1 < last && next_weight != 0.0f)
-                start(r + 1, next);
+            if (r + step < rows && next_weight != 0.0f)
+                start(r + step, next);
             if (passes == 2) {
                 ok = warp_wait(&sh.written, active & 1) && ok;
                 raw *const g = static_cast<raw *>(a.grad.data) + row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
@@ -490,10 +490,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
         }
     } else {
         Cursor<kStages> c;
-        for (int64_t r = first; r < last; ++r) {
+        for (int64_t r = first; r < rows; r += step) {
             const float weight = next_weight;
-            if (r + 1 < last && a.weight)
-                next_weight = a.weight[r + 1];
+            if (r + step < rows && a.weight)
+                next_weight = a.weight[r + step];
             const Row<T> row(a.in, r);
             const Part p = part_of(row, rank, size);
             raw *g = static_cast<raw *>(a.grad.data);
@@ -667,14 +667,13 @@ cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream
 {
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     a.mark_words = marks ? (int)(vecs + 3) / 4 : 0;
-    // A few rows one after the other, where there are many. For the loss alone all
-    // of a CTA's rows in one turn, below the size where CTAs drift apart: us in
-    // short turns / one, 2048 x 50257 F16 44.1 / 39.5, 8192 x 50257 BF16 133 /
+    // A few rows one after the other, where there are many. For the loss alone the
+    // CTAs that fit take all rows, below the size where they drift apart: us with
+    // few rows each / all, 2048 x 50257 F16 44.1 / 39.5, 8192 x 50257 BF16 133 /
     // 124, 8192 x 1000 25.6 / 22.7; 8192 x 100000 236 / 253.
-    a.rows_each = (int)std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
-    if (!a.grad.data && size == 1 && a.in.rows * a.in.vocab * (int64_t)sizeof(typename T::raw) <= kOneTurn)
-        a.rows_each = (int)((a.in.rows + ctas - 1) / ctas);
-    const int64_t clusters = (a.in.rows + a.rows_each - 1) / a.rows_each;
+    const int64_t each = std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
+    const bool all = !a.grad.data && size == 1 && a.in.rows * a.in.vocab * (int64_t)sizeof(typename T::raw) <= kOneTurn;
+    const int64_t clusters = all ? std::min(a.in.rows, ctas) : (a.in.rows + each - 1) / each;
     const size_t shared = (size_t)kStages * 4 * kWarps * 32 * 16 + (size_t)a.mark_words * 4;
     const int threads = kWarps * 32 + 64;
     if (a.teacher.tail)

@@ -64,9 +64,7 @@ struct DistillArgs {
     float *loss;             // may be null
     float4 *stats;           // may be null
     GradRows grad;           // data may be null
-    // set by the launch: rows that a cluster takes one after the other, and
-    // words of shared memory for its marks (fo_distill.cu)
-    int32_t rows_each, mark_words;
+    int32_t mark_words;      // set by the launch: shared memory for marks (fo_distill.cu)
 };
 
 struct DistillGradArgs {
