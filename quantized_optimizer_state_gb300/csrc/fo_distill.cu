@@ -20,13 +20,17 @@ constexpr int kLong = 8, kShort = 2;              // warps that walk over a row:
 constexpr int kStages = 4;                        // copies of four vectors a thread, in flight or in use
 constexpr int kCtasPerSm = 3;                     // of kLong warps; of kShort ones kShortPerSm
 constexpr int kShortPerSm = 8;
-constexpr int kMaxRowsEach = 2;
-// Of the 129 MB L2 cache, for rows between their passes. 116 MB is slower (877
-// against 761 us on the first case above), 60 MB the same.
-constexpr int64_t kCacheBytes = 80 << 20;
+constexpr int64_t kMaxRowsEach = 2;
+constexpr int64_t kRing = 64 * 1024;              // bytes of the stages of kLong warps
+// Of the 129 MB L2 cache: for the rows at work, between their passes, and for
+// these and what the rings run ahead with. Measured in the launch's choices:
+// rows of 78 MB at work take 785 us on the first case above against 688 in
+// clusters of two (59 MB); 8192 x 64128 BF16 (58 MB, 88 with the rings) takes 358
+// us with two rows in turn against 328, 8192 x 50257 (46 and 76 MB) 267 against 276.
+constexpr int64_t kCacheBytes = 64 << 20, kCacheAhead = 75 << 20;
 constexpr int64_t kOneTurn = 800 << 20;           // bytes of all rows
 constexpr int64_t kShortRow = 32 * 1024;
-constexpr int64_t kMaxPart = 128 * 1024;          // bytes of a part: its marks are a 16th of that
+constexpr int64_t kMaxPart = 146 * 1024;          // bytes of a part: its marks, a 16th of that, leave room for three CTAs
 constexpr int64_t kMinPart = 16 * 1024;           // bytes of a row that are worth a CTA of their own
 constexpr int kGradThreads = 256;
 constexpr float kLn2High = 0x1.62e4p-1f;          // 15 bits of ln 2
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) distill_grad_kernel(DistillGr
 }
 
 template <class T, int kWarps>
-cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream_t stream)
+cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, int64_t most, cudaStream_t stream)
 {
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     a.mark_words = marks ? (int)(vecs + 3) / 4 : 0;
@@ -671,7 +675,7 @@ cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream
     // CTAs that fit take all rows, below the size where they drift apart: us with
     // few rows each / all, 2048 x 50257 F16 44.1 / 39.5, 8192 x 50257 BF16 133 /
     // 124, 8192 x 1000 25.6 / 22.7; 8192 x 100000 236 / 253.
-    const int64_t each = std::min<int64_t>(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
+    const int64_t each = std::min(most, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
     const bool all = !a.grad.data && size == 1 && a.in.rows * a.in.vocab * (int64_t)sizeof(typename T::raw) <= kOneTurn;
     const int64_t clusters = all ? std::min(a.in.rows, ctas) : (a.in.rows + each - 1) / each;
     const size_t shared = (size_t)kStages * 4 * kWarps * 32 * 16 + (size_t)a.mark_words * 4;
@@ -693,25 +697,25 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
     // 174 / 210.
     int64_t ctas = (int64_t)sm_count() * kShortPerSm;
     if (bytes <= kShortRow && a.in.rows >= ctas)
-        return launch<T, kShort>(a, 1, marks, ctas, stream);
+        return launch<T, kShort>(a, 1, marks, ctas, kMaxRowsEach, stream);
     // One CTA a row, or a cluster that shares it:
     //   - while the rows at work at once would not stay in the L2 cache between
-    //     the passes;
-    //   - while a part's marks would leave room for two CTAs on an SM and there
-    //     are rows for three (in clusters all the same, 300 x 128256 BF16 takes
-    //     44 us against 35);
+    //     the passes (kCacheBytes);
     //   - until half of the CTAs that fit are there. All of them measured slower,
     //     a second set of clusters waiting for the first: 64 x 50257 BF16 14.6 us
     //     against 9.3, 100 x 128256 BF16 19.3 against 13.7.
-    // (Loss with gradient, 64 ids.)
+    // Not for room for the marks: where they leave two CTAs to an SM and not
+    // three, clusters that bring back the third are slower (8192 x 80000 BF16 528
+    // us against 444, 300 x 128256 44 against 35). (Loss with gradient, 64 ids.)
     const int64_t sms = sm_count();
-    ctas = sms * kCtasPerSm;
+    const auto fit = [&](int size) { return sms * (marks && bytes > size * kMaxPart ? kCtasPerSm - 1 : kCtasPerSm); };
+    const auto at_work = [&](int size) { return std::min(a.in.rows, fit(size) / size) * bytes; };
     int size = 1;
-    while (size < kMaxCluster && ((a.grad.data && bytes * std::min(a.in.rows, ctas / size) > kCacheBytes) ||
-                                  (marks && a.in.rows * size > 2 * sms && bytes > size * kMaxPart) ||
-                                  (2 * a.in.rows * size < ctas && bytes > size * kMinPart)))
+    while (size < kMaxCluster && ((a.grad.data && at_work(size) > kCacheBytes) || (2 * a.in.rows * size < sms * kCtasPerSm && bytes > size * kMinPart)))
         size *= 2;
-    return launch<T, kLong>(a, size, marks, ctas, stream);
+    ctas = fit(size);
+    const int64_t most = size == 1 && at_work(size) + ctas * kRing > kCacheAhead ? 1 : kMaxRowsEach;
+    return launch<T, kLong>(a, size, marks, ctas, most, stream);
 }
 
 template <class T>
