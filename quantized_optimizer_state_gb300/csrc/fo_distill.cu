@@ -12,23 +12,21 @@ namespace {
 // CTAs an SM of 8 walking warps with 4 stages of 16 KB. 4 CTAs (48 registers,
 // spills) with 3 such stages: 809 / 393 / 214 against 709 / 358 / 203 at the
 // same rows in turn; 8 stages of 8 KB: 761 / 383 / 224 against 749 / 358 / 202;
-// 2 CTAs of 16 warps: 813 / 493 / 212 against 778 / 393 / 225. Two rows in turn
-// against 1, 4 and 8: 700 / 345 / 203 against 757 / 343 / 204, 709 / 358 / 203
-// and 749 / 358 / 202: the fetching runs on into the second row, and short
-// turns spread the end of the grid. (Listed tokens were dearer then.)
+// 2 CTAs of 16 warps: 813 / 493 / 212 against 778 / 393 / 225. (Each pair is of
+// one build; what came later took 688 / 280 / 198.) Two rows in turn against 1
+// and 4: 687 / 279 / 196 against 733 / 287 / 201 and 689 / 282 / 197: the
+// fetching runs on into the second row, and short turns spread the grid's end.
 constexpr int kLong = 8, kShort = 2;              // warps that walk over a row: see launch
 constexpr int kStages = 4;                        // copies of four vectors a thread, in flight or in use
 constexpr int kCtasPerSm = 3;                     // of kLong warps; of kShort ones kShortPerSm
 constexpr int kShortPerSm = 8;
 constexpr int64_t kMaxRowsEach = 2;
-constexpr int64_t kRing = 64 * 1024;              // bytes of the stages of kLong warps
-// Of the 129 MB L2 cache: for the rows at work, between their passes, and for
-// these and what the rings run ahead with. Measured in the launch's choices:
-// rows of 78 MB at work take 785 us on the first case above against 688 in
-// clusters of two (59 MB); 8192 x 64128 BF16 (58 MB, 88 with the rings) takes 358
-// us with two rows in turn against 328, 8192 x 50257 (46 and 76 MB) 267 against 276.
-constexpr int64_t kCacheBytes = 64 << 20, kCacheAhead = 75 << 20;
-constexpr int64_t kOneTurn = 800 << 20;           // bytes of all rows
+// Of the 129 MB L2 cache, for the rows at work between their passes. 78 MB are
+// too many: 8192 x 128256 BF16 692 us against 672 in clusters of two (59 MB), 1001
+// x 128256 FP32 with a tail 206 in clusters of two against 191 of four; 73 MB are
+// not (4096 x 120000 BF16 336 against 354).
+constexpr int64_t kCacheBytes = 70 << 20;
+constexpr int64_t kOneTurn = 800 << 20;           // bytes of all rows and gradients
 constexpr int64_t kShortRow = 32 * 1024;
 constexpr int64_t kMaxPart = 146 * 1024;          // bytes of a part: its marks, a 16th of that, leave room for three CTAs
 constexpr int64_t kMinPart = 16 * 1024;           // bytes of a row that are worth a CTA of their own
@@ -239,9 +237,11 @@ __device__ __forceinline__ uint32_t merge_twice(Shared &sh, const TeacherRow &t,
 // a row sums the exponentials, a second writes the gradient,
 //   dKL/dx_j = (w/T) [ p_j (A - [j not listed] q_rest / p_rest) - q_j ];
 // it reads the row again, but from the L2 cache: the launch keeps the rows at
-// work at once well below its size (97 % of the second pass hits; device memory
-// gives 1.02 times the logits). 8192 x 128256 BF16: 0.70 ms, 0.85 of the
-// measured copy rate for one read and one write. It is bound by the mixed
+// work at once well below its size, and the first pass asks it to keep their
+// lines, the second to let them go (98 % of it hits; device memory
+// gives 1.02 times the logits). 8192 x 128256 BF16: 0.68 ms, 0.89
+// of the measured copy rate for one read and one write (without these requests
+// 0.69). It is bound by the mixed
 // traffic: the second pass adds half as much again in the L2 cache, which moves
 // 10.2 TB/s, and instructions issue in half of the cycles. Rows held in shared
 // memory between the passes were slower (1.02 ms at best): their clusters are
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
     float next_weight = a.weight ? a.weight[first] : 1.0f;
     if (warp == kFetcher) {
         Cursor<kStages> c;
+        const uint64_t keep = keep_policy(), drop = drop_policy();
         for (int64_t r = first; r < rows && ok; r += step) {
             const float weight = next_weight;
             if (r + step < rows && a.weight)
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (ok)
-                        fill_stage<T>(row, p.v0 + i, p.v0 + min(p.n, i + kStageVecs), stages + c.at * kStageVecs, &sh.full[c.at]);
+                        fill_stage<T>(row, p.v0 + i, p.v0 + min(p.n, i + kStageVecs), stages + c.at * kStageVecs, &sh.full[c.at], pass + 1 < passes ? keep : drop);
                 }
         }
         // copies that are still on their way are not left behind
@@ -667,16 +668,19 @@ __global__ void __launch_bounds__(kGradThreads, 4) distill_grad_kernel(DistillGr
 }
 
 template <class T, int kWarps>
-cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, int64_t most, cudaStream_t stream)
+cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream_t stream)
 {
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     a.mark_words = marks ? (int)(vecs + 3) / 4 : 0;
-    // A few rows one after the other, where there are many. For the loss alone the
-    // CTAs that fit take all rows, below the size where they drift apart: us with
-    // few rows each / all, 2048 x 50257 F16 44.1 / 39.5, 8192 x 50257 BF16 133 /
-    // 124, 8192 x 1000 25.6 / 22.7; 8192 x 100000 236 / 253.
-    const int64_t each = std::min(most, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
-    const bool all = !a.grad.data && size == 1 && a.in.rows * a.in.vocab * (int64_t)sizeof(typename T::raw) <= kOneTurn;
+    // The CTAs that fit take all rows, below the size where they drift apart;
+    // above it a few rows each, so that short turns spread the grid's end. In us
+    // with a few each / all: loss alone, 2048 x 50257 F16 44.1 / 39.5, 8192 x
+    // 50257 BF16 133 / 124, 8192 x 1000 25.6 / 22.7, 8192 x 100000 236 / 253; with
+    // gradient, 1400 x 80000 90.4 / 85.8, 4096 x 16000 61.5 / 58.0, 4096 x 64128
+    // 170 / 188.
+    const int64_t each = std::min(kMaxRowsEach, std::max<int64_t>(1, a.in.rows * size / (4 * ctas)));
+    const int64_t moved = a.in.rows * a.in.vocab * (int64_t)sizeof(typename T::raw) * (a.grad.data ? 2 : 1);
+    const bool all = size == 1 && moved <= kOneTurn;
     const int64_t clusters = all ? std::min(a.in.rows, ctas) : (a.in.rows + each - 1) / each;
     const size_t shared = (size_t)kStages * 4 * kWarps * 32 * 16 + (size_t)a.mark_words * 4;
     const int threads = kWarps * 32 + 64;
@@ -697,7 +701,7 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
     // 174 / 210.
     int64_t ctas = (int64_t)sm_count() * kShortPerSm;
     if (bytes <= kShortRow && a.in.rows >= ctas)
-        return launch<T, kShort>(a, 1, marks, ctas, kMaxRowsEach, stream);
+        return launch<T, kShort>(a, 1, marks, ctas, stream);
     // One CTA a row, or a cluster that shares it:
     //   - while the rows at work at once would not stay in the L2 cache between
     //     the passes (kCacheBytes);
@@ -714,8 +718,7 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream)
     while (size < kMaxCluster && ((a.grad.data && at_work(size) > kCacheBytes) || (2 * a.in.rows * size < sms * kCtasPerSm && bytes > size * kMinPart)))
         size *= 2;
     ctas = fit(size);
-    const int64_t most = size == 1 && at_work(size) + ctas * kRing > kCacheAhead ? 1 : kMaxRowsEach;
-    return launch<T, kLong>(a, size, marks, ctas, most, stream);
+    return launch<T, kLong>(a, size, marks, ctas, stream);
 }
 
 template <class T>

@@ -10,7 +10,7 @@ constexpr int kWide = 256, kMiddle = 128, kNarrow = 64;   // threads to a row: s
 constexpr int kGroup = 4;                      // vectors of a thread that one maximum is kept for
 constexpr int kThreadsPerSm = 1280;            // of resident rows
 constexpr int64_t kMinPart = 32 * 1024;        // bytes of a row that are worth a CTA of their own
-constexpr int kAheadBytes = 128;               // for each thread of a row: see logprobs_kernel
+constexpr int kAheadBytes = 128;               // fetched ahead for each thread: see logprobs_kernel
 
 // What the kN threads of a row share.
 template <int kN>
@@ -368,11 +368,14 @@ __device__ __forceinline__ float load_token(const LogprobArgs &a, int64_t r, con
 
 // One row by a cluster of CTAs of kN threads (one CTA where there are many
 // rows): one pass over the row by plain loads, sums in registers. 4096 x 128256
-// BF16: 168 us, 0.92 of the measured copy rate; it issues 7.8 instructions an
-// element in 55 % of the cycles, so loads and instructions are near to one
-// another. With alternatives (3001 x 50257 BF16, 64 of them: 83 us, 0.53) it is
-// bound by the end of a row: the bound, the vectors read again and the ranking
-// are chains of short steps that take as long as the pass. Bulk copies into a
+// BF16: 166 us, 0.93 of the measured copy rate; it issues 6.7 instructions an
+// element in half of the cycles. With alternatives (3001 x 50257 BF16, 64 of
+// them: 76 us, 0.59) it is bound by the end of a row: the bound, the vectors
+// read again and the ranking are chains of short steps, half as long as the
+// pass. Meanwhile the CTA has the first bytes of the row that comes next to its
+// place on its way into the L2 cache, 128 a thread (a.ahead rows on; 3001 x
+// 50257 with 8 68.3 / 65.5 us, 4096 x 128256 with 64 225 / 213, without any 171
+// / 166; twice as much 76.5 against 74.9 on the case above). Bulk copies into a
 // ring that run ahead into the next row were slower (206 and 147 us): the same
 // warps finish the row, and fewer of them fit.
 template <class T, int kN>

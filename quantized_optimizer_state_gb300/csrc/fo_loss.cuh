@@ -454,7 +454,7 @@ struct Running {
     }
 };
 
-// --- rows held in the shared memory of a cluster -----------------------------------
+// --- clusters, and a ring of bulk copies --------------------------------------------
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -550,12 +550,26 @@ struct Cursor {
     }
 };
 
+// What the L2 cache does with lines that are read: keeps them longest, or lets them go first.
+__device__ __forceinline__ uint64_t keep_policy()
+{
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t drop_policy()
+{
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // Starts the copy of vectors [i0, i1) of a row into a stage, by one warp. The
 // vectors wholly inside the row come by a bulk copy; those that reach beyond
 // its ends element by element (no byte outside the row is read), filled up
 // with -inf. `full` counts the copy's bytes and two arrivals.
 template <class T>
-__device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, uint4 *stage, uint64_t *full)
+__device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, uint4 *stage, uint64_t *full, uint64_t policy)
 {
     typedef typename T::raw raw;
     const int lane = threadIdx.x & 31;
@@ -564,9 +578,9 @@ __device__ __forceinline__ void fill_stage(const Row<T> &row, int i0, int i1, ui
         const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
         barrier_expect(full, bytes);
         if (bytes)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
                              shared_address(stage + (lo - i0))),
-                         "l"(row.vec(lo)), "r"(bytes), "r"(shared_address(full))
+                         "l"(row.vec(lo)), "r"(bytes), "r"(shared_address(full)), "l"(policy)
                          : "memory");
     }
     if (lo > i0 || hi < i1) {
