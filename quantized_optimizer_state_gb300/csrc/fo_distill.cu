@@ -238,14 +238,14 @@ __device__ __forceinline__ uint32_t merge_twice(Shared &sh, const TeacherRow &t,
 //   dKL/dx_j = (w/T) [ p_j (A - [j not listed] q_rest / p_rest) - q_j ];
 // it reads the row again, but from the L2 cache: the launch keeps the rows at
 // work at once well below its size, and the first pass asks it to keep their
-// lines, the second to let them go (98 % of it hits; device memory
-// gives 1.02 times the logits). 8192 x 128256 BF16: 0.68 ms, 0.89
-// of the measured copy rate for one read and one write (without these requests
-// 0.69). It is bound by the mixed
-// traffic: the second pass adds half as much again in the L2 cache, which moves
-// 10.2 TB/s, and instructions issue in half of the cycles. Rows held in shared
-// memory between the passes were slower (1.02 ms at best): their clusters are
-// larger, and each row waits for the exchange of its sums with less in flight.
+// lines, the second to let them go (98 % of the second pass hits; device memory
+// gives 1.02 times the logits). 8192 x 128256 BF16: 0.674 ms, 0.89 of the
+// measured copy rate for one read and one write (0.689 without these requests).
+// It is bound by the mixed traffic: the second pass adds half as much again in
+// the L2 cache, which moves 10.2 TB/s, and instructions issue in half of the
+// cycles. Rows held in shared memory between the passes were slower (1.02 ms at
+// best): their clusters are larger, and each row waits for the exchange of its
+// sums with less in flight.
 // In each CTA
 //   - a warp keeps bulk copies in flight into a ring of stages, running ahead
 //     over the passes and rows, so that the memory is not idle while sums are
