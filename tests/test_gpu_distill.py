@@ -345,3 +345,25 @@ def test_long_lists_with_tokens_listed_twice(dtype):
     lse = torch.logsumexp(y, 1) + 0.2
     check(x, ids, y)
     check(x, ids, y, lse, tail=True)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("n,v,dtype", [(40, 16385, F32), (180, 200003, BF), (310, 128256, F16), (330, 80000, BF), (470, 50257, BF),
+                                       (500, 130001, F32), (1300, 20011, F16), (4000, 60011, BF)])
+def test_rows_shared_and_taken_in_every_way(n, v, dtype, tail):
+    """One CTA a row, clusters, all rows in one turn or a few, two CTAs to an SM and three."""
+    x = make(n, v, dtype, seed=n)
+    ids, y, lse = make_teacher(n, v, 40, seed=v)
+    w = torch.rand(n, generator=gen(5), device="cuda") / n
+    w[::5] = 0.0
+    how = dict(tail=tail, teacher_lse=lse if tail else None, temperature=1.3)
+    loss, g = losses.distill_loss_grad(x, ids, y, row_weight=w, **how)
+    alone = losses.distill_loss(x, ids, y, **how)
+    for i in range(0, n, 250):                # in parts, for the reference's 64-bit arrays
+        at = slice(i, i + 250)
+        part = (x[at], ids[at], y[at], 1.3, 1.0, tail, lse[at] if tail else None)
+        want, grad, tol, scale = ref.distill(*part, w[at])
+        ref.close(loss[at], want, tol, "loss")
+        ref.close(g[at], grad, ref.grad_tolerance(grad, scale, dtype), "gradient")
+        want, _, tol, _ = ref.distill(*part)
+        ref.close(alone[at], want, tol, "loss alone")

@@ -399,3 +399,24 @@ def test_alternatives_of_rows_with_nan():
         assert o.top_ids[0, :3].tolist() == [3, v // 2, v - 1]
         assert o.top_ids[1].tolist() == list(range(10))
         assert o.top_ids[0].unique().numel() == 10 and o.top_logp[:2].isnan().all()
+
+
+@pytest.mark.parametrize("k", [0, 1, 32, 33, 64, 65, 128])
+@pytest.mark.parametrize("n,v,dtype", [(100, 20001, BF), (300, 100003, F16), (761, 8192, BF), (1600, 16001, F32), (3100, 5003, BF), (1700, 70001, F16)])
+def test_rows_shared_in_every_way(n, v, dtype, k):
+    """Clusters and single CTAs of each width, lists below and above half of a CTA's threads."""
+    x = make(n, v, dtype, seed=n + k)
+    t = torch.randint(0, v, (n,), generator=gen(1), device="cuda")
+    o = losses.token_logprobs(x, t, top_k=k, temperature=0.8)
+    for i in range(0, n, 400):                # in parts, for the reference's 64-bit arrays
+        at = slice(i, i + 400)
+        d, p, lp, lnz = ref.row_stats(x[at], 0.8)
+        tol = lambda dd: 2.0 ** -19 + 4 * 2.0 ** -24 * (dd.abs() + lnz.abs())
+        one = t[at, None]
+        ref.close(o.logp[at, None], lp.gather(1, one), tol(d.gather(1, one)), "logp")
+        spread = (p * d).sum(1).abs()
+        ref.close(o.entropy[at], ref.entropy(p, lp), 2.0 ** -18 + 2.0 ** -19 * (lnz[:, 0].abs() + spread), "entropy")
+        if k:
+            ids = ref.top(x[at], k)
+            assert torch.equal(o.top_ids[at].long(), ids)
+            ref.close(o.top_logp[at], lp.gather(1, ids), tol(d.gather(1, ids)), "top_logp")
