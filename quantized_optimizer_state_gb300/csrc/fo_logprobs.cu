@@ -1,5 +1,7 @@
 // fo_logprobs.cu -- log probabilities of given tokens with entropy and top
 // alternatives, and their gradient.
+#include <algorithm>
+
 #include "fo_loss.cuh"
 
 namespace fo {
@@ -543,6 +545,21 @@ cudaError_t launch(LogprobArgs a, int size, cudaStream_t stream)
     return launch_cluster(logprobs_kernel<T, kN>, a, a.in.rows, size, a.k ? groups * kN * 4 : 0, kN, stream);
 }
 
+// Whether rows without alternatives are better off with kMiddle threads than
+// with kWide. A last turn that is not full takes at least half of a full one's
+// time, which costs long rows in few turns more than wide CTAs do: 2048 x 128256
+// BF16 101 us with 128 threads, 91 with 256; 1700 x 50257 42.4 / 39.3; but 2700 x
+// 128256 115 / 116, 8000 x 128256 311 / 318, 3100 x 32000 43.6 / 43.9.
+bool fits_middle(int64_t rows, int64_t bytes)
+{
+    const auto time = [&](int threads) {
+        const int64_t fit = (int64_t)sm_count() * (kThreadsPerSm / threads);
+        const double rest = (double)(rows % fit) / (double)fit;
+        return ((double)(rows / fit) + (rest == 0.0 ? 0.0 : std::max(rest, 0.5))) / threads;
+    };
+    return bytes <= 96 * 1024 || rows > 4 * sm_count() * (kThreadsPerSm / kMiddle) || time(kMiddle) <= time(kWide) * 1.03;
+}
+
 template <class T>
 cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
 {
@@ -559,7 +576,7 @@ cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
     if (a.in.rows > ctas) {
         if (bytes <= 16 * 1024 && a.k <= kNarrow / 2)
             return launch<T, kNarrow>(a, 1, stream);
-        if (a.k == 0 || (a.k <= 64 && bytes <= 128 * 1024))
+        if (a.k == 0 ? fits_middle(a.in.rows, bytes) : a.k <= 64 && bytes <= 128 * 1024)
             return launch<T, kMiddle>(a, 1, stream);
         return launch<T, kWide>(a, 1, stream);
     }
