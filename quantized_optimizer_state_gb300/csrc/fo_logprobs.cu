@@ -568,7 +568,7 @@ cudaError_t launch(const LogprobArgs &a, cudaStream_t stream)
     // the row and its list leave busy, so that more rows are on an SM at once and
     // their joins and lists overlap. A list of k wants 2 k threads: the bound is
     // the k-th of their maxima, and as the lowest of all it would let in more
-    // candidates than there is room for (4096 x 8192 BF16 with 64 alternatives,
+    // candidates than there is room for (610 x 8192 BF16 with 64 alternatives,
     // 64 threads: 246 us, found the exact way, against 10). Measured at 256 / 128
     // / 64 threads: 16384 x 1000 BF16 54 / - / 18 us, with 20 alternatives 124 /
     // - / 53; 3001 x 50257 with 64 of them 91 / 81 / - us; 4096 x 128256 without
