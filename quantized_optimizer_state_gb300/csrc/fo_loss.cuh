@@ -357,7 +357,13 @@ struct Running {
         const float low = to - fmaxf(reach, fabsf(to) * 0x1p-6f);   // where 2^t is 0, at the type's precision
         const bool c = !(fabsf(to) < 0x1p60f) || (kEntropy && !T::finite(low));
         const float r = __fmul_rn(to, in.c);
-        float t = c || careful ? __fmul_rn(to == m ? 0.0f : __fsub_rn(m, to), in.c) : __fsub_rn(ref, r);
+        // From what the sums were taken beside to what they are taken beside
+        // from here on: each is m c, rounded to `ref` where it is not careful.
+        float t;
+        if (careful)
+            t = c ? __fmul_rn(to == m ? 0.0f : __fsub_rn(m, to), in.c) : __fmaf_rn(m, in.c, -r);
+        else
+            t = c ? __fmaf_rn(-to, in.c, ref) : __fsub_rn(ref, r);
         t = max_nan(t, -160.0f);
         const float f = m == -kInf ? 0.0f : exp2_approx(t);
         if (kEntropy)
