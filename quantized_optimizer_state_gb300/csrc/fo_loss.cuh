@@ -333,10 +333,12 @@ __device__ __forceinline__ Stat block_join(Stat s, Stat *part, const LogitRows &
 // rounded, and the rounding is undone at the end. m follows the maximum
 // loosely: it is moved where a vector reaches 16 powers of two above it, which
 // after the first vector is rare, and saves the rescaling of most vectors.
-// `careful` marks references beside which x c - M does not do: of 2^60 and
-// more (x c may overflow, and the difference of two unequal logits is beyond
-// any exponent there), and, for the entropy, those next to the type's lowest
-// value; vectors are then taken element by element through x - m.
+// `careful` marks references beside which x c - M does not do: M of 2^24 and more,
+// NaN among them (the rounding of M, up to half of its last place, is undone by
+// 2^(M - m c), which must stay near 1: for a mask value of -1e9 at T = 0.1 that
+// rounding may be 2^9, and the sums would be infinities and zeros), and, for the
+// entropy, those next to the type's lowest value. Vectors are then taken element
+// by element through x - m.
 template <class T, bool kEntropy>
 struct Running {
     float m, ref;                       // the reference and RN(m c)
@@ -355,8 +357,8 @@ struct Running {
     {
         const float to = top.value(), reach = __fmul_rn(-in.d_min, 1.02f);
         const float low = to - fmaxf(reach, fabsf(to) * 0x1p-6f);   // where 2^t is 0, at the type's precision
-        const bool c = !(fabsf(to) < 0x1p60f) || (kEntropy && !T::finite(low));
         const float r = __fmul_rn(to, in.c);
+        const bool c = !(fabsf(r) < 0x1p24f) || (kEntropy && !T::finite(low));
         // From what the sums were taken beside to what they are taken beside
         // from here on: each is m c, rounded to `ref` where it is not careful.
         float t;
