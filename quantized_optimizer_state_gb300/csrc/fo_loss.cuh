@@ -43,6 +43,7 @@ struct Bf16 {
         return d != 0;
     }
     static __device__ __forceinline__ uint32_t twice(float f) { return (uint32_t)narrow(f) * 0x10001u; }
+    static constexpr float kLargest = 0x1.fep127f;        // the largest finite value
     static __device__ __forceinline__ bool finite(float f) { return fabsf(f) < 0x1p126f; }
 };
 struct F16 {
@@ -74,6 +75,7 @@ struct F16 {
         return d != 0;
     }
     static __device__ __forceinline__ uint32_t twice(float f) { return (uint32_t)narrow(f) * 0x10001u; }
+    static constexpr float kLargest = 65504.0f;
     static __device__ __forceinline__ bool finite(float f) { return fabsf(f) < 65000.0f; }
 };
 struct F32 {
@@ -83,6 +85,7 @@ struct F32 {
     static constexpr uint32_t kKeyBits = 0xffffffffu;
     static __device__ __forceinline__ float widen(raw v) { return v; }
     static __device__ __forceinline__ raw narrow(float f) { return f; }
+    static constexpr float kLargest = 0x1.fffffep127f;
     static __device__ __forceinline__ bool finite(float f) { return fabsf(f) < 0x1p126f; }
 };
 
@@ -374,7 +377,8 @@ struct Running {
         m = to;
         ref = r;
         careful = c;
-        limit = Largest<T>::bound(c ? to : __fmaf_rn(-in.d_min, 0.1f, to));   // -d_min c = 160
+        // -d_min c = 160; +inf is above every limit, so that it becomes the reference
+        limit = Largest<T>::bound(c ? to : fminf(__fmaf_rn(-in.d_min, 0.1f, to), T::kLargest));
         floor_ = Largest<T>::bound(low);
     }
 

@@ -112,3 +112,24 @@ def test_sums_carried_over_from_the_edge_of_fp16(temperature, first, then):
     x = torch.full((n, v), first, dtype=F16, device="cuda")
     x[:, 8192:8192 + 2048:8] = then           # one for each thread, after its first 32 elements
     check_forward(x, torch.full((n,), 8192, device="cuda"), 0, temperature)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("temperature", [1.0, 100.0, 4096.0, 2.0 ** 20])
+def test_infinity_makes_the_row_nan_at_every_temperature(temperature, dtype):
+    """Wherever +inf lies, first or last, and however far the reference may lie above the row's other logits."""
+    v, most = 20001, 64500.0 if dtype == F16 else 1e6
+    x = (torch.randn((6, v), generator=gen(3), device="cuda") * 2).to(dtype)
+    x[3:] = most
+    for r, at in enumerate((0, v // 2, v - 1) * 2):
+        x[r, at] = INF
+    t = torch.full((6,), 7, device="cuda")
+    o = losses.token_logprobs(x, t, top_k=3, temperature=temperature)
+    assert o.logp.isnan().all() and o.entropy.isnan().all() and o.top_logp.isnan().all()
+    assert o.top_ids[:, 0].tolist() == [0, v // 2, v - 1] * 2
+    ids = torch.tensor([[5, 6, 9]] * 6, dtype=torch.int32, device="cuda")
+    y = torch.zeros(6, 3, device="cuda") - 2
+    for tail in (False, True):
+        loss, grad = losses.distill_loss_grad(x, ids, y, temperature=temperature, tail=tail)
+        assert loss.isnan().all() and grad.isnan().all()
+        assert losses.distill_loss(x, ids, y, temperature=temperature, tail=tail).isnan().all()
