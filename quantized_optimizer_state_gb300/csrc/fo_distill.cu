@@ -685,8 +685,8 @@ cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream
     const size_t shared = (size_t)kStages * 4 * kWarps * 32 * 16 + (size_t)a.mark_words * 4;
     const int threads = kWarps * 32 + 64;
     if (a.teacher.tail)
-        return launch_cluster(distill_kernel<T, true, kWarps>, a, clusters, size, shared, threads, stream);
-    return launch_cluster(distill_kernel<T, false, kWarps>, a, clusters, size, shared, threads, stream);
+        return launch_cluster<distill_kernel<T, true, kWarps>>(a, clusters, size, shared, threads, stream);
+    return launch_cluster<distill_kernel<T, false, kWarps>>(a, clusters, size, shared, threads, stream);
 }
 
 template <class T>

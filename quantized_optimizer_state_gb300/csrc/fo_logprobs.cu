@@ -542,7 +542,7 @@ cudaError_t launch(LogprobArgs a, int size, cudaStream_t stream)
     a.ahead = size == 1 ? sm_count() * (kThreadsPerSm / kN) : 0;
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     const int64_t groups = (vecs + kGroup * kN - 1) / (kGroup * kN);
-    return launch_cluster(logprobs_kernel<T, kN>, a, a.in.rows, size, a.k ? groups * kN * 4 : 0, kN, stream);
+    return launch_cluster<logprobs_kernel<T, kN>>(a, a.in.rows, size, a.k ? groups * kN * 4 : 0, kN, stream);
 }
 
 // Whether rows without alternatives are better off with kMiddle threads than

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "fo_internal.h"
@@ -673,18 +674,43 @@ __device__ __forceinline__ f2 grad_exp2(f2 d, const LogitRows &in, f2 &t)
 
 constexpr int kMaxCluster = 8;
 
-// A row by a cluster of `size` CTAs.
+// Lets a kernel take the dynamic shared memory that the device has beside its
+// static part. The limit belongs to the kernel on its device, and threads that
+// launch it share it: so it is set once, to the most there is, and never to what
+// one call needs, which would refuse another thread's larger launch. `done` has
+// a bit for each device; beyond 64 of them it is set each time, to the same value.
 template <class Args>
-cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, int size, size_t shared_bytes, int threads,
-                           cudaStream_t stream)
+cudaError_t allow_shared(void (*kernel)(Args), std::atomic<uint64_t> &done)
 {
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit))
+        return cudaSuccess;
+    cudaFuncAttributes attr;
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncGetAttributes(&attr, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)attr.sharedSizeBytes);
+    if (e != cudaSuccess)
+        (void)cudaGetLastError();
+    else
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+// A row by a cluster of `size` CTAs.
+template <auto kKernel, class Args>
+cudaError_t launch_cluster(const Args &a, int64_t rows, int size, size_t shared_bytes, int threads, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> allowed{0};
     cudaError_t e = cudaSuccess;
     if (shared_bytes > 32 * 1024)   // with the static part, beyond what a kernel gets unasked
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_bytes);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
+        e = allow_shared(kKernel, allowed);
+    if (e != cudaSuccess)
         return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * size));
     cfg.blockDim = dim3(threads);
@@ -696,7 +722,7 @@ cudaError_t launch_cluster(void (*kernel)(Args), const Args &a, int64_t rows, in
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = size > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    e = cudaLaunchKernelEx(&cfg, kKernel, a);
     count_launch();
     const cudaError_t last = cudaGetLastError();
     return e != cudaSuccess ? e : last;
