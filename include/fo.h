@@ -300,6 +300,10 @@ fo_status_t fo_verify_fast_arithmetic(uint64_t *counts, fo_stream_t stream);
  * Accuracy: statistics and sums are FP32. An exponential of (x - m) / T is
  * within 2^-22 plus 3 roundings of its argument, relatively, and a row's sum is
  * of short chains of them; a gradient is rounded once, to the logits' type.
+ * A teacher's q is within (3 |d| + 3 E|d| + 19) 2^-24, relatively, with d its
+ * logit less its largest, over its temperature, and E the mean under q: where
+ * its logits lie does not matter. With a tail, ln q is within two roundings of
+ * its own size.
  * Every result is the same bit for bit on every run with the same arrays at
  * the same addresses modulo 16: no atomics join partial sums.
  * Rules for masked and special values, in every call:

@@ -88,42 +88,62 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// v / T - minus, for the teacher's T: 1 / T has two parts and the difference is
+// fused with the product, so that the result is rounded at its own size and not
+// at that of v.
+__device__ __forceinline__ float over_temperature(const Teacher &t, float v, float minus)
+{
+    const float d = __fmaf_rn(v, t.inv_t, -minus);
+    return fabsf(v) < kInf ? __fmaf_rn(v, t.inv_t_lo, d) : d;   // -inf times the lower part may be +inf
+}
+
+// The largest logit is subtracted before anything is rounded: a softmax does not
+// depend on where its logits lie, and neither does the precision of q.
 __device__ __forceinline__ TeacherRow make_teacher(const Teacher &t, const TeacherRaw &w, int vocab)
 {
     TeacherRow s;
-    float m = -kInf;
+    float m = -kInf, logit[kSlots];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
         s.id[i] = id_at(t, w, i);
-        const float logit = t.dtype == FO_LOGITS_F32    ? __uint_as_float(w.bits[i])
-                            : t.dtype == FO_LOGITS_BF16 ? Bf16::widen((uint16_t)w.bits[i])
-                                                        : F16::widen((uint16_t)w.bits[i]);
-        s.logq[i] = s.id[i] < 0 ? -kInf : logit * t.inv_t;
-        m = fmaxf(m, s.logq[i]);
+        const float x = t.dtype == FO_LOGITS_F32    ? __uint_as_float(w.bits[i])
+                        : t.dtype == FO_LOGITS_BF16 ? Bf16::widen((uint16_t)w.bits[i])
+                                                    : F16::widen((uint16_t)w.bits[i]);
+        logit[i] = s.id[i] < 0 ? -kInf : x;
+        m = fmaxf(m, logit[i]);
         bad = bad || s.id[i] >= vocab;
     }
-    float norm = w.lse, z = 1.0f;
-    if (!t.tail) {
+    float sum = 0.0f, z = 1.0f;
+    if (t.tail) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            s.logq[i] = over_temperature(t, logit[i], w.lse);
+            s.q[i] = expf(s.logq[i]);
+            sum += s.q[i];
+        }
+        sum = warp_sum(sum);
+    } else {
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         m = safe_max(m);
         z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            z += expf(s.logq[i] - m);
+        for (int i = 0; i < kSlots; ++i) {
+            s.logq[i] = over_temperature(t, logit[i] - m, 0.0f);
+            s.q[i] = expf(s.logq[i]);
+            z += s.q[i];
+        }
         z = warp_sum(z);
-        norm = z == 0.0f ? 0.0f : m + logf(z);
-    }
-    float sum = 0.0f;
+        const float ln_z = z == 0.0f ? 0.0f : logf(z), inv_z = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        s.logq[i] -= norm;
-        s.q[i] = expf(s.logq[i]);
-        sum += s.q[i];
+        for (int i = 0; i < kSlots; ++i) {
+            s.logq[i] -= ln_z;
+            s.q[i] *= inv_z;
+        }
+        sum = z;
     }
-    sum = warp_sum(sum);
     bad = __any_sync(~0u, bad) || !(sum < kInf);
     s.rest = t.tail ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
     s.sum = bad ? __int_as_float(0x7fffffff) : t.tail ? fmaxf(1.0f, sum) : z == 0.0f ? 0.0f : 1.0f;

@@ -53,7 +53,7 @@ struct Teacher {
     const int32_t *ids;
     const void *logits;
     const float *lse;        // may be null
-    float inv_t;
+    float inv_t, inv_t_lo;   // 1 / its temperature, in two parts
     int32_t k, dtype, tail;
 };
 

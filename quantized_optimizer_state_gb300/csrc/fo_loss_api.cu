@@ -144,7 +144,8 @@ fo::GradRows grad_of(const fo_logits_grad_t *g)
 
 fo::Teacher teacher_of(const fo_teacher_t &t)
 {
-    return fo::Teacher{t.ids, t.logits, t.tail ? t.lse : nullptr, (float)(1.0 / t.temperature), t.k, t.dtype, t.tail};
+    const float inv_t = (float)(1.0 / t.temperature);
+    return fo::Teacher{t.ids, t.logits, t.tail ? t.lse : nullptr, inv_t, (float)(1.0 / t.temperature - (double)inv_t), t.k, t.dtype, t.tail};
 }
 
 Range logits_range(const fo_logits_t &x) { return Range(x.data, span(x, x.row_stride, x.outer_stride) * element_size(x.dtype), false); }
