@@ -363,8 +363,11 @@ typedef struct fo_logits_grad {
  * softmax(logits / temperature) over the row's ids; with tail = 1 it is
  * q_k = exp(logits_k / temperature - lse) and the rest of the mass,
  * max(0, 1 - sum q), is one more outcome, compared with the student's
- * probability of all tokens that are not listed. An id listed twice counts
- * twice in q. */
+ * probability of all tokens that are not listed. Where that probability is 0
+ * (below e^-746), a rest of at most 2^-16 is none: roundings leave that much
+ * beside a list that holds all tokens a mask allows. A larger one counts as it
+ * is, and makes KL infinite where all unlisted logits are -inf. An id listed
+ * twice counts twice in q. */
 typedef struct fo_teacher {
     const int32_t *ids;
     const void *logits;

@@ -33,6 +33,11 @@ constexpr int64_t kMinPart = 16 * 1024;           // bytes of a row that are wor
 constexpr int kGradThreads = 256;
 constexpr float kLn2High = 0x1.62e4p-1f;          // 15 bits of ln 2
 constexpr float kLn2Low = (float)(0.69314718055994531 - 0x1.62e4p-1);
+// Log probabilities that add up to 1 leave a rest of up to 2^-18 by their own
+// roundings (and one at the size of lse), although the list holds all that a
+// mask has left. Where the student's rest is 0, in 64 bits too (e^-746), KL would
+// be infinite, or as large as the mask's value, for that.
+constexpr float kNoRest = 0x1p-16f, kNoLogRest = -746.0f;
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -454,7 +459,13 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
             const float m = kTail ? fmaxf(s.x, l.m) : s.x, mm = safe_max(m), m_rest = safe_max(s.x);
             const float down = exp2_approx(distance(s.x, mm, a.in) * a.in.c);
             const float z = kTail ? __fmaf_rn(s.y, down, l.z * exp2_approx(distance(l.m, mm, a.in) * a.in.c)) : s.y;
-            const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = ok ? t.sum : __int_as_float(0x7fffffff), q_rest = t.rest;
+            const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = ok ? t.sum : __int_as_float(0x7fffffff);
+            const auto ln_rest = [&](float ln_z) {   // ln p_rest
+                return s.y == 0.0f ? -kInf : __fmaf_rn(quarter_distance(s.x, m), 4.0f * a.in.inv_t, logf(s.y)) - ln_z;
+            };
+            float q_rest = t.rest;
+            if (kTail && q_rest <= kNoRest && ln_rest(logf(z)) < kNoLogRest)
+                q_rest = 0.0f;
             // an unlisted token: p - q_rest p / p_rest, by 2^((x - m_rest) c)
             const float f = __fsub_rn(down * (sum * inv_z), !kTail || s.y == 0.0f ? 0.0f : q_rest / s.y);
             const float scale = weight * a.in.inv_t;
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                 if (z == 0.0f && sum != 0.0f)
                     kl = kInf;
                 if (kTail && q_rest > 0.0f)
-                    kl = s.y == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - (__fmaf_rn(quarter_distance(s.x, m), four, logf(s.y)) - ln_z));
+                    kl = s.y == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - ln_rest(ln_z));
                 if (sum != sum || z != z)
                     kl = __int_as_float(0x7fffffff);
                 if (a.loss)

@@ -1,4 +1,5 @@
-"""The teacher's distribution in the distillation losses: its precision, wherever its logits lie."""
+"""The teacher's distribution in the distillation losses: its precision wherever its logits lie, and lists that
+hold all that the teacher has."""
 import math
 
 import pytest
@@ -9,7 +10,8 @@ from tests import loss_reference as ref
 from tests.test_gpu_logprobs import gen
 
 pytestmark = pytest.mark.gpu
-U = 2.0 ** -24
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+INF, U = math.inf, 2.0 ** -24
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -71,3 +73,41 @@ def test_precision_with_a_tail(shift, temperature):
     ref.close(loss, want, tol, "loss")
     allowed = (16 * U / v + off_rest / (v - k))[:, None].expand_as(grad).clone().scatter_add_(1, ids.long(), q * off_q)
     ref.close(g, grad, allowed + 2 * U * grad.abs(), "gradient")
+
+
+@pytest.mark.parametrize("fill", [-INF, "lowest"])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_a_list_that_holds_all_that_a_mask_leaves(dtype, fill):
+    """A grammar leaves fewer tokens than are listed, to the teacher and to the student: what the roundings of its log
+    probabilities leave beside a sum of 1 is no mass, and the loss is not infinite for it."""
+    fill = torch.finfo(dtype).min if fill == "lowest" else fill
+    n, v, k = 400, 1003, 8
+    live = torch.rand((n, v), generator=gen(1), device="cuda").topk(k, dim=1).indices
+    left = 1 + torch.arange(n, device="cuda") % k                  # tokens that the mask leaves, 1 to k
+    live = torch.where(torch.arange(k, device="cuda") < left[:, None], live, live[:, :1])
+    rows = []
+    for seed in (2, 3):
+        x = torch.full((n, v), fill, dtype=dtype, device="cuda")
+        rows.append(x.scatter_(1, live, (torch.randn((n, v), generator=gen(seed), device="cuda") * 2).to(dtype).gather(1, live)))
+    told = losses.token_logprobs(rows[0], top_k=k)
+    loss, grad = losses.distill_loss_grad(rows[1], told.top_ids, told.top_logp, tail=True)
+    p = torch.softmax(rows[0].double(), 1)
+    lp = torch.log_softmax(rows[1].double(), 1)
+    want = torch.where(p > 0, p * (torch.log_softmax(rows[0].double(), 1) - lp), 0.0).sum(1)
+    # each log probability within 2^-18 of its own, in the teacher's list and in the student's row
+    assert ((loss.double() - want).abs() <= 2.0 ** -17 * (1 + (p * lp.abs().clamp(max=1e4)).sum(1))).all()
+    assert torch.isfinite(grad.float()).all()
+    alone = losses.distill_loss(rows[1], told.top_ids, told.top_logp, tail=True)
+    assert ((alone - loss).abs() <= 2.0 ** -17 * (1 + loss.abs())).all()
+    same, grad = losses.distill_loss_grad(rows[0], told.top_ids, told.top_logp, tail=True)
+    assert same.abs().max() < 2.0 ** -16 and grad.float().abs().max() < 2.0 ** -16
+
+
+def test_a_rest_that_the_student_excludes_is_infinite():
+    """More than roundings leave: a teacher that holds tokens possible which the student excludes."""
+    x = torch.full((3, 100), -INF, device="cuda")
+    x[:, :2] = 0.0
+    ids = torch.tensor([[0, 1]] * 3, dtype=torch.int32, device="cuda")
+    y = torch.log(torch.tensor([[0.5, 0.4], [0.5, 0.4999], [0.5, 0.5]], device="cuda"))
+    loss = losses.distill_loss(x, ids, y, tail=True)
+    assert loss[:2].tolist() == [INF, INF] and abs(float(loss[2])) < 1e-6
