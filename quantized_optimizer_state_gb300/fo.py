@@ -505,6 +505,14 @@ def _teacher(ids, logits, lse, rows: int, temperature: float, tail: bool, cur: i
                      _array(lse, "teacher_lse", torch.float32, rows, cur), temperature, k, dt, 1 if tail else 0, 0)
 
 
+def _modified(*tensors) -> None:
+    """Tells autograd that the library has written to these tensors, which it
+    cannot see from an address: a graph that saved one of them for its backward
+    pass then says so."""
+    import torch
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def fo_token_logprobs(logits, tokens=None, top_k: int = 0, logp=None, entropy=None, top_ids=None, top_logp=None,
                       stats=None, temperature: float = 1.0, stream=None):
     import torch
@@ -517,6 +525,7 @@ def fo_token_logprobs(logits, tokens=None, top_k: int = 0, logp=None, entropy=No
         _stream(stream))
     if status:
         _check("fo_token_logprobs", status)
+    _modified(logp, entropy, top_ids, top_logp, stats)
 
 
 def fo_token_logprobs_grad(logits, stats, grad, tokens=None, g_logp=None, g_entropy=None, top_ids=None, g_top=None,
@@ -532,6 +541,7 @@ def fo_token_logprobs_grad(logits, stats, grad, tokens=None, g_logp=None, g_entr
         _array(g_top, "g_top", f32, n * top_k, cur), None if g is None else ctypes.byref(g), _stream(stream))
     if status:
         _check("fo_token_logprobs_grad", status)
+    _modified(grad)
 
 
 def fo_distill(logits, teacher_ids, teacher_logits, teacher_lse=None, row_weight=None, loss=None, stats=None,
@@ -546,6 +556,7 @@ def fo_distill(logits, teacher_ids, teacher_logits, teacher_lse=None, row_weight
         _array(stats, "stats", f32, n * FO_LOSS_STATS, cur), None if g is None else ctypes.byref(g), _stream(stream))
     if status:
         _check("fo_distill", status)
+    _modified(loss, stats, grad)
 
 
 def fo_distill_grad(logits, teacher_ids, teacher_logits, stats, g_loss, grad, teacher_lse=None,
@@ -560,6 +571,7 @@ def fo_distill_grad(logits, teacher_ids, teacher_logits, stats, g_loss, grad, te
         _array(g_loss, "g_loss", f32, n, cur), None if g is None else ctypes.byref(g), _stream(stream))
     if status:
         _check("fo_distill_grad", status)
+    _modified(grad)
 
 
 FO_VERIFY_COUNTS = 6

@@ -163,6 +163,8 @@ def _distill(logits, ids, teacher, lse, weight, temperature, teacher_temperature
                                  None if to is None else ctypes.byref(to), fo._stream(None))
     if status:
         fo._check("fo_distill", status)
+    if out is not None:
+        fo._modified(out)
     return loss, grad, stats
 
 
@@ -232,7 +234,8 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
 
     ``row_weight`` (float32, 1 where None): for a mean over n tokens 1 / n, and
     0 for padding, whatever its logits hold. ``out``: where to write the
-    gradient; it may be ``logits`` itself, which the gradient then replaces.
+    gradient; it may be ``logits`` itself, which the gradient then replaces (and
+    a graph that keeps the logits for its own backward pass refuses to run it).
     """
     _check_teacher(logits, teacher_ids, teacher_logits, teacher_lse)
     _check_rows("row_weight", row_weight, logits.shape[:-1])
