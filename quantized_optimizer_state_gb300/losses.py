@@ -16,7 +16,8 @@ library's kernels: what stands between a model's head and the optimizers of
 Logits are bfloat16, float16 or float32 CUDA tensors ``[..., vocab]`` whose
 last dimension is contiguous; a slice like ``logits[:, :-1]`` is read where it
 lies. The rules for masked, infinite and invalid entries stand in
-``include/fo.h``. Work is enqueued on the current stream.
+``include/fo.h``. Work is enqueued on the current stream. Derivatives are of the
+first order and in reverse mode; a tangent of forward mode is refused.
 """
 from __future__ import annotations
 
@@ -25,6 +26,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import fo
 
@@ -39,6 +41,12 @@ class TokenLogprobs(NamedTuple):
 def _check_rows(name: str, x: Optional[torch.Tensor], shape) -> None:
     if x is not None and x.shape != shape:
         raise ValueError(f"{name} must have the logits' leading shape {tuple(shape)}, not {tuple(x.shape)}")
+
+
+def _check_tangent(logits: torch.Tensor) -> None:
+    """A tensor with a tangent need not require a gradient, and its address carries none."""
+    if forward_ad.unpack_dual(logits).tangent is not None:
+        raise NotImplementedError("the losses have no forward-mode derivative: logits carry a tangent")
 
 
 # The functions below hand the C calls the addresses of tensors that they have
@@ -134,6 +142,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     ascending id. Differentiable in the logits through ``logp``, ``entropy``
     and ``top_logp``.
     """
+    _check_tangent(logits)
     rows = logits.shape[:-1]
     if tokens is not None:
         _check_rows("tokens", tokens, rows)
@@ -196,6 +205,7 @@ class _Distill(torch.autograd.Function):
 
 
 def _check_teacher(logits, ids, teacher, lse) -> None:
+    _check_tangent(logits)
     if ids.shape[:-1] != logits.shape[:-1] or teacher.shape != ids.shape:
         raise ValueError(f"teacher_ids and teacher_logits must be [..., k] over the logits' leading shape "
                          f"{tuple(logits.shape[:-1])}, not {tuple(ids.shape)} and {tuple(teacher.shape)}")

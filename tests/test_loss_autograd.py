@@ -1,8 +1,44 @@
-"""What automatic differentiation is told: tensors that the losses overwrite count as modified."""
+"""What automatic differentiation is told: derivatives that the losses do not have are refused, and tensors that
+they overwrite count as modified."""
 import pytest
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from quantized_optimizer_state_gb300 import fo, losses
+
+CALLS = {
+    "token_logprobs": lambda x: losses.token_logprobs(x, torch.zeros(3, dtype=torch.long, device=x.device), top_k=2),
+    "distill_loss": lambda x: losses.distill_loss(x, torch.zeros(3, 2, dtype=torch.int32, device=x.device), torch.zeros(3, 2, device=x.device)),
+    "distill_loss_grad": lambda x: losses.distill_loss_grad(x, torch.zeros(3, 2, dtype=torch.int32, device=x.device),
+                                                            torch.zeros(3, 2, device=x.device)),
+}
+
+
+def refused(call, device):
+    x, tangent = torch.randn(3, 10, device=device), torch.ones(3, 10, device=device)
+    with forward_ad.dual_level():
+        for leaf in (x, x.clone().requires_grad_(True)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call(forward_ad.make_dual(leaf, tangent))
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+                call(forward_ad.make_dual(leaf, tangent))
+    return x
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_forward_mode_is_refused(name):
+    refused(CALLS[name], "cpu")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CALLS)
+def test_forward_mode_is_refused_on_the_gpu(name):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    x = refused(CALLS[name], "cuda")
+    CALLS[name](x)                            # no level is open any more
+    with forward_ad.dual_level():
+        CALLS[name](x)                        # and without a tangent there is nothing to lose
 
 
 @pytest.mark.gpu
