@@ -38,6 +38,7 @@ constexpr float kLn2Low = (float)(0.69314718055994531 - 0x1.62e4p-1);
 // mask has left. Where the student's rest is 0, in 64 bits too (e^-746), KL would
 // be infinite, or as large as the mask's value, for that.
 constexpr float kNoRest = 0x1p-16f, kNoLogRest = -746.0f;
+constexpr float kNan = __builtin_nanf("");
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -151,7 +152,7 @@ __device__ __forceinline__ TeacherRow make_teacher(const Teacher &t, const Teach
     }
     bad = __any_sync(~0u, bad) || !(sum < kInf);
     s.rest = t.tail ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
-    s.sum = bad ? __int_as_float(0x7fffffff) : t.tail ? fmaxf(1.0f, sum) : z == 0.0f ? 0.0f : 1.0f;
+    s.sum = bad ? kNan : t.tail ? fmaxf(1.0f, sum) : z == 0.0f ? 0.0f : 1.0f;
     return s;
 }
 
@@ -319,7 +320,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
         __syncthreads();
 
     const int passes = a.grad.data ? 2 : 1;
-    bool ok = true;          // false: a wait ran out
+    // false: a wait ran out. What the warp has not done of its rows by then, of
+    // their sums, losses, statistics and gradients, becomes NaN; the others' waits
+    // for it run out in turn.
+    bool ok = true;
     uint32_t active = 0;     // rows done with a weight other than 0
     float next_weight = a.weight ? a.weight[first] : 1.0f;
     if (warp == kFetcher) {
@@ -384,7 +388,9 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
             const bool writes = (uint32_t)r % size == rank && lane == 0;   // the loss, in turn
             if (weight == 0.0f || !ok) {   // the same in all CTAs of the cluster
                 if (writes && a.loss)
-                    a.loss[r] = ok ? 0.0f : __int_as_float(0x7fffffff);
+                    a.loss[r] = ok ? 0.0f : kNan;
+                if (writes && a.stats && weight != 0.0f)
+                    a.stats[r] = make_float4(kNan, kNan, kNan, kNan);
                 if (r + step < rows && next_weight != 0.0f)
                     start(r + step, next);
                 continue;
@@ -425,11 +431,13 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
             l.dot = warp_sum(l.dot);
             ql = warp_sum(ql);
 
-            ok = warp_wait(&sh.summed, active & 1) && ok;
+            ok = warp_wait(&sh.summed, active & 1);
             float2 s = make_float2(-kInf, 0.0f);
             if (lane < kWarps)
                 s = sh.part[lane];
             s = join_pairs(s.x, s.y, a.in);
+            if (!ok)   // NaN for the row's other CTAs too
+                s.y = kNan;
             if (size > 1) {
                 const int turn = active & 1;
                 if (lane < (int)size) {
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                     fence_cluster();
                     arrive_cluster(map_shared(&sh.cluster[turn], lane));
                 }
-                ok = warp_wait(&sh.cluster[turn], (active >> 1) & 1) && ok;
+                ok = ok && warp_wait(&sh.cluster[turn], (active >> 1) & 1);
                 fence_cluster();
                 float4 v = make_float4(-kInf, 0.0f, 0.0f, 0.0f);
                 s = make_float2(-kInf, 0.0f);
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
             const float m = kTail ? fmaxf(s.x, l.m) : s.x, mm = safe_max(m), m_rest = safe_max(s.x);
             const float down = exp2_approx(distance(s.x, mm, a.in) * a.in.c);
             const float z = kTail ? __fmaf_rn(s.y, down, l.z * exp2_approx(distance(l.m, mm, a.in) * a.in.c)) : s.y;
-            const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = ok ? t.sum : __int_as_float(0x7fffffff);
+            const float inv_z = z == 0.0f ? 0.0f : 1.0f / z, sum = ok ? t.sum : kNan;
             const auto ln_rest = [&](float ln_z) {   // ln p_rest
                 return s.y == 0.0f ? -kInf : __fmaf_rn(quarter_distance(s.x, m), 4.0f * a.in.inv_t, logf(s.y)) - ln_z;
             };
@@ -493,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                 if (kTail && q_rest > 0.0f)
                     kl = s.y == 0.0f ? kInf : kl + q_rest * (logf(q_rest) - ln_rest(ln_z));
                 if (sum != sum || z != z)
-                    kl = __int_as_float(0x7fffffff);
+                    kl = kNan;
                 if (a.loss)
                     a.loss[r] = kl * weight;
                 if (a.stats)
@@ -515,12 +523,12 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
             if (r + step < rows && next_weight != 0.0f)
                 start(r + step, next);
             if (passes == 2) {
-                ok = warp_wait(&sh.written, active & 1) && ok;
+                ok = ok && warp_wait(&sh.written, active & 1);
                 raw *const g = static_cast<raw *>(a.grad.data) + row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
 #pragma unroll
                 for (int i = 0; i < kSlots; ++i)   // the listed tokens' places once more, after the vectors
-                    if (ok && done[i] >= 0 && !(again >> i & 1))
-                        g[done[i]] = T::narrow(z == 0.0f ? 0.0f : grad_listed<T>(xf[i], mm, q_all[i], sum, inv_z, scale, a.in));
+                    if (done[i] >= 0 && !(again >> i & 1))
+                        g[done[i]] = T::narrow(!ok ? kNan : z == 0.0f ? 0.0f : grad_listed<T>(xf[i], mm, q_all[i], sum, inv_z, scale, a.in));
             }
             ++active;
         }
@@ -581,11 +589,11 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                 ok = ok && warp_wait(&sh.joined, (active - 1) & 1);
             const Stat s = warp_join<false>(run.stat(a.in), a.in);
             if (lane == 0) {
-                sh.part[warp] = make_float2(s.m, s.z);
+                sh.part[warp] = make_float2(s.m, ok ? s.z : kNan);
                 barrier_arrive(&sh.summed);
             }
             if (passes == 2) {
-                ok = warp_wait(&sh.joined, active & 1) && ok;
+                ok = ok && warp_wait(&sh.joined, active & 1);
                 const f2 nm = splat(-sh.m), f = splat(sh.f);
                 for (int i0 = 0; i0 < p.n && ok; i0 += kStageVecs, c.next()) {
                     ok = warp_wait(&sh.full[c.at], c.turn);
@@ -606,6 +614,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
                     if (lane == 0)
                         barrier_arrive(&sh.empty[c.at]);
                 }
+                for (int i = p.v0 + tid; !ok && i < p.v0 + p.n; i += kStream)
+                    write(i, make_uint4(0x7fffffff, 0x7fffffff, 0x7fffffff, 0x7fffffff));   // NaN in every type
                 __syncwarp();
                 if (lane == 0)
                     barrier_arrive(&sh.written);
