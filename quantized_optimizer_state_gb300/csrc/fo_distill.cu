@@ -13,7 +13,7 @@ namespace {
 // spills) with 3 such stages: 809 / 393 / 214 against 709 / 358 / 203 at the
 // same rows in turn; 8 stages of 8 KB: 761 / 383 / 224 against 749 / 358 / 202;
 // 2 CTAs of 16 warps: 813 / 493 / 212 against 778 / 393 / 225. (Each pair is of
-// one build; what came later took 688 / 280 / 198.) Two rows in turn against 1
+// one build; what came later took 667 / 283 / 194.) Two rows in turn against 1
 // and 4: 687 / 279 / 196 against 733 / 287 / 201 and 689 / 282 / 197: the
 // fetching runs on into the second row, and short turns spread the grid's end.
 constexpr int kLong = 8, kShort = 2;              // warps that walk over a row: see launch
@@ -265,8 +265,9 @@ __device__ __forceinline__ uint32_t merge_twice(Shared &sh, const TeacherRow &t,
 // it reads the row again, but from the L2 cache: the launch keeps the rows at
 // work at once well below its size, and the first pass asks it to keep their
 // lines, the second to let them go (98 % of the second pass hits; device memory
-// gives 1.02 times the logits). 8192 x 128256 BF16: 0.674 ms, 0.89 of the
-// measured copy rate for one read and one write (0.689 without these requests).
+// gives 1.02 times the logits). 8192 x 128256 BF16: 0.667 ms, 0.90 of the
+// measured copy rate for one read and one write (an earlier build took 0.674, and
+// 0.689 without these requests).
 // It is bound by the mixed traffic: the second pass adds half as much again in
 // the L2 cache, which moves 10.2 TB/s, and instructions issue in half of the
 // cycles. Rows held in shared memory between the passes were slower (1.02 ms at
@@ -713,9 +714,9 @@ cudaError_t launch(DistillArgs a, int size, bool marks, int64_t ctas, cudaStream
 {
     const int64_t vecs = part_vecs(a.in.vocab * (int64_t)sizeof(typename T::raw), size);
     a.mark_words = marks ? (int)(vecs + 3) / 4 : 0;
-    // The CTAs that fit take all rows, below the size where they drift apart;
-    // above it a few rows each, so that short turns spread the grid's end. In us
-    // with a few each / all: loss alone, 2048 x 50257 F16 44.1 / 39.5, 8192 x
+    // The CTAs that fit take all rows up to kOneTurn, a bound that lies between the
+    // sizes measured faster so and those measured slower; above it a few rows
+    // each, so that short turns spread the grid's end. In us with a few each / all: loss alone, 2048 x 50257 F16 44.1 / 39.5, 8192 x
     // 50257 BF16 133 / 124, 8192 x 1000 25.6 / 22.7, 8192 x 100000 236 / 253; with
     // gradient, 1400 x 80000 90.4 / 85.8, 4096 x 16000 61.5 / 58.0, 4096 x 64128
     // 170 / 188.

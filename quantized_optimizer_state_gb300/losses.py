@@ -55,8 +55,10 @@ def _check_tangent(logits: torch.Tensor) -> None:
 def _empty_grad(logits: torch.Tensor, x: fo.FoLogits):
     """An uninitialised gradient for ``logits`` and its layout. Its rows start at
     the same alignment (modulo 16 bytes) as the logits', so that the kernels'
-    vectors of both line up: rows of an odd vocabulary in a padded matrix would
-    otherwise not. At most 7 elements are added to a row."""
+    vectors of both line up, where these are contiguous from an aligned base or
+    the rows of a padded matrix with one (at most 7 elements are added to a row).
+    In other layouts of an odd vocabulary the two do not line up, and most rows
+    are stored element by element (3.5 times as long)."""
     vocab = x.vocab
     if x.inner_rows == x.rows and x.rows > 1 and x.row_stride > vocab and logits.dim() == 2:
         pitch = vocab + (x.row_stride - vocab) % (16 // logits.element_size())
