@@ -303,7 +303,7 @@ def _exact_kept(x):
         n, w = piece.shape
         y = torch.nn.functional.pad(piece, (0, -w % 32)).reshape(n, -1, 32)
         mantissa, exponent = torch.frexp((y.abs().max(2).values / 127).clamp(min=2.0 ** -126))
-        step = torch.ldexp(torch.ceil(mantissa * 256) / 256, exponent)
+        step = torch.ldexp(torch.ceil(mantissa * 256) / 256, exponent).float().double()   # undoes a rounding of the power
         r = (1 / step).float().double()
         parts.append((torch.round(y * r[:, :, None]) * step[:, :, None]).reshape(n, -1)[:, :w])
     return torch.cat(parts, 1)
