@@ -15,8 +15,9 @@
  *     and v, rebuild theta, apply the standard AdamW / SGD / Lion update,
  *     requantize m and v and re-split theta, in one pass over memory;
  *
- * and the losses on a language model's logits whose gradients that step
- * consumes (last section, with rules of their own on accuracy and alignment).
+ * the losses on a language model's logits whose gradients that step consumes,
+ * and operators whose activations are kept for the backward pass in 8 bits (last
+ * two sections, with rules of their own on accuracy and alignment).
  *
  * Exact arithmetic contract of the step and its codecs (bit for bit):
  *   theta' = BF16(theta), round to nearest even.
@@ -287,14 +288,17 @@ fo_status_t fo_verify_fast_arithmetic(uint64_t *counts, fo_stream_t stream);
 /* --- losses on the logits of a language model ---------------------------------
  *
  * The step above consumes gradients; these calls stand at the other end of the
- * backward pass. Both work on rows of logits x[vocab] at a temperature T:
+ * backward pass. All work on rows of logits x[vocab] at a temperature T:
  * s = x / T, m = max s, Z = sum exp(s - m), p = exp(s - m) / Z.
  *   - fo_token_logprobs: log p of given tokens, the entropy, the top
  *     alternatives (what a distillation teacher writes down), and
  *     fo_token_logprobs_grad, their gradient;
  *   - fo_distill: KL(q || p) for a teacher distribution q known by its top
  *     logits, optionally with its gradient in the same pass, and
- *     fo_distill_grad, the gradient alone.
+ *     fo_distill_grad, the gradient alone;
+ *   - fo_policy_loss: the clipped loss of policy training on sampled tokens,
+ *     with a KL term, optionally with its gradient in the same pass, and
+ *     fo_policy_loss_grad, the gradient alone.
  * Arrays need the alignment of their element type only, stats that of 16
  * bytes. Nothing here needs a workspace.
  * Accuracy: statistics and sums are FP32. An exponential of (x - m) / T is
@@ -427,6 +431,127 @@ fo_status_t fo_distill(const fo_logits_t *logits, const fo_teacher_t *teacher, c
  */
 fo_status_t fo_distill_grad(const fo_logits_t *logits, const fo_teacher_t *teacher, const float *stats,
                             const float *g_loss, const fo_logits_grad_t *grad, fo_stream_t stream);
+
+/* Tokens that an earlier state of the policy sampled, one by row, and how the
+ * loss of a row is formed. With l = log p[token], q = exp(l - old_logp), A the
+ * advantage:
+ *   loss = -min(q A, clip(q, 1 - clip_low, 1 + clip_high) A)
+ *          + kl_weight (exp(ref_logp - l) - (ref_logp - l) - 1),
+ *   dloss/dl = -A q where the minimum is taken by q A (at the border too), else 0,
+ *              + kl_weight (1 - exp(ref_logp - l)).
+ * A negative token is no position (padding): loss, log probability and gradient
+ * are 0, and the row is not read. An advantage of 0 has no policy term, whatever
+ * q is; ref_logp is read where kl_weight is not 0. A row whose dloss/dl is NaN or
+ * beyond FP32 gets a gradient of NaN (of 0 where the row has no distribution). */
+typedef struct fo_policy {
+    const int64_t *tokens;      /* [rows]                                   */
+    const float *old_logp;      /* [rows]: of the policy that sampled       */
+    const float *advantages;    /* [rows]                                   */
+    const float *ref_logp;      /* [rows], of a reference; NULL: no KL term */
+    double clip_low, clip_high; /* in [0, 1]; finite, not negative          */
+    double kl_weight;           /* finite, not negative                     */
+} fo_policy_t;
+
+/*
+ * fo_policy_loss -- loss[r] = w[r] (the loss above), w = row_weight or 1 where
+ * that is NULL, and logp[r] = log p[token]. With `grad`, also the gradient of
+ * sum_r loss[r] with respect to the logits, in the same call: the logits come
+ * from device memory once and the gradient goes there once. A row of weight 0 is
+ * not read: its loss, logp and gradient are 0. stats[rows, FO_LOSS_STATS],
+ * optional, is what fo_policy_loss_grad needs (of the unweighted loss). loss,
+ * logp and grad may each be NULL. Errors as fo_token_logprobs.
+ */
+fo_status_t fo_policy_loss(const fo_logits_t *logits, const fo_policy_t *policy, const float *row_weight, float *loss,
+                           float *logp, float *stats, const fo_logits_grad_t *grad, fo_stream_t stream);
+
+/*
+ * fo_policy_loss_grad -- the gradient of sum_r g_loss[r] loss[r] with respect to
+ * the logits, from the stats that fo_policy_loss wrote for them (with no
+ * row_weight, or of rows whose weight was not 0). Errors as fo_token_logprobs.
+ */
+fo_status_t fo_policy_loss_grad(const fo_logits_t *logits, const int64_t *tokens, const float *stats,
+                                const float *g_loss, const fo_logits_grad_t *grad, fo_stream_t stream);
+
+/* --- activations kept in 8 bits ------------------------------------------------
+ *
+ * What a training step keeps for its backward pass, in the manner of the
+ * optimizer state: int8 codes with one BF16 step for every 32 elements of a row
+ * (FO_GROUP; the last group of a row may be partial).
+ *   a    = max |x| of the group
+ *   step = the smallest BF16 number that is at least max(a / 127, 2^-126)
+ *   code = rint(x r), half to even, r = 1 / step rounded to FP32; the product is
+ *          not rounded before
+ *   x^   = code * step, exact in FP32
+ * so |x^ - x| is at most (1 + 2^-15) step / 2. A NaN or an infinity in a group
+ * makes its step NaN, and with it all that the group stands for.
+ *
+ * Matrices are rows of contiguous elements of BF16, FP16 or FP32 (fo_rows_t), all
+ * of one call of one type, aligned to it. Rows that are only read may overlap;
+ * rows that are written may not, and share no byte with another array. For a
+ * matrix of `width` columns and G = ceil(width / 32), codes is [rows, 32 G] (0
+ * beyond the width), aligned to 16 bytes, and steps [rows, G]. All arithmetic is
+ * FP32, results are rounded once, to the matrices' type. Every result is the
+ * same bit for bit on every run of the same call on the same kind of device.
+ * Rows beside others have no effect on them.
+ */
+typedef struct fo_rows {
+    void *data;             /* only read where the call names the matrix in, up or grad_y */
+    int64_t rows, width;    /* rows * ceil(width / 32) <= FO_MAX_ACT_GROUPS            */
+    int64_t row_stride;     /* elements, not negative                                  */
+    int32_t dtype;          /* fo_logit_dtype_t                                        */
+    int32_t reserved;       /* 0                                                       */
+} fo_rows_t;
+
+#define FO_MAX_ACT_GROUPS (1 << 29)
+#define FO_NORM_PARTS 1024  /* rows of fo_rms_norm_grad's workspace, at most */
+
+/* Activation functions. */
+typedef enum fo_act {
+    FO_ACT_SILU = 0,        /* x / (1 + e^-x)                               */
+    FO_ACT_GELU = 1         /* x Phi(x), Phi the normal distribution's      */
+} fo_act_t;
+
+/*
+ * fo_compress -- codes and steps of x. fo_expand -- x^, rounded to x's type,
+ * into x. Errors of every call of this section: FO_ERR_NULL, FO_ERR_MISALIGNED,
+ * FO_ERR_SIZE (rows < 0, width < 1, too many groups), FO_ERR_BAD_ARG (dtype,
+ * stride, reserved, matrices of unlike sizes or types, eps), FO_ERR_ALIAS,
+ * FO_ERR_CUDA. rows = 0 is a no-op.
+ */
+fo_status_t fo_compress(const fo_rows_t *in, int8_t *codes, uint16_t *steps, fo_stream_t stream);
+fo_status_t fo_expand(const int8_t *codes, const uint16_t *steps, const fo_rows_t *x, fo_stream_t stream);
+
+/*
+ * fo_activation -- y = f(x), or y = f(x) up where `up` is not NULL (a gated MLP:
+ * x the gate), and, where codes is not NULL, the codes of x and of up. The
+ * function is taken of x itself, not of its code.
+ * fo_activation_grad -- from the codes: grad_x = grad_y f'(x^) (times up^), and
+ * grad_up = grad_y f(x^). grad_up, up_codes and up_steps are NULL without `up`.
+ * x and up may be the halves of one matrix, and so may grad_x and grad_up.
+ */
+fo_status_t fo_activation(fo_act_t kind, const fo_rows_t *in, const fo_rows_t *up, const fo_rows_t *y, int8_t *codes,
+                          uint16_t *steps, int8_t *up_codes, uint16_t *up_steps, fo_stream_t stream);
+fo_status_t fo_activation_grad(fo_act_t kind, const int8_t *codes, const uint16_t *steps, const int8_t *up_codes,
+                               const uint16_t *up_steps, const fo_rows_t *grad_y, const fo_rows_t *grad_x,
+                               const fo_rows_t *grad_up, fo_stream_t stream);
+
+/*
+ * fo_rms_norm -- y = x r weight, r = 1 / sqrt(mean x^2 + eps) over a row; weight
+ * [width] of weight_dtype (fo_logit_dtype_t), NULL: 1. eps in [2^-80, 2^20].
+ * Where codes is not NULL: the codes of x and inv_rms[rows] = r. A row with a NaN
+ * or an infinity gives NaN.
+ * fo_rms_norm_grad -- from the codes, with h = x^ r (r as it was):
+ *   grad_x = r (grad_y w - h mean(grad_y w h)),  grad_weight = sum over rows of grad_y h.
+ * grad_x or grad_weight may be NULL. workspace: FP32, fo_rms_norm_workspace(rows,
+ * width) elements (NULL without grad_weight); its contents are of no use after
+ * the call. With rows = 0, grad_weight is 0.
+ */
+fo_status_t fo_rms_norm(const fo_rows_t *in, const void *weight, int32_t weight_dtype, double eps, const fo_rows_t *y,
+                        float *inv_rms, int8_t *codes, uint16_t *steps, fo_stream_t stream);
+int64_t fo_rms_norm_workspace(int64_t rows, int64_t width);
+fo_status_t fo_rms_norm_grad(const int8_t *codes, const uint16_t *steps, const float *inv_rms, const void *weight,
+                             int32_t weight_dtype, const fo_rows_t *grad_y, const fo_rows_t *grad_x, void *grad_weight,
+                             float *workspace, fo_stream_t stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 const char *fo_status_string(fo_status_t status);

@@ -38,7 +38,6 @@ constexpr float kLn2Low = (float)(0.69314718055994531 - 0x1.62e4p-1);
 // mask has left. Where the student's rest is 0, in 64 bits too (e^-746), KL would
 // be infinite, or as large as the mask's value, for that.
 constexpr float kNoRest = 0x1p-16f, kNoLogRest = -746.0f;
-constexpr float kNan = __builtin_nanf("");
 constexpr int kSlots = FO_MAX_TOP_K / 32;         // entries of a lane of one warp that holds them all
 
 // A teacher's row in one warp: entry lane + 32 i at place i.
@@ -84,14 +83,6 @@ __device__ __forceinline__ TeacherRaw load_teacher(const Teacher &t, int64_t r)
 __device__ __forceinline__ int32_t id_at(const Teacher &t, const TeacherRaw &w, int i)
 {
     return (int)(threadIdx.x & 31) + 32 * i < t.k ? w.id[i] : -1;
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v += __shfl_xor_sync(~0u, v, o);
-    return v;
 }
 
 // v / T - minus, for the teacher's T: 1 / T has two parts and the difference is
@@ -156,25 +147,6 @@ __device__ __forceinline__ TeacherRow make_teacher(const Teacher &t, const Teach
     return s;
 }
 
-// 2^t f for a vector of logits: the gradient of tokens that are not listed.
-template <class T>
-__device__ __forceinline__ uint4 grad_vec(const uint4 &v, f2 nm, f2 f, const LogitRows &in)
-{
-    f2 x[T::kPerVec / 2];
-    widen_vec<T>(v, x);
-#pragma unroll
-    for (int k = 0; k < T::kPerVec / 2; ++k) {
-        f2 d = add2(x[k], nm), t;
-        if (sizeof(typename T::raw) == 4) {
-            float a, b;
-            unpk(d, a, b);
-            d = pk(max_nan(a, in.d_min), max_nan(b, in.d_min));
-        }
-        x[k] = mul2(grad_exp2<T>(d, in, t), f);
-    }
-    return narrow_vec<T>(x);
-}
-
 template <class T>
 __device__ __forceinline__ float grad_listed(float x, float m, float q, float a, float inv_z, float scale, const LogitRows &in)
 {
@@ -200,16 +172,6 @@ struct Shared {
     __align__(16) int32_t ids[FO_MAX_TOP_K];
     float q[FO_MAX_TOP_K];
 };
-
-// m, z pairs joined over a warp: the largest m, and z at that.
-__device__ __forceinline__ float2 join_pairs(float m, float z, const LogitRows &in)
-{
-    float top = m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    return make_float2(top, warp_sum(z * exp2_approx(distance(m, safe_max(top), in) * in.c)));
-}
 
 // A byte in shared memory for each vector of a part, with a bit for each of
 // its elements that is a listed token.

@@ -455,7 +455,12 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobGrad
     if (tid <= a.k) {
         const int i = tid - 1;
         ids[tid] = i < 0 ? (a.g_logp ? a.tokens[r] : -1) : a.top_ids[r * a.k + i];
-        weight[tid] = i < 0 ? (a.g_logp ? a.g_logp[r] : 0.0f) : a.g_top[r * a.k + i];
+        float w = i < 0 ? (a.g_logp ? a.g_logp[r] : 0.0f) : a.g_top[r * a.k + i];
+        if (a.by_slope && w != 0.0f) {   // what is not finite makes the row NaN
+            w = __fmul_rn(w, st.z);
+            w = fabsf(w) < kInf ? w : kNan;
+        }
+        weight[tid] = w;
     }
     for (int i = tid; i < kVecs * kGradThreads * T::kPerVec / 32; i += kGradThreads)
         taken[i] = 0;

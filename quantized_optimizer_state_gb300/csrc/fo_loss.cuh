@@ -92,6 +92,7 @@ struct F32 {
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kInf = __builtin_huge_valf();
+constexpr float kNan = __builtin_nanf("");
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -294,6 +295,24 @@ __device__ __forceinline__ void rescale(Stat &s, float m, const LogitRows &in)
         s.w = __fmul_rn(__fmaf_rn(t, s.z, s.w), f);
     s.z = __fmul_rn(s.z, f);
     s.m = m;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+// m, z pairs joined over a warp: the largest m, and z at that.
+__device__ __forceinline__ float2 join_pairs(float m, float z, const LogitRows &in)
+{
+    float top = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    return make_float2(top, warp_sum(z * exp2_approx(distance(m, safe_max(top), in) * in.c)));
 }
 
 // Over the first `n` lanes of a warp (a power of two), in every lane of them.
@@ -668,6 +687,25 @@ __device__ __forceinline__ f2 grad_exp2(f2 d, const LogitRows &in, f2 &t)
     const f2 e = pk(a, b), minus_one = splat(-1.0f);
     const f2 r = fma2(d, splat(in.c_lo), fma2(d, c, mul2(t, minus_one)));
     return fma2(e, mul2(r, splat(kLn2)), e);
+}
+
+// 2^t f for a vector of logits: the gradient of a token that is not listed, or not the row's own.
+template <class T>
+__device__ __forceinline__ uint4 grad_vec(const uint4 &v, f2 nm, f2 f, const LogitRows &in)
+{
+    f2 x[T::kPerVec / 2];
+    widen_vec<T>(v, x);
+#pragma unroll
+    for (int k = 0; k < T::kPerVec / 2; ++k) {
+        f2 d = add2(x[k], nm), t;
+        if (sizeof(typename T::raw) == 4) {
+            float a, b;
+            unpk(d, a, b);
+            d = pk(max_nan(a, in.d_min), max_nan(b, in.d_min));
+        }
+        x[k] = mul2(grad_exp2<T>(d, in, t), f);
+    }
+    return narrow_vec<T>(x);
 }
 
 // --- launches ------------------------------------------------------------------

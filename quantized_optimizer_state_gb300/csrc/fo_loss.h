@@ -1,6 +1,6 @@
 // fo_loss.h -- interface between the C-ABI layer of the loss operators
-// (fo_loss_api.cu) and their kernels (fo_logprobs.cu, fo_distill.cu). Not
-// installed; not part of the ABI.
+// (fo_loss_api.cu) and their kernels (fo_logprobs.cu, fo_distill.cu,
+// fo_policy.cu). Not installed; not part of the ABI.
 #pragma once
 
 #include <cstdint>
@@ -28,6 +28,7 @@ struct GradRows {
 //   log probabilities: {m, Z, H, unused}
 //   distillation:      {m, Z, m_r, F}: m_r the largest logit that is not listed,
 //                      F 2^((x_j - m_r) c) the gradient of KL by s_j at such a j
+//   policy loss:       {m, Z, dloss/dlogp, 0}; Z = 0 for a row that is no position
 struct LogprobArgs {
     LogitRows in;
     const int64_t *tokens;   // may be null (then logp is)
@@ -47,6 +48,7 @@ struct LogprobGradArgs {
     const int32_t *top_ids;
     const float4 *stats;
     const float *g_logp, *g_entropy, *g_top;   // null: 0
+    bool by_slope;           // g_logp is times stats' third (policy loss)
 };
 
 struct Teacher {
@@ -75,9 +77,21 @@ struct DistillGradArgs {
     const float *g_loss;
 };
 
+struct PolicyArgs {
+    LogitRows in;
+    const int64_t *tokens;
+    const float *old_logp, *advantages, *ref_logp;   // ref_logp may be null
+    float ratio_low, ratio_high, kl_weight;
+    const float *weight;     // may be null: 1
+    float *loss, *logp;      // each may be null
+    float4 *stats;           // may be null
+    GradRows grad;           // data may be null
+};
+
 cudaError_t launch_token_logprobs(int dtype, const LogprobArgs &a, cudaStream_t stream);
 cudaError_t launch_token_logprobs_grad(int dtype, const LogprobGradArgs &a, cudaStream_t stream);
 cudaError_t launch_distill(int dtype, const DistillArgs &a, cudaStream_t stream);
 cudaError_t launch_distill_grad(int dtype, const DistillGradArgs &a, cudaStream_t stream);
+cudaError_t launch_policy(int dtype, const PolicyArgs &a, cudaStream_t stream);
 
 }  // namespace fo

@@ -4,41 +4,18 @@
 #include <cmath>
 
 #include "fo.h"
+#include "fo_check.h"
 #include "fo_internal.h"
 #include "fo_loss.h"
 
 namespace {
 
+using namespace fo::check;
+
 constexpr double kLog2E = 1.4426950408889634;
 constexpr int64_t kMaxStride = (int64_t)1 << 44;
 
-int64_t element_size(int32_t dtype) { return dtype == FO_LOGITS_F32 ? 4 : 2; }
-bool dtype_ok(int32_t dtype) { return dtype == FO_LOGITS_BF16 || dtype == FO_LOGITS_F32 || dtype == FO_LOGITS_F16; }
 bool temperature_ok(double t) { return std::isfinite(t) && t >= 0x1p-20 && t <= 0x1p20; }
-bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
-// One array of a call: bytes [lo, hi), empty where the pointer is null.
-struct Range {
-    uintptr_t lo = 0, hi = 0;
-    bool written = false;
-    Range() = default;
-    Range(const void *p, int64_t bytes, bool w) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo), written(w)
-    {
-        if (p)
-            hi = lo + (uintptr_t)bytes;
-    }
-};
-
-// A written array may share no byte with any other array of the call.
-bool aliases(const Range *r, int n)
-{
-    for (int a = 0; a < n; ++a)
-        for (int b = a + 1; b < n; ++b)
-            if ((r[a].written || r[b].written) && r[a].lo < r[b].hi && r[b].lo < r[a].hi)
-                return true;
-    return false;
-}
-
 int64_t outer_rows(const fo_logits_t &x) { return x.rows / x.inner_rows; }
 
 // Elements from the first row's start to the last row's end.
@@ -235,6 +212,7 @@ fo_status_t fo_token_logprobs_grad(const fo_logits_t *logits, const int64_t *tok
     a.g_logp = g_logp;
     a.g_entropy = g_entropy;
     a.g_top = g_top;
+    a.by_slope = false;
     return fo::cuda_status(fo::launch_token_logprobs_grad(logits->dtype, a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -309,6 +287,87 @@ fo_status_t fo_distill_grad(const fo_logits_t *logits, const fo_teacher_t *teach
     a.stats = reinterpret_cast<const float4 *>(stats);
     a.g_loss = g_loss;
     return fo::cuda_status(fo::launch_distill_grad(logits->dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+fo_status_t fo_policy_loss(const fo_logits_t *logits, const fo_policy_t *policy, const float *row_weight, float *loss,
+                           float *logp, float *stats, const fo_logits_grad_t *grad, fo_stream_t stream)
+{
+    fo_status_t st = check_logits(logits);
+    if (st != FO_OK)
+        return st;
+    if (!policy)
+        return FO_ERR_NULL;
+    const fo_policy_t &p = *policy;
+    if (!(p.clip_low >= 0.0 && p.clip_low <= 1.0) || !(p.clip_high >= 0.0 && p.clip_high <= 0x1p100) ||
+        !(p.kl_weight >= 0.0 && p.kl_weight <= 0x1p100))
+        return FO_ERR_BAD_ARG;
+    if (logits->rows == 0)
+        return FO_OK;
+    const int64_t n = logits->rows;
+    const float *ref = p.kl_weight != 0.0 ? p.ref_logp : nullptr;
+    if (!p.tokens || !p.old_logp || !p.advantages || (p.kl_weight != 0.0 && !ref))
+        return FO_ERR_NULL;
+    if (grad && (st = check_grad(*logits, grad)) != FO_OK)
+        return st;
+    if (misaligned(p.tokens, 8) || misaligned(p.old_logp, 4) || misaligned(p.advantages, 4) || misaligned(ref, 4) ||
+        misaligned(row_weight, 4) || misaligned(loss, 4) || misaligned(logp, 4) || misaligned(stats, 16))
+        return FO_ERR_MISALIGNED;
+    const Range r[10] = {grad_range(*logits, grad), grad && in_place(*logits, *grad) ? Range() : logits_range(*logits),
+                         Range(p.tokens, 8 * n, false), Range(p.old_logp, 4 * n, false), Range(p.advantages, 4 * n, false),
+                         Range(ref, 4 * n, false), Range(row_weight, 4 * n, false), Range(loss, 4 * n, true),
+                         Range(logp, 4 * n, true), Range(stats, 16 * n, true)};
+    if (aliases(r, 10))
+        return FO_ERR_ALIAS;
+    if (!loss && !logp && !stats && !grad)
+        return FO_OK;
+    if ((st = fo::pending_error()) != FO_OK)
+        return st;
+    fo::PolicyArgs a;
+    a.in = rows_of(*logits);
+    a.tokens = p.tokens;
+    a.old_logp = p.old_logp;
+    a.advantages = p.advantages;
+    a.ref_logp = ref;
+    a.ratio_low = (float)(1.0 - p.clip_low);
+    a.ratio_high = (float)(1.0 + p.clip_high);
+    a.kl_weight = (float)p.kl_weight;
+    a.weight = row_weight;
+    a.loss = loss;
+    a.logp = logp;
+    a.stats = reinterpret_cast<float4 *>(stats);
+    a.grad = grad_of(grad);
+    return fo::cuda_status(fo::launch_policy(logits->dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+fo_status_t fo_policy_loss_grad(const fo_logits_t *logits, const int64_t *tokens, const float *stats,
+                                const float *g_loss, const fo_logits_grad_t *grad, fo_stream_t stream)
+{
+    fo_status_t st = check_logits(logits);
+    if (st != FO_OK)
+        return st;
+    if (logits->rows == 0)
+        return FO_OK;
+    const int64_t n = logits->rows;
+    if (!tokens || !stats || !g_loss)
+        return FO_ERR_NULL;
+    if ((st = check_grad(*logits, grad)) != FO_OK)
+        return st;
+    if (misaligned(tokens, 8) || misaligned(stats, 16) || misaligned(g_loss, 4))
+        return FO_ERR_MISALIGNED;
+    const Range r[5] = {grad_range(*logits, grad), in_place(*logits, *grad) ? Range() : logits_range(*logits),
+                        Range(tokens, 8 * n, false), Range(stats, 16 * n, false), Range(g_loss, 4 * n, false)};
+    if (aliases(r, 5))
+        return FO_ERR_ALIAS;
+    if ((st = fo::pending_error()) != FO_OK)
+        return st;
+    fo::LogprobGradArgs a = {};
+    a.in = rows_of(*logits);
+    a.out = grad_of(grad);
+    a.tokens = tokens;
+    a.stats = reinterpret_cast<const float4 *>(stats);
+    a.g_logp = g_loss;
+    a.by_slope = true;
+    return fo::cuda_status(fo::launch_token_logprobs_grad(logits->dtype, a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

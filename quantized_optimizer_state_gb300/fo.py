@@ -91,8 +91,28 @@ class FoTeacher(ctypes.Structure):
                 ("tail", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class FoPolicy(ctypes.Structure):
+    """Mirror of ``fo_policy_t``."""
+    _fields_ = [("tokens", ctypes.c_void_p), ("old_logp", ctypes.c_void_p), ("advantages", ctypes.c_void_p),
+                ("ref_logp", ctypes.c_void_p), ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl_weight", ctypes.c_double)]
+
+
+FO_ACT_SILU = 0         # fo_act_t
+FO_ACT_GELU = 1
+FO_MAX_ACT_GROUPS = 1 << 29
+FO_NORM_PARTS = 1024
+
+
+class FoRows(ctypes.Structure):
+    """Mirror of ``fo_rows_t``."""
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 assert ctypes.sizeof(FoTensor) == 80
 assert ctypes.sizeof(FoLogits) == 64 and ctypes.sizeof(FoLogitsGrad) == 24 and ctypes.sizeof(FoTeacher) == 48
+assert ctypes.sizeof(FoPolicy) == 56 and ctypes.sizeof(FoRows) == 40
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -113,6 +133,15 @@ SIGNATURES = {
     "fo_token_logprobs_grad": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     "fo_distill": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     "fo_distill_grad": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_policy_loss": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_policy_loss_grad": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_compress": (ctypes.c_int, [_VP, _VP, _VP, _VP]),
+    "fo_expand": (ctypes.c_int, [_VP, _VP, _VP, _VP]),
+    "fo_activation": (ctypes.c_int, [ctypes.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_activation_grad": (ctypes.c_int, [ctypes.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "fo_rms_norm": (ctypes.c_int, [_VP, _VP, _I32, ctypes.c_double, _VP, _VP, _VP, _VP, _VP]),
+    "fo_rms_norm_workspace": (_I64, [_I64, _I64]),
+    "fo_rms_norm_grad": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
     "fo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fo_last_cuda_error": (ctypes.c_int, []),
     "fo_kernel_launch_count": (ctypes.c_uint64, []),
@@ -572,6 +601,187 @@ def fo_distill_grad(logits, teacher_ids, teacher_logits, stats, g_loss, grad, te
     if status:
         _check("fo_distill_grad", status)
     _modified(grad)
+
+
+def policy(tokens, old_logp, advantages, ref_logp, rows: int, clip_low: float, clip_high: float, kl_weight: float,
+           cur: int) -> FoPolicy:
+    """The ``fo_policy_t`` of per-row arrays (tokens int64, the others float32)."""
+    import torch
+    f32 = torch.float32
+    return FoPolicy(_array(tokens, "tokens", torch.int64, rows, cur), _array(old_logp, "old_logp", f32, rows, cur),
+                    _array(advantages, "advantages", f32, rows, cur), _array(ref_logp, "ref_logp", f32, rows, cur),
+                    clip_low, clip_high, kl_weight)
+
+
+def fo_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, row_weight=None, loss=None, logp=None,
+                   stats=None, grad=None, clip_low: float = 0.2, clip_high: float = 0.2, kl_weight: float = 0.0,
+                   temperature: float = 1.0, stream=None):
+    import torch
+    x = logits_rows(logits, temperature)
+    g = _logits_grad(x, logits, grad)
+    n, f32, cur = x.rows, torch.float32, _current_device()
+    p = policy(tokens, old_logp, advantages, ref_logp, n, clip_low, clip_high, kl_weight, cur)
+    status = lib().fo_policy_loss(
+        ctypes.byref(x), ctypes.byref(p), _array(row_weight, "row_weight", f32, n, cur), _array(loss, "loss", f32, n, cur),
+        _array(logp, "logp", f32, n, cur), _array(stats, "stats", f32, n * FO_LOSS_STATS, cur),
+        None if g is None else ctypes.byref(g), _stream(stream))
+    if status:
+        _check("fo_policy_loss", status)
+    _modified(loss, logp, stats, grad)
+
+
+def fo_policy_loss_grad(logits, tokens, stats, g_loss, grad, temperature: float = 1.0, stream=None):
+    import torch
+    x = logits_rows(logits, temperature)
+    g = _logits_grad(x, logits, grad)
+    n, f32, cur = x.rows, torch.float32, _current_device()
+    status = lib().fo_policy_loss_grad(
+        ctypes.byref(x), _array(tokens, "tokens", torch.int64, n, cur), _array(stats, "stats", f32, n * FO_LOSS_STATS, cur),
+        _array(g_loss, "g_loss", f32, n, cur), None if g is None else ctypes.byref(g), _stream(stream))
+    if status:
+        _check("fo_policy_loss_grad", status)
+    _modified(grad)
+
+
+# --- activations kept in 8 bits ----------------------------------------------------
+
+def _rows_of(x):
+    """(rows, stride) of the leading dimensions of a tensor [..., width], or None
+    where one stride does not cover them or the last dimension is not contiguous."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) < 1 or (stride[-1] != 1 and shape[-1] > 1):
+        return None
+    if len(shape) == 2:
+        return shape[0], stride[0]
+    rows, apart = 1, shape[-1]
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if rows == 1:
+            apart = s
+        elif s != apart * rows:
+            return (0, apart) if 0 in shape[:-1] else None
+        rows *= n
+    return rows, apart
+
+
+def matrix(x, name: str = "x", like: Optional[FoRows] = None) -> FoRows:
+    """The ``fo_rows_t`` of a tensor [..., width] of bfloat16, float16 or float32
+    whose last dimension is contiguous and whose rows are one stride apart."""
+    dt = _LOGIT_DTYPES.get(x.dtype)
+    if dt is None:
+        dt = _logit_dtype(x.dtype, name)
+    ptr = _device_ptr(x, name, _current_device())
+    rows = _rows_of(x)
+    if rows is None:
+        raise ValueError(f"{name}: the last dimension must be contiguous and one stride must cover the others "
+                         "(make it contiguous)")
+    rows, stride = rows
+    if like is not None and (rows != like.rows or x.shape[-1] != like.width or dt != like.dtype):
+        raise ValueError(f"{name} must have {like.rows} rows of {like.width} elements of the other matrices' type, not "
+                         f"{rows} of {x.shape[-1]} of {str(x.dtype).replace('torch.', '')}")
+    return FoRows(ptr, rows, x.shape[-1], stride, dt, 0)
+
+
+def groups(width: int) -> int:
+    return -(-width // GROUP)
+
+
+def _kept(codes, steps, m: FoRows, cur: int, name: str = ""):
+    """The addresses of the codes and steps of a matrix of m's size."""
+    import torch
+    n = m.rows * groups(m.width)
+    return (_array(codes, name + "codes", torch.int8, n * GROUP, cur), _array(steps, name + "steps", torch.bfloat16, n, cur))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def fo_compress(x, codes, steps, stream=None):
+    """codes int8 [rows, 32 G] and steps bfloat16 [rows, G] of x, G = ceil(width / 32)."""
+    m = matrix(x)
+    c, s = _kept(codes, steps, m, _current_device())
+    status = lib().fo_compress(ctypes.byref(m), c, s, _stream(stream))
+    if status:
+        _check("fo_compress", status)
+    _modified(codes, steps)
+
+
+def fo_expand(codes, steps, x, stream=None):
+    m = matrix(x)
+    c, s = _kept(codes, steps, m, _current_device())
+    status = lib().fo_expand(c, s, ctypes.byref(m), _stream(stream))
+    if status:
+        _check("fo_expand", status)
+    _modified(x)
+
+
+def fo_activation(kind: int, x, y, codes=None, steps=None, up=None, up_codes=None, up_steps=None, stream=None):
+    m = matrix(x)
+    u, to = None if up is None else matrix(up, "up", m), matrix(y, "y", m)
+    cur = _current_device()
+    c, s = _kept(codes, steps, m, cur)
+    uc, us = _kept(up_codes, up_steps, m, cur, "up_")
+    status = lib().fo_activation(int(kind), ctypes.byref(m), _ref(u), ctypes.byref(to), c, s, uc, us, _stream(stream))
+    if status:
+        _check("fo_activation", status)
+    _modified(y, codes, steps, up_codes, up_steps)
+
+
+def fo_activation_grad(kind: int, codes, steps, grad_y, grad_x, up_codes=None, up_steps=None, grad_up=None, stream=None):
+    m = matrix(grad_y, "grad_y")
+    to, to_up = matrix(grad_x, "grad_x", m), None if grad_up is None else matrix(grad_up, "grad_up", m)
+    cur = _current_device()
+    c, s = _kept(codes, steps, m, cur)
+    uc, us = _kept(up_codes, up_steps, m, cur, "up_")
+    status = lib().fo_activation_grad(int(kind), c, s, uc, us, ctypes.byref(m), ctypes.byref(to), _ref(to_up), _stream(stream))
+    if status:
+        _check("fo_activation_grad", status)
+    _modified(grad_x, grad_up)
+
+
+def _weight(weight, name: str, width: int, cur: int):
+    """(address, fo_logit_dtype_t) of a norm's weight [width], or of its gradient."""
+    if weight is None:
+        return None, 0
+    return _array(weight, name, weight.dtype, width, cur), _logit_dtype(weight.dtype, name)
+
+
+def fo_rms_norm(x, y, weight=None, eps: float = 1e-6, inv_rms=None, codes=None, steps=None, stream=None):
+    import torch
+    m = matrix(x)
+    to, cur = matrix(y, "y", m), _current_device()
+    w, wt = _weight(weight, "weight", m.width, cur)
+    c, s = _kept(codes, steps, m, cur)
+    status = lib().fo_rms_norm(ctypes.byref(m), w, wt, eps, ctypes.byref(to),
+                               _array(inv_rms, "inv_rms", torch.float32, m.rows, cur), c, s, _stream(stream))
+    if status:
+        _check("fo_rms_norm", status)
+    _modified(y, inv_rms, codes, steps)
+
+
+def fo_rms_norm_workspace(rows: int, width: int) -> int:
+    """Elements of fo_rms_norm_grad's float32 workspace."""
+    return int(lib().fo_rms_norm_workspace(rows, width))
+
+
+def fo_rms_norm_grad(codes, steps, inv_rms, grad_y, grad_x=None, weight=None, grad_weight=None, workspace=None, stream=None):
+    import torch
+    m = matrix(grad_y, "grad_y")
+    to, cur = None if grad_x is None else matrix(grad_x, "grad_x", m), _current_device()
+    w, wt = _weight(weight, "weight", m.width, cur)
+    gw, gt = _weight(grad_weight, "grad_weight", m.width, cur)
+    if w is not None and gw is not None and wt != gt:
+        raise TypeError("grad_weight must be of weight's type")
+    c, s = _kept(codes, steps, m, cur)
+    need = 0 if grad_weight is None else min(m.rows, FO_NORM_PARTS) * m.width
+    status = lib().fo_rms_norm_grad(
+        c, s, _array(inv_rms, "inv_rms", torch.float32, m.rows, cur), w, wt if gw is None else gt, ctypes.byref(m), _ref(to), gw,
+        _array(workspace, "workspace", torch.float32, need, cur), _stream(stream))
+    if status:
+        _check("fo_rms_norm_grad", status)
+    _modified(grad_x, grad_weight, workspace)
 
 
 FO_VERIFY_COUNTS = 6

@@ -11,7 +11,9 @@ library's kernels: what stands between a model's head and the optimizers of
   logits come from device memory once and the gradient goes there once, where
   loss and backward pass fetch them twice. For training loops that know the
   weight of each row beforehand:
-  ``loss, grad = distill_loss_grad(...); logits.backward(grad)``.
+  ``loss, grad = distill_loss_grad(...); logits.backward(grad)``;
+* :func:`policy_loss`, :func:`policy_loss_grad` -- the clipped loss of policy
+  training on sampled tokens, with a KL term, in the same two forms.
 
 Logits are bfloat16, float16 or float32 CUDA tensors ``[..., vocab]`` whose
 last dimension is contiguous; a slice like ``logits[:, :-1]`` is read where it
@@ -253,3 +255,117 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
     _check_rows("row_weight", row_weight, logits.shape[:-1])
     return _distill(logits, teacher_ids.contiguous(), teacher_logits.contiguous(), _dense(teacher_lse), _dense(row_weight),
                     temperature, teacher_temperature, tail, False, True, out)[:2]
+
+
+class PolicyLoss(NamedTuple):
+    loss: torch.Tensor       # [...]
+    logp: torch.Tensor       # [...], of the tokens; not differentiable
+
+
+class PolicyLossGrad(NamedTuple):
+    loss: torch.Tensor       # [...], times row_weight
+    logp: torch.Tensor
+    grad: torch.Tensor       # of the logits
+
+
+def _policy(logits, tokens, old, advantages, ref, weight, how, with_stats, with_grad, out=None):
+    clip_low, clip_high, kl_weight, temperature = how
+    x = fo.logits_rows(logits, temperature)
+    dev, n = logits.device, x.rows
+    p = fo.policy(tokens, old, advantages, ref, n, clip_low, clip_high, kl_weight, dev.index)
+    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
+    logp = torch.empty_like(loss)
+    grad = to = stats = p_stats = None
+    if out is not None:
+        grad, to = out, fo._logits_grad(x, logits, out)
+    elif with_grad:
+        grad, to = _empty_grad(logits, x)
+    if with_stats:
+        stats = torch.empty((n, fo.FO_LOSS_STATS), dtype=torch.float32, device=dev)
+        p_stats = stats.data_ptr()
+    status = fo.lib().fo_policy_loss(ctypes.byref(x), ctypes.byref(p), fo._array(weight, "row_weight", torch.float32, n, dev.index),
+                                     loss.data_ptr(), logp.data_ptr(), p_stats, None if to is None else ctypes.byref(to),
+                                     fo._stream(None))
+    if status:
+        fo._check("fo_policy_loss", status)
+    if out is not None:
+        fo._modified(out)
+    return loss, logp, grad, stats
+
+
+class _Policy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, old, advantages, ref, how):
+        loss, logp, _, stats = _policy(logits, tokens, old, advantages, ref, None, how, True, False)
+        ctx.save_for_backward(logits, tokens, stats)
+        ctx.temperature = how[3]
+        ctx.mark_non_differentiable(logp)
+        ctx.set_materialize_grads(False)
+        return loss, logp
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_loss, _):
+        if g_loss is None:
+            return None, None, None, None, None, None
+        logits, tokens, stats = ctx.saved_tensors
+        with _on_device_of(logits):
+            x = fo.logits_rows(logits, ctx.temperature)
+            grad, to = _empty_grad(logits, x)
+            g_loss = g_loss.contiguous()
+            status = fo.lib().fo_policy_loss_grad(ctypes.byref(x), tokens.data_ptr(), stats.data_ptr(),
+                                                  fo._array(g_loss, "g_loss", torch.float32, x.rows, logits.device.index),
+                                                  ctypes.byref(to), fo._stream(None))
+            if status:
+                fo._check("fo_policy_loss_grad", status)
+        return grad, None, None, None, None, None
+
+
+def _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight):
+    _check_tangent(logits)
+    rows = logits.shape[:-1]
+    for name, x in (("tokens", tokens), ("old_logp", old_logp), ("advantages", advantages), ("ref_logp", ref_logp)):
+        _check_rows(name, x, rows)
+    if kl_weight and ref_logp is None:
+        raise ValueError("kl_weight needs ref_logp")
+    dense = [x if x is None else x.detach().contiguous() for x in (old_logp, advantages, ref_logp if kl_weight else None)]
+    return (tokens.contiguous(), *dense)
+
+
+def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
+                clip_low: float = 0.2, clip_high: float = 0.2, ref_logp: Optional[torch.Tensor] = None,
+                kl_weight: float = 0.0, temperature: float = 1.0) -> PolicyLoss:
+    """The clipped policy loss by position, in float32, and the log probabilities
+    ``l`` of ``tokens`` under ``softmax(logits / temperature)``:
+    ``-min(q A, clip(q, 1 - clip_low, 1 + clip_high) A)`` with ``q = exp(l - old_logp)``
+    and ``A`` the advantage, plus ``kl_weight * (exp(k) - k - 1)`` with
+    ``k = ref_logp - l``.
+
+    ``tokens``: int64 ids of the logits' leading shape, negative where there is no
+    position (loss, log probability and gradient 0). ``old_logp``, ``advantages``
+    and ``ref_logp``: float32 of that shape, constants of the gradient. The loss is
+    differentiable in ``logits``.
+    """
+    tokens, old, advantages, ref = _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight)
+    how = (clip_low, clip_high, kl_weight, temperature)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return PolicyLoss(*_Policy.apply(logits, tokens, old, advantages, ref, how))
+    return PolicyLoss(*_policy(logits, tokens, old, advantages, ref, None, how, False, False)[:2])
+
+
+def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
+                     clip_low: float = 0.2, clip_high: float = 0.2, ref_logp: Optional[torch.Tensor] = None,
+                     kl_weight: float = 0.0, temperature: float = 1.0, row_weight: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> PolicyLossGrad:
+    """``(loss, logp, grad)``: ``loss = row_weight * policy_loss(...).loss`` by
+    position and the gradient of its sum with respect to the logits, in one call:
+    ``o = policy_loss_grad(...); logits.backward(o.grad)``.
+
+    ``row_weight`` (float32, 1 where None): for a mean over n tokens 1 / n, and 0
+    for padding, whose logits are not read. ``out``: where to write the gradient;
+    it may be ``logits`` itself, which the gradient then replaces.
+    """
+    tokens, old, advantages, ref = _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight)
+    _check_rows("row_weight", row_weight, logits.shape[:-1])
+    how = (clip_low, clip_high, kl_weight, temperature)
+    return PolicyLossGrad(*_policy(logits, tokens, old, advantages, ref, _dense(row_weight), how, False, True, out)[:3])
