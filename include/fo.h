@@ -489,7 +489,7 @@ fo_status_t fo_policy_loss_grad(const fo_logits_t *logits, const int64_t *tokens
  * of one call of one type, aligned to it. Rows that are only read may overlap;
  * rows that are written may not, and share no byte with another array. For a
  * matrix of `width` columns and G = ceil(width / 32), codes is [rows, 32 G] (0
- * beyond the width), aligned to 16 bytes, and steps [rows, G]. All arithmetic is
+ * beyond the width, beside a step that is a number), aligned to 16 bytes, and steps [rows, G]. All arithmetic is
  * FP32, results are rounded once, to the matrices' type. Every result is the
  * same bit for bit on every run of the same call on the same kind of device.
  * Rows beside others have no effect on them.

@@ -129,30 +129,306 @@ __device__ __forceinline__ Curve curve(float x)
 template <class T>
 constexpr bool kExactType = sizeof(typename T::raw) == 4;
 
-// Element `c` of row `r`.
-template <class T>
-__device__ __forceinline__ float load_at(const RowsIn &x, int64_t r, int64_t c)
+// --- units -----------------------------------------------------------------------------
+//
+// A thread works on units of 8 contiguous elements, neighbouring lanes on
+// neighbouring units, four lanes to a group: 16 bytes of a 16-bit type a lane
+// and load, whole lines a warp. Units are numbered through the rows, U = 4 groups
+// to a row, so that unit q has the codes from 8 q on and the step q / 4.
+
+constexpr int kUnit = 8;
+
+// Division of numbers below 2^31 by a fixed one: n / d = (n m / 2^32 + n) / 2^shift
+// (T. Granlund, P. Montgomery, "Division by invariant integers using
+// multiplication", PLDI 1994).
+struct Divisor {
+    uint32_t d, m, shift;
+};
+inline Divisor divisor(uint32_t d)
 {
-    return T::widen(static_cast<const typename T::raw *>(x.data)[r * x.stride + c]);
+    Divisor r = {d, 0, 0};
+    while (r.shift < 31 && (1u << r.shift) < d)
+        ++r.shift;
+    r.m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << r.shift) - d)) / d + 1);
+    return r;
 }
-template <class T>
-__device__ __forceinline__ void store_at(const RowsOut &x, int64_t r, int64_t c, float v)
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor &d) { return (__umulhi(n, d.m) + n) >> d.shift; }
+
+// Where a unit lies. `left`: elements of the row from its first one on (0 or
+// less beyond the row's end). Beyond the last row: row -1, and `left` far below 0.
+struct Place {
+    int64_t row, col, left;
+};
+__device__ __forceinline__ Place place(uint32_t unit, uint32_t units, const Divisor &per_row, int64_t width)
 {
-    static_cast<typename T::raw *>(x.data)[r * x.stride + c] = T::narrow(v);
+    const uint32_t r = quotient(unit, per_row);
+    Place p;
+    p.row = unit < units ? (int64_t)r : -1;
+    p.col = (int64_t)(unit - r * per_row.d) * kUnit;
+    p.left = unit < units ? width - p.col : -64;
+    return p;
 }
 
-// A group by a warp, an element a lane.
-__device__ __forceinline__ void keep_group(const KeptOut &k, int64_t group, float x)
+// The 32-bit words of a unit, as they lie in memory.
+template <class T>
+struct Words {
+    static constexpr int kN = kUnit * sizeof(typename T::raw) / 4;
+    uint32_t w[kN];
+};
+
+// Whether vectors of 16 bytes line up with the units of every row.
+template <class T>
+inline bool wide(const void *data, int64_t stride)
 {
-    const float step = step_of(__reduce_max_sync(~0u, magnitude(x)));
-    const int lane = threadIdx.x & 31;
-    k.codes[group * kGroup + lane] = (int8_t)code_word(x, __frcp_rn(step));
-    if (lane == 0)
-        k.steps[group] = step_bits(step);
+    return (reinterpret_cast<uintptr_t>(data) & 15) == 0 && stride * (int64_t)sizeof(typename T::raw) % 16 == 0;
 }
-__device__ __forceinline__ float kept_at(const KeptIn &k, int64_t group, int lane)
+
+// The words from element `from` on of a longer run of them; `from` < 8 of 16 bits
+// or < 4 of 32. Three (two) steps, by the bits of `from`.
+template <class T, int kIn, int kOut>
+__device__ __forceinline__ void shifted(uint32_t (&in)[kIn], int from, uint32_t (&out)[kOut])
 {
-    return __fmul_rn((float)k.codes[group * kGroup + lane], step_value(k.steps[group]));
+    constexpr bool kHalves = sizeof(typename T::raw) == 2;
+    const int words = kHalves ? from >> 1 : from;
+#pragma unroll
+    for (int i = 0; i + 2 < kIn; ++i)
+        in[i] = words & 2 ? in[i + 2] : in[i];
+#pragma unroll
+    for (int i = 0; i + 1 < kIn; ++i)
+        in[i] = words & 1 ? in[i + 1] : in[i];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i)
+        out[i] = kHalves ? __funnelshift_r(in[i], in[i + 1 < kIn ? i + 1 : i], from & 1 ? 16 : 0) : in[i];
+}
+
+// A unit; 0 beyond the row's end. No byte outside the row is read. Without kWide
+// the row may start anywhere: the aligned vectors that hold the unit are read
+// and shifted.
+template <class T, bool kWide>
+__device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
+{
+    typedef typename T::raw raw;
+    constexpr int kSize = sizeof(raw), kVecs = kUnit * kSize / 16;
+    Words<T> v;
+    const raw *at = static_cast<const raw *>(x.data) + p.row * x.stride + p.col;
+    const int phase = kWide ? 0 : (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize);
+    if (phase == 0 && p.left >= kUnit) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(at) + i);
+            v.w[4 * i] = a.x; v.w[4 * i + 1] = a.y; v.w[4 * i + 2] = a.z; v.w[4 * i + 3] = a.w;
+        }
+        return v;
+    }
+    if (!kWide && p.col >= phase && p.left + phase >= (kVecs + 1) * 16 / kSize) {
+        uint32_t in[4 * (kVecs + 1)];
+#pragma unroll
+        for (int i = 0; i <= kVecs; ++i) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(at - phase) + i);
+            in[4 * i] = a.x; in[4 * i + 1] = a.y; in[4 * i + 2] = a.z; in[4 * i + 3] = a.w;
+        }
+        shifted<T>(in, phase, v.w);
+        return v;
+    }
+#pragma unroll
+    for (int i = 0; i < Words<T>::kN; ++i)
+        v.w[i] = 0;
+    raw *e = reinterpret_cast<raw *>(v.w);
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i)
+        if (i < p.left)
+            e[i] = at[i];
+    return v;
+}
+
+// Stores a unit. Without kWide by all lanes of a warp, whose units follow one
+// another: a lane stores the aligned vectors that begin in the unit before its
+// own and end in its own, with what that unit's lane hands over; what has no such
+// lane goes element by element.
+template <class T, bool kWide>
+__device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, const Words<T> &v)
+{
+    typedef typename T::raw raw;
+    constexpr int kSize = sizeof(raw), kVecs = kUnit * kSize / 16, kN = Words<T>::kN;
+    raw *const at = static_cast<raw *>(x.data) + p.row * x.stride + p.col;
+    const int phase = kWide ? 0 : (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize);
+    uint32_t out[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        out[i] = v.w[i];
+    int64_t lo = 0, hi = p.left;         // places of `out`, from the vectors' first on, that are the row's
+    if (!kWide) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kOver = kSize == 2 ? 4 : 3;   // words that a unit hands over at most
+        uint32_t in[kOver + kN];
+#pragma unroll
+        for (int i = 0; i < kOver; ++i)
+            in[i] = __shfl_up_sync(~0u, v.w[kN - kOver + i], 1);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            in[kOver + i] = v.w[i];
+        const int64_t next_row = __shfl_down_sync(~0u, p.row, 1);
+        const bool before = lane > 0 && p.col > 0, after = lane < 31 && next_row == p.row;
+        if (phase) {
+            shifted<T>(in, (kSize == 2 ? 8 : 3) - phase, out);
+            lo = before ? 0 : phase;
+            hi = p.left + phase;
+            if (!after) {                // the unit's last elements
+                const raw *e = reinterpret_cast<const raw *>(v.w);
+#pragma unroll
+                for (int i = 1; i < kUnit; ++i)
+                    if (i >= kUnit - phase && i < p.left)
+                        at[i] = e[i];
+            }
+        }
+    }
+    raw *const to = at - phase;
+    const raw *e = reinterpret_cast<const raw *>(out);
+    constexpr int kPer = 16 / kSize;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        if (lo <= kPer * i && hi >= kPer * (i + 1))
+            __stcs(reinterpret_cast<uint4 *>(to) + i, make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
+        else
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                if (kPer * i + k >= lo && kPer * i + k < hi)
+                    to[kPer * i + k] = e[kPer * i + k];
+    }
+}
+
+// A unit's values in pairs, and back, rounded once.
+template <class T>
+__device__ __forceinline__ void widen_unit(const Words<T> &v, f2 (&x)[kUnit / 2])
+{
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i)
+        if constexpr (sizeof(typename T::raw) == 2)
+            x[i] = T::widen2(v.w[i]);
+        else
+            x[i] = pk(__uint_as_float(v.w[2 * i]), __uint_as_float(v.w[2 * i + 1]));
+}
+template <class T>
+__device__ __forceinline__ Words<T> narrow_unit(const f2 (&x)[kUnit / 2])
+{
+    Words<T> v;
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i)
+        if constexpr (sizeof(typename T::raw) == 2)
+            v.w[i] = T::narrow2(x[i]);
+        else {
+            float a, b;
+            unpk(x[i], a, b);
+            v.w[2 * i] = __float_as_uint(a);
+            v.w[2 * i + 1] = __float_as_uint(b);
+        }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The step of the group that this lane's unit and those of the three lanes beside
+// it make up. As unsigned numbers the magnitudes of any of the types order as
+// their values do, infinity and NaN on top: two 16-bit ones to a word.
+template <class T>
+__device__ __forceinline__ float group_step(const Words<T> &v)
+{
+    uint32_t m;
+    if constexpr (sizeof(typename T::raw) == 2) {
+        const uint32_t k = 0x7fff7fffu;
+        m = max_u16x2(max_u16x2(v.w[0] & k, v.w[1] & k), max_u16x2(v.w[2] & k, v.w[3] & k));
+        m = max_u16x2(m, __shfl_xor_sync(~0u, m, 1));
+        m = max_u16x2(m, __shfl_xor_sync(~0u, m, 2));
+        m = __float_as_uint(T::widen((typename T::raw)max(m & 0xffffu, m >> 16)));
+    } else {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i)
+            m = max(m, v.w[i] & 0x7fffffffu);
+        m = max(m, __shfl_xor_sync(~0u, m, 1));
+        m = max(m, __shfl_xor_sync(~0u, m, 2));
+    }
+    return step_of(m);
+}
+
+// RN(1 / step): the hardware's approximation and a step of Newton's, which is
+// the correctly rounded reciprocal of every FP32 number in [2^-100, 2^100]
+// (enumerated by fo_verify_fast_arithmetic) and, steps and their reciprocals being
+// normal numbers, of their multiples by powers of two.
+__device__ __forceinline__ float step_reciprocal(float step)
+{
+    const float y = rcp_approx(step);
+    return __fmaf_rn(y, __fmaf_rn(-step, y, 1.0f), y);
+}
+
+// The lowest bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// The codes and the step of unit `unit` of a matrix of `units` units.
+template <class T>
+__device__ __forceinline__ void keep_unit(const KeptOut &k, uint32_t unit, uint32_t units, const Words<T> &v, const f2 (&x)[kUnit / 2])
+{
+    const float step = group_step<T>(v);
+    const f2 r = splat(step_reciprocal(step)), round = splat(kRound);
+    uint32_t c[kUnit];
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) {
+        float a, b;
+        unpk(fma2(x[i], r, round), a, b);
+        c[2 * i] = __float_as_uint(a);
+        c[2 * i + 1] = __float_as_uint(b);
+    }
+    if (unit < units) {
+        __stcs(reinterpret_cast<uint2 *>(k.codes) + unit, make_uint2(low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])));
+        if (unit % 4 == 0)
+            k.steps[unit / 4] = step_bits(step);
+    }
+}
+
+// A unit's codes and step as loaded, and the values x^ they stand for. A code
+// becomes the low byte of 2^23 + 128 + code, from which FP32 takes the rest away.
+struct Kept {
+    uint2 codes;
+    uint16_t step;
+};
+__device__ __forceinline__ Kept load_kept(const KeptIn &k, uint32_t unit, uint32_t units)
+{
+    Kept v = {make_uint2(0, 0), 0};
+    if (unit < units) {
+        v.codes = __ldcs(reinterpret_cast<const uint2 *>(k.codes) + unit);
+        v.step = __ldg(k.steps + unit / 4);
+    }
+    return v;
+}
+__device__ __forceinline__ void kept_unit(const Kept &v, f2 (&x)[kUnit / 2])
+{
+    const f2 base = splat(-(8388608.0f + 128.0f)), step = splat(step_value(v.step));
+    const uint32_t lo = v.codes.x ^ 0x80808080u, hi = v.codes.y ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) {
+        const uint32_t w = i < 2 ? lo : hi;
+        const f2 n = pk(__uint_as_float(__byte_perm(w, 0x4b000000u, i % 2 ? 0x7442 : 0x7440)),
+                        __uint_as_float(__byte_perm(w, 0x4b000000u, i % 2 ? 0x7443 : 0x7441)));
+        x[i] = mul2(add2(n, base), step);
+    }
+}
+
+// The grid of a launch over all units, kUnits a thread.
+struct UnitGrid {
+    uint32_t units;
+    Divisor per_row;
+};
+inline UnitGrid unit_grid(int64_t rows, int64_t groups)
+{
+    return UnitGrid{(uint32_t)(rows * groups * 4), divisor((uint32_t)(groups * 4))};
 }
 
 }  // namespace fo

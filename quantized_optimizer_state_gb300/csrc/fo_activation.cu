@@ -1,66 +1,111 @@
 // fo_activation.cu -- activation functions, plain and gated, whose input is kept
 // as 8-bit codes for the backward pass.
-#include <algorithm>
-
 #include "fo_act.cuh"
 
 namespace fo {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;
 
-// A warp a group, an element a lane.
-template <class T, int kKind, bool kGated>
-__global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a)
+template <class T, int kKind, bool kGated, bool kWide, int kUnits>
+__global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, UnitGrid g)
 {
-    const int64_t step = (int64_t)gridDim.x * kWarps, all = a.rows * a.groups;
-    for (int64_t g = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; g < all; g += step) {
-        const int64_t r = g / a.groups, c = (g - r * a.groups) * kGroup + (threadIdx.x & 31);
-        const float x = c < a.width ? load_at<T>(a.x, r, c) : 0.0f;
-        const float up = kGated && c < a.width ? load_at<T>(a.up, r, c) : 0.0f;
-        const float f = curve<kKind, kExactType<T>, false>(x).value;
-        if (c < a.width)
-            store_at<T>(a.y, r, c, kGated ? __fmul_rn(f, up) : f);
-        if (a.kept.codes) {
-            keep_group(a.kept, g, x);
+    const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    Words<T> v[kUnits], up[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const Place p = place(first + i * kThreads, g.units, g.per_row, a.width);
+        v[i] = load_unit<T, kWide>(a.x, p);
+        if (kGated)
+            up[i] = load_unit<T, kWide>(a.up, p);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const uint32_t unit = first + i * kThreads;
+        f2 x[kUnit / 2], u[kUnit / 2], y[kUnit / 2];
+        widen_unit<T>(v[i], x);
+        if (kGated)
+            widen_unit<T>(up[i], u);
+#pragma unroll
+        for (int k = 0; k < kUnit / 2; ++k) {
+            float p, q;
+            unpk(x[k], p, q);
+            y[k] = pk(curve<kKind, kExactType<T>, false>(p).value, curve<kKind, kExactType<T>, false>(q).value);
             if (kGated)
-                keep_group(a.kept_up, g, up);
+                y[k] = mul2(y[k], u[k]);
+        }
+        store_unit<T, kWide>(a.y, place(unit, g.units, g.per_row, a.width), narrow_unit<T>(y));
+        if (a.kept.codes) {
+            keep_unit<T>(a.kept, unit, g.units, v[i], x);
+            if (kGated)
+                keep_unit<T>(a.kept_up, unit, g.units, up[i], u);
         }
     }
 }
 
-template <class T, int kKind, bool kGated>
-__global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGradArgs a)
+template <class T, int kKind, bool kGated, bool kWide, int kUnits>
+__global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGradArgs a, UnitGrid g)
 {
-    const int64_t step = (int64_t)gridDim.x * kWarps, all = a.rows * a.groups;
-    for (int64_t g = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; g < all; g += step) {
-        const int lane = threadIdx.x & 31;
-        const int64_t r = g / a.groups, c = (g - r * a.groups) * kGroup + lane;
-        if (c >= a.width)
-            continue;
-        const float dy = load_at<T>(a.grad_y, r, c);
-        const Curve f = curve<kKind, kExactType<T>, true>(kept_at(a.kept, g, lane));
-        if (kGated) {
-            store_at<T>(a.grad, r, c, __fmul_rn(__fmul_rn(dy, kept_at(a.kept_up, g, lane)), f.slope));
-            store_at<T>(a.grad_up, r, c, __fmul_rn(dy, f.value));
-        } else
-            store_at<T>(a.grad, r, c, __fmul_rn(dy, f.slope));
+    const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    Words<T> dy[kUnits];
+    Kept v[kUnits], up[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const uint32_t unit = first + i * kThreads;
+        dy[i] = load_unit<T, kWide>(a.grad_y, place(unit, g.units, g.per_row, a.width));
+        v[i] = load_kept(a.kept, unit, g.units);
+        if (kGated)
+            up[i] = load_kept(a.kept_up, unit, g.units);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        f2 x[kUnit / 2], u[kUnit / 2], d[kUnit / 2], du[kUnit / 2];
+        widen_unit<T>(dy[i], d);
+        kept_unit(v[i], x);
+        if (kGated)
+            kept_unit(up[i], u);
+#pragma unroll
+        for (int k = 0; k < kUnit / 2; ++k) {
+            float p, q;
+            unpk(x[k], p, q);
+            const Curve f = curve<kKind, kExactType<T>, true>(p), h = curve<kKind, kExactType<T>, true>(q);
+            if (kGated) {
+                du[k] = mul2(d[k], pk(f.value, h.value));
+                d[k] = mul2(d[k], u[k]);
+            }
+            d[k] = mul2(d[k], pk(f.slope, h.slope));
+        }
+        const Place p = place(first + i * kThreads, g.units, g.per_row, a.width);
+        store_unit<T, kWide>(a.grad, p, narrow_unit<T>(d));
+        if (kGated)
+            store_unit<T, kWide>(a.grad_up, p, narrow_unit<T>(du));
     }
 }
 
-int64_t ctas_for(int64_t groups) { return std::min<int64_t>((groups + kWarps - 1) / kWarps, (int64_t)sm_count() * 8); }
+template <int kUnits>
+unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * kUnits - 1) / (kThreads * kUnits); }
 
 template <class T, int kKind, bool kGated>
 cudaError_t launch(const ActivationArgs &a, cudaStream_t stream)
 {
-    activation_kernel<T, kKind, kGated><<<(unsigned)ctas_for(a.rows * a.groups), kThreads, 0, stream>>>(a);
+    constexpr int kUnits = 2;
+    const UnitGrid g = unit_grid(a.rows, a.groups);
+    if (wide<T>(a.x.data, a.x.stride) && wide<T>(a.up.data, a.up.stride) && wide<T>(a.y.data, a.y.stride))
+        activation_kernel<T, kKind, kGated, true, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
+    else
+        activation_kernel<T, kKind, kGated, false, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
     count_launch();
     return cudaGetLastError();
 }
 template <class T, int kKind, bool kGated>
 cudaError_t launch(const ActivationGradArgs &a, cudaStream_t stream)
 {
-    activation_grad_kernel<T, kKind, kGated><<<(unsigned)ctas_for(a.rows * a.groups), kThreads, 0, stream>>>(a);
+    constexpr int kUnits = 2;
+    const UnitGrid g = unit_grid(a.rows, a.groups);
+    if (wide<T>(a.grad_y.data, a.grad_y.stride) && wide<T>(a.grad.data, a.grad.stride) && wide<T>(a.grad_up.data, a.grad_up.stride))
+        activation_grad_kernel<T, kKind, kGated, true, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
+    else
+        activation_grad_kernel<T, kKind, kGated, false, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
     count_launch();
     return cudaGetLastError();
 }

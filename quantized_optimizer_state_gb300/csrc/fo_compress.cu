@@ -1,49 +1,78 @@
 // fo_compress.cu -- activations to 8-bit codes and back.
-#include <algorithm>
-
 #include "fo_act.cuh"
 
 namespace fo {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;
+constexpr int kUnits = 4;   // units of a thread, all loaded before the first is used
 
-// A warp a group, an element a lane.
-template <class T>
-__global__ void __launch_bounds__(kThreads) compress_kernel(CompressArgs a)
+template <class T, bool kWide>
+__global__ void __launch_bounds__(kThreads) compress_kernel(CompressArgs a, UnitGrid g)
 {
-    const int64_t step = (int64_t)gridDim.x * kWarps, all = a.rows * a.groups;
-    for (int64_t g = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; g < all; g += step) {
-        const int64_t r = g / a.groups, c = (g - r * a.groups) * kGroup + (threadIdx.x & 31);
-        keep_group(a.kept, g, c < a.width ? load_at<T>(a.x, r, c) : 0.0f);
+    const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    Words<T> v[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+        v[i] = load_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, a.width));
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        f2 x[kUnit / 2];
+        widen_unit<T>(v[i], x);
+        keep_unit<T>(a.kept, first + i * kThreads, g.units, v[i], x);
+    }
+}
+
+template <class T, bool kWide>
+__global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs a, UnitGrid g)
+{
+    const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    Kept k[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+        k[i] = load_kept(a.kept, first + i * kThreads, g.units);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        f2 x[kUnit / 2];
+        kept_unit(k[i], x);
+        store_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, a.width), narrow_unit<T>(x));
+    }
+}
+
+unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * kUnits - 1) / (kThreads * kUnits); }
+
+// Rows that follow one another without a gap, of whole groups, are one row.
+template <class A>
+void join_rows(A &a, int64_t stride)
+{
+    if (stride == a.width && a.width % kGroup == 0) {
+        a.width *= a.rows;
+        a.groups *= a.rows;
+        a.rows = 1;
     }
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs a)
+cudaError_t launch(CompressArgs a, cudaStream_t stream)
 {
-    const int64_t step = (int64_t)gridDim.x * kWarps, all = a.rows * a.groups;
-    for (int64_t g = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; g < all; g += step) {
-        const int lane = threadIdx.x & 31;
-        const int64_t r = g / a.groups, c = (g - r * a.groups) * kGroup + lane;
-        if (c < a.width)
-            store_at<T>(a.x, r, c, kept_at(a.kept, g, lane));
-    }
-}
-
-int64_t ctas_for(int64_t groups) { return std::min<int64_t>((groups + kWarps - 1) / kWarps, (int64_t)sm_count() * 8); }
-
-template <class T>
-cudaError_t launch(const CompressArgs &a, cudaStream_t stream)
-{
-    compress_kernel<T><<<(unsigned)ctas_for(a.rows * a.groups), kThreads, 0, stream>>>(a);
+    join_rows(a, a.x.stride);
+    const UnitGrid g = unit_grid(a.rows, a.groups);
+    if (wide<T>(a.x.data, a.x.stride))
+        compress_kernel<T, true><<<ctas(g), kThreads, 0, stream>>>(a, g);
+    else
+        compress_kernel<T, false><<<ctas(g), kThreads, 0, stream>>>(a, g);
     count_launch();
     return cudaGetLastError();
 }
 template <class T>
-cudaError_t launch(const ExpandArgs &a, cudaStream_t stream)
+cudaError_t launch(ExpandArgs a, cudaStream_t stream)
 {
-    expand_kernel<T><<<(unsigned)ctas_for(a.rows * a.groups), kThreads, 0, stream>>>(a);
+    join_rows(a, a.x.stride);
+    const UnitGrid g = unit_grid(a.rows, a.groups);
+    if (wide<T>(a.x.data, a.x.stride))
+        expand_kernel<T, true><<<ctas(g), kThreads, 0, stream>>>(a, g);
+    else
+        expand_kernel<T, false><<<ctas(g), kThreads, 0, stream>>>(a, g);
     count_launch();
     return cudaGetLastError();
 }

@@ -11,6 +11,32 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
+// Element `c` of row `r`.
+template <class T>
+__device__ __forceinline__ float load_at(const RowsIn &x, int64_t r, int64_t c)
+{
+    return T::widen(static_cast<const typename T::raw *>(x.data)[r * x.stride + c]);
+}
+template <class T>
+__device__ __forceinline__ void store_at(const RowsOut &x, int64_t r, int64_t c, float v)
+{
+    static_cast<typename T::raw *>(x.data)[r * x.stride + c] = T::narrow(v);
+}
+
+// A group by a warp, an element a lane.
+__device__ __forceinline__ void keep_group(const KeptOut &k, int64_t group, float x)
+{
+    const float step = step_of(__reduce_max_sync(~0u, magnitude(x)));
+    const int lane = threadIdx.x & 31;
+    k.codes[group * kGroup + lane] = (int8_t)code_word(x, __frcp_rn(step));
+    if (lane == 0)
+        k.steps[group] = step_bits(step);
+}
+__device__ __forceinline__ float kept_at(const KeptIn &k, int64_t group, int lane)
+{
+    return __fmul_rn((float)k.codes[group * kGroup + lane], step_value(k.steps[group]));
+}
+
 __device__ __forceinline__ float weight_at(const void *w, int dtype, int64_t i)
 {
     if (!w)
