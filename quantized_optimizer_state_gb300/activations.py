@@ -272,7 +272,7 @@ def _norm_backward(kept, grad_y, need_x, need_weight):
         to = fo.FoRows(grad.data_ptr(), m.rows, m.width, m.width, m.dtype, 0)
     if need_weight and weight is not None:
         grad_weight = torch.empty_like(weight)
-        parts = torch.empty(min(m.rows, fo.FO_NORM_PARTS) * m.width, dtype=f32, device=dev)
+        parts = torch.empty(min(m.rows, fo.FO_NORM_PARTS) * fo.groups(m.width) * fo.GROUP, dtype=f32, device=dev)
         gw, ws = grad_weight.data_ptr(), parts.data_ptr()
     status = fo.lib().fo_rms_norm_grad(c, s, fo._array(inv, "inv_rms", f32, m.rows, cur), w, wt, ctypes.byref(m), fo._ref(to),
                                        gw, ws, fo._stream(None))

@@ -62,6 +62,8 @@ struct NormArgs {
     RowsOut y;
     float *inv_rms;
     KeptOut kept;           // inv_rms is null where it is
+    float inv_width;        // these two are set by the launch
+    bool weight_aligned;
 };
 struct NormGradArgs {
     int64_t rows, width, groups;
@@ -72,7 +74,9 @@ struct NormGradArgs {
     RowsIn grad_y;
     RowsOut grad;
     void *grad_weight;      // may be null
-    float *parts;           // [FO_NORM_PARTS or rows, width] partial sums of grad_weight
+    float *parts;           // [FO_NORM_PARTS or rows, 32 groups] partial sums of grad_weight
+    float inv_width;        // these two are set by the launch
+    bool weight_aligned;
 };
 
 cudaError_t launch_compress(int dtype, const CompressArgs &a, cudaStream_t stream);

@@ -209,7 +209,7 @@ fo_status_t fo_rms_norm(const fo_rows_t *in, const void *weight, int32_t weight_
     if ((st = fo::pending_error()) != FO_OK)
         return st;
     fo::NormArgs a = {in->rows, in->width, groups_of(in->width), in_of(in), weight, weight_dtype, (float)eps, out_of(y),
-                      codes ? inv_rms : nullptr, {nullptr, nullptr}};
+                      codes ? inv_rms : nullptr, {nullptr, nullptr}, 0.0f, false};
     if (codes)
         a.kept = {codes, steps};
     return fo::cuda_status(fo::launch_norm(in->dtype, a, static_cast<cudaStream_t>(stream)));
@@ -217,7 +217,7 @@ fo_status_t fo_rms_norm(const fo_rows_t *in, const void *weight, int32_t weight_
 
 int64_t fo_rms_norm_workspace(int64_t rows, int64_t width)
 {
-    return rows <= 0 || width <= 0 ? 0 : std::min<int64_t>(rows, FO_NORM_PARTS) * width;
+    return rows <= 0 || width <= 0 ? 0 : std::min<int64_t>(rows, FO_NORM_PARTS) * groups_of(width) * FO_GROUP;
 }
 
 fo_status_t fo_rms_norm_grad(const int8_t *codes, const uint16_t *steps, const float *inv_rms, const void *weight,
@@ -251,7 +251,7 @@ fo_status_t fo_rms_norm_grad(const int8_t *codes, const uint16_t *steps, const f
     if ((st = fo::pending_error()) != FO_OK)
         return st;
     const fo::NormGradArgs a = {rows, width, groups_of(width), {codes, steps}, inv_rms, weight, weight_dtype, in_of(grad_y),
-                                rows ? out_of(grad_x) : fo::RowsOut{nullptr, 0}, grad_weight, workspace};
+                                rows ? out_of(grad_x) : fo::RowsOut{nullptr, 0}, grad_weight, workspace, 0.0f, false};
     return fo::cuda_status(fo::launch_norm_grad(grad_y->dtype, a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -11,6 +11,299 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
+// --- 1 / rms -----------------------------------------------------------------------
+
+// Squares of a row whose sum reaches 2^120 may lie outside FP32: such rows, which
+// are rare, are summed again at 2^-96 of their size, where a sum that is not
+// finite means that the row holds a NaN or an infinity.
+constexpr float kLargeSum = 0x1p120f, kDown = 0x1p-96f;
+
+// 1 / sqrt(m) for m in [2^-80, 2^121]: the hardware's approximation and a step of Newton's.
+__device__ __forceinline__ float reciprocal_root(float m)
+{
+    const float y = rsqrt_approx(m), e = __fmaf_rn(-__fmul_rn(m, y), y, 1.0f);
+    return __fmaf_rn(__fmul_rn(0.5f, y), e, y);
+}
+__device__ __forceinline__ float inverse_rms(float sum, const NormArgs &a) { return reciprocal_root(__fmaf_rn(sum, a.inv_width, a.eps)); }
+__device__ __forceinline__ float inverse_rms_down(float sum, const NormArgs &a)
+{
+    return sum < kInf ? __fmul_rn(reciprocal_root(__fmul_rn(sum, a.inv_width)), kDown) : kNan;
+}
+
+__device__ __forceinline__ float weight_at(const void *w, int dtype, int64_t i)
+{
+    if (!w)
+        return 1.0f;
+    return dtype == FO_LOGITS_F32    ? static_cast<const float *>(w)[i]
+           : dtype == FO_LOGITS_BF16 ? Bf16::widen(static_cast<const uint16_t *>(w)[i])
+                                     : F16::widen(static_cast<const uint16_t *>(w)[i]);
+}
+__device__ __forceinline__ void store_weight(void *w, int dtype, int64_t i, float v)
+{
+    if (dtype == FO_LOGITS_F32)
+        static_cast<float *>(w)[i] = v;
+    else
+        static_cast<uint16_t *>(w)[i] = dtype == FO_LOGITS_BF16 ? Bf16::narrow(v) : F16::narrow(v);
+}
+
+
+// The weight of a unit; 1 without one.
+__device__ __forceinline__ void weight_unit(const void *w, int dtype, bool aligned, const Place &p, f2 (&x)[kUnit / 2])
+{
+    if (w && aligned && p.left >= kUnit) {
+        if (dtype == FO_LOGITS_F32) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + p.col));
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + p.col) + 1);
+            x[0] = pk(a.x, a.y);
+            x[1] = pk(a.z, a.w);
+            x[2] = pk(b.x, b.y);
+            x[3] = pk(b.z, b.w);
+            return;
+        }
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + p.col));
+        if (dtype == FO_LOGITS_BF16)
+            widen_vec<Bf16>(a, x);
+        else
+            widen_vec<F16>(a, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i)
+        x[i] = pk(2 * i < p.left ? weight_at(w, dtype, p.col + 2 * i) : 0.0f, 2 * i + 1 < p.left ? weight_at(w, dtype, p.col + 2 * i + 1) : 0.0f);
+}
+
+__device__ __forceinline__ float both(f2 v)
+{
+    float a, b;
+    unpk(v, a, b);
+    return __fadd_rn(a, b);
+}
+
+// The sum of v over the kLanes threads of a row, in every one of them. More than
+// a warp: they are a CTA, and `part` holds its warps' sums (two sets in turn, so
+// that one barrier a sum is enough).
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float v, float *part)
+{
+#pragma unroll
+    for (int o = (kLanes < 32 ? kLanes : 32) / 2; o; o >>= 1)
+        v += __shfl_xor_sync(~0u, v, o);
+    if constexpr (kLanes > 32) {
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = part[threadIdx.x % (kLanes / 32)];
+#pragma unroll
+        for (int o = kLanes / 64; o; o >>= 1)
+            v += __shfl_xor_sync(~0u, v, o);
+    }
+    return v;
+}
+
+// The place of unit u of row r; beyond the rows, and beyond the row's units, it is none.
+__device__ __forceinline__ Place row_place(int64_t r, int64_t rows, int u, int units, int64_t width)
+{
+    Place p;
+    const bool there = r < rows && u < units;
+    p.row = there ? r : -1;
+    p.col = (int64_t)u * kUnit;
+    p.left = there ? width - p.col : -64;
+    return p;
+}
+
+template <int kLanes>
+constexpr int kBlockOf = kLanes > 32 ? kLanes : kThreads;   // threads of a CTA
+
+// --- rows held in registers --------------------------------------------------------------
+
+// kLanes threads to a row, each with kVecs of its units (kLanes apart), for kRows
+// rows at once.
+template <class T, bool kWide, int kLanes, int kVecs, int kRows>
+__global__ void __launch_bounds__(kBlockOf<kLanes>) norm_kernel(NormArgs a)
+{
+    __shared__ float part[2][kLanes > 32 ? kLanes / 32 : 1];
+    constexpr int kTeams = kBlockOf<kLanes> / kLanes;
+    const int lane = threadIdx.x % kLanes, units = (int)a.groups * 4;
+    const int64_t first = ((int64_t)blockIdx.x * kTeams + threadIdx.x / kLanes) * kRows;
+    Words<T> v[kRows][kVecs];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            v[i][k] = load_unit<T, kWide>(a.x, row_place(first + i, a.rows, lane + k * kLanes, units, a.width));
+    float inv[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const auto squares = [&](float scale, float *to) {
+            f2 sum = 0;
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                f2 x[kUnit / 2];
+                widen_unit<T>(v[i][k], x);
+#pragma unroll
+                for (int j = 0; j < kUnit / 2; ++j) {
+                    if (scale != 1.0f)
+                        x[j] = mul2(x[j], splat(scale));
+                    sum = fma2(x[j], x[j], sum);
+                }
+            }
+            return row_sum<kLanes>(both(sum), to);
+        };
+        const float sum = squares(1.0f, part[0]);
+        const bool large = !(sum < kLargeSum);
+        inv[i] = inverse_rms(sum, a);
+        if (kLanes > 32 ? large : __any_sync(~0u, large)) {   // the same in a CTA; other rows of a warp keep theirs
+            const float down = inverse_rms_down(squares(kDown, part[1]), a);
+            inv[i] = large ? down : inv[i];
+        }
+        if (lane == 0 && a.inv_rms && first + i < a.rows)
+            a.inv_rms[first + i] = inv[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        const int u = lane + k * kLanes;
+        f2 w[kUnit / 2];
+        weight_unit(a.weight, a.weight_dtype, a.weight_aligned, row_place(0, 1, u, units, a.width), w);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const Place p = row_place(first + i, a.rows, u, units, a.width);
+            f2 x[kUnit / 2], y[kUnit / 2];
+            widen_unit<T>(v[i][k], x);
+#pragma unroll
+            for (int j = 0; j < kUnit / 2; ++j)
+                y[j] = mul2(mul2(x[j], splat(inv[i])), w[j]);
+            store_unit<T, kWide>(a.y, p, narrow_unit<T>(y));
+            if (a.kept.codes)
+                keep_unit<T>(a.kept, (uint32_t)((first + i) * units + u), p.row < 0 ? 0u : ~0u, v[i][k], x);
+        }
+    }
+}
+
+// A unit of dy and of the kept x, as loaded.
+template <class T>
+struct GradUnit {
+    Words<T> dy;
+    Kept x;
+};
+template <class T, bool kWide>
+__device__ __forceinline__ GradUnit<T> load_grad_unit(const NormGradArgs &a, const Place &p, int units, int u)
+{
+    GradUnit<T> v;
+    v.dy = load_unit<T, kWide>(a.grad_y, p);
+    v.x = load_kept(a.kept, (uint32_t)(p.row * units + u), p.row < 0 ? 0u : ~0u);
+    return v;
+}
+
+// The same for the gradient. A team of kLanes threads takes rows a grid apart,
+// the next one's loads on their way while one is summed, and adds up the
+// weight's gradient of its columns in registers; a CTA's teams are joined in
+// shared memory and leave one row of partial sums.
+template <class T, bool kWide, int kLanes, int kVecs>
+__global__ void __launch_bounds__(kBlockOf<kLanes>) norm_grad_kernel(NormGradArgs a)
+{
+    constexpr int kTeams = kBlockOf<kLanes> / kLanes;
+    __shared__ float part[2][kLanes > 32 ? kLanes / 32 : 1];
+    __shared__ __align__(16) float joined[kTeams > 1 ? kTeams : 1][kTeams > 1 ? kLanes * kVecs * kUnit : 4];
+    const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes, units = (int)a.groups * 4;
+    f2 w[kVecs][kUnit / 2], dw[kVecs][kUnit / 2];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        weight_unit(a.weight, a.weight_dtype, a.weight_aligned, row_place(0, 1, lane + k * kLanes, units, a.width), w[k]);
+#pragma unroll
+        for (int j = 0; j < kUnit / 2; ++j)
+            dw[k][j] = 0;
+    }
+    const int64_t step = (int64_t)gridDim.x * kTeams;
+    GradUnit<T> next[kVecs];
+    float next_inv;
+    const auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            next[k] = load_grad_unit<T, kWide>(a, row_place(r, a.rows, lane + k * kLanes, units, a.width), units, lane + k * kLanes);
+        next_inv = r < a.rows ? __ldg(a.inv_rms + r) : 0.0f;
+    };
+    int64_t r = (int64_t)blockIdx.x * kTeams + team;
+    fetch(r);
+    int turn = 0;
+    // every thread takes as many turns as the CTA's first team: barriers and shuffles are all threads'
+    for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += step, r += step, turn ^= 1) {
+        f2 t[kVecs][kUnit / 2], h[kVecs][kUnit / 2], dot = 0;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            widen_unit<T>(next[k].dy, t[k]);
+            kept_unit(next[k].x, h[k]);
+#pragma unroll
+            for (int j = 0; j < kUnit / 2; ++j) {
+                h[k][j] = mul2(h[k][j], splat(next_inv));
+                dw[k][j] = fma2(t[k][j], h[k][j], dw[k][j]);
+                t[k][j] = mul2(t[k][j], w[k][j]);
+                dot = fma2(t[k][j], h[k][j], dot);
+            }
+        }
+        const float inv = next_inv;
+        fetch(r + step);
+        if (a.grad.data) {
+            const float mean = __fmul_rn(row_sum<kLanes>(both(dot), part[turn]), a.inv_width);
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+#pragma unroll
+                for (int j = 0; j < kUnit / 2; ++j)
+                    t[k][j] = mul2(fma2(h[k][j], splat(-mean), t[k][j]), splat(inv));
+                store_unit<T, kWide>(a.grad, row_place(r, a.rows, lane + k * kLanes, units, a.width), narrow_unit<T>(t[k]));
+            }
+        }
+    }
+    if (!a.grad_weight)
+        return;
+    float *const to = a.parts + (int64_t)blockIdx.x * a.groups * kGroup;
+    if constexpr (kTeams > 1) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+#pragma unroll
+            for (int j = 0; j < kUnit / 2; ++j)
+                *reinterpret_cast<f2 *>(&joined[team][(lane + k * kLanes) * kUnit + 2 * j]) = dw[k][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < units * kUnit; c += kThreads) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kTeams; ++i)
+                sum += joined[i][c];
+            to[c] = sum;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int u = lane + k * kLanes;
+            if (u < units)
+#pragma unroll
+                for (int j = 0; j < kUnit / 4; ++j)
+                    reinterpret_cast<ulonglong2 *>(to + u * kUnit)[j] = make_ulonglong2(dw[k][2 * j], dw[k][2 * j + 1]);
+        }
+    }
+}
+
+// The parts of 32 columns by a CTA: eight chains a column, joined pairwise.
+__global__ void __launch_bounds__(kThreads) norm_weight_kernel(NormGradArgs a, int parts)
+{
+    __shared__ float part[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float sum = 0.0f;
+    for (int p = warp; c < a.width && p < parts; p += kWarps)
+        sum += a.parts[p * a.groups * kGroup + c];
+    part[warp][lane] = sum;
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1) {
+        __syncthreads();
+        if (warp < o)
+            part[warp][lane] += part[warp + o][lane];
+    }
+    if (warp == 0 && c < a.width)
+        store_weight(a.grad_weight, a.weight_dtype, c, part[0][lane]);
+}
+
+// --- longer rows: read again from the L2 cache -----------------------------------------------
+
 // Element `c` of row `r`.
 template <class T>
 __device__ __forceinline__ float load_at(const RowsIn &x, int64_t r, int64_t c)
@@ -37,22 +330,6 @@ __device__ __forceinline__ float kept_at(const KeptIn &k, int64_t group, int lan
     return __fmul_rn((float)k.codes[group * kGroup + lane], step_value(k.steps[group]));
 }
 
-__device__ __forceinline__ float weight_at(const void *w, int dtype, int64_t i)
-{
-    if (!w)
-        return 1.0f;
-    return dtype == FO_LOGITS_F32    ? static_cast<const float *>(w)[i]
-           : dtype == FO_LOGITS_BF16 ? Bf16::widen(static_cast<const uint16_t *>(w)[i])
-                                     : F16::widen(static_cast<const uint16_t *>(w)[i]);
-}
-__device__ __forceinline__ void store_weight(void *w, int dtype, int64_t i, float v)
-{
-    if (dtype == FO_LOGITS_F32)
-        static_cast<float *>(w)[i] = v;
-    else
-        static_cast<uint16_t *>(w)[i] = dtype == FO_LOGITS_BF16 ? Bf16::narrow(v) : F16::narrow(v);
-}
-
 // The sum of v over the CTA, in every thread.
 __device__ __forceinline__ float block_sum(float v, float *part)
 {
@@ -68,47 +345,27 @@ __device__ __forceinline__ float block_sum(float v, float *part)
     return v;
 }
 
-// 1 / sqrt(mean x^2 + eps) from the sum of squares of x / scale.
-__device__ __forceinline__ float inverse_rms(float sum, float scale, const NormArgs &a)
-{
-    const float mean = sum / (float)a.width;
-    return 1.0f / scale / sqrtf(mean + a.eps / scale / scale);
-}
-
 // A row a CTA.
 template <class T>
-__global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs a)
+__global__ void __launch_bounds__(kThreads) norm_long_kernel(NormArgs a)
 {
     __shared__ float part[kWarps];
     const int64_t r = blockIdx.x;
-    float sum = 0.0f, most = 0.0f;
+    float sum = 0.0f;
     for (int64_t c = threadIdx.x; c < a.width; c += kThreads) {
         const float x = load_at<T>(a.x, r, c);
         sum = __fmaf_rn(x, x, sum);
     }
     sum = block_sum(sum, part);
-    float scale = 1.0f;
-    if (!(sum < 0x1p120f)) {   // rare: x^2 may lie outside FP32, or x is not finite
-        for (int64_t c = threadIdx.x; c < a.width; c += kThreads)
-            most = max_nan(most, fabsf(load_at<T>(a.x, r, c)));
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            most = max_nan(most, __shfl_xor_sync(~0u, most, o));
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x / 32] = most;
-        __syncthreads();
-        for (int i = 0; i < kWarps; ++i)
-            most = max_nan(most, part[i]);
-        scale = most < kInf ? 0x1p96f : kNan;
+    float inv = inverse_rms(sum, a);
+    if (!(sum < kLargeSum)) {   // the same in the whole CTA
         sum = 0.0f;
         for (int64_t c = threadIdx.x; c < a.width; c += kThreads) {
-            const float x = load_at<T>(a.x, r, c) / scale;
+            const float x = __fmul_rn(load_at<T>(a.x, r, c), kDown);
             sum = __fmaf_rn(x, x, sum);
         }
-        sum = block_sum(sum, part);
+        inv = inverse_rms_down(block_sum(sum, part), a);
     }
-    const float inv = inverse_rms(sum, scale, a);
     if (threadIdx.x == 0 && a.inv_rms)
         a.inv_rms[r] = inv;
     for (int64_t g = threadIdx.x / 32; g < a.groups; g += kWarps) {
@@ -122,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs a)
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) norm_grad_kernel(NormGradArgs a)
+__global__ void __launch_bounds__(kThreads) norm_long_grad_kernel(NormGradArgs a)
 {
     __shared__ float part[kWarps];
     const int64_t r = blockIdx.x;
@@ -142,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(NormGradArgs a)
 
 // Columns by a thread each, rows part, part + parts, ... by a CTA.
 template <class T>
-__global__ void __launch_bounds__(kThreads) norm_weight_parts_kernel(NormGradArgs a)
+__global__ void __launch_bounds__(kThreads) norm_long_weight_kernel(NormGradArgs a)
 {
     const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
     if (c >= a.width)
@@ -152,50 +409,114 @@ __global__ void __launch_bounds__(kThreads) norm_weight_parts_kernel(NormGradArg
         const float h = __fmul_rn(kept_at(a.kept, r * a.groups + c / kGroup, (int)(c % kGroup)), a.inv_rms[r]);
         sum = __fmaf_rn(load_at<T>(a.grad_y, r, c), h, sum);
     }
-    a.parts[blockIdx.x * a.width + c] = sum;
+    a.parts[blockIdx.x * a.groups * kGroup + c] = sum;
 }
 
-// The parts of 32 columns by a CTA: eight chains a column, joined pairwise.
-__global__ void __launch_bounds__(kThreads) norm_weight_kernel(NormGradArgs a, int parts)
-{
-    __shared__ float part[kWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    float sum = 0.0f;
-    for (int p = warp; c < a.width && p < parts; p += kWarps)
-        sum += a.parts[p * a.width + c];
-    part[warp][lane] = sum;
-#pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) {
-        __syncthreads();
-        if (warp < o)
-            part[warp][lane] += part[warp + o][lane];
-    }
-    if (warp == 0 && c < a.width)
-        store_weight(a.grad_weight, a.weight_dtype, c, part[0][lane]);
-}
 
-template <class T>
+constexpr int64_t kMaxUnits = 2048;   // of a row in registers: 16384 elements
+
+template <class T, bool kWide, int kLanes, int kVecs>
 cudaError_t launch(const NormArgs &a, cudaStream_t stream)
 {
-    norm_kernel<T><<<(unsigned)a.rows, kThreads, 0, stream>>>(a);
+    constexpr int kRows = kLanes > 32 ? 1 : 4 / kVecs;
+    constexpr int kBlock = kBlockOf<kLanes>, kEach = kBlock / kLanes * kRows;
+    norm_kernel<T, kWide, kLanes, kVecs, kRows><<<(unsigned)((a.rows + kEach - 1) / kEach), kBlock, 0, stream>>>(a);
     count_launch();
     return cudaGetLastError();
 }
-template <class T>
-cudaError_t launch(const NormGradArgs &a, cudaStream_t stream)
+template <class T, bool kWide>
+cudaError_t launch(const NormArgs &a, cudaStream_t stream)
 {
-    if (a.grad.data) {
-        norm_grad_kernel<T><<<(unsigned)a.rows, kThreads, 0, stream>>>(a);
-        count_launch();
-    }
-    if (a.grad_weight) {
-        const int parts = (int)std::min<int64_t>(a.rows, FO_NORM_PARTS);
-        const unsigned columns = (unsigned)((a.width + kThreads - 1) / kThreads);
-        if (parts) {
-            norm_weight_parts_kernel<T><<<dim3((unsigned)parts, columns), kThreads, 0, stream>>>(a);
+    const int64_t units = a.groups * 4;
+    if (units <= 4)
+        return launch<T, kWide, 4, 1>(a, stream);
+    if (units <= 8)
+        return launch<T, kWide, 8, 1>(a, stream);
+    if (units <= 16)
+        return launch<T, kWide, 16, 1>(a, stream);
+    if (units <= 32)
+        return launch<T, kWide, 32, 1>(a, stream);
+    if (units <= 64)
+        return launch<T, kWide, 32, 2>(a, stream);
+    if (units <= 128)
+        return launch<T, kWide, 32, 4>(a, stream);
+    if (units <= 256)
+        return launch<T, kWide, 64, 4>(a, stream);
+    if (units <= 512)
+        return launch<T, kWide, 128, 4>(a, stream);
+    if (units <= 1024)
+        return launch<T, kWide, 256, 4>(a, stream);
+    return launch<T, kWide, 512, 4>(a, stream);
+}
+template <class T>
+cudaError_t launch(NormArgs a, cudaStream_t stream)
+{
+    a.inv_width = (float)(1.0 / (double)a.width);
+    a.weight_aligned = (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
+    if (a.groups * 4 <= kMaxUnits)
+        return wide<T>(a.x.data, a.x.stride) && wide<T>(a.y.data, a.y.stride) ? launch<T, true>(a, stream) : launch<T, false>(a, stream);
+    norm_long_kernel<T><<<(unsigned)a.rows, kThreads, 0, stream>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// The CTAs that are on the device at once, or one for each set of teams; the
+// parts they leave are then added up.
+template <class T, bool kWide, int kLanes, int kVecs>
+int launch_parts(const NormGradArgs &a, cudaStream_t stream)
+{
+    constexpr int kBlock = kBlockOf<kLanes>, kTeams = kBlock / kLanes;
+    const int64_t fit = std::min<int64_t>(FO_NORM_PARTS, (int64_t)sm_count() * std::max(1, 1024 / kBlock));
+    const int ctas = (int)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, fit);
+    norm_grad_kernel<T, kWide, kLanes, kVecs><<<ctas, kBlock, 0, stream>>>(a);
+    count_launch();
+    return ctas;
+}
+template <class T, bool kWide>
+int launch_parts(const NormGradArgs &a, cudaStream_t stream)
+{
+    const int64_t units = a.groups * 4;
+    if (units <= 4)
+        return launch_parts<T, kWide, 4, 1>(a, stream);
+    if (units <= 8)
+        return launch_parts<T, kWide, 8, 1>(a, stream);
+    if (units <= 16)
+        return launch_parts<T, kWide, 16, 1>(a, stream);
+    if (units <= 32)
+        return launch_parts<T, kWide, 32, 1>(a, stream);
+    if (units <= 64)
+        return launch_parts<T, kWide, 32, 2>(a, stream);
+    if (units <= 128)
+        return launch_parts<T, kWide, 64, 2>(a, stream);
+    if (units <= 256)
+        return launch_parts<T, kWide, 128, 2>(a, stream);
+    if (units <= 512)
+        return launch_parts<T, kWide, 256, 2>(a, stream);
+    if (units <= 1024)
+        return launch_parts<T, kWide, 512, 2>(a, stream);
+    return launch_parts<T, kWide, 1024, 2>(a, stream);
+}
+template <class T>
+cudaError_t launch(NormGradArgs a, cudaStream_t stream)
+{
+    a.inv_width = (float)(1.0 / (double)a.width);
+    a.weight_aligned = (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
+    int parts = 0;
+    if (a.rows > 0 && a.groups * 4 <= kMaxUnits)
+        parts = wide<T>(a.grad_y.data, a.grad_y.stride) && wide<T>(a.grad.data, a.grad.stride) ? launch_parts<T, true>(a, stream)
+                                                                                               : launch_parts<T, false>(a, stream);
+    else if (a.rows > 0) {
+        if (a.grad.data) {
+            norm_long_grad_kernel<T><<<(unsigned)a.rows, kThreads, 0, stream>>>(a);
             count_launch();
         }
+        if (a.grad_weight) {
+            parts = (int)std::min<int64_t>(a.rows, FO_NORM_PARTS);
+            norm_long_weight_kernel<T><<<dim3((unsigned)parts, (unsigned)((a.width + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
+            count_launch();
+        }
+    }
+    if (a.grad_weight) {
         norm_weight_kernel<<<(unsigned)((a.width + 31) / 32), kThreads, 0, stream>>>(a, parts);
         count_launch();
     }

@@ -775,7 +775,7 @@ def fo_rms_norm_grad(codes, steps, inv_rms, grad_y, grad_x=None, weight=None, gr
     if w is not None and gw is not None and wt != gt:
         raise TypeError("grad_weight must be of weight's type")
     c, s = _kept(codes, steps, m, cur)
-    need = 0 if grad_weight is None else min(m.rows, FO_NORM_PARTS) * m.width
+    need = 0 if grad_weight is None else min(m.rows, FO_NORM_PARTS) * groups(m.width) * GROUP
     status = lib().fo_rms_norm_grad(
         c, s, _array(inv_rms, "inv_rms", torch.float32, m.rows, cur), w, wt if gw is None else gt, ctypes.byref(m), _ref(to), gw,
         _array(workspace, "workspace", torch.float32, need, cur), _stream(stream))
