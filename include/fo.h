@@ -496,13 +496,15 @@ fo_status_t fo_policy_loss_grad(const fo_logits_t *logits, const int64_t *tokens
  */
 typedef struct fo_rows {
     void *data;             /* only read where the call names the matrix in, up or grad_y */
-    int64_t rows, width;    /* rows * ceil(width / 32) <= FO_MAX_ACT_GROUPS            */
+    int64_t rows, width;    /* width <= FO_MAX_ACT_WIDTH, rows * ceil(width / 32) <=
+                             * FO_MAX_ACT_GROUPS                                      */
     int64_t row_stride;     /* elements, not negative                                  */
     int32_t dtype;          /* fo_logit_dtype_t                                        */
     int32_t reserved;       /* 0                                                       */
 } fo_rows_t;
 
 #define FO_MAX_ACT_GROUPS (1 << 29)
+#define FO_MAX_ACT_WIDTH (1 << 30)
 #define FO_NORM_PARTS 1024  /* rows of fo_rms_norm_grad's workspace, at most */
 
 /* Activation functions. */

@@ -17,21 +17,23 @@
 
 namespace fo {
 
-// The bits of |x| of a value in FP32, as an unsigned number: it orders as |x|
-// does, infinity and NaN above everything finite.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// The step of a group whose largest magnitude has these bits. a times RN(1/127)
-// is within a rounding and a half of a / 127: cut to BF16 it is at most two
-// BF16 numbers short of the smallest s with 127 s >= a, a product that is exact.
+// The step of a group whose largest magnitude a has these bits. kBelow is less
+// than 1 / 127 by 3 roundings, so that t = RN(a kBelow) is below a / 127, but
+// by less than 2^-21 of it. Cut to BF16, t is then the largest BF16 number below
+// a / 127, and the next one is the step: also where a / 127 is a BF16 number
+// itself. Only where it lies above one by less than 2^-21, which the 8 or 11 bits
+// of a BF16 or FP16 value do not reach, is that one short: 127 s, which is
+// exact, says so. An infinity's t becomes NaN by the last addition; that of NaN
+// runs over, and is taken back.
+template <bool kFewBits>
 __device__ __forceinline__ float step_of(uint32_t magnitude_bits)
 {
-    if (magnitude_bits >= 0x7f800000u)
-        return kNan;
+    constexpr float kBelow = 0x1.020402p-7f;
     const float a = __uint_as_float(magnitude_bits);
-    uint32_t s = __float_as_uint(fmaxf(__fmul_rn(a, 0x1.020408p-7f), 0x1p-126f)) & 0xffff0000u;
-    s += __fmul_rn(127.0f, __uint_as_float(s)) < a ? 0x10000u : 0u;
-    s += __fmul_rn(127.0f, __uint_as_float(s)) < a ? 0x10000u : 0u;
+    const uint32_t t = max(__float_as_uint(__fmul_rn(a, kBelow)), 0x007fffffu);   // at least just below 2^-126
+    uint32_t s = min((t & 0xffff0000u) + 0x10000u, 0x7fc00000u);
+    if (!kFewBits && __fmul_rn(127.0f, __uint_as_float(s)) < a)
+        s += 0x10000u;
     return __uint_as_float(s);
 }
 
@@ -41,7 +43,6 @@ __device__ __forceinline__ float step_value(uint16_t bits) { return __uint_as_fl
 // In the sum of x r and 1.5 2^23 the last place is 1: the one rounding of the
 // fused operation is rint(x r), whose lowest byte is the code.
 constexpr float kRound = 12582912.0f;
-__device__ __forceinline__ uint32_t code_word(float x, float r) { return __float_as_uint(__fmaf_rn(x, r, kRound)); }
 
 // --- activation functions --------------------------------------------------------------
 
@@ -157,14 +158,14 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor &d) { ret
 // Where a unit lies. `left`: elements of the row from its first one on (0 or
 // less beyond the row's end). Beyond the last row: row -1, and `left` far below 0.
 struct Place {
-    int64_t row, col, left;
+    int row, col, left;
 };
-__device__ __forceinline__ Place place(uint32_t unit, uint32_t units, const Divisor &per_row, int64_t width)
+__device__ __forceinline__ Place place(uint32_t unit, uint32_t units, const Divisor &per_row, int width)
 {
     const uint32_t r = quotient(unit, per_row);
     Place p;
-    p.row = unit < units ? (int64_t)r : -1;
-    p.col = (int64_t)(unit - r * per_row.d) * kUnit;
+    p.row = unit < units ? (int)r : -1;
+    p.col = (int)((unit - r * per_row.d) * kUnit);
     p.left = unit < units ? width - p.col : -64;
     return p;
 }
@@ -176,11 +177,13 @@ struct Words {
     uint32_t w[kN];
 };
 
-// Whether vectors of 16 bytes line up with the units of every row.
+// Whether every unit of a matrix lies wholly in its row and in aligned vectors of
+// 16 bytes (kWide below; so it is where widths and strides are multiples of 8 and
+// the matrix starts at such a boundary), or wholly beyond its width.
 template <class T>
-inline bool wide(const void *data, int64_t stride)
+inline bool wide(int64_t width, const void *data, int64_t stride)
 {
-    return (reinterpret_cast<uintptr_t>(data) & 15) == 0 && stride * (int64_t)sizeof(typename T::raw) % 16 == 0;
+    return width % kUnit == 0 && (reinterpret_cast<uintptr_t>(data) & 15) == 0 && stride * (int64_t)sizeof(typename T::raw) % 16 == 0;
 }
 
 // The words from element `from` on of a longer run of them; `from` < 8 of 16 bits
@@ -201,6 +204,16 @@ __device__ __forceinline__ void shifted(uint32_t (&in)[kIn], int from, uint32_t 
         out[i] = kHalves ? __funnelshift_r(in[i], in[i + 1 < kIn ? i + 1 : i], from & 1 ? 16 : 0) : in[i];
 }
 
+template <class T>
+__device__ __forceinline__ void load_vector(const uint4 *at, uint32_t *w)
+{
+    const uint4 a = __ldcs(at);
+    w[0] = a.x;
+    w[1] = a.y;
+    w[2] = a.z;
+    w[3] = a.w;
+}
+
 // A unit; 0 beyond the row's end. No byte outside the row is read. Without kWide
 // the row may start anywhere: the aligned vectors that hold the unit are read
 // and shifted.
@@ -210,17 +223,23 @@ __device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
     typedef typename T::raw raw;
     constexpr int kSize = sizeof(raw), kVecs = kUnit * kSize / 16;
     Words<T> v;
-    const raw *at = static_cast<const raw *>(x.data) + p.row * x.stride + p.col;
-    const int phase = kWide ? 0 : (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize);
-    if (phase == 0 && p.left >= kUnit) {
+    const raw *at = static_cast<const raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(at) + i);
-            v.w[4 * i] = a.x; v.w[4 * i + 1] = a.y; v.w[4 * i + 2] = a.z; v.w[4 * i + 3] = a.w;
-        }
+    for (int i = 0; i < Words<T>::kN; ++i)
+        v.w[i] = 0;
+    if (kWide) {
+        if (p.left > 0)
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                load_vector<T>(reinterpret_cast<const uint4 *>(at) + i, v.w + 4 * i);
         return v;
     }
-    if (!kWide && p.col >= phase && p.left + phase >= (kVecs + 1) * 16 / kSize) {
+    const int phase = (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize);
+    if (phase == 0 && p.left >= kUnit) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            load_vector<T>(reinterpret_cast<const uint4 *>(at) + i, v.w + 4 * i);
+    } else if (p.col >= phase && p.left + phase >= (kVecs + 1) * 16 / kSize) {
         uint32_t in[4 * (kVecs + 1)];
 #pragma unroll
         for (int i = 0; i <= kVecs; ++i) {
@@ -228,16 +247,13 @@ __device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
             in[4 * i] = a.x; in[4 * i + 1] = a.y; in[4 * i + 2] = a.z; in[4 * i + 3] = a.w;
         }
         shifted<T>(in, phase, v.w);
-        return v;
+    } else {
+        raw *e = reinterpret_cast<raw *>(v.w);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i)
+            if (i < p.left)
+                e[i] = at[i];
     }
-#pragma unroll
-    for (int i = 0; i < Words<T>::kN; ++i)
-        v.w[i] = 0;
-    raw *e = reinterpret_cast<raw *>(v.w);
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i)
-        if (i < p.left)
-            e[i] = at[i];
     return v;
 }
 
@@ -250,36 +266,36 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
 {
     typedef typename T::raw raw;
     constexpr int kSize = sizeof(raw), kVecs = kUnit * kSize / 16, kN = Words<T>::kN;
-    raw *const at = static_cast<raw *>(x.data) + p.row * x.stride + p.col;
-    const int phase = kWide ? 0 : (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize);
-    uint32_t out[kN];
+    raw *const at = static_cast<raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
+    if (kWide) {
+        if (p.left > 0)
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                __stcs(reinterpret_cast<uint4 *>(at) + i, make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]));
+        return;
+    }
+    const int phase = (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize), lane = threadIdx.x & 31;
+    constexpr int kOver = kSize == 2 ? 4 : 3;   // words that a unit hands over at most
+    uint32_t in[kOver + kN], out[kN];
+#pragma unroll
+    for (int i = 0; i < kOver; ++i)
+        in[i] = __shfl_up_sync(~0u, v.w[kN - kOver + i], 1);
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-        out[i] = v.w[i];
-    int64_t lo = 0, hi = p.left;         // places of `out`, from the vectors' first on, that are the row's
-    if (!kWide) {
-        const int lane = threadIdx.x & 31;
-        constexpr int kOver = kSize == 2 ? 4 : 3;   // words that a unit hands over at most
-        uint32_t in[kOver + kN];
+        in[kOver + i] = out[i] = v.w[i];
+    const int next_row = __shfl_down_sync(~0u, p.row, 1);
+    const bool before = lane > 0 && p.col > 0, after = lane < 31 && next_row == p.row;
+    int lo = 0, hi = p.left;             // places of `out`, from the vectors' first on, that are the row's
+    if (phase) {
+        shifted<T>(in, (kSize == 2 ? 8 : 3) - phase, out);
+        lo = before ? 0 : phase;
+        hi = p.left + phase;
+        if (!after) {                    // the unit's last elements
+            const raw *e = reinterpret_cast<const raw *>(v.w);
 #pragma unroll
-        for (int i = 0; i < kOver; ++i)
-            in[i] = __shfl_up_sync(~0u, v.w[kN - kOver + i], 1);
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-            in[kOver + i] = v.w[i];
-        const int64_t next_row = __shfl_down_sync(~0u, p.row, 1);
-        const bool before = lane > 0 && p.col > 0, after = lane < 31 && next_row == p.row;
-        if (phase) {
-            shifted<T>(in, (kSize == 2 ? 8 : 3) - phase, out);
-            lo = before ? 0 : phase;
-            hi = p.left + phase;
-            if (!after) {                // the unit's last elements
-                const raw *e = reinterpret_cast<const raw *>(v.w);
-#pragma unroll
-                for (int i = 1; i < kUnit; ++i)
-                    if (i >= kUnit - phase && i < p.left)
-                        at[i] = e[i];
-            }
+            for (int i = 1; i < kUnit; ++i)
+                if (i >= kUnit - phase && i < p.left)
+                    at[i] = e[i];
         }
     }
     raw *const to = at - phase;
@@ -344,7 +360,7 @@ __device__ __forceinline__ float group_step(const Words<T> &v)
         m = max_u16x2(max_u16x2(v.w[0] & k, v.w[1] & k), max_u16x2(v.w[2] & k, v.w[3] & k));
         m = max_u16x2(m, __shfl_xor_sync(~0u, m, 1));
         m = max_u16x2(m, __shfl_xor_sync(~0u, m, 2));
-        m = __float_as_uint(T::widen((typename T::raw)max(m & 0xffffu, m >> 16)));
+        return step_of<true>(__float_as_uint(T::widen((typename T::raw)max(m & 0xffffu, m >> 16))));
     } else {
         m = 0;
 #pragma unroll
@@ -352,8 +368,8 @@ __device__ __forceinline__ float group_step(const Words<T> &v)
             m = max(m, v.w[i] & 0x7fffffffu);
         m = max(m, __shfl_xor_sync(~0u, m, 1));
         m = max(m, __shfl_xor_sync(~0u, m, 2));
+        return step_of<false>(m);
     }
-    return step_of(m);
 }
 
 // RN(1 / step): the hardware's approximation and a step of Newton's, which is
@@ -395,6 +411,7 @@ __device__ __forceinline__ void keep_unit(const KeptOut &k, uint32_t unit, uint3
 
 // A unit's codes and step as loaded, and the values x^ they stand for. A code
 // becomes the low byte of 2^23 + 128 + code, from which FP32 takes the rest away.
+// `factor` is multiplied into the step first.
 struct Kept {
     uint2 codes;
     uint16_t step;
@@ -408,9 +425,9 @@ __device__ __forceinline__ Kept load_kept(const KeptIn &k, uint32_t unit, uint32
     }
     return v;
 }
-__device__ __forceinline__ void kept_unit(const Kept &v, f2 (&x)[kUnit / 2])
+__device__ __forceinline__ void kept_unit(const Kept &v, f2 (&x)[kUnit / 2], float factor = 1.0f)
 {
-    const f2 base = splat(-(8388608.0f + 128.0f)), step = splat(step_value(v.step));
+    const f2 base = splat(-(8388608.0f + 128.0f)), step = splat(__fmul_rn(step_value(v.step), factor));
     const uint32_t lo = v.codes.x ^ 0x80808080u, hi = v.codes.y ^ 0x80808080u;
 #pragma unroll
     for (int i = 0; i < kUnit / 2; ++i) {

@@ -22,7 +22,7 @@ fo_status_t check_rows(const fo_rows_t *x, bool written, const fo_rows_t *like =
 {
     if (!x)
         return FO_ERR_NULL;
-    if (x->rows < 0 || x->width < 1 || x->width > (int64_t)FO_MAX_ACT_GROUPS * FO_GROUP || x->rows > FO_MAX_ACT_GROUPS / groups_of(x->width))
+    if (x->rows < 0 || x->width < 1 || x->width > FO_MAX_ACT_WIDTH || x->rows > FO_MAX_ACT_GROUPS / groups_of(x->width))
         return FO_ERR_SIZE;
     if (!dtype_ok(x->dtype) || x->reserved != 0 || x->row_stride < 0 || x->row_stride > kMaxStride)
         return FO_ERR_BAD_ARG;

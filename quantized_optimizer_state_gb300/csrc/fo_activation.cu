@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, 
     Words<T> v[kUnits], up[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const Place p = place(first + i * kThreads, g.units, g.per_row, a.width);
+        const Place p = place(first + i * kThreads, g.units, g.per_row, (int)a.width);
         v[i] = load_unit<T, kWide>(a.x, p);
         if (kGated)
             up[i] = load_unit<T, kWide>(a.up, p);
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, 
             if (kGated)
                 y[k] = mul2(y[k], u[k]);
         }
-        store_unit<T, kWide>(a.y, place(unit, g.units, g.per_row, a.width), narrow_unit<T>(y));
+        store_unit<T, kWide>(a.y, place(unit, g.units, g.per_row, (int)a.width), narrow_unit<T>(y));
         if (a.kept.codes) {
             keep_unit<T>(a.kept, unit, g.units, v[i], x);
             if (kGated)
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGra
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t unit = first + i * kThreads;
-        dy[i] = load_unit<T, kWide>(a.grad_y, place(unit, g.units, g.per_row, a.width));
+        dy[i] = load_unit<T, kWide>(a.grad_y, place(unit, g.units, g.per_row, (int)a.width));
         v[i] = load_kept(a.kept, unit, g.units);
         if (kGated)
             up[i] = load_kept(a.kept_up, unit, g.units);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGra
             }
             d[k] = mul2(d[k], pk(f.slope, h.slope));
         }
-        const Place p = place(first + i * kThreads, g.units, g.per_row, a.width);
+        const Place p = place(first + i * kThreads, g.units, g.per_row, (int)a.width);
         store_unit<T, kWide>(a.grad, p, narrow_unit<T>(d));
         if (kGated)
             store_unit<T, kWide>(a.grad_up, p, narrow_unit<T>(du));
@@ -90,7 +90,7 @@ cudaError_t launch(const ActivationArgs &a, cudaStream_t stream)
 {
     constexpr int kUnits = 2;
     const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.x.data, a.x.stride) && wide<T>(a.up.data, a.up.stride) && wide<T>(a.y.data, a.y.stride))
+    if (wide<T>(a.width, a.x.data, a.x.stride) && wide<T>(a.width, a.up.data, a.up.stride) && wide<T>(a.width, a.y.data, a.y.stride))
         activation_kernel<T, kKind, kGated, true, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
     else
         activation_kernel<T, kKind, kGated, false, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
@@ -102,7 +102,7 @@ cudaError_t launch(const ActivationGradArgs &a, cudaStream_t stream)
 {
     constexpr int kUnits = 2;
     const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.grad_y.data, a.grad_y.stride) && wide<T>(a.grad.data, a.grad.stride) && wide<T>(a.grad_up.data, a.grad_up.stride))
+    if (wide<T>(a.width, a.grad_y.data, a.grad_y.stride) && wide<T>(a.width, a.grad.data, a.grad.stride) && wide<T>(a.width, a.grad_up.data, a.grad_up.stride))
         activation_grad_kernel<T, kKind, kGated, true, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
     else
         activation_grad_kernel<T, kKind, kGated, false, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);

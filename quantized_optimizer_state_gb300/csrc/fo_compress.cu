@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(kThreads) compress_kernel(CompressArgs a, Unit
     Words<T> v[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-        v[i] = load_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, a.width));
+        v[i] = load_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, (int)a.width));
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         f2 x[kUnit / 2];
@@ -35,29 +35,17 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs a, UnitGrid
     for (int i = 0; i < kUnits; ++i) {
         f2 x[kUnit / 2];
         kept_unit(k[i], x);
-        store_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, a.width), narrow_unit<T>(x));
+        store_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, (int)a.width), narrow_unit<T>(x));
     }
 }
 
 unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * kUnits - 1) / (kThreads * kUnits); }
 
-// Rows that follow one another without a gap, of whole groups, are one row.
-template <class A>
-void join_rows(A &a, int64_t stride)
-{
-    if (stride == a.width && a.width % kGroup == 0) {
-        a.width *= a.rows;
-        a.groups *= a.rows;
-        a.rows = 1;
-    }
-}
-
 template <class T>
-cudaError_t launch(CompressArgs a, cudaStream_t stream)
+cudaError_t launch(const CompressArgs &a, cudaStream_t stream)
 {
-    join_rows(a, a.x.stride);
     const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.x.data, a.x.stride))
+    if (wide<T>(a.width, a.x.data, a.x.stride))
         compress_kernel<T, true><<<ctas(g), kThreads, 0, stream>>>(a, g);
     else
         compress_kernel<T, false><<<ctas(g), kThreads, 0, stream>>>(a, g);
@@ -65,11 +53,10 @@ cudaError_t launch(CompressArgs a, cudaStream_t stream)
     return cudaGetLastError();
 }
 template <class T>
-cudaError_t launch(ExpandArgs a, cudaStream_t stream)
+cudaError_t launch(const ExpandArgs &a, cudaStream_t stream)
 {
-    join_rows(a, a.x.stride);
     const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.x.data, a.x.stride))
+    if (wide<T>(a.width, a.x.data, a.x.stride))
         expand_kernel<T, true><<<ctas(g), kThreads, 0, stream>>>(a, g);
     else
         expand_kernel<T, false><<<ctas(g), kThreads, 0, stream>>>(a, g);

@@ -101,6 +101,7 @@ class FoPolicy(ctypes.Structure):
 FO_ACT_SILU = 0         # fo_act_t
 FO_ACT_GELU = 1
 FO_MAX_ACT_GROUPS = 1 << 29
+FO_MAX_ACT_WIDTH = 1 << 30
 FO_NORM_PARTS = 1024
 
 
