@@ -48,83 +48,109 @@ constexpr float kRound = 12582912.0f;
 
 enum : int { kSilu = 0, kGelu = 1 };
 
-// f(x) and, with kSlope, its derivative. kExact: for FP32, whose results keep
-// what 16-bit ones lose in their own rounding: the exponential's argument in two
-// parts, the reciprocal with a step of Newton's.
+// Both functions are, with u = |x|,
+//   f(x) = max(x, 0) - u q(u),   f'(x) = v(u) for x < 0, 1 - v(u) else
+//   silu: q = e / (1 + e), e = e^-u;         v = q (1 - u / (1 + e))
+//   gelu: q = the normal tail Phi(-u) = Q(1 / (1 + 0.3 u)) e^(-u^2 / 2), Q a
+//         polynomial;                        v = q - u phi(u)
+// so that far on the negative side results keep their relative precision, which
+// 1 - s and 1 + erf lose, and the limit at -inf is 0. u is held at 120 (15),
+// beyond which u q and v are 0 in FP32. Pairs of values: two operations an
+// instruction. Below, q and v are formed with their signs turned, which saves
+// negations.
+// kExact is for FP32, whose results keep what 16-bit ones lose in their own
+// rounding: the exponential's argument in two parts, the reciprocal with a step of
+// Newton's, and Q of degree 8 instead of 6. Q has the least relative error for u
+// in [0, 15]: 5.8e-8 and 1.9e-6, as evaluated in FP32 3.7e-7 and 2.2e-6.
 struct Curve {
-    float value, slope;
+    f2 value, slope;
 };
 
 // e^-(u v), u v >= 0
 template <bool kExact>
-__device__ __forceinline__ float exp_minus(float u, float v)
+__device__ __forceinline__ f2 exp_minus(f2 u, f2 v)
 {
     constexpr float kHigh = 1.44269504088896341f, kLow = (float)(1.44269504088896341 - (double)1.44269504088896341f);
-    const float p = __fmul_rn(u, v), t = __fmul_rn(-p, kHigh);
+    const f2 p = mul2(u, v), t = mul2(p, splat(-kHigh));
+    float a, b;
+    unpk(t, a, b);
     if (!kExact)
-        return exp2_approx(t);
-    float e;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+        return pk(exp2_approx(a), exp2_approx(b));
+    asm("ex2.approx.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.f32 %0, %0;" : "+f"(b));
     // t, p and kHigh as they were rounded, to first order
-    const float rest = __fmaf_rn(-__fmaf_rn(u, v, -p), kHigh, __fmaf_rn(-p, kLow, __fmaf_rn(-p, kHigh, -t)));
-    return __fmaf_rn(e, __fmul_rn(rest, kLn2), e);
+    const f2 e = pk(a, b), minus = splat(-1.0f), np = mul2(p, minus), lost = fma2(u, v, np);
+    const f2 rest = fma2(lost, splat(-kHigh), fma2(np, splat(kLow), fma2(np, splat(kHigh), mul2(t, minus))));
+    return fma2(e, mul2(rest, splat(kLn2)), e);
 }
 
 template <bool kExact>
-__device__ __forceinline__ float reciprocal(float x)
+__device__ __forceinline__ f2 reciprocal(f2 x)
 {
-    const float y = rcp_approx(x);
-    return kExact ? __fmaf_rn(y, __fmaf_rn(-x, y, 1.0f), y) : y;
+    float a, b;
+    unpk(x, a, b);
+    const f2 y = pk(rcp_approx(a), rcp_approx(b));
+    return kExact ? fma2(y, fma2(mul2(x, splat(-1.0f)), y, splat(1.0f)), y) : y;
 }
 
-// silu(x) = x s with s = 1 / (1 + e^-x), silu'(x) = s (1 + x (1 - s)). From
-// e = e^-|x|, both s and 1 - s are quotients without cancellation. Below -120
-// everything is 0 in FP32, and so is the limit at -inf.
-template <bool kExact, bool kSlope>
-__device__ __forceinline__ Curve silu(float x)
+__device__ __forceinline__ float min_nan(float a, float b)
 {
-    x = max_nan(x, -120.0f);
-    const float e = exp_minus<kExact>(fminf(fabsf(x), 200.0f), 1.0f);
-    const float big = reciprocal<kExact>(__fadd_rn(1.0f, e)), small = __fmul_rn(e, big);
-    const float s = x >= 0.0f ? big : small, rest = x >= 0.0f ? small : big;
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+template <int kKind, bool kExact>
+__device__ __forceinline__ Curve curve(f2 x)
+{
+    constexpr float kFar = kKind == kSilu ? 120.0f : 15.0f;
+    float a, b;
+    unpk(x, a, b);
+    const f2 u = pk(min_nan(fabsf(a), kFar), min_nan(fabsf(b), kFar));
+    f2 nq, nv;   // -q and -v
+    if (kKind == kSilu) {
+        const f2 e = exp_minus<kExact>(u, splat(1.0f));
+        const f2 n = reciprocal<kExact>(fma2(e, splat(-1.0f), splat(-1.0f)));   // -1 / (1 + e)
+        nq = mul2(e, n);
+        nv = mul2(nq, fma2(u, n, splat(1.0f)));
+    } else {
+        const f2 e = exp_minus<kExact>(u, mul2(u, splat(0.5f))), t = reciprocal<kExact>(fma2(u, splat(0.3f), splat(1.0f)));
+        f2 q;
+        const auto next = [&](float c) { q = fma2(q, t, splat(c)); };
+        if (kExact) {
+            q = splat(-0x1.3ac79cp-5f);
+            next(0x1.5aeb4cp-3f);
+            next(-0x1.d54246p-3f);
+            next(0x1.3b91b6p-4f);
+            next(-0x1.24ab96p-3f);
+            next(-0x1.832e2ap-4f);
+            next(-0x1.f38cbcp-4f);
+            next(-0x1.e96612p-4f);
+            next(-0x1.f6f9aap-18f);
+        } else {
+            q = splat(0x1.5a7e80p-4f);
+            next(-0x1.ecb18ep-3f);
+            next(0x1.8e7f86p-5f);
+            next(-0x1.517030p-3f);
+            next(-0x1.b50fb0p-4f);
+            next(-0x1.f0bdc4p-4f);
+            next(0x1.4eab20p-14f);
+        }
+        nq = mul2(q, e);
+        nv = fma2(mul2(u, splat(0.398942280401432678f)), e, nq);
+    }
     Curve c;
-    c.value = __fmul_rn(x, s);
-    c.slope = kSlope ? __fmul_rn(s, __fmaf_rn(x, rest, 1.0f)) : 0.0f;
+    c.value = fma2(u, nq, pk(fmaxf(a, 0.0f), fmaxf(b, 0.0f)));   // NaN by u
+    // v where x has a sign, 1 - v where it has none
+    const auto slope = [](float v, float x) {
+        const uint32_t sign = __float_as_uint(x);
+        const float one = __uint_as_float(~(uint32_t)((int32_t)sign >> 31) & 0x3f800000u);
+        return __fadd_rn(one, __uint_as_float(__float_as_uint(v) ^ (sign & 0x80000000u)));
+    };
+    float p, q;
+    unpk(nv, p, q);
+    c.slope = pk(slope(p, a), slope(q, b));
     return c;
-}
-
-// gelu(x) = x Phi(x), gelu'(x) = Phi(x) + x phi(x). The normal distribution's
-// tail Phi(-u) is Q(1 / (1 + 0.3 u)) e^(-u^2 / 2), Q the polynomial of degree 8
-// with the least relative error on u in [0, 15] (5.8e-8; 3.6e-7 as evaluated in
-// FP32), so that far on the negative side the result keeps its relative
-// precision, which 1 + erf(x / sqrt 2) loses. Beyond 15 the tail is 0 in FP32.
-template <bool kExact, bool kSlope>
-__device__ __forceinline__ Curve gelu(float x)
-{
-    x = max_nan(x, -15.0f);
-    const float u = fminf(fabsf(x), 15.0f);
-    const float e = exp_minus<kExact>(u, 0.5f * u), t = reciprocal<kExact>(__fmaf_rn(0.3f, u, 1.0f));
-    float q = 0x1.3ac79cp-5f;
-    q = __fmaf_rn(q, t, -0x1.5aeb4cp-3f);
-    q = __fmaf_rn(q, t, 0x1.d54246p-3f);
-    q = __fmaf_rn(q, t, -0x1.3b91b6p-4f);
-    q = __fmaf_rn(q, t, 0x1.24ab96p-3f);
-    q = __fmaf_rn(q, t, 0x1.832e2ap-4f);
-    q = __fmaf_rn(q, t, 0x1.f38cbcp-4f);
-    q = __fmaf_rn(q, t, 0x1.e96612p-4f);
-    q = __fmaf_rn(q, t, 0x1.f6f9aap-18f);
-    const float tail = __fmul_rn(q, e), cdf = x >= 0.0f ? __fsub_rn(1.0f, tail) : tail;
-    Curve c;
-    c.value = __fmul_rn(x, cdf);
-    // x phi(x) with |x| held at 15 as in e; NaN stays NaN
-    c.slope = kSlope ? __fmaf_rn(__fmul_rn(x > 15.0f ? 15.0f : x, 0.398942280401432678f), e, cdf) : 0.0f;
-    return c;
-}
-
-template <int kKind, bool kExact, bool kSlope>
-__device__ __forceinline__ Curve curve(float x)
-{
-    return kKind == kSilu ? silu<kExact, kSlope>(x) : gelu<kExact, kSlope>(x);
 }
 
 template <class T>

@@ -28,9 +28,7 @@ __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, 
             widen_unit<T>(up[i], u);
 #pragma unroll
         for (int k = 0; k < kUnit / 2; ++k) {
-            float p, q;
-            unpk(x[k], p, q);
-            y[k] = pk(curve<kKind, kExactType<T>, false>(p).value, curve<kKind, kExactType<T>, false>(q).value);
+            y[k] = curve<kKind, kExactType<T>>(x[k]).value;
             if (kGated)
                 y[k] = mul2(y[k], u[k]);
         }
@@ -66,14 +64,12 @@ __global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGra
             kept_unit(up[i], u);
 #pragma unroll
         for (int k = 0; k < kUnit / 2; ++k) {
-            float p, q;
-            unpk(x[k], p, q);
-            const Curve f = curve<kKind, kExactType<T>, true>(p), h = curve<kKind, kExactType<T>, true>(q);
+            const Curve f = curve<kKind, kExactType<T>>(x[k]);
             if (kGated) {
-                du[k] = mul2(d[k], pk(f.value, h.value));
+                du[k] = mul2(d[k], f.value);
                 d[k] = mul2(d[k], u[k]);
             }
-            d[k] = mul2(d[k], pk(f.slope, h.slope));
+            d[k] = mul2(d[k], f.slope);
         }
         const Place p = place(first + i * kThreads, g.units, g.per_row, (int)a.width);
         store_unit<T, kWide>(a.grad, p, narrow_unit<T>(d));

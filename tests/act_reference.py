@@ -8,7 +8,8 @@ exact: their definition fixes every rounding. What is computed from them:
   reciprocal  2^-23 (16-bit), 2 u (FP32)
   silu        e and the reciprocal, 1 + e, two products: 2^-22 + 2^-23 + 4 u (16-bit:
               + |x| u), taken as 2^-21 + |x| 2^-23
-  gelu        the tail's polynomial 3.7e-7 < 2^-21, with e and products: 2^-20 + (x^2 / 2) 2^-22
+  gelu        the tail's polynomial: 3.7e-7 < 2^-21 for FP32, 2.2e-6 < 2^-18.7 for
+              16-bit types; with e and products 2^-20 or 2^-18, + (x^2 / 2) 2^-22
   slopes      the same relative errors of each of their terms, and a rounding of the sum
   inverse rms a chain of width / 128 + 32 additions of squares at most, halved by the root
   a row's dot product, a column's sum: their number of additions in a chain, of the terms' sizes
@@ -51,8 +52,9 @@ def kept(x: torch.Tensor) -> torch.Tensor:
     return z.flatten(-2)[..., :x.shape[-1]]
 
 
-def act(kind: str, x: torch.Tensor):
-    """value, slope, and the sizes of their terms, in 64 bits."""
+def act(kind: str, x: torch.Tensor, dtype=None):
+    """value, slope, the size of the slope's terms and their relative error for inputs of a type, in 64 bits."""
+    dtype = dtype or x.dtype
     x = x.double()
     if kind in ("silu", "swiglu"):
         s, rest = torch.sigmoid(x), torch.sigmoid(-x)
@@ -64,7 +66,7 @@ def act(kind: str, x: torch.Tensor):
         pdf = torch.exp(-x * x / 2) / math.sqrt(2 * math.pi)
         value = torch.where(x == -math.inf, torch.zeros_like(x), x * cdf)
         slope, size = cdf + x * pdf, cdf + x.abs() * pdf
-        rel = 2.0 ** -20 + x * x * 2.0 ** -23
+        rel = (2.0 ** -20 if dtype == torch.float32 else 2.0 ** -18) + x * x * 2.0 ** -23
     return value, slope, size, torch.where(torch.isfinite(rel), rel, torch.zeros_like(rel)).clamp(max=1.0)
 
 
@@ -80,7 +82,7 @@ def forward(kind, x, up=None):
 def backward(kind, x, dy, up=None):
     """grad, grad_up and their tolerances, at the numbers that the codes of x and up stand for."""
     xh, dy = kept(x), dy.double()
-    v, slope, size, rel = act(kind, xh)
+    v, slope, size, rel = act(kind, xh, x.dtype)
     if up is None:
         return dy * slope, dy.abs() * size * (rel + 2 * u)
     uh = kept(up)
