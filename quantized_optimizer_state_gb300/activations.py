@@ -47,22 +47,46 @@ class Compressed(NamedTuple):
 class KeptActivation(NamedTuple):
     """What :func:`activation_backward` needs."""
     kind: str
-    codes: torch.Tensor      # [..., 32 G] int8; [2, ..., 32 G] of a gated kind: the gate's and the other half's
-    steps: torch.Tensor      # [..., G] or [2, ..., G] bfloat16
+    kept: torch.Tensor       # bytes: codes of the input (of a gated kind the gate's, then the other half's), then steps
     shape: torch.Size        # of the result
     dtype: torch.dtype
     halves: bool             # gate and other half are those of one tensor
 
+    def inputs(self) -> Tuple[Compressed, ...]:
+        """The input, or the gate and the other half."""
+        n, width = self.shape[:-1].numel(), self.shape[-1]
+        g, parts = fo.groups(width), 2 if KINDS[self.kind][1] else 1
+        codes = self.kept[:parts * n * g * fo.GROUP].view((parts,) + self.shape[:-1] + (g * fo.GROUP,))
+        steps = self.kept[parts * n * g * fo.GROUP:].view(torch.bfloat16).view((parts,) + self.shape[:-1] + (g,))
+        return tuple(Compressed(c, s, width, self.dtype) for c, s in zip(codes, steps))
+
 
 class KeptNorm(NamedTuple):
     """What :func:`rms_norm_backward` needs. ``weight`` is the tensor itself, not a copy."""
-    x: Compressed
-    inv_rms: torch.Tensor    # [...] float32
+    kept: torch.Tensor       # bytes: codes of the input, then 1 / rms of each row, then steps
+    shape: torch.Size
+    dtype: torch.dtype
     weight: Optional[torch.Tensor]
+
+    @property
+    def x(self) -> Compressed:
+        """The input."""
+        n, g = self.shape[:-1].numel(), fo.groups(self.shape[-1])
+        codes = self.kept[:n * g * fo.GROUP].view(self.shape[:-1] + (g * fo.GROUP,))
+        steps = self.kept[n * (g * fo.GROUP + 4):].view(torch.bfloat16).view(self.shape[:-1] + (g,))
+        return Compressed(codes, steps, self.shape[-1], self.dtype)
+
+    @property
+    def inv_rms(self) -> torch.Tensor:
+        """1 / rms of each row, float32."""
+        at = self.shape[:-1].numel() * fo.groups(self.shape[-1]) * fo.GROUP
+        return self.kept[at:at + 4 * self.shape[:-1].numel()].view(torch.float32).view(self.shape[:-1])
 
 
 def _check_tangent(*tensors: Optional[torch.Tensor]) -> None:
     """A tensor with a tangent need not require a gradient, and its address carries none."""
+    if getattr(forward_ad, "_current_level", 0) < 0:     # outside of every forward-mode level there are none
+        return
     for x in tensors:
         if x is not None and forward_ad.unpack_dual(x).tangent is not None:
             raise NotImplementedError("operators on activations have no forward-mode derivative: an input carries a tangent")
@@ -74,20 +98,23 @@ def _check_width(x: torch.Tensor) -> None:
 
 
 # The functions below hand the C calls the addresses of tensors that they have
-# just made themselves; what the caller passes is checked by fo's helpers.
+# just made themselves; what the caller passes is checked by fo's helpers. A call
+# is a few microseconds of host time, which is what small tensors take.
 
-def _empty_kept(lead, width: int, device):
-    g = fo.groups(width)
-    return (torch.empty(lead + (g * fo.GROUP,), dtype=torch.int8, device=device),
-            torch.empty(lead + (g,), dtype=torch.bfloat16, device=device))
+_empty = torch.empty
 
 
-def _grad_of(grad: torch.Tensor, shape, dtype, name: str = "grad_y") -> torch.Tensor:
-    """An incoming gradient in a layout that the kernels read (an expanded one, for example, is copied)."""
+def _readable(grad: torch.Tensor, shape, dtype) -> fo.FoRows:
+    """An incoming gradient's rows. One in a layout that the kernels do not read (an expanded
+    one, for example) is copied; the copy is kept by the result."""
     if grad.shape != shape or grad.dtype != dtype:
-        raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')} of shape {tuple(shape)}, not "
+        raise ValueError(f"grad_y must be {str(dtype).replace('torch.', '')} of shape {tuple(shape)}, not "
                          f"{str(grad.dtype).replace('torch.', '')} of shape {tuple(grad.shape)}")
-    return grad if fo._rows_of(grad) is not None else grad.contiguous()
+    if fo._rows_of(grad) is None:
+        grad = grad.contiguous()
+    m = fo.matrix(grad, "grad_y")
+    m.keep = grad
+    return m
 
 
 def compress(x: torch.Tensor) -> Compressed:
@@ -96,34 +123,43 @@ def compress(x: torch.Tensor) -> Compressed:
     _check_tangent(x)
     _check_width(x)
     m = fo.matrix(x)
-    codes, steps = _empty_kept(x.shape[:-1], x.shape[-1], x.device)
+    shape, dev = x.shape, x.device
+    g = -(-m.width // fo.GROUP)
+    lead = shape[:-1]
+    codes = _empty(lead + (g * fo.GROUP,), dtype=torch.int8, device=dev)
+    steps = _empty(lead + (g,), dtype=torch.bfloat16, device=dev)
     status = fo.lib().fo_compress(ctypes.byref(m), codes.data_ptr(), steps.data_ptr(), fo._stream(None))
     if status:
         fo._check("fo_compress", status)
-    return Compressed(codes, steps, x.shape[-1], x.dtype)
+    return Compressed(codes, steps, m.width, x.dtype)
 
 
 def expand(kept: Compressed, *, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The tensor that the codes stand for, rounded once to ``dtype`` (that of the
     compressed tensor where None). ``out``: where to write it."""
     codes, steps, width, own = kept
-    lead = codes.shape[:-1]
-    if steps.shape != lead + (fo.groups(width),) or codes.shape[-1] != fo.groups(width) * fo.GROUP:
+    lead, g = codes.shape[:-1], -(-width // fo.GROUP)
+    if steps.shape != lead + (g,) or codes.shape[-1] != g * fo.GROUP:
         raise ValueError(f"codes {tuple(codes.shape)} and steps {tuple(steps.shape)} are not those of {width} columns")
-    if out is None:
-        x = torch.empty(lead + (width,), dtype=dtype or own, device=codes.device)
-    elif out.shape != lead + (width,) or (dtype is not None and out.dtype != dtype):
-        raise ValueError(f"out must be of shape {tuple(lead + (width,))}" + (f" and {dtype}" if dtype else "") +
-                         f", not {tuple(out.shape)} and {out.dtype}")
-    else:
-        x = out
-    fo.fo_expand(codes, steps, x)
+    if out is not None:
+        if out.shape != lead + (width,) or (dtype is not None and out.dtype != dtype):
+            raise ValueError(f"out must be of shape {tuple(lead + (width,))}" + (f" and {dtype}" if dtype else "") +
+                             f", not {tuple(out.shape)} and {out.dtype}")
+        fo.fo_expand(codes, steps, out)
+        return out
+    x = _empty(lead + (width,), dtype=dtype or own, device=codes.device)
+    m = fo.matrix(x)
+    c, s = fo._kept(codes, steps, m, x.device.index)
+    status = fo.lib().fo_expand(c, s, ctypes.byref(m), fo._stream(None))
+    if status:
+        fo._check("fo_expand", status)
     return x
 
 
 # --- activation functions ------------------------------------------------------------------
 
 def _activation(x, kind, up, keep):
+    """The result and, with ``keep``, the bytes that are kept; else None."""
     try:
         act, gated = KINDS[kind]
     except (KeyError, TypeError):
@@ -131,91 +167,99 @@ def _activation(x, kind, up, keep):
     _check_width(x)
     if up is not None and not gated:
         raise ValueError(f"{kind} takes no second input")
-    halves = gated and up is None
-    m, u = fo.matrix(x), None
-    shape = x.shape
-    if halves:
-        if shape[-1] % 2:
-            raise ValueError(f"{kind} halves the last dimension, which must be even, not {shape[-1]}")
-        shape = shape[:-1] + (shape[-1] // 2,)
-        m.width = shape[-1]
-        u = fo.FoRows(m.data + m.width * x.element_size(), m.rows, m.width, m.row_stride, m.dtype, 0)
-    elif gated:
-        if up.shape != shape:
-            raise ValueError(f"up must have the gate's shape {tuple(shape)}, not {tuple(up.shape)}")
-        u = fo.matrix(up, "up", m)
-    y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    width = shape[-1]
-    to = fo.FoRows(y.data_ptr(), m.rows, width, width, m.dtype, 0)
-    codes = steps = c = s = uc = us = None
+    m, u, shape, dtype, dev = fo.matrix(x), None, x.shape, x.dtype, x.device
+    width, rows, dt = m.width, m.rows, m.dtype
+    if gated:
+        if up is None:
+            if width % 2:
+                raise ValueError(f"{kind} halves the last dimension, which must be even, not {width}")
+            width //= 2
+            shape = shape[:-1] + (width,)
+            m.width = width
+            u = ctypes.byref(fo.FoRows((m.data or 0) + width * x.element_size(), rows, width, m.row_stride, dt, 0))
+        else:
+            if up.shape != shape:
+                raise ValueError(f"up must have the gate's shape {tuple(shape)}, not {tuple(up.shape)}")
+            u = ctypes.byref(fo.matrix(up, "up", m))
+    y = _empty(shape, dtype=dtype, device=dev)
+    kept = c = s = uc = us = None
     if keep:
-        codes, steps = _empty_kept(((2,) if gated else ()) + shape[:-1], width, x.device)
-        c, s = codes.data_ptr(), steps.data_ptr()
+        n = rows * -(-width // fo.GROUP)          # groups
+        kept = _empty(n * (68 if gated else 34), dtype=torch.int8, device=dev)
+        c = kept.data_ptr()
+        s = c + n * fo.GROUP
         if gated:
-            half = m.rows * fo.groups(width)
-            uc, us = c + half * fo.GROUP, s + half * 2
-    status = fo.lib().fo_activation(act, ctypes.byref(m), fo._ref(u), ctypes.byref(to), c, s, uc, us, fo._stream(None))
+            uc, s = s, s + n * fo.GROUP
+            us = s + 2 * n
+    status = fo.lib().fo_activation(act, ctypes.byref(m), u, ctypes.byref(fo.FoRows(y.data_ptr(), rows, width, width, dt, 0)),
+                                    c, s, uc, us, fo._stream(None))
     if status:
         fo._check("fo_activation", status)
-    return y, KeptActivation(kind, codes, steps, shape, x.dtype, halves) if keep else None
+    return y, kept
+
+
+def _activation_grad(kind, kept, shape, dtype, halves, grad_y):
+    act, gated = KINDS[kind]
+    m = _readable(grad_y, shape, dtype)
+    width, rows, dt, dev = m.width, m.rows, m.dtype, grad_y.device
+    n = rows * -(-width // fo.GROUP)
+    c = fo._array(kept, "kept", torch.int8, n * (68 if gated else 34), dev.index)
+    s = c + n * fo.GROUP
+    grad_up = uc = us = to_up = None
+    if halves:
+        stride = 2 * width
+        grad = _empty(shape[:-1] + (stride,), dtype=dtype, device=dev)
+    else:
+        stride = width
+        grad = _empty(shape, dtype=dtype, device=dev)
+    at = grad.data_ptr()
+    if gated:
+        uc, s = s, s + n * fo.GROUP
+        us = s + 2 * n
+        if not halves:
+            grad_up = torch.empty_like(grad)
+        to_up = ctypes.byref(fo.FoRows(at + width * grad.element_size() if halves else grad_up.data_ptr(), rows, width, stride, dt, 0))
+    status = fo.lib().fo_activation_grad(act, c, s, uc, us, ctypes.byref(m), ctypes.byref(fo.FoRows(at, rows, width, stride, dt, 0)),
+                                         to_up, fo._stream(None))
+    if status:
+        fo._check("fo_activation_grad", status)
+    return grad, grad_up
 
 
 def activation_forward(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, KeptActivation]:
     """``(y, kept)``: :func:`activation` and what :func:`activation_backward` needs."""
     _check_tangent(x, up)
-    return _activation(x, kind, up, True)
+    y, kept = _activation(x, kind, up, True)
+    return y, KeptActivation(kind, kept, y.shape, y.dtype, up is None and KINDS[kind][1])
 
 
 def activation_backward(kept: KeptActivation, grad_y: torch.Tensor):
     """The gradient of ``x`` (of ``(x, up)`` where ``up`` was given) for that of ``y``."""
-    kind, codes, steps, shape, dtype, halves = kept
-    act, gated = KINDS[kind]
-    grad_y = _grad_of(grad_y, shape, dtype)
-    m = fo.matrix(grad_y, "grad_y")
-    width, size = m.width, grad_y.element_size()
-    cur = grad_y.device.index
-    n = m.rows * fo.groups(width) * (2 if gated else 1)
-    c = fo._array(codes, "codes", torch.int8, n * fo.GROUP, cur)
-    s = fo._array(steps, "steps", torch.bfloat16, n, cur)
-    grad_up = to_up = uc = us = None
-    stride = 2 * width if halves else width
-    grad = torch.empty(shape[:-1] + (stride,), dtype=dtype, device=grad_y.device)
-    to = fo.FoRows(grad.data_ptr(), m.rows, width, stride, m.dtype, 0)
-    if gated:
-        if halves:
-            at = to.data + width * size if m.rows else None
-        else:
-            grad_up = torch.empty_like(grad)
-            at = grad_up.data_ptr()
-        to_up = fo.FoRows(at, m.rows, width, stride, m.dtype, 0)
-        if m.rows:
-            uc, us = c + n // 2 * fo.GROUP, s + n // 2 * 2
-    status = fo.lib().fo_activation_grad(act, c, s, uc, us, ctypes.byref(m), ctypes.byref(to), fo._ref(to_up), fo._stream(None))
-    if status:
-        fo._check("fo_activation_grad", status)
-    return (grad, grad_up) if gated and not halves else grad
+    grad, grad_up = _activation_grad(*kept, grad_y)
+    return grad if grad_up is None else (grad, grad_up)
 
 
 class _Activation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, up, kind):
         y, kept = _activation(x, kind, up, True)
-        ctx.save_for_backward(kept.codes, kept.steps)
-        ctx.how = (kept.shape, kept.dtype, kept.halves)
+        ctx.save_for_backward(kept)
+        ctx.how = (y.shape, y.dtype, up is None and KINDS[kind][1])
         ctx.kind = kind
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_y):
-        codes, steps = ctx.saved_tensors
-        with _on_device_of(codes):
-            grad = activation_backward(KeptActivation(ctx.kind, codes, steps, *ctx.how), grad_y)
-        return (*grad, None) if isinstance(grad, tuple) else (grad, None, None)
+        kept, = ctx.saved_tensors
+        if kept.get_device() == fo._current_device():
+            return (*_activation_grad(ctx.kind, kept, *ctx.how, grad_y), None)
+        with torch.cuda.device(kept.device):
+            return (*_activation_grad(ctx.kind, kept, *ctx.how, grad_y), None)
 
 
 def _differentiable(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    return torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in tensors])
 
 
 def activation(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -232,84 +276,90 @@ def activation(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None)
 # --- norm ------------------------------------------------------------------------------------
 
 def _norm(x, weight, eps, keep):
+    """The result and, with ``keep``, the bytes that are kept; else None."""
     _check_width(x)
-    m, width, dev = fo.matrix(x), x.shape[-1], x.device
+    m, dev, shape = fo.matrix(x), x.device, x.shape
+    width, rows = m.width, m.rows
     w, wt = None, 0
     if weight is not None:
-        if weight.shape != (width,):
+        if weight.shape != shape[-1:]:
             raise ValueError(f"weight must be of shape ({width},), not {tuple(weight.shape)}")
         w, wt = fo._weight(weight, "weight", width, dev.index)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    to = fo.FoRows(y.data_ptr(), m.rows, width, width, m.dtype, 0)
-    codes = steps = inv = c = s = p_inv = None
+    y = _empty(shape, dtype=x.dtype, device=dev)
+    kept = c = s = inv = None
     if keep:
-        codes, steps = _empty_kept(x.shape[:-1], width, dev)
-        inv = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        c, s, p_inv = codes.data_ptr(), steps.data_ptr(), inv.data_ptr()
-    status = fo.lib().fo_rms_norm(ctypes.byref(m), w, wt, eps, ctypes.byref(to), p_inv, c, s, fo._stream(None))
+        n = rows * -(-width // fo.GROUP)          # groups
+        kept = _empty(n * 34 + 4 * rows, dtype=torch.int8, device=dev)
+        c = kept.data_ptr()
+        inv = c + n * fo.GROUP
+        s = inv + 4 * rows
+    status = fo.lib().fo_rms_norm(ctypes.byref(m), w, wt, eps, ctypes.byref(fo.FoRows(y.data_ptr(), rows, width, width, m.dtype, 0)),
+                                  inv, c, s, fo._stream(None))
     if status:
         fo._check("fo_rms_norm", status)
-    return y, KeptNorm(Compressed(codes, steps, width, x.dtype), inv, weight) if keep else None
+    return y, kept
 
 
-def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> Tuple[torch.Tensor, KeptNorm]:
-    """``(y, kept)``: :func:`rms_norm` and what :func:`rms_norm_backward` needs."""
-    _check_tangent(x, weight)
-    return _norm(x, weight, eps, True)
-
-
-def _norm_backward(kept, grad_y, need_x, need_weight):
-    x, inv, weight = kept
-    shape = x.codes.shape[:-1] + (x.width,)
-    grad_y = _grad_of(grad_y, shape, x.dtype)
-    m, dev, f32 = fo.matrix(grad_y, "grad_y"), grad_y.device, torch.float32
-    cur = dev.index
-    c, s = fo._kept(x.codes, x.steps, m, cur)
-    w, wt = fo._weight(weight, "weight", m.width, cur)
+def _norm_grad(kept, shape, dtype, weight, grad_y, need_x, need_weight):
+    m = _readable(grad_y, shape, dtype)
+    width, rows, dev = m.width, m.rows, grad_y.device
+    cur, g = dev.index, -(-width // fo.GROUP)
+    n = rows * g
+    c = fo._array(kept, "kept", torch.int8, n * 34 + 4 * rows, cur)
+    inv = c + n * fo.GROUP
+    w, wt = fo._weight(weight, "weight", width, cur)
     grad = to = grad_weight = gw = parts = ws = None
     if need_x:
-        grad = torch.empty(shape, dtype=x.dtype, device=dev)
-        to = fo.FoRows(grad.data_ptr(), m.rows, m.width, m.width, m.dtype, 0)
+        grad = _empty(shape, dtype=dtype, device=dev)
+        to = ctypes.byref(fo.FoRows(grad.data_ptr(), rows, width, width, m.dtype, 0))
     if need_weight and weight is not None:
         grad_weight = torch.empty_like(weight)
-        parts = torch.empty(min(m.rows, fo.FO_NORM_PARTS) * fo.groups(m.width) * fo.GROUP, dtype=f32, device=dev)
+        parts = _empty(min(rows, fo.FO_NORM_PARTS) * g * fo.GROUP, dtype=torch.float32, device=dev)
         gw, ws = grad_weight.data_ptr(), parts.data_ptr()
-    status = fo.lib().fo_rms_norm_grad(c, s, fo._array(inv, "inv_rms", f32, m.rows, cur), w, wt, ctypes.byref(m), fo._ref(to),
-                                       gw, ws, fo._stream(None))
+    status = fo.lib().fo_rms_norm_grad(c, inv + 4 * rows, inv, w, wt, ctypes.byref(m), to, gw, ws, fo._stream(None))
     if status:
         fo._check("fo_rms_norm_grad", status)
     return grad, grad_weight
 
 
+def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> Tuple[torch.Tensor, KeptNorm]:
+    """``(y, kept)``: :func:`rms_norm` and what :func:`rms_norm_backward` needs."""
+    _check_tangent(x, weight)
+    y, kept = _norm(x, weight, eps, True)
+    return y, KeptNorm(kept, y.shape, y.dtype, weight)
+
+
 def rms_norm_backward(kept: KeptNorm, grad_y: torch.Tensor) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """``(grad_x, grad_weight)`` for the gradient of ``y``; ``grad_weight``, of the
     weight's type, is None without one."""
-    return _norm_backward(kept, grad_y, True, True)
+    return _norm_grad(*kept, grad_y, True, True)
 
 
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, eps):
         y, kept = _norm(x, weight, eps, True)
-        ctx.save_for_backward(kept.x.codes, kept.x.steps, kept.inv_rms, weight)
-        ctx.how = (kept.x.width, kept.x.dtype)
+        ctx.save_for_backward(kept, weight)
+        ctx.how = (y.shape, y.dtype)
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_y):
-        codes, steps, inv, weight = ctx.saved_tensors
-        with _on_device_of(codes):
-            kept = KeptNorm(Compressed(codes, steps, *ctx.how), inv, weight)
-            return (*_norm_backward(kept, grad_y, ctx.needs_input_grad[0], ctx.needs_input_grad[1]), None)
+        kept, weight = ctx.saved_tensors
+        need_x, need_weight, _ = ctx.needs_input_grad
+        if kept.get_device() == fo._current_device():
+            return (*_norm_grad(kept, *ctx.how, weight, grad_y, need_x, need_weight), None)
+        with torch.cuda.device(kept.device):
+            return (*_norm_grad(kept, *ctx.how, weight, grad_y, need_x, need_weight), None)
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> torch.Tensor:
     """``x / sqrt(mean(x^2) + eps) * weight`` over the last dimension, in ``x``'s type;
     ``weight`` [width] may be of another one. ``eps`` in [2^-80, 2^20].
     Differentiable; ``x`` is kept in 8 bits where a gradient is asked for. The
-    gradient of ``weight`` sums the rows in FP32, in an order that depends on
-    their number only."""
+    gradient of ``weight`` sums the rows in FP32, in an order that depends on their
+    number and the device only."""
     _check_tangent(x, weight)
     if _differentiable(x, weight):
         return _Norm.apply(x, weight, eps)

@@ -286,8 +286,8 @@ __device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
 // Stores a unit. Without kWide by all lanes of a warp, whose units follow one
 // another: a lane stores the aligned vectors that begin in the unit before its
 // own and end in its own, with what that unit's lane hands over; what has no such
-// lane goes element by element.
-template <class T, bool kWide>
+// lane goes element by element. Runs of kRun lanes have units that follow one another.
+template <class T, bool kWide, int kRun = 32>
 __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, const Words<T> &v)
 {
     typedef typename T::raw raw;
@@ -300,7 +300,7 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
                 __stcs(reinterpret_cast<uint4 *>(at) + i, make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]));
         return;
     }
-    const int phase = (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize), lane = threadIdx.x & 31;
+    const int phase = (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize), lane = threadIdx.x % kRun;
     constexpr int kOver = kSize == 2 ? 4 : 3;   // words that a unit hands over at most
     uint32_t in[kOver + kN], out[kN];
 #pragma unroll
@@ -310,7 +310,7 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
     for (int i = 0; i < kN; ++i)
         in[kOver + i] = out[i] = v.w[i];
     const int next_row = __shfl_down_sync(~0u, p.row, 1);
-    const bool before = lane > 0 && p.col > 0, after = lane < 31 && next_row == p.row;
+    const bool before = lane > 0 && p.col > 0, after = lane < kRun - 1 && next_row == p.row;
     int lo = 0, hi = p.left;             // places of `out`, from the vectors' first on, that are the row's
     if (phase) {
         shifted<T>(in, (kSize == 2 ? 8 : 3) - phase, out);

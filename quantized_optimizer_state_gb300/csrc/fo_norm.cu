@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kThreadsPerSm / kBlockOf<kLa
 #pragma unroll
             for (int j = 0; j < kUnit / 2; ++j)
                 x[k][j] = mul2(mul2(x[k][j], splat(inv)), w[k][j]);
-            store_unit<T, kWide>(a.y, row_place(r, rows, lane + k * kLanes, units, width), narrow_unit<T>(x[k]));
+            store_unit<T, kWide, (kLanes < 32 ? kLanes : 32)>(a.y, row_place(r, rows, lane + k * kLanes, units, width), narrow_unit<T>(x[k]));
         }
     }
 }
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kGradThreadsPerSm<kVecs> / k
 #pragma unroll
                 for (int j = 0; j < kUnit / 2; ++j)
                     t[k][j] = mul2(fma2(h[k][j], mean, t[k][j]), splat(inv));
-                store_unit<T, kWide>(a.grad, row_place(r, rows, lane + k * kLanes, units, width), narrow_unit<T>(t[k]));
+                store_unit<T, kWide, (kLanes < 32 ? kLanes : 32)>(a.grad, row_place(r, rows, lane + k * kLanes, units, width), narrow_unit<T>(t[k]));
             }
         }
     }

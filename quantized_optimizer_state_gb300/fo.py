@@ -673,7 +673,11 @@ def matrix(x, name: str = "x", like: Optional[FoRows] = None) -> FoRows:
     if dt is None:
         dt = _logit_dtype(x.dtype, name)
     ptr = _device_ptr(x, name, _current_device())
-    rows = _rows_of(x)
+    shape = x.shape
+    if len(shape) == 2 and x.is_contiguous():
+        rows = shape
+    else:
+        rows = _rows_of(x)
     if rows is None:
         raise ValueError(f"{name}: the last dimension must be contiguous and one stride must cover the others "
                          "(make it contiguous)")

@@ -328,8 +328,7 @@ def _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight):
         _check_rows(name, x, rows)
     if kl_weight and ref_logp is None:
         raise ValueError("kl_weight needs ref_logp")
-    dense = [x if x is None else x.detach().contiguous() for x in (old_logp, advantages, ref_logp if kl_weight else None)]
-    return (tokens.contiguous(), *dense)
+    return tokens.contiguous(), old_logp.contiguous(), advantages.contiguous(), _dense(ref_logp if kl_weight else None)
 
 
 def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,

@@ -173,7 +173,8 @@ def fake(shape, stride, dtype=torch.bfloat16, device=0):
     n = 1
     for s in shape:
         n *= s
-    return types.SimpleNamespace(shape=torch.Size(shape), stride=lambda: stride, dtype=dtype, is_cuda=True,
+    dense = stride == torch.empty(shape, device="meta").stride()
+    return types.SimpleNamespace(shape=torch.Size(shape), stride=lambda: stride, is_contiguous=lambda: dense, dtype=dtype, is_cuda=True,
                                  device=types.SimpleNamespace(index=device), data_ptr=lambda: 4096, numel=lambda: n)
 
 

@@ -190,7 +190,9 @@ def test_activation_of_rows_anywhere(cut, pad, w, dtype, kind):
     y, kept, grad = check_activation(x, kind, dy)
     y2, kept2, grad2 = check_activation(placed(x, cut, pad), kind, placed(dy, cut, pad))
     assert torch.equal(y, y2) and torch.equal(grad, grad2)
-    assert torch.equal(kept.codes, kept2.codes) and torch.equal(kept.steps, kept2.steps)
+    for p, q, half in zip(kept.inputs(), kept2.inputs(), halves(x) if gated else (x,)):
+        check_codes(half, p)
+        assert torch.equal(p.codes, q.codes) and torch.equal(p.steps, q.steps)
     if gated:
         a, b = halves(placed(x, cut, pad))
         y3, kept3 = A.activation_forward(a, kind, up=b.contiguous())
