@@ -158,12 +158,15 @@ constexpr bool kExactType = sizeof(typename T::raw) == 4;
 
 // --- units -----------------------------------------------------------------------------
 //
-// A thread works on units of 8 contiguous elements, neighbouring lanes on
-// neighbouring units, four lanes to a group: 16 bytes of a 16-bit type a lane
-// and load, whole lines a warp. Units are numbered through the rows, U = 4 groups
-// to a row, so that unit q has the codes from 8 q on and the step q / 4.
+// A thread works on units of W contiguous elements, neighbouring lanes on
+// neighbouring units. Where rows line up with vectors of 16 bytes (kWide) W is 8,
+// four lanes to a group: 16 bytes of a 16-bit type a lane and load, whole lines a
+// warp. Elsewhere it is 16, two lanes to a group: what the shifting of vectors
+// and their edges cost is for twice the elements. Units are numbered
+// through the rows, 32 / W to a group, so that unit q has the codes from W q on.
 
-constexpr int kUnit = 8;
+template <bool kWide>
+constexpr int kUnitOf = kWide ? 8 : 16;
 
 // Division of numbers below 2^31 by a fixed one: n / d = (n m / 2^32 + n) / 2^shift
 // (T. Granlund, P. Montgomery, "Division by invariant integers using
@@ -186,20 +189,21 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor &d) { ret
 struct Place {
     int row, col, left;
 };
+template <int W>
 __device__ __forceinline__ Place place(uint32_t unit, uint32_t units, const Divisor &per_row, int width)
 {
     const uint32_t r = quotient(unit, per_row);
     Place p;
     p.row = unit < units ? (int)r : -1;
-    p.col = (int)((unit - r * per_row.d) * kUnit);
+    p.col = (int)((unit - r * per_row.d) * W);
     p.left = unit < units ? width - p.col : -64;
     return p;
 }
 
 // The 32-bit words of a unit, as they lie in memory.
-template <class T>
+template <class T, int W>
 struct Words {
-    static constexpr int kN = kUnit * sizeof(typename T::raw) / 4;
+    static constexpr int kN = W * sizeof(typename T::raw) / 4;
     uint32_t w[kN];
 };
 
@@ -209,7 +213,7 @@ struct Words {
 template <class T>
 inline bool wide(int64_t width, const void *data, int64_t stride)
 {
-    return width % kUnit == 0 && (reinterpret_cast<uintptr_t>(data) & 15) == 0 && stride * (int64_t)sizeof(typename T::raw) % 16 == 0;
+    return width % kUnitOf<true> == 0 && (reinterpret_cast<uintptr_t>(data) & 15) == 0 && stride * (int64_t)sizeof(typename T::raw) % 16 == 0;
 }
 
 // The words from element `from` on of a longer run of them; `from` < 8 of 16 bits
@@ -243,15 +247,15 @@ __device__ __forceinline__ void load_vector(const uint4 *at, uint32_t *w)
 // A unit; 0 beyond the row's end. No byte outside the row is read. Without kWide
 // the row may start anywhere: the aligned vectors that hold the unit are read
 // and shifted.
-template <class T, bool kWide>
-__device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
+template <class T, bool kWide, int W = kUnitOf<kWide>>
+__device__ __forceinline__ Words<T, W> load_unit(const RowsIn &x, const Place &p)
 {
     typedef typename T::raw raw;
-    constexpr int kSize = sizeof(raw), kVecs = kUnit * kSize / 16;
-    Words<T> v;
+    constexpr int kSize = sizeof(raw), kVecs = W * kSize / 16;
+    Words<T, W> v;
     const raw *at = static_cast<const raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
 #pragma unroll
-    for (int i = 0; i < Words<T>::kN; ++i)
+    for (int i = 0; i < Words<T, W>::kN; ++i)
         v.w[i] = 0;
     if (kWide) {
         if (p.left > 0)
@@ -261,7 +265,7 @@ __device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
         return v;
     }
     const int phase = (int)((reinterpret_cast<uintptr_t>(at) & 15) / kSize);
-    if (phase == 0 && p.left >= kUnit) {
+    if (phase == 0 && p.left >= W) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
             load_vector<T>(reinterpret_cast<const uint4 *>(at) + i, v.w + 4 * i);
@@ -276,7 +280,7 @@ __device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
     } else {
         raw *e = reinterpret_cast<raw *>(v.w);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i)
+        for (int i = 0; i < W; ++i)
             if (i < p.left)
                 e[i] = at[i];
     }
@@ -287,11 +291,11 @@ __device__ __forceinline__ Words<T> load_unit(const RowsIn &x, const Place &p)
 // another: a lane stores the aligned vectors that begin in the unit before its
 // own and end in its own, with what that unit's lane hands over; what has no such
 // lane goes element by element. Runs of kRun lanes have units that follow one another.
-template <class T, bool kWide, int kRun = 32>
-__device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, const Words<T> &v)
+template <class T, bool kWide, int kRun = 32, int W = kUnitOf<kWide>>
+__device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, const Words<T, W> &v)
 {
     typedef typename T::raw raw;
-    constexpr int kSize = sizeof(raw), kVecs = kUnit * kSize / 16, kN = Words<T>::kN;
+    constexpr int kSize = sizeof(raw), kVecs = W * kSize / 16, kN = Words<T, W>::kN;
     raw *const at = static_cast<raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
     if (kWide) {
         if (p.left > 0)
@@ -319,8 +323,8 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
         if (!after) {                    // the unit's last elements
             const raw *e = reinterpret_cast<const raw *>(v.w);
 #pragma unroll
-            for (int i = 1; i < kUnit; ++i)
-                if (i >= kUnit - phase && i < p.left)
+            for (int i = W - 16 / kSize + 1; i < W; ++i)
+                if (i >= W - phase && i < p.left)
                     at[i] = e[i];
         }
     }
@@ -340,22 +344,22 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
 }
 
 // A unit's values in pairs, and back, rounded once.
-template <class T>
-__device__ __forceinline__ void widen_unit(const Words<T> &v, f2 (&x)[kUnit / 2])
+template <class T, int W>
+__device__ __forceinline__ void widen_unit(const Words<T, W> &v, f2 (&x)[W / 2])
 {
 #pragma unroll
-    for (int i = 0; i < kUnit / 2; ++i)
+    for (int i = 0; i < W / 2; ++i)
         if constexpr (sizeof(typename T::raw) == 2)
             x[i] = T::widen2(v.w[i]);
         else
             x[i] = pk(__uint_as_float(v.w[2 * i]), __uint_as_float(v.w[2 * i + 1]));
 }
-template <class T>
-__device__ __forceinline__ Words<T> narrow_unit(const f2 (&x)[kUnit / 2])
+template <class T, int W>
+__device__ __forceinline__ Words<T, W> narrow_unit(const f2 (&x)[W / 2])
 {
-    Words<T> v;
+    Words<T, W> v;
 #pragma unroll
-    for (int i = 0; i < kUnit / 2; ++i)
+    for (int i = 0; i < W / 2; ++i)
         if constexpr (sizeof(typename T::raw) == 2)
             v.w[i] = T::narrow2(x[i]);
         else {
@@ -374,28 +378,24 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// The step of the group that this lane's unit and those of the three lanes beside
-// it make up. As unsigned numbers the magnitudes of any of the types order as
-// their values do, infinity and NaN on top: two 16-bit ones to a word.
-template <class T>
-__device__ __forceinline__ float group_step(const Words<T> &v)
+// The step of the group that this lane's unit and those of the 32 / W - 1 lanes
+// beside it make up. As unsigned numbers the magnitudes of any of the types order
+// as their values do, infinity and NaN on top: two 16-bit ones to a word.
+template <class T, int W>
+__device__ __forceinline__ float group_step(const Words<T, W> &v)
 {
-    uint32_t m;
-    if constexpr (sizeof(typename T::raw) == 2) {
-        const uint32_t k = 0x7fff7fffu;
-        m = max_u16x2(max_u16x2(v.w[0] & k, v.w[1] & k), max_u16x2(v.w[2] & k, v.w[3] & k));
-        m = max_u16x2(m, __shfl_xor_sync(~0u, m, 1));
-        m = max_u16x2(m, __shfl_xor_sync(~0u, m, 2));
-        return step_of<true>(__float_as_uint(T::widen((typename T::raw)max(m & 0xffffu, m >> 16))));
-    } else {
-        m = 0;
+    constexpr bool kHalves = sizeof(typename T::raw) == 2;
+    const auto most = [](uint32_t a, uint32_t b) { return kHalves ? max_u16x2(a, b) : max(a, b); };
+    uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i)
-            m = max(m, v.w[i] & 0x7fffffffu);
-        m = max(m, __shfl_xor_sync(~0u, m, 1));
-        m = max(m, __shfl_xor_sync(~0u, m, 2));
-        return step_of<false>(m);
-    }
+    for (int i = 0; i < Words<T, W>::kN; ++i)
+        m = most(m, v.w[i] & (kHalves ? 0x7fff7fffu : 0x7fffffffu));
+#pragma unroll
+    for (int o = 1; o < 32 / W; o *= 2)
+        m = most(m, __shfl_xor_sync(~0u, m, o));
+    if constexpr (kHalves)
+        m = __float_as_uint(T::widen((typename T::raw)max(m & 0xffffu, m >> 16)));
+    return step_of<kHalves>(m);
 }
 
 // RN(1 / step): the hardware's approximation and a step of Newton's, which is
@@ -414,50 +414,74 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// The codes of a unit, as one vector.
+template <int W>
+struct CodeVec {
+    typedef uint2 type;
+};
+template <>
+struct CodeVec<16> {
+    typedef uint4 type;
+};
+
 // The codes and the step of unit `unit` of a matrix of `units` units.
-template <class T>
-__device__ __forceinline__ void keep_unit(const KeptOut &k, uint32_t unit, uint32_t units, const Words<T> &v, const f2 (&x)[kUnit / 2])
+template <class T, int W>
+__device__ __forceinline__ void keep_unit(const KeptOut &k, uint32_t unit, uint32_t units, const Words<T, W> &v, const f2 (&x)[W / 2])
 {
-    const float step = group_step<T>(v);
+    const float step = group_step<T, W>(v);
     const f2 r = splat(step_reciprocal(step)), round = splat(kRound);
-    uint32_t c[kUnit];
+    uint32_t c[W];
 #pragma unroll
-    for (int i = 0; i < kUnit / 2; ++i) {
+    for (int i = 0; i < W / 2; ++i) {
         float a, b;
         unpk(fma2(x[i], r, round), a, b);
         c[2 * i] = __float_as_uint(a);
         c[2 * i + 1] = __float_as_uint(b);
     }
     if (unit < units) {
-        __stcs(reinterpret_cast<uint2 *>(k.codes) + unit, make_uint2(low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])));
-        if (unit % 4 == 0)
-            k.steps[unit / 4] = step_bits(step);
+        typename CodeVec<W>::type codes;
+        codes.x = low_bytes(c[0], c[1], c[2], c[3]);
+        codes.y = low_bytes(c[4], c[5], c[6], c[7]);
+        if constexpr (W == 16) {
+            codes.z = low_bytes(c[8], c[9], c[10], c[11]);
+            codes.w = low_bytes(c[12], c[13], c[14], c[15]);
+        }
+        __stcs(reinterpret_cast<typename CodeVec<W>::type *>(k.codes) + unit, codes);
+        if (unit % (32 / W) == 0)
+            k.steps[unit / (32 / W)] = step_bits(step);
     }
 }
 
 // A unit's codes and step as loaded, and the values x^ they stand for. A code
 // becomes the low byte of 2^23 + 128 + code, from which FP32 takes the rest away.
 // `factor` is multiplied into the step first.
+template <int W>
 struct Kept {
-    uint2 codes;
+    typename CodeVec<W>::type codes;
     uint16_t step;
 };
-__device__ __forceinline__ Kept load_kept(const KeptIn &k, uint32_t unit, uint32_t units)
+template <int W>
+__device__ __forceinline__ Kept<W> load_kept(const KeptIn &k, uint32_t unit, uint32_t units)
 {
-    Kept v = {make_uint2(0, 0), 0};
+    Kept<W> v = {};
     if (unit < units) {
-        v.codes = __ldcs(reinterpret_cast<const uint2 *>(k.codes) + unit);
-        v.step = __ldg(k.steps + unit / 4);
+        v.codes = __ldcs(reinterpret_cast<const typename CodeVec<W>::type *>(k.codes) + unit);
+        v.step = __ldg(k.steps + unit / (32 / W));
     }
     return v;
 }
-__device__ __forceinline__ void kept_unit(const Kept &v, f2 (&x)[kUnit / 2], float factor = 1.0f)
+template <int W>
+__device__ __forceinline__ void kept_unit(const Kept<W> &v, f2 (&x)[W / 2], float factor = 1.0f)
 {
     const f2 base = splat(-(8388608.0f + 128.0f)), step = splat(__fmul_rn(step_value(v.step), factor));
-    const uint32_t lo = v.codes.x ^ 0x80808080u, hi = v.codes.y ^ 0x80808080u;
+    uint32_t words[W / 4] = {v.codes.x, v.codes.y};
+    if constexpr (W == 16) {
+        words[2] = v.codes.z;
+        words[3] = v.codes.w;
+    }
 #pragma unroll
-    for (int i = 0; i < kUnit / 2; ++i) {
-        const uint32_t w = i < 2 ? lo : hi;
+    for (int i = 0; i < W / 2; ++i) {
+        const uint32_t w = words[i / 2] ^ 0x80808080u;
         const f2 n = pk(__uint_as_float(__byte_perm(w, 0x4b000000u, i % 2 ? 0x7442 : 0x7440)),
                         __uint_as_float(__byte_perm(w, 0x4b000000u, i % 2 ? 0x7443 : 0x7441)));
         x[i] = mul2(add2(n, base), step);
@@ -469,9 +493,10 @@ struct UnitGrid {
     uint32_t units;
     Divisor per_row;
 };
+template <int W>
 inline UnitGrid unit_grid(int64_t rows, int64_t groups)
 {
-    return UnitGrid{(uint32_t)(rows * groups * 4), divisor((uint32_t)(groups * 4))};
+    return UnitGrid{(uint32_t)(rows * groups * (32 / W)), divisor((uint32_t)(groups * (32 / W)))};
 }
 
 }  // namespace fo

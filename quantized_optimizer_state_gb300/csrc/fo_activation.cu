@@ -6,15 +6,19 @@ namespace fo {
 namespace {
 
 constexpr int kThreads = 256;
+#ifndef UG
+#define UG 4
+#endif
 
 template <class T, int kKind, bool kGated, bool kWide, int kUnits>
 __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, UnitGrid g)
 {
+    constexpr int W = kUnitOf<kWide>;
     const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    Words<T> v[kUnits], up[kUnits];
+    Words<T, W> v[kUnits], up[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const Place p = place(first + i * kThreads, g.units, g.per_row, (int)a.width);
+        const Place p = place<W>(first + i * kThreads, g.units, g.per_row, (int)a.width);
         v[i] = load_unit<T, kWide>(a.x, p);
         if (kGated)
             up[i] = load_unit<T, kWide>(a.up, p);
@@ -22,21 +26,21 @@ __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, 
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t unit = first + i * kThreads;
-        f2 x[kUnit / 2], u[kUnit / 2], y[kUnit / 2];
-        widen_unit<T>(v[i], x);
+        f2 x[W / 2], u[W / 2], y[W / 2];
+        widen_unit<T, W>(v[i], x);
         if (kGated)
-            widen_unit<T>(up[i], u);
+            widen_unit<T, W>(up[i], u);
 #pragma unroll
-        for (int k = 0; k < kUnit / 2; ++k) {
+        for (int k = 0; k < W / 2; ++k) {
             y[k] = curve<kKind, kExactType<T>>(x[k]).value;
             if (kGated)
                 y[k] = mul2(y[k], u[k]);
         }
-        store_unit<T, kWide>(a.y, place(unit, g.units, g.per_row, (int)a.width), narrow_unit<T>(y));
+        store_unit<T, kWide>(a.y, place<W>(unit, g.units, g.per_row, (int)a.width), narrow_unit<T, W>(y));
         if (a.kept.codes) {
-            keep_unit<T>(a.kept, unit, g.units, v[i], x);
+            keep_unit<T, W>(a.kept, unit, g.units, v[i], x);
             if (kGated)
-                keep_unit<T>(a.kept_up, unit, g.units, up[i], u);
+                keep_unit<T, W>(a.kept_up, unit, g.units, up[i], u);
         }
     }
 }
@@ -44,26 +48,27 @@ __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, 
 template <class T, int kKind, bool kGated, bool kWide, int kUnits>
 __global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGradArgs a, UnitGrid g)
 {
+    constexpr int W = kUnitOf<kWide>;
     const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    Words<T> dy[kUnits];
-    Kept v[kUnits], up[kUnits];
+    Words<T, W> dy[kUnits];
+    Kept<W> v[kUnits], up[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t unit = first + i * kThreads;
-        dy[i] = load_unit<T, kWide>(a.grad_y, place(unit, g.units, g.per_row, (int)a.width));
-        v[i] = load_kept(a.kept, unit, g.units);
+        dy[i] = load_unit<T, kWide>(a.grad_y, place<W>(unit, g.units, g.per_row, (int)a.width));
+        v[i] = load_kept<W>(a.kept, unit, g.units);
         if (kGated)
-            up[i] = load_kept(a.kept_up, unit, g.units);
+            up[i] = load_kept<W>(a.kept_up, unit, g.units);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        f2 x[kUnit / 2], u[kUnit / 2], d[kUnit / 2], du[kUnit / 2];
-        widen_unit<T>(dy[i], d);
-        kept_unit(v[i], x);
+        f2 x[W / 2], u[W / 2], d[W / 2], du[W / 2];
+        widen_unit<T, W>(dy[i], d);
+        kept_unit<W>(v[i], x);
         if (kGated)
-            kept_unit(up[i], u);
+            kept_unit<W>(up[i], u);
 #pragma unroll
-        for (int k = 0; k < kUnit / 2; ++k) {
+        for (int k = 0; k < W / 2; ++k) {
             const Curve f = curve<kKind, kExactType<T>>(x[k]);
             if (kGated) {
                 du[k] = mul2(d[k], f.value);
@@ -71,37 +76,54 @@ __global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGra
             }
             d[k] = mul2(d[k], f.slope);
         }
-        const Place p = place(first + i * kThreads, g.units, g.per_row, (int)a.width);
-        store_unit<T, kWide>(a.grad, p, narrow_unit<T>(d));
+        const Place p = place<W>(first + i * kThreads, g.units, g.per_row, (int)a.width);
+        store_unit<T, kWide>(a.grad, p, narrow_unit<T, W>(d));
         if (kGated)
-            store_unit<T, kWide>(a.grad_up, p, narrow_unit<T>(du));
+            store_unit<T, kWide>(a.grad_up, p, narrow_unit<T, W>(du));
     }
 }
 
-template <int kUnits>
-unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * kUnits - 1) / (kThreads * kUnits); }
+// Units of a thread, all loaded before the first is used.
+template <bool kGated, bool kWide>
+constexpr int kUnits = kGated || !kWide ? (kWide ? 2 : 1) : UG;
 
-template <class T, int kKind, bool kGated>
-cudaError_t launch(const ActivationArgs &a, cudaStream_t stream)
+template <int N>
+unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * N - 1) / (kThreads * N); }
+
+template <class T, int kKind, bool kGated, bool kWide>
+void run(const ActivationArgs &a, cudaStream_t stream)
 {
-    constexpr int kUnits = 2;
-    const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.width, a.x.data, a.x.stride) && wide<T>(a.width, a.up.data, a.up.stride) && wide<T>(a.width, a.y.data, a.y.stride))
-        activation_kernel<T, kKind, kGated, true, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
-    else
-        activation_kernel<T, kKind, kGated, false, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
-    count_launch();
-    return cudaGetLastError();
+    constexpr int N = kUnits<kGated, kWide>;
+    const UnitGrid g = unit_grid<kUnitOf<kWide>>(a.rows, a.groups);
+    activation_kernel<T, kKind, kGated, kWide, N><<<ctas<N>(g), kThreads, 0, stream>>>(a, g);
 }
-template <class T, int kKind, bool kGated>
-cudaError_t launch(const ActivationGradArgs &a, cudaStream_t stream)
+template <class T, int kKind, bool kGated, bool kWide>
+void run(const ActivationGradArgs &a, cudaStream_t stream)
 {
-    constexpr int kUnits = 2;
-    const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.width, a.grad_y.data, a.grad_y.stride) && wide<T>(a.width, a.grad.data, a.grad.stride) && wide<T>(a.width, a.grad_up.data, a.grad_up.stride))
-        activation_grad_kernel<T, kKind, kGated, true, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
+    constexpr int N = kUnits<kGated, kWide>;
+    const UnitGrid g = unit_grid<kUnitOf<kWide>>(a.rows, a.groups);
+    activation_grad_kernel<T, kKind, kGated, kWide, N><<<ctas<N>(g), kThreads, 0, stream>>>(a, g);
+}
+
+template <class T>
+bool all_wide(const ActivationArgs &a)
+{
+    return wide<T>(a.width, a.x.data, a.x.stride) && wide<T>(a.width, a.up.data, a.up.stride) && wide<T>(a.width, a.y.data, a.y.stride);
+}
+template <class T>
+bool all_wide(const ActivationGradArgs &a)
+{
+    return wide<T>(a.width, a.grad_y.data, a.grad_y.stride) && wide<T>(a.width, a.grad.data, a.grad.stride) &&
+           wide<T>(a.width, a.grad_up.data, a.grad_up.stride);
+}
+
+template <class T, int kKind, bool kGated, class A>
+cudaError_t launch(const A &a, cudaStream_t stream)
+{
+    if (all_wide<T>(a))
+        run<T, kKind, kGated, true>(a, stream);
     else
-        activation_grad_kernel<T, kKind, kGated, false, kUnits><<<ctas<kUnits>(g), kThreads, 0, stream>>>(a, g);
+        run<T, kKind, kGated, false>(a, stream);
     count_launch();
     return cudaGetLastError();
 }

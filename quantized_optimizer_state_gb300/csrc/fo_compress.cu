@@ -5,61 +5,64 @@ namespace fo {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;   // units of a thread, all loaded before the first is used
+// units of a thread, all loaded before the first is used
+template <bool kWide>
+constexpr int kUnits = kWide ? 4 : 2;
 
 template <class T, bool kWide>
 __global__ void __launch_bounds__(kThreads) compress_kernel(CompressArgs a, UnitGrid g)
 {
-    const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    Words<T> v[kUnits];
+    constexpr int W = kUnitOf<kWide>, N = kUnits<kWide>;
+    const uint32_t first = blockIdx.x * (kThreads * N) + threadIdx.x;
+    Words<T, W> v[N];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-        v[i] = load_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, (int)a.width));
+    for (int i = 0; i < N; ++i)
+        v[i] = load_unit<T, kWide>(a.x, place<W>(first + i * kThreads, g.units, g.per_row, (int)a.width));
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        f2 x[kUnit / 2];
-        widen_unit<T>(v[i], x);
-        keep_unit<T>(a.kept, first + i * kThreads, g.units, v[i], x);
+    for (int i = 0; i < N; ++i) {
+        f2 x[W / 2];
+        widen_unit<T, W>(v[i], x);
+        keep_unit<T, W>(a.kept, first + i * kThreads, g.units, v[i], x);
     }
 }
 
 template <class T, bool kWide>
 __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs a, UnitGrid g)
 {
-    const uint32_t first = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    Kept k[kUnits];
+    constexpr int W = kUnitOf<kWide>, N = kUnits<kWide>;
+    const uint32_t first = blockIdx.x * (kThreads * N) + threadIdx.x;
+    Kept<W> k[N];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-        k[i] = load_kept(a.kept, first + i * kThreads, g.units);
+    for (int i = 0; i < N; ++i)
+        k[i] = load_kept<W>(a.kept, first + i * kThreads, g.units);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        f2 x[kUnit / 2];
-        kept_unit(k[i], x);
-        store_unit<T, kWide>(a.x, place(first + i * kThreads, g.units, g.per_row, (int)a.width), narrow_unit<T>(x));
+    for (int i = 0; i < N; ++i) {
+        f2 x[W / 2];
+        kept_unit<W>(k[i], x);
+        store_unit<T, kWide>(a.x, place<W>(first + i * kThreads, g.units, g.per_row, (int)a.width), narrow_unit<T, W>(x));
     }
 }
 
-unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * kUnits - 1) / (kThreads * kUnits); }
-
-template <class T>
-cudaError_t launch(const CompressArgs &a, cudaStream_t stream)
+template <class T, bool kWide>
+void run(const CompressArgs &a, cudaStream_t stream)
 {
-    const UnitGrid g = unit_grid(a.rows, a.groups);
-    if (wide<T>(a.width, a.x.data, a.x.stride))
-        compress_kernel<T, true><<<ctas(g), kThreads, 0, stream>>>(a, g);
-    else
-        compress_kernel<T, false><<<ctas(g), kThreads, 0, stream>>>(a, g);
-    count_launch();
-    return cudaGetLastError();
+    const UnitGrid g = unit_grid<kUnitOf<kWide>>(a.rows, a.groups);
+    compress_kernel<T, kWide><<<(g.units + kThreads * kUnits<kWide> - 1) / (kThreads * kUnits<kWide>), kThreads, 0, stream>>>(a, g);
 }
-template <class T>
-cudaError_t launch(const ExpandArgs &a, cudaStream_t stream)
+template <class T, bool kWide>
+void run(const ExpandArgs &a, cudaStream_t stream)
 {
-    const UnitGrid g = unit_grid(a.rows, a.groups);
+    const UnitGrid g = unit_grid<kUnitOf<kWide>>(a.rows, a.groups);
+    expand_kernel<T, kWide><<<(g.units + kThreads * kUnits<kWide> - 1) / (kThreads * kUnits<kWide>), kThreads, 0, stream>>>(a, g);
+}
+
+template <class T, class A>
+cudaError_t launch(const A &a, cudaStream_t stream)
+{
     if (wide<T>(a.width, a.x.data, a.x.stride))
-        expand_kernel<T, true><<<ctas(g), kThreads, 0, stream>>>(a, g);
+        run<T, true>(a, stream);
     else
-        expand_kernel<T, false><<<ctas(g), kThreads, 0, stream>>>(a, g);
+        run<T, false>(a, stream);
     count_launch();
     return cudaGetLastError();
 }

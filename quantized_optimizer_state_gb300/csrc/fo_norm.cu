@@ -48,27 +48,32 @@ __device__ __forceinline__ void store_weight(void *w, int dtype, int64_t i, floa
 
 
 // The weight of a unit; 1 without one.
-__device__ __forceinline__ void weight_unit(const void *w, int dtype, bool aligned, const Place &p, f2 (&x)[kUnit / 2])
+template <int W>
+__device__ __forceinline__ void weight_unit(const void *w, int dtype, bool aligned, const Place &p, f2 (&x)[W / 2])
 {
-    if (w && aligned && p.left >= kUnit) {
-        if (dtype == FO_LOGITS_F32) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + p.col));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + p.col) + 1);
-            x[0] = pk(a.x, a.y);
-            x[1] = pk(a.z, a.w);
-            x[2] = pk(b.x, b.y);
-            x[3] = pk(b.z, b.w);
-            return;
+    if (w && aligned && p.left >= W) {
+#pragma unroll
+        for (int i = 0; i < W / 8; ++i) {
+            f2(&to)[4] = *reinterpret_cast<f2(*)[4]>(&x[4 * i]);
+            if (dtype == FO_LOGITS_F32) {
+                const float4 *const at = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + p.col) + 2 * i;
+                const float4 a = __ldg(at), b = __ldg(at + 1);
+                to[0] = pk(a.x, a.y);
+                to[1] = pk(a.z, a.w);
+                to[2] = pk(b.x, b.y);
+                to[3] = pk(b.z, b.w);
+            } else {
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + p.col) + i);
+                if (dtype == FO_LOGITS_BF16)
+                    widen_vec<Bf16>(a, to);
+                else
+                    widen_vec<F16>(a, to);
+            }
         }
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + p.col));
-        if (dtype == FO_LOGITS_BF16)
-            widen_vec<Bf16>(a, x);
-        else
-            widen_vec<F16>(a, x);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kUnit / 2; ++i)
+    for (int i = 0; i < W / 2; ++i)
         x[i] = pk(2 * i < p.left ? weight_at(w, dtype, p.col + 2 * i) : 0.0f, 2 * i + 1 < p.left ? weight_at(w, dtype, p.col + 2 * i + 1) : 0.0f);
 }
 
@@ -79,78 +84,75 @@ __device__ __forceinline__ float both(f2 v)
     return __fadd_rn(a, b);
 }
 
-// The sum of v over the kLanes threads of a row, in every one of them. More than
-// a warp: they are a CTA, and `part` holds its warps' sums (two sets in turn, so
-// that one barrier a sum is enough).
+// A row is worked on by a team: kLanes threads of a warp, or (kLanes = 0) a whole
+// CTA, of as many warps as the row fills. The sum of v over the team, in every one
+// of its threads. `part` holds a CTA's warps' sums; two sets in turn, so that one
+// barrier a sum is enough.
 template <int kLanes>
 __device__ __forceinline__ float row_sum(float v, float *part)
 {
 #pragma unroll
-    for (int o = (kLanes < 32 ? kLanes : 32) / 2; o; o >>= 1)
+    for (int o = (kLanes ? kLanes : 32) / 2; o; o >>= 1)
         v += __shfl_xor_sync(~0u, v, o);
-    if constexpr (kLanes > 32) {
-        if ((threadIdx.x & 31) == 0)
+    if constexpr (kLanes == 0) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0)
             part[threadIdx.x / 32] = v;
         __syncthreads();
-        v = part[threadIdx.x % (kLanes / 32)];
-#pragma unroll
-        for (int o = kLanes / 64; o; o >>= 1)
-            v += __shfl_xor_sync(~0u, v, o);
+        v = warp_sum(lane < (int)blockDim.x / 32 ? part[lane] : 0.0f);
     }
     return v;
 }
 
 // The place of unit u of row r; beyond the rows, and beyond the row's units, it is none.
+template <int W>
 __device__ __forceinline__ Place row_place(int r, int rows, int u, int units, int width)
 {
     Place p;
     const bool there = r < rows && u < units;
     p.row = there ? r : -1;
-    p.col = u * kUnit;
+    p.col = u * W;
     p.left = there ? width - p.col : -64;
     return p;
 }
 
-template <int kLanes>
-constexpr int kBlockOf = kLanes > 32 ? kLanes : kThreads;   // threads of a CTA
-
 // --- rows held in registers --------------------------------------------------------------
 
-// A team of kLanes threads to a row, each thread with kVecs of its units (kLanes
-// apart) and their weights. A team takes rows a grid apart, the next one's loads
-// on their way while one is worked on.
-constexpr int kThreadsPerSm = 1024;   // of norm_kernel
-template <int kVecs>
-constexpr int kGradThreadsPerSm = kVecs == 1 ? 1024 : 512;   // of norm_grad_kernel
-template <class T, bool kWide, int kLanes, int kVecs>
-__global__ void __launch_bounds__(kBlockOf<kLanes>, kThreadsPerSm / kBlockOf<kLanes>) norm_kernel(NormArgs a)
+// Each thread of a team has kVecs units of the row (a team apart) and their
+// weights. A team takes rows a grid apart, the next one's loads on their way while
+// one is worked on. kBlock: threads of a CTA at most, kCtas: on an SM at least.
+template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
+__global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
 {
-    __shared__ float part[4][kLanes > 32 ? kLanes / 32 : 1];
-    constexpr int kTeams = kBlockOf<kLanes> / kLanes;
-    const int lane = threadIdx.x % kLanes, units = (int)a.groups * 4, rows = (int)a.rows, width = (int)a.width;
-    const int step = gridDim.x * kTeams;
-    int r = blockIdx.x * kTeams + threadIdx.x / kLanes;
-    Words<T> next[kVecs];
-    f2 w[kVecs][kUnit / 2];
+    constexpr int W = kUnitOf<kWide>;
+    __shared__ float part[4][32];
+    const int lanes = kLanes ? kLanes : blockDim.x, teams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1;
+    const int lane = kLanes ? threadIdx.x % lanes : threadIdx.x;
+    const int units = (int)a.groups * (32 / W), rows = (int)a.rows, width = (int)a.width;
+    const int step = gridDim.x * teams;
+    int r = blockIdx.x * teams + (kLanes ? threadIdx.x / lanes : 0);
+    Words<T, W> next[kVecs];
+    f2 w[kVecs][W / 2];
     const auto fetch = [&](int row) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
-            next[k] = load_unit<T, kWide>(a.x, row_place(row, rows, lane + k * kLanes, units, width));
+            next[k] = load_unit<T, kWide>(a.x, row_place<W>(row, rows, lane + k * lanes, units, width));
     };
     fetch(r);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k)
-        weight_unit(a.weight, a.weight_dtype, a.weight_aligned, row_place(0, 1, lane + k * kLanes, units, width), w[k]);
+        weight_unit<W>(a.weight, a.weight_dtype, a.weight_aligned, row_place<W>(0, 1, lane + k * lanes, units, width), w[k]);
     int turn = 0;
     // every thread takes as many turns as the CTA's first team: barriers and shuffles are all threads'
-    for (int base = blockIdx.x * kTeams; base < rows; base += step, r += step, turn ^= 2) {
+    for (int base = blockIdx.x * teams; base < rows; base += step, r += step, turn ^= 2) {
         // what needs no sum comes first, so that less waits for it
-        f2 x[kVecs][kUnit / 2];
+        f2 x[kVecs][W / 2];
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            widen_unit<T>(next[k], x[k]);
+            const int u = lane + k * lanes;
+            widen_unit<T, W>(next[k], x[k]);
             if (a.kept.codes)
-                keep_unit<T>(a.kept, (uint32_t)r * units + lane + k * kLanes, r < rows && lane + k * kLanes < units ? ~0u : 0u, next[k], x[k]);
+                keep_unit<T, W>(a.kept, (uint32_t)r * units + u, r < rows && u < units ? ~0u : 0u, next[k], x[k]);
         }
         fetch(r + step);
         const auto squares = [&](float scale) {
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kThreadsPerSm / kBlockOf<kLa
 #pragma unroll
             for (int k = 0; k < kVecs; ++k)
 #pragma unroll
-                for (int j = 0; j < kUnit / 2; ++j) {
+                for (int j = 0; j < W / 2; ++j) {
                     const f2 v = scale != 1.0f ? mul2(x[k][j], splat(scale)) : x[k][j];
                     sum = fma2(v, v, sum);
                 }
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kThreadsPerSm / kBlockOf<kLa
         const float sum = row_sum<kLanes>(squares(1.0f), part[turn]);
         const bool large = !(sum < kLargeSum);
         float inv = inverse_rms(sum, a);
-        if (kLanes > 32 ? large : __any_sync(~0u, large)) {   // the same in a CTA; other rows of a warp keep theirs
+        if (kLanes ? __any_sync(~0u, large) : large) {   // the same in a CTA; other rows of a warp keep theirs
             const float down = inverse_rms_down(row_sum<kLanes>(squares(kDown), part[turn + 1]), a);
             inv = large ? down : inv;
         }
@@ -176,41 +178,37 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kThreadsPerSm / kBlockOf<kLa
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
 #pragma unroll
-            for (int j = 0; j < kUnit / 2; ++j)
+            for (int j = 0; j < W / 2; ++j)
                 x[k][j] = mul2(mul2(x[k][j], splat(inv)), w[k][j]);
-            store_unit<T, kWide, (kLanes < 32 ? kLanes : 32)>(a.y, row_place(r, rows, lane + k * kLanes, units, width), narrow_unit<T>(x[k]));
+            store_unit<T, kWide, (kLanes ? kLanes : 32)>(a.y, row_place<W>(r, rows, lane + k * lanes, units, width), narrow_unit<T, W>(x[k]));
         }
     }
 }
 
-// A unit of dy and of the kept x, as loaded.
-template <class T>
-struct GradUnit {
-    Words<T> dy;
-    Kept x;
-};
-
 // The same for the gradient; the weight's gradient of a thread's columns is added
 // up in registers. A CTA's teams are joined in shared memory and leave one row of
 // partial sums.
-template <class T, bool kWide, int kLanes, int kVecs>
-__global__ void __launch_bounds__(kBlockOf<kLanes>, kGradThreadsPerSm<kVecs> / kBlockOf<kLanes>) norm_grad_kernel(NormGradArgs a)
+template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
+__global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a)
 {
-    constexpr int kTeams = kBlockOf<kLanes> / kLanes;
-    __shared__ float part[2][kLanes > 32 ? kLanes / 32 : 1];
-    __shared__ __align__(16) float joined[kTeams > 1 ? kTeams : 1][kTeams > 1 ? kLanes * kVecs * kUnit : 4];
-    const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes, units = (int)a.groups * 4, rows = (int)a.rows, width = (int)a.width;
-    f2 w[kVecs][kUnit / 2], dw[kVecs][kUnit / 2];
+    constexpr int W = kUnitOf<kWide>, kTeams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1;
+    __shared__ float part[2][32];
+    __shared__ __align__(16) float joined[kTeams][kTeams > 1 ? kLanes * kVecs * W : 4];
+    const int lanes = kLanes ? kLanes : blockDim.x;
+    const int lane = kLanes ? threadIdx.x % lanes : threadIdx.x, team = kLanes ? threadIdx.x / lanes : 0;
+    const int units = (int)a.groups * (32 / W), rows = (int)a.rows, width = (int)a.width;
+    f2 w[kVecs][W / 2], dw[kVecs][W / 2];
     const int step = gridDim.x * kTeams;
-    GradUnit<T> next[kVecs];
+    Words<T, W> next[kVecs];
+    Kept<W> next_x[kVecs];
     float next_inv;
     const auto fetch = [&](int r) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int u = lane + k * kLanes;
-            const Place p = row_place(r, rows, u, units, width);
-            next[k].dy = load_unit<T, kWide>(a.grad_y, p);
-            next[k].x = load_kept(a.kept, (uint32_t)r * units + u, p.row < 0 ? 0u : ~0u);
+            const int u = lane + k * lanes;
+            const Place p = row_place<W>(r, rows, u, units, width);
+            next[k] = load_unit<T, kWide>(a.grad_y, p);
+            next_x[k] = load_kept<W>(a.kept, (uint32_t)r * units + u, p.row < 0 ? 0u : ~0u);
         }
         next_inv = r < rows ? __ldg(a.inv_rms + r) : 0.0f;
     };
@@ -218,20 +216,20 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kGradThreadsPerSm<kVecs> / k
     fetch(r);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-        weight_unit(a.weight, a.weight_dtype, a.weight_aligned, row_place(0, 1, lane + k * kLanes, units, width), w[k]);
+        weight_unit<W>(a.weight, a.weight_dtype, a.weight_aligned, row_place<W>(0, 1, lane + k * lanes, units, width), w[k]);
 #pragma unroll
-        for (int j = 0; j < kUnit / 2; ++j)
+        for (int j = 0; j < W / 2; ++j)
             dw[k][j] = 0;
     }
     int turn = 0;
     for (int base = blockIdx.x * kTeams; base < rows; base += step, r += step, turn ^= 1) {
-        f2 t[kVecs][kUnit / 2], h[kVecs][kUnit / 2], dot = 0;
+        f2 t[kVecs][W / 2], h[kVecs][W / 2], dot = 0;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            widen_unit<T>(next[k].dy, t[k]);
-            kept_unit(next[k].x, h[k], next_inv);
+            widen_unit<T, W>(next[k], t[k]);
+            kept_unit<W>(next_x[k], h[k], next_inv);
 #pragma unroll
-            for (int j = 0; j < kUnit / 2; ++j) {
+            for (int j = 0; j < W / 2; ++j) {
                 dw[k][j] = fma2(t[k][j], h[k][j], dw[k][j]);
                 t[k][j] = mul2(t[k][j], w[k][j]);
                 dot = fma2(t[k][j], h[k][j], dot);
@@ -244,9 +242,9 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kGradThreadsPerSm<kVecs> / k
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
 #pragma unroll
-                for (int j = 0; j < kUnit / 2; ++j)
+                for (int j = 0; j < W / 2; ++j)
                     t[k][j] = mul2(fma2(h[k][j], mean, t[k][j]), splat(inv));
-                store_unit<T, kWide, (kLanes < 32 ? kLanes : 32)>(a.grad, row_place(r, rows, lane + k * kLanes, units, width), narrow_unit<T>(t[k]));
+                store_unit<T, kWide, (kLanes ? kLanes : 32)>(a.grad, row_place<W>(r, rows, lane + k * lanes, units, width), narrow_unit<T, W>(t[k]));
             }
         }
     }
@@ -257,10 +255,10 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kGradThreadsPerSm<kVecs> / k
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
 #pragma unroll
-            for (int j = 0; j < kUnit / 2; ++j)
-                *reinterpret_cast<f2 *>(&joined[team][(lane + k * kLanes) * kUnit + 2 * j]) = dw[k][j];
+            for (int j = 0; j < W / 2; ++j)
+                *reinterpret_cast<f2 *>(&joined[team][(lane + k * lanes) * W + 2 * j]) = dw[k][j];
         __syncthreads();
-        for (int c = threadIdx.x; c < units * kUnit; c += kThreads) {
+        for (int c = threadIdx.x; c < units * W; c += kBlock) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kTeams; ++i)
@@ -270,11 +268,11 @@ __global__ void __launch_bounds__(kBlockOf<kLanes>, kGradThreadsPerSm<kVecs> / k
     } else {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int u = lane + k * kLanes;
+            const int u = lane + k * lanes;
             if (u < units)
 #pragma unroll
-                for (int j = 0; j < kUnit / 4; ++j)
-                    reinterpret_cast<ulonglong2 *>(to + u * kUnit)[j] = make_ulonglong2(dw[k][2 * j], dw[k][2 * j + 1]);
+                for (int j = 0; j < W / 4; ++j)
+                    reinterpret_cast<ulonglong2 *>(to + u * W)[j] = make_ulonglong2(dw[k][2 * j], dw[k][2 * j + 1]);
         }
     }
 }
@@ -408,106 +406,112 @@ __global__ void __launch_bounds__(kThreads) norm_long_weight_kernel(NormGradArgs
 }
 
 
-constexpr int64_t kMaxUnits = 2048;   // of a row in registers: 16384 elements
+constexpr int64_t kMaxWidth = 16384;   // of a row in registers
 
-template <class T, bool kWide, int kLanes, int kVecs>
-cudaError_t launch(const NormArgs &a, cudaStream_t stream)
+// CTAs of `block` threads that an SM holds at once, by the launch bounds.
+constexpr int64_t ctas_per_sm(int block, int most, int ctas) { return most * ctas / block; }
+
+// A grid of as many CTAs as the device holds at once, or as the rows need.
+template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
+int run(const NormArgs &a, int block, cudaStream_t stream)
 {
-    constexpr int kBlock = kBlockOf<kLanes>, kTeams = kBlock / kLanes;
-    const int64_t ctas = std::min((a.rows + kTeams - 1) / kTeams, (int64_t)sm_count() * (kThreadsPerSm / kBlock));
-    norm_kernel<T, kWide, kLanes, kVecs><<<(unsigned)ctas, kBlock, 0, stream>>>(a);
+    const int64_t teams = kLanes ? block / (kLanes ? kLanes : 1) : 1;
+    const int64_t ctas = std::min((a.rows + teams - 1) / teams, sm_count() * ctas_per_sm(block, kBlock, kCtas));
+    norm_kernel<T, kWide, kLanes, kVecs, kBlock, kCtas><<<(unsigned)ctas, block, 0, stream>>>(a);
     count_launch();
-    return cudaGetLastError();
+    return (int)ctas;
 }
-template <class T, bool kWide>
-cudaError_t launch(const NormArgs &a, cudaStream_t stream)
+template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
+int run(const NormGradArgs &a, int block, cudaStream_t stream)
 {
-    // 32 bytes of x a thread. 16384 x 4096: BF16 with one unit a thread 65 us, two
-    // 57, four 71 (spills); FP32 99 with one, 108 with two. 131072 x 128 BF16 18.2
-    // with one, 17.3 with two.
-    constexpr int k = sizeof(typename T::raw) == 2 ? 2 : 1;
-    const int64_t units = a.groups * 4;
-    if (units <= 4)
-        return launch<T, kWide, 4, 1>(a, stream);
-    if (units <= 8)
-        return launch<T, kWide, 8 / k, k>(a, stream);
-    if (units <= 16)
-        return launch<T, kWide, 16 / k, k>(a, stream);
-    if (units <= 32)
-        return launch<T, kWide, 32 / k, k>(a, stream);
-    if (units <= 64)
-        return launch<T, kWide, 32, 2>(a, stream);
-    if (units <= 128)
-        return launch<T, kWide, 128 / k, k>(a, stream);
-    if (units <= 256)
-        return launch<T, kWide, 256 / k, k>(a, stream);
-    if (units <= 512)
-        return launch<T, kWide, 512 / k, k>(a, stream);
-    if (units <= 1024)
-        return launch<T, kWide, 1024 / k, k>(a, stream);
-    return launch<T, kWide, 1024, 2>(a, stream);
+    const int64_t teams = kLanes ? block / (kLanes ? kLanes : 1) : 1;
+    const int64_t fit = std::min<int64_t>(FO_NORM_PARTS, sm_count() * ctas_per_sm(block, kBlock, kCtas));
+    const int64_t ctas = std::min((a.rows + teams - 1) / teams, fit);
+    norm_grad_kernel<T, kWide, kLanes, kVecs, kBlock, kCtas><<<(unsigned)ctas, block, 0, stream>>>(a);
+    count_launch();
+    return (int)ctas;
 }
+
+// Teams of a warp's lanes, kVecs units each.
+template <class T, bool kWide, int kVecs, int kCtas, class A>
+int by_lanes(const A &a, int64_t units, cudaStream_t stream)
+{
+    if (units <= 4 * kVecs)
+        return run<T, kWide, 4, kVecs, kThreads, kCtas>(a, kThreads, stream);
+    if (units <= 8 * kVecs)
+        return run<T, kWide, 8, kVecs, kThreads, kCtas>(a, kThreads, stream);
+    if (units <= 16 * kVecs)
+        return run<T, kWide, 16, kVecs, kThreads, kCtas>(a, kThreads, stream);
+    return run<T, kWide, 32, kVecs, kThreads, kCtas>(a, kThreads, stream);
+}
+inline int block_for(int64_t units, int vecs) { return (int)((units + 32 * vecs - 1) / (32 * vecs)) * 32; }
+
+// Registers of a thread hold 32 bytes of a row and as much of the next one. In us
+// (forward), 16384 x 4096: BF16 with one unit of 8 a thread 65, two 57, four 71
+// (spills); FP32 99 with one, 108 with two. 131072 x 128 BF16 18.2 with one, 17.3
+// with two.
+template <class T, bool kWide>
+int by_size(const NormArgs &a, cudaStream_t stream)
+{
+    const int64_t units = a.groups * (32 / kUnitOf<kWide>);
+    constexpr int k = kWide && sizeof(typename T::raw) == 2 ? 2 : 1;
+    if (units <= 32 * k)
+        return by_lanes<T, kWide, k, 4>(a, units, stream);
+    const int block = block_for(units, k);
+    if (block <= 512)
+        return run<T, kWide, 0, k, 512, 2>(a, block, stream);
+    if constexpr (kWide)
+        if (block > 1024)
+            return run<T, kWide, 0, 2, 1024, 1>(a, block_for(units, 2), stream);
+    return run<T, kWide, 0, k, 1024, 1>(a, block, stream);
+}
+
+// The gradient: a warp with two units a thread where they hold the row, one unit a
+// thread of more warps beyond (65536 x 512 FP32 49 us, by 64 threads 61; 65536 x
+// 768 BF16 by 64 threads 59, by 128 56; 16384 x 4096 BF16 64.6 and 63.6; 4096 x
+// 16384 BF16 by 512 threads of four units 125, by 1024 of two 96).
+template <class T, bool kWide>
+int by_size(const NormGradArgs &a, cudaStream_t stream)
+{
+    const int64_t units = a.groups * (32 / kUnitOf<kWide>);
+    constexpr int k = kWide ? 2 : 1;
+    if (units <= 32 * k)
+        return by_lanes<T, kWide, k, 2>(a, units, stream);
+    const int block = block_for(units, 1);
+    if constexpr (!kWide) {
+        if (block <= 512)
+            return run<T, kWide, 0, 1, 512, 1>(a, block, stream);
+    } else if (block <= 576)
+        return run<T, kWide, 0, 1, 576, 2>(a, block, stream);
+    if constexpr (kWide)
+        if (block > 1024)
+            return run<T, kWide, 0, 2, 1024, 1>(a, block_for(units, 2), stream);
+    return run<T, kWide, 0, 1, 1024, 1>(a, block, stream);
+}
+
 template <class T>
 cudaError_t launch(NormArgs a, cudaStream_t stream)
 {
     a.inv_width = (float)(1.0 / (double)a.width);
     a.weight_aligned = (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
-    if (a.groups * 4 <= kMaxUnits)
-        return wide<T>(a.width, a.x.data, a.x.stride) && wide<T>(a.width, a.y.data, a.y.stride) ? launch<T, true>(a, stream) : launch<T, false>(a, stream);
+    if (a.width <= kMaxWidth) {
+        wide<T>(a.width, a.x.data, a.x.stride) && wide<T>(a.width, a.y.data, a.y.stride) ? by_size<T, true>(a, stream) : by_size<T, false>(a, stream);
+        return cudaGetLastError();
+    }
     norm_long_kernel<T><<<(unsigned)a.rows, kThreads, 0, stream>>>(a);
     count_launch();
     return cudaGetLastError();
 }
 
-// The CTAs that are on the device at once, or one for each set of teams; the
-// parts they leave are then added up.
-template <class T, bool kWide, int kLanes, int kVecs>
-int launch_parts(const NormGradArgs &a, cudaStream_t stream)
-{
-    constexpr int kBlock = kBlockOf<kLanes>, kTeams = kBlock / kLanes;
-    const int64_t fit = std::min<int64_t>(FO_NORM_PARTS, (int64_t)sm_count() * std::max(1, kGradThreadsPerSm<kVecs> / kBlock));
-    const int ctas = (int)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, fit);
-    norm_grad_kernel<T, kWide, kLanes, kVecs><<<ctas, kBlock, 0, stream>>>(a);
-    count_launch();
-    return ctas;
-}
-template <class T, bool kWide>
-int launch_parts(const NormGradArgs &a, cudaStream_t stream)
-{
-    const int64_t units = a.groups * 4;
-    // A warp with two units a thread where they hold the row, one unit a thread of
-    // more warps beyond (65536 x 512 FP32 49 us, by 64 threads 61; 65536 x 768 BF16
-    // by 64 threads 59, by 128 56; 16384 x 4096 BF16 64.6 and 63.6); 4096 x 16384
-    // BF16 by 512 threads of four units 125, by 1024 of two 96.
-    if (units <= 4)
-        return launch_parts<T, kWide, 4, 1>(a, stream);
-    if (units <= 8)
-        return launch_parts<T, kWide, 4, 2>(a, stream);
-    if (units <= 16)
-        return launch_parts<T, kWide, 8, 2>(a, stream);
-    if (units <= 32)
-        return launch_parts<T, kWide, 16, 2>(a, stream);
-    if (units <= 64)
-        return launch_parts<T, kWide, 32, 2>(a, stream);
-    if (units <= 128)
-        return launch_parts<T, kWide, 128, 1>(a, stream);
-    if (units <= 256)
-        return launch_parts<T, kWide, 256, 1>(a, stream);
-    if (units <= 512)
-        return launch_parts<T, kWide, 512, 1>(a, stream);
-    if (units <= 1024)
-        return launch_parts<T, kWide, 1024, 1>(a, stream);
-    return launch_parts<T, kWide, 1024, 2>(a, stream);
-}
 template <class T>
 cudaError_t launch(NormGradArgs a, cudaStream_t stream)
 {
     a.inv_width = (float)(1.0 / (double)a.width);
     a.weight_aligned = (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
     int parts = 0;
-    if (a.rows > 0 && a.groups * 4 <= kMaxUnits)
-        parts = wide<T>(a.width, a.grad_y.data, a.grad_y.stride) && wide<T>(a.width, a.grad.data, a.grad.stride) ? launch_parts<T, true>(a, stream)
-                                                                                               : launch_parts<T, false>(a, stream);
+    if (a.rows > 0 && a.width <= kMaxWidth)
+        parts = wide<T>(a.width, a.grad_y.data, a.grad_y.stride) && wide<T>(a.width, a.grad.data, a.grad.stride) ? by_size<T, true>(a, stream)
+                                                                                                                 : by_size<T, false>(a, stream);
     else if (a.rows > 0) {
         if (a.grad.data) {
             norm_long_grad_kernel<T><<<(unsigned)a.rows, kThreads, 0, stream>>>(a);
