@@ -505,7 +505,6 @@ typedef struct fo_rows {
 
 #define FO_MAX_ACT_GROUPS (1 << 29)
 #define FO_MAX_ACT_WIDTH (1 << 30)
-#define FO_NORM_PARTS 1024  /* rows of fo_rms_norm_grad's workspace, at most */
 
 /* Activation functions. */
 typedef enum fo_act {

@@ -104,9 +104,12 @@ def _check_width(x: torch.Tensor) -> None:
 _empty = torch.empty
 
 
-def _readable(grad: torch.Tensor, shape, dtype) -> fo.FoRows:
-    """An incoming gradient's rows. One in a layout that the kernels do not read (an expanded
-    one, for example) is copied; the copy is kept by the result."""
+def _grad_rows(grad: torch.Tensor, shape, dtype, rows: int, dt: int) -> fo.FoRows:
+    """An incoming gradient of the result's shape and type (``rows`` and ``dt`` are theirs). One in a
+    layout that the kernels do not read (an expanded one, for example) is copied; the rows hold the copy."""
+    if grad.dtype is dtype and grad.shape == shape and grad.is_contiguous() and grad.get_device() == fo._current_device():
+        width = shape[-1]
+        return fo.FoRows(grad.data_ptr(), rows, width, width, dt, 0)
     if grad.shape != shape or grad.dtype != dtype:
         raise ValueError(f"grad_y must be {str(dtype).replace('torch.', '')} of shape {tuple(shape)}, not "
                          f"{str(grad.dtype).replace('torch.', '')} of shape {tuple(grad.shape)}")
@@ -159,7 +162,7 @@ def expand(kept: Compressed, *, dtype: Optional[torch.dtype] = None, out: Option
 # --- activation functions ------------------------------------------------------------------
 
 def _activation(x, kind, up, keep):
-    """The result and, with ``keep``, the bytes that are kept; else None."""
+    """(the result, the bytes that are kept or None, what :func:`_activation_grad` needs beside them)"""
     try:
         act, gated = KINDS[kind]
     except (KeyError, TypeError):
@@ -195,15 +198,15 @@ def _activation(x, kind, up, keep):
                                     c, s, uc, us, fo._stream(None))
     if status:
         fo._check("fo_activation", status)
-    return y, kept
+    return y, kept, (act, gated, gated and up is None, shape, dtype, rows, dt)
 
 
-def _activation_grad(kind, kept, shape, dtype, halves, grad_y):
-    act, gated = KINDS[kind]
-    m = _readable(grad_y, shape, dtype)
-    width, rows, dt, dev = m.width, m.rows, m.dtype, grad_y.device
+def _activation_grad(kept, how, grad_y):
+    act, gated, halves, shape, dtype, rows, dt = how
+    m = _grad_rows(grad_y, shape, dtype, rows, dt)
+    width, dev = shape[-1], kept.device
     n = rows * -(-width // fo.GROUP)
-    c = fo._array(kept, "kept", torch.int8, n * (68 if gated else 34), dev.index)
+    c = kept.data_ptr()
     s = c + n * fo.GROUP
     grad_up = uc = us = to_up = None
     if halves:
@@ -229,23 +232,25 @@ def _activation_grad(kind, kept, shape, dtype, halves, grad_y):
 def activation_forward(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, KeptActivation]:
     """``(y, kept)``: :func:`activation` and what :func:`activation_backward` needs."""
     _check_tangent(x, up)
-    y, kept = _activation(x, kind, up, True)
-    return y, KeptActivation(kind, kept, y.shape, y.dtype, up is None and KINDS[kind][1])
+    y, kept, how = _activation(x, kind, up, True)
+    return y, KeptActivation(kind, kept, y.shape, y.dtype, how[2])
 
 
 def activation_backward(kept: KeptActivation, grad_y: torch.Tensor):
     """The gradient of ``x`` (of ``(x, up)`` where ``up`` was given) for that of ``y``."""
-    grad, grad_up = _activation_grad(*kept, grad_y)
+    kind, buffer, shape, dtype, halves = kept
+    act, gated = KINDS[kind]
+    rows = shape[:-1].numel()
+    fo._array(buffer, "kept", torch.int8, rows * -(-shape[-1] // fo.GROUP) * (68 if gated else 34), fo._current_device())
+    grad, grad_up = _activation_grad(buffer, (act, gated, halves, shape, dtype, rows, fo._logit_dtype(dtype, "kept")), grad_y)
     return grad if grad_up is None else (grad, grad_up)
 
 
 class _Activation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, up, kind):
-        y, kept = _activation(x, kind, up, True)
+        y, kept, ctx.how = _activation(x, kind, up, True)
         ctx.save_for_backward(kept)
-        ctx.how = (y.shape, y.dtype, up is None and KINDS[kind][1])
-        ctx.kind = kind
         return y
 
     @staticmethod
@@ -253,9 +258,9 @@ class _Activation(torch.autograd.Function):
     def backward(ctx, grad_y):
         kept, = ctx.saved_tensors
         if kept.get_device() == fo._current_device():
-            return (*_activation_grad(ctx.kind, kept, *ctx.how, grad_y), None)
+            return (*_activation_grad(kept, ctx.how, grad_y), None)
         with torch.cuda.device(kept.device):
-            return (*_activation_grad(ctx.kind, kept, *ctx.how, grad_y), None)
+            return (*_activation_grad(kept, ctx.how, grad_y), None)
 
 
 def _differentiable(*tensors) -> bool:
@@ -276,7 +281,7 @@ def activation(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None)
 # --- norm ------------------------------------------------------------------------------------
 
 def _norm(x, weight, eps, keep):
-    """The result and, with ``keep``, the bytes that are kept; else None."""
+    """(the result, the bytes that are kept or None, what :func:`_norm_grad` needs beside them)"""
     _check_width(x)
     m, dev, shape = fo.matrix(x), x.device, x.shape
     width, rows = m.width, m.rows
@@ -297,24 +302,23 @@ def _norm(x, weight, eps, keep):
                                   inv, c, s, fo._stream(None))
     if status:
         fo._check("fo_rms_norm", status)
-    return y, kept
+    return y, kept, (shape, x.dtype, rows, m.dtype, wt)
 
 
-def _norm_grad(kept, shape, dtype, weight, grad_y, need_x, need_weight):
-    m = _readable(grad_y, shape, dtype)
-    width, rows, dev = m.width, m.rows, grad_y.device
-    cur, g = dev.index, -(-width // fo.GROUP)
-    n = rows * g
-    c = fo._array(kept, "kept", torch.int8, n * 34 + 4 * rows, cur)
-    inv = c + n * fo.GROUP
-    w, wt = fo._weight(weight, "weight", width, cur)
+def _norm_grad(kept, weight, how, grad_y, need_x, need_weight):
+    shape, dtype, rows, dt, wt = how
+    m = _grad_rows(grad_y, shape, dtype, rows, dt)
+    width, dev = shape[-1], kept.device
+    c = kept.data_ptr()
+    inv = c + rows * -(-width // fo.GROUP) * fo.GROUP
+    w = None if weight is None else weight.data_ptr()
     grad = to = grad_weight = gw = parts = ws = None
     if need_x:
         grad = _empty(shape, dtype=dtype, device=dev)
-        to = ctypes.byref(fo.FoRows(grad.data_ptr(), rows, width, width, m.dtype, 0))
+        to = ctypes.byref(fo.FoRows(grad.data_ptr(), rows, width, width, dt, 0))
     if need_weight and weight is not None:
         grad_weight = torch.empty_like(weight)
-        parts = _empty(min(rows, fo.FO_NORM_PARTS) * g * fo.GROUP, dtype=torch.float32, device=dev)
+        parts = _empty(fo.lib().fo_rms_norm_workspace(rows, width), dtype=torch.float32, device=dev)
         gw, ws = grad_weight.data_ptr(), parts.data_ptr()
     status = fo.lib().fo_rms_norm_grad(c, inv + 4 * rows, inv, w, wt, ctypes.byref(m), to, gw, ws, fo._stream(None))
     if status:
@@ -325,22 +329,25 @@ def _norm_grad(kept, shape, dtype, weight, grad_y, need_x, need_weight):
 def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> Tuple[torch.Tensor, KeptNorm]:
     """``(y, kept)``: :func:`rms_norm` and what :func:`rms_norm_backward` needs."""
     _check_tangent(x, weight)
-    y, kept = _norm(x, weight, eps, True)
+    y, kept, _ = _norm(x, weight, eps, True)
     return y, KeptNorm(kept, y.shape, y.dtype, weight)
 
 
 def rms_norm_backward(kept: KeptNorm, grad_y: torch.Tensor) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """``(grad_x, grad_weight)`` for the gradient of ``y``; ``grad_weight``, of the
     weight's type, is None without one."""
-    return _norm_grad(*kept, grad_y, True, True)
+    buffer, shape, dtype, weight = kept
+    rows, cur = shape[:-1].numel(), fo._current_device()
+    fo._array(buffer, "kept", torch.int8, rows * (-(-shape[-1] // fo.GROUP) * 34 + 4), cur)
+    _, wt = fo._weight(weight, "weight", shape[-1], cur)
+    return _norm_grad(buffer, weight, (shape, dtype, rows, fo._logit_dtype(dtype, "kept"), wt), grad_y, True, True)
 
 
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, eps):
-        y, kept = _norm(x, weight, eps, True)
+        y, kept, ctx.how = _norm(x, weight, eps, True)
         ctx.save_for_backward(kept, weight)
-        ctx.how = (y.shape, y.dtype)
         return y
 
     @staticmethod
@@ -349,9 +356,9 @@ class _Norm(torch.autograd.Function):
         kept, weight = ctx.saved_tensors
         need_x, need_weight, _ = ctx.needs_input_grad
         if kept.get_device() == fo._current_device():
-            return (*_norm_grad(kept, *ctx.how, weight, grad_y, need_x, need_weight), None)
+            return (*_norm_grad(kept, weight, ctx.how, grad_y, need_x, need_weight), None)
         with torch.cuda.device(kept.device):
-            return (*_norm_grad(kept, *ctx.how, weight, grad_y, need_x, need_weight), None)
+            return (*_norm_grad(kept, weight, ctx.how, grad_y, need_x, need_weight), None)
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> torch.Tensor:

@@ -234,6 +234,9 @@ __device__ __forceinline__ void shifted(uint32_t (&in)[kIn], int from, uint32_t 
         out[i] = kHalves ? __funnelshift_r(in[i], in[i + 1 < kIn ? i + 1 : i], from & 1 ? 16 : 0) : in[i];
 }
 
+// n ones, for n below 32; none for n <= 0.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n > 0 ? ~(~0u << min(n, 31)) : 0u; }
+
 template <class T>
 __device__ __forceinline__ void load_vector(const uint4 *at, uint32_t *w)
 {
@@ -279,9 +282,10 @@ __device__ __forceinline__ Words<T, W> load_unit(const RowsIn &x, const Place &p
         shifted<T>(in, phase, v.w);
     } else {
         raw *e = reinterpret_cast<raw *>(v.w);
+        const uint32_t there = low_bits(p.left);
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            if (i < p.left)
+            if (there >> i & 1)
                 e[i] = at[i];
     }
     return v;
@@ -322,23 +326,26 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
         hi = p.left + phase;
         if (!after) {                    // the unit's last elements
             const raw *e = reinterpret_cast<const raw *>(v.w);
+            const uint32_t there = low_bits(p.left) & ~low_bits(W - phase);
 #pragma unroll
             for (int i = W - 16 / kSize + 1; i < W; ++i)
-                if (i >= W - phase && i < p.left)
+                if (there >> i & 1)
                     at[i] = e[i];
         }
     }
     raw *const to = at - phase;
     const raw *e = reinterpret_cast<const raw *>(out);
     constexpr int kPer = 16 / kSize;
+    const uint32_t there = low_bits(hi) & ~low_bits(lo), all = (1u << kPer) - 1;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        if (lo <= kPer * i && hi >= kPer * (i + 1))
+        const uint32_t mine = there >> kPer * i & all;
+        if (mine == all)
             __stcs(reinterpret_cast<uint4 *>(to) + i, make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
-        else
+        else if (mine)
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
-                if (kPer * i + k >= lo && kPer * i + k < hi)
+                if (mine >> k & 1)
                     to[kPer * i + k] = e[kPer * i + k];
     }
 }

@@ -74,10 +74,18 @@ struct NormGradArgs {
     RowsIn grad_y;
     RowsOut grad;
     void *grad_weight;      // may be null
-    float *parts;           // [FO_NORM_PARTS or rows, 32 groups] partial sums of grad_weight
+    float *parts;           // [norm_parts, 32 groups] partial sums of grad_weight
     float inv_width;        // these two are set by the launch
     bool weight_aligned;
 };
+
+// Rows of partial sums that the norm's gradient leaves at most: 1024, and more of
+// short rows, whose CTAs are small (up to 16 MB).
+inline int64_t norm_parts(int64_t rows, int64_t groups)
+{
+    const int64_t most = groups < 4096 ? ((int64_t)1 << 17) / groups : 32, parts = most < 1024 ? 1024 : most;
+    return rows < parts ? rows : parts;
+}
 
 cudaError_t launch_compress(int dtype, const CompressArgs &a, cudaStream_t stream);
 cudaError_t launch_expand(int dtype, const ExpandArgs &a, cudaStream_t stream);

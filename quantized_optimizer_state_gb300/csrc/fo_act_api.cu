@@ -217,7 +217,7 @@ fo_status_t fo_rms_norm(const fo_rows_t *in, const void *weight, int32_t weight_
 
 int64_t fo_rms_norm_workspace(int64_t rows, int64_t width)
 {
-    return rows <= 0 || width <= 0 ? 0 : std::min<int64_t>(rows, FO_NORM_PARTS) * groups_of(width) * FO_GROUP;
+    return rows <= 0 || width <= 0 ? 0 : fo::norm_parts(rows, groups_of(width)) * groups_of(width) * FO_GROUP;
 }
 
 fo_status_t fo_rms_norm_grad(const int8_t *codes, const uint16_t *steps, const float *inv_rms, const void *weight,

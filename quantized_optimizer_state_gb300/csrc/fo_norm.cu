@@ -425,7 +425,7 @@ template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
 int run(const NormGradArgs &a, int block, cudaStream_t stream)
 {
     const int64_t teams = kLanes ? block / (kLanes ? kLanes : 1) : 1;
-    const int64_t fit = std::min<int64_t>(FO_NORM_PARTS, sm_count() * ctas_per_sm(block, kBlock, kCtas));
+    const int64_t fit = std::min(norm_parts(a.rows, a.groups), sm_count() * ctas_per_sm(block, kBlock, kCtas));
     const int64_t ctas = std::min((a.rows + teams - 1) / teams, fit);
     norm_grad_kernel<T, kWide, kLanes, kVecs, kBlock, kCtas><<<(unsigned)ctas, block, 0, stream>>>(a);
     count_launch();
@@ -479,8 +479,8 @@ int by_size(const NormGradArgs &a, cudaStream_t stream)
         return by_lanes<T, kWide, k, 2>(a, units, stream);
     const int block = block_for(units, 1);
     if constexpr (!kWide) {
-        if (block <= 512)
-            return run<T, kWide, 0, 1, 512, 1>(a, block, stream);
+        if (block <= 576)
+            return run<T, kWide, 0, 1, 576, 1>(a, block, stream);
     } else if (block <= 576)
         return run<T, kWide, 0, 1, 576, 2>(a, block, stream);
     if constexpr (kWide)
@@ -518,7 +518,7 @@ cudaError_t launch(NormGradArgs a, cudaStream_t stream)
             count_launch();
         }
         if (a.grad_weight) {
-            parts = (int)std::min<int64_t>(a.rows, FO_NORM_PARTS);
+            parts = (int)norm_parts(a.rows, a.groups);
             norm_long_weight_kernel<T><<<dim3((unsigned)parts, (unsigned)((a.groups * kGroup + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
             count_launch();
         }

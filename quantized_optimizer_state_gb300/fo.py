@@ -102,7 +102,6 @@ FO_ACT_SILU = 0         # fo_act_t
 FO_ACT_GELU = 1
 FO_MAX_ACT_GROUPS = 1 << 29
 FO_MAX_ACT_WIDTH = 1 << 30
-FO_NORM_PARTS = 1024
 
 
 class FoRows(ctypes.Structure):
@@ -780,7 +779,7 @@ def fo_rms_norm_grad(codes, steps, inv_rms, grad_y, grad_x=None, weight=None, gr
     if w is not None and gw is not None and wt != gt:
         raise TypeError("grad_weight must be of weight's type")
     c, s = _kept(codes, steps, m, cur)
-    need = 0 if grad_weight is None else min(m.rows, FO_NORM_PARTS) * groups(m.width) * GROUP
+    need = 0 if grad_weight is None else fo_rms_norm_workspace(m.rows, m.width)
     status = lib().fo_rms_norm_grad(
         c, s, _array(inv_rms, "inv_rms", torch.float32, m.rows, cur), w, wt if gw is None else gt, ctypes.byref(m), _ref(to), gw,
         _array(workspace, "workspace", torch.float32, need, cur), _stream(stream))

@@ -56,7 +56,7 @@ def norm_grad(dy, dx=None, weight=5 * MB, wtype=0, inv=6 * MB, gw=7 * MB, ws=8 *
 
 def test_layout_matches_the_header():
     hdr = open(os.path.join(ROOT, "include", "fo.h")).read()
-    assert int(re.search(r"#define FO_NORM_PARTS (\d+)", hdr).group(1)) == fo.FO_NORM_PARTS
+    assert re.search(r"#define FO_MAX_ACT_WIDTH \(1 << (\d+)\)", hdr).group(1) == "30" and fo.FO_MAX_ACT_WIDTH == 1 << 30
     assert re.search(r"#define FO_MAX_ACT_GROUPS \(1 << (\d+)\)", hdr).group(1) == "29" and fo.FO_MAX_ACT_GROUPS == 1 << 29
     assert ctypes.sizeof(fo.FoRows) == 40 and fo.FoRows.dtype.offset == 32
     assert re.search(r"FO_ACT_SILU = 0", hdr) and re.search(r"FO_ACT_GELU = 1", hdr)
@@ -128,7 +128,8 @@ def test_norm_arguments():
     assert norm_grad(dy, dy) == ALIAS and norm_grad(dy, dx, gw=5 * MB) == ALIAS and norm_grad(dy, dx, ws=7 * MB + 16 - 1600) == ALIAS
     assert norm_grad(dy, dx, wtype=7) == BAD and norm_grad(dy, rows(128 * MB, width=99)) == BAD
     assert norm_grad(dy, None, gw=None) == 0                        # nothing asked for
-    assert fo.fo_rms_norm_workspace(10, 64) == 640 and fo.fo_rms_norm_workspace(10 ** 6, 64) == fo.FO_NORM_PARTS * 64
+    assert fo.fo_rms_norm_workspace(10, 64) == 640 and fo.fo_rms_norm_workspace(10, 65) == 960
+    assert fo.fo_rms_norm_workspace(10 ** 6, 64) == 1 << 22 and fo.fo_rms_norm_workspace(10 ** 6, 1 << 20) == 1 << 30
     assert fo.fo_rms_norm_workspace(0, 64) == 0
 
 
