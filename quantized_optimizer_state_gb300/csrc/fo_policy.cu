@@ -75,6 +75,23 @@ __device__ __forceinline__ RowLoss row_loss(const PolicyArgs &a, const Sample &s
     return o;
 }
 
+// What the gradient takes of it: w slope / T, of the token itself, and -1 / Z of
+// that, of every probability. A slope beyond FP32 makes the row's gradient NaN,
+// not infinities and NaN; a row without a distribution has none.
+struct Scaled {
+    float slope, f;
+};
+__device__ __forceinline__ Scaled scaled(float slope, float weight, float sum, const LogitRows &in)
+{
+    const float c = __fmul_rn(slope, weight);
+    Scaled o = {0.0f, 0.0f};
+    if (sum != 0.0f) {
+        o.slope = fabsf(c) < kInf ? __fmul_rn(c, in.inv_t) : kNan;
+        o.f = -o.slope * (1.0f / sum);
+    }
+    return o;
+}
+
 struct Shared {
     uint64_t full[kStages], empty[kStages];   // of a stage: copied; used
     uint64_t summed, joined, written;         // of a row
@@ -204,10 +221,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
             const float x = there ? T::widen(xr) : kNan, sum = ok && there ? z.y : kNan, mm = safe_max(z.x);
             const float logp = sum == 0.0f ? -kInf : sum != sum ? kNan : log_prob(x, z.x, sum, logf(sum), a.in.inv_t);
             const RowLoss o = row_loss(a, s, logp);
-            // a slope beyond FP32 makes the row's gradient NaN, not infinities and NaN
-            const float scaled = __fmul_rn(o.slope, s.weight);
-            const float slope = sum == 0.0f ? 0.0f : fabsf(scaled) < kInf ? __fmul_rn(scaled, a.in.inv_t) : kNan;
-            const float f = sum == 0.0f ? 0.0f : -slope * (1.0f / sum) / T::kShift;
+            const Scaled c = scaled(o.slope, s.weight, sum, a.in);
+            const float slope = c.slope, f = c.f / T::kShift;
             if (lane == 0) {
                 sh.m = mm;
                 sh.f = f;
@@ -323,6 +338,124 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm
     }
 }
 
+// Rows short enough for the registers of a team of kTeam threads, kTeamVecs
+// vectors each: read once, the next one's loads on their way while one is worked
+// on. What a row of policy_kernel waits for, this one's neighbours on the SM hide.
+// Bound by instructions: a row's sums are joined and its loss is formed by every
+// lane, as much work as 32 elements of each.
+constexpr int kTeamThreads = 256;
+template <class T, int kTeam, int kTeamVecs, int kCtas>
+__global__ void __launch_bounds__(kTeamThreads, kCtas) policy_rows_kernel(PolicyArgs a)
+{
+    typedef typename T::raw raw;
+    constexpr int kTeams = kTeamThreads / kTeam;
+    __shared__ Stat part[2][kTeamThreads / 32];
+    const int tid = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
+    const int64_t rows = a.in.rows, step = (int64_t)gridDim.x * kTeams;
+    const uint32_t low = sizeof(raw) == 2 ? T::narrow(-kInf) * 0x10001u : __float_as_uint(-kInf);
+    const uint4 none = make_uint4(low, low, low, low);
+    uint4 next[kTeamVecs];
+    raw next_x;
+    const auto fetch = [&](int64_t r, const Sample &next_sample) {
+        if (next_sample.weight == 0.0f)
+            return;
+        const Row<T> row(a.in, r);
+        next_x = row.x[next_sample.token < row.vocab ? next_sample.token : 0];
+#pragma unroll
+        for (int k = 0; k < kTeamVecs; ++k)
+            next[k] = tid + k * kTeam < row.vecs ? load_vec(row, tid + k * kTeam) : none;
+    };
+    // samples are loaded two rows ahead: which logit a row needs is known when its vectors are asked for
+    int64_t r = (int64_t)blockIdx.x * kTeams + team;
+    if (r >= rows)
+        return;
+    Sample next_sample = load_sample(a, r, true), later = load_sample(a, r + step < rows ? r + step : r, true);
+    fetch(r, next_sample);
+    for (int turn = 0; r < rows; r += step, turn ^= 1) {
+        const Row<T> row(a.in, r);
+        const Sample s = next_sample;
+        const bool there = s.token < row.vocab;
+        const float x = there ? T::widen(next_x) : kNan;
+        uint4 v[kTeamVecs];
+#pragma unroll
+        for (int k = 0; k < kTeamVecs; ++k)
+            v[k] = next[k];
+        next_sample = later;
+        if (r + 2 * step < rows)
+            later = load_sample(a, r + 2 * step, true);
+        if (r + step < rows)
+            fetch(r + step, next_sample);
+        raw *g = static_cast<raw *>(a.grad.data);
+        if (g)
+            g += row_offset(a.in, r, a.grad.row_stride, a.grad.outer_stride);
+        float loss = 0.0f, logp = 0.0f, f = 0.0f, slope = 0.0f, mm = 0.0f;
+        float4 stats = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const bool active = s.weight != 0.0f;   // the same in the team
+        if (active) {
+            Running<T, false> run;
+            run.add(v, a.in);
+            Stat z = warp_join<false>(run.stat(a.in), a.in);
+            if constexpr (kTeam > 32) {
+                if ((threadIdx.x & 31) == 0)
+                    part[turn][threadIdx.x / 32] = z;
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(kTeam) : "memory");
+                z = warp_join<false>(part[turn][team * (kTeam / 32) + tid % (kTeam / 32)], a.in, kTeam / 32);
+            }
+            const float sum = there ? z.z : kNan;
+            mm = safe_max(z.m);
+            logp = sum == 0.0f ? -kInf : sum != sum ? kNan : log_prob(x, z.m, sum, logf(sum), a.in.inv_t);
+            const RowLoss o = row_loss(a, s, logp);
+            loss = __fmul_rn(o.loss, s.weight);
+            const Scaled c = scaled(o.slope, s.weight, sum, a.in);
+            slope = c.slope;
+            f = c.f / T::kShift;
+            stats = make_float4(z.m, sum, o.slope, 0.0f);
+        }
+        if (tid == 0) {
+            if (a.loss)
+                a.loss[r] = loss;
+            if (a.logp)
+                a.logp[r] = logp;
+            if (a.stats)
+                a.stats[r] = stats;
+        }
+        if (!g)
+            continue;
+        // the token's own gradient takes its place in the vector that holds it
+        float t;
+        const raw own = T::narrow(stats.y == 0.0f ? 0.0f : __fmaf_rn(grad_exp<T>(distance(x, mm, a.in), a.in, t), f, slope));
+        const bool aligned = same_phase(row, g);
+        const int at = active && there ? (int)s.token + row.phase : -1;
+#pragma unroll
+        for (int k = 0; k < kTeamVecs; ++k) {
+            const int i = tid + k * kTeam;
+            if (i >= row.vecs)
+                break;
+            uint4 d = active ? grad_vec<T>(v[k], splat(-mm), splat(f), a.in) : make_uint4(0, 0, 0, 0);
+            if (at >= 0 && at / T::kPerVec == i) {
+                raw *const e = reinterpret_cast<raw *>(&d);
+#pragma unroll
+                for (int j = 0; j < T::kPerVec; ++j)
+                    e[j] = at % T::kPerVec == j ? own : e[j];
+            }
+            if (aligned && i >= row.full0 && i < row.full1)
+                store_stream(g + row.id(i, 0), d);
+            else
+                store_edge<T>(g, row, i, d);
+        }
+    }
+}
+
+template <class T, int kTeam, int kTeamVecs, int kCtas>
+cudaError_t launch_rows(const PolicyArgs &a, cudaStream_t stream)
+{
+    constexpr int kTeams = kTeamThreads / kTeam;
+    const int64_t ctas = std::min((a.in.rows + kTeams - 1) / kTeams, (int64_t)sm_count() * kCtas);
+    policy_rows_kernel<T, kTeam, kTeamVecs, kCtas><<<(unsigned)ctas, kTeamThreads, 0, stream>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
+
 template <class T, int kWarps>
 cudaError_t launch(const PolicyArgs &a, int size, int64_t ctas, cudaStream_t stream)
 {
@@ -336,7 +469,17 @@ cudaError_t launch(const PolicyArgs &a, int size, int64_t ctas, cudaStream_t str
 template <class T>
 cudaError_t launch(const PolicyArgs &a, cudaStream_t stream)
 {
-    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), sms = sm_count();
+    const int64_t bytes = a.in.vocab * (int64_t)sizeof(typename T::raw), sms = sm_count(), vecs = row_vecs(bytes);
+    // Loss with gradient, us, in registers / by two warps and the ring: 16384 x 1000
+    // BF16 21 / 42, 8000 x 2000 19 / 27, 8000 x 4000 34 / 36, 10000 x 2000 FP32 36 /
+    // 42, 8000 x 6000 BF16 57 / 45. (A warp with four vectors where they hold the row:
+    // with eight 16384 x 1000 takes 27.)
+    if (vecs <= 128)
+        return launch_rows<T, 32, 4, 3>(a, stream);
+    if (vecs <= 256)
+        return launch_rows<T, 32, 8, 2>(a, stream);
+    if (vecs <= 512)
+        return launch_rows<T, 64, 8, 2>(a, stream);
     if (bytes <= kShortRow && a.in.rows >= sms * kShortPerSm)
         return launch<T, kShort>(a, 1, sms * kShortPerSm, stream);
     const int64_t ctas = sms * kCtasPerSm;
