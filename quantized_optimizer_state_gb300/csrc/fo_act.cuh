@@ -188,6 +188,7 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor &d) { ret
 // less beyond the row's end). Beyond the last row: row -1, and `left` far below 0.
 struct Place {
     int row, col, left;
+    bool last;   // of its row's units
 };
 template <int W>
 __device__ __forceinline__ Place place(uint32_t unit, uint32_t units, const Divisor &per_row, int width)
@@ -195,6 +196,7 @@ __device__ __forceinline__ Place place(uint32_t unit, uint32_t units, const Divi
     const uint32_t r = quotient(unit, per_row);
     Place p;
     p.row = unit < units ? (int)r : -1;
+    p.last = unit - r * per_row.d + 1 == per_row.d;
     p.col = (int)((unit - r * per_row.d) * W);
     p.left = unit < units ? width - p.col : -64;
     return p;
@@ -251,12 +253,11 @@ __device__ __forceinline__ void load_vector(const uint4 *at, uint32_t *w)
 // the row may start anywhere: the aligned vectors that hold the unit are read
 // and shifted.
 template <class T, bool kWide, int W = kUnitOf<kWide>>
-__device__ __forceinline__ Words<T, W> load_unit(const RowsIn &x, const Place &p)
+__device__ __forceinline__ Words<T, W> load_unit(const typename T::raw *at, const Place &p)
 {
     typedef typename T::raw raw;
     constexpr int kSize = sizeof(raw), kVecs = W * kSize / 16;
     Words<T, W> v;
-    const raw *at = static_cast<const raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
 #pragma unroll
     for (int i = 0; i < Words<T, W>::kN; ++i)
         v.w[i] = 0;
@@ -291,16 +292,21 @@ __device__ __forceinline__ Words<T, W> load_unit(const RowsIn &x, const Place &p
     return v;
 }
 
+template <class T, bool kWide>
+__device__ __forceinline__ Words<T, kUnitOf<kWide>> load_unit(const RowsIn &x, const Place &p)
+{
+    return load_unit<T, kWide>(static_cast<const typename T::raw *>(x.data) + (int64_t)p.row * x.stride + p.col, p);
+}
+
 // Stores a unit. Without kWide by all lanes of a warp, whose units follow one
 // another: a lane stores the aligned vectors that begin in the unit before its
 // own and end in its own, with what that unit's lane hands over; what has no such
 // lane goes element by element. Runs of kRun lanes have units that follow one another.
 template <class T, bool kWide, int kRun = 32, int W = kUnitOf<kWide>>
-__device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, const Words<T, W> &v)
+__device__ __forceinline__ void store_unit(typename T::raw *at, const Place &p, const Words<T, W> &v)
 {
     typedef typename T::raw raw;
     constexpr int kSize = sizeof(raw), kVecs = W * kSize / 16, kN = Words<T, W>::kN;
-    raw *const at = static_cast<raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
     if (kWide) {
         if (p.left > 0)
 #pragma unroll
@@ -317,8 +323,7 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
 #pragma unroll
     for (int i = 0; i < kN; ++i)
         in[kOver + i] = out[i] = v.w[i];
-    const int next_row = __shfl_down_sync(~0u, p.row, 1);
-    const bool before = lane > 0 && p.col > 0, after = lane < kRun - 1 && next_row == p.row;
+    const bool before = lane > 0 && p.col > 0, after = lane < kRun - 1 && !p.last;
     int lo = 0, hi = p.left;             // places of `out`, from the vectors' first on, that are the row's
     if (phase) {
         shifted<T>(in, (kSize == 2 ? 8 : 3) - phase, out);
@@ -348,6 +353,12 @@ __device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, con
                 if (mine >> k & 1)
                     to[kPer * i + k] = e[kPer * i + k];
     }
+}
+
+template <class T, bool kWide, int W>
+__device__ __forceinline__ void store_unit(const RowsOut &x, const Place &p, const Words<T, W> &v)
+{
+    store_unit<T, kWide>(static_cast<typename T::raw *>(x.data) + (int64_t)p.row * x.stride + p.col, p, v);
 }
 
 // A unit's values in pairs, and back, rounded once.

@@ -85,21 +85,28 @@ __device__ __forceinline__ float both(f2 v)
 }
 
 // A row is worked on by a team: kLanes threads of a warp, or (kLanes = 0) a whole
-// CTA, of as many warps as the row fills. The sum of v over the team, in every one
-// of its threads. `part` holds a CTA's warps' sums; two sets in turn, so that one
-// barrier a sum is enough.
-template <int kLanes>
+// CTA, of as many warps as the row fills, kWarps at most. The sum of v over the
+// team, in every one of its threads. `part` holds a CTA's warps' sums, and zeros
+// for the warps that it does not have; two sets in turn, so that one barrier a sum
+// is enough.
+template <int kLanes, int kWarps>
 __device__ __forceinline__ float row_sum(float v, float *part)
 {
 #pragma unroll
     for (int o = (kLanes ? kLanes : 32) / 2; o; o >>= 1)
         v += __shfl_xor_sync(~0u, v, o);
     if constexpr (kLanes == 0) {
-        const int lane = threadIdx.x & 31;
-        if (lane == 0)
+        if ((threadIdx.x & 31) == 0)
             part[threadIdx.x / 32] = v;
         __syncthreads();
-        v = warp_sum(lane < (int)blockDim.x / 32 ? part[lane] : 0.0f);
+        f2 sum = 0, other = 0;
+#pragma unroll
+        for (int i = 0; i < (kWarps + 3) / 4; ++i) {
+            const ulonglong2 s = reinterpret_cast<const ulonglong2 *>(part)[i];
+            sum = add2(sum, s.x);
+            other = add2(other, s.y);
+        }
+        v = both(add2(sum, other));
     }
     return v;
 }
@@ -111,9 +118,28 @@ __device__ __forceinline__ Place row_place(int r, int rows, int u, int units, in
     Place p;
     const bool there = r < rows && u < units;
     p.row = there ? r : -1;
+    p.last = u + 1 >= units;
     p.col = u * W;
     p.left = there ? width - p.col : -64;
     return p;
+}
+
+// A unit at an address that moves on with the rows; where rows line up with no
+// vector, registers are short, and it is computed from the place.
+template <class T, bool kWide>
+__device__ __forceinline__ Words<T, kUnitOf<kWide>> load(const RowsIn &x, const typename T::raw *at, const Place &p)
+{
+    if constexpr (kWide)
+        return load_unit<T, kWide>(at, p);
+    else
+        return load_unit<T, kWide>(x, p);
+}
+template <class T, bool kWide, int kLanes>
+__device__ __forceinline__ void store(const RowsOut &x, typename T::raw *at, const Place &p, const Words<T, kUnitOf<kWide>> &v)
+{
+    if constexpr (!kWide)
+        at = static_cast<typename T::raw *>(x.data) + (int64_t)p.row * x.stride + p.col;
+    store_unit<T, kWide, (kLanes ? kLanes : 32)>(at, p, v);
 }
 
 // --- rows held in registers --------------------------------------------------------------
@@ -124,8 +150,12 @@ __device__ __forceinline__ Place row_place(int r, int rows, int u, int units, in
 template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
 __global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
 {
-    constexpr int W = kUnitOf<kWide>;
-    __shared__ float part[4][32];
+    typedef typename T::raw raw;
+    constexpr int W = kUnitOf<kWide>, kWarps = kBlock / 32;
+    __shared__ __align__(16) float part[4][32];
+    if (kLanes == 0 && threadIdx.x < 4 * 32)
+        part[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
+    __syncthreads();
     const int lanes = kLanes ? kLanes : blockDim.x, teams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1;
     const int lane = kLanes ? threadIdx.x % lanes : threadIdx.x;
     const int units = (int)a.groups * (32 / W), rows = (int)a.rows, width = (int)a.width;
@@ -133,10 +163,13 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
     int r = blockIdx.x * teams + (kLanes ? threadIdx.x / lanes : 0);
     Words<T, W> next[kVecs];
     f2 w[kVecs][W / 2];
+    const raw *from = static_cast<const raw *>(a.x.data) + (int64_t)r * a.x.stride + lane * W;
+    raw *to = static_cast<raw *>(a.y.data) + (int64_t)r * a.y.stride + lane * W;
     const auto fetch = [&](int row) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
-            next[k] = load_unit<T, kWide>(a.x, row_place<W>(row, rows, lane + k * lanes, units, width));
+            next[k] = load<T, kWide>(a.x, from + k * lanes * W, row_place<W>(row, rows, lane + k * lanes, units, width));
+        from += step * a.x.stride;
     };
     fetch(r);
 #pragma unroll
@@ -166,11 +199,11 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
                 }
             return both(sum);
         };
-        const float sum = row_sum<kLanes>(squares(1.0f), part[turn]);
+        const float sum = row_sum<kLanes, kWarps>(squares(1.0f), part[turn]);
         const bool large = !(sum < kLargeSum);
         float inv = inverse_rms(sum, a);
         if (kLanes ? __any_sync(~0u, large) : large) {   // the same in a CTA; other rows of a warp keep theirs
-            const float down = inverse_rms_down(row_sum<kLanes>(squares(kDown), part[turn + 1]), a);
+            const float down = inverse_rms_down(row_sum<kLanes, kWarps>(squares(kDown), part[turn + 1]), a);
             inv = large ? down : inv;
         }
         if (lane == 0 && a.inv_rms && r < rows)
@@ -180,8 +213,9 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
 #pragma unroll
             for (int j = 0; j < W / 2; ++j)
                 x[k][j] = mul2(mul2(x[k][j], splat(inv)), w[k][j]);
-            store_unit<T, kWide, (kLanes ? kLanes : 32)>(a.y, row_place<W>(r, rows, lane + k * lanes, units, width), narrow_unit<T, W>(x[k]));
+            store<T, kWide, kLanes>(a.y, to + k * lanes * W, row_place<W>(r, rows, lane + k * lanes, units, width), narrow_unit<T, W>(x[k]));
         }
+        to += step * a.y.stride;
     }
 }
 
@@ -191,8 +225,12 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
 template <class T, bool kWide, int kLanes, int kVecs, int kBlock, int kCtas>
 __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a)
 {
-    constexpr int W = kUnitOf<kWide>, kTeams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1;
-    __shared__ float part[2][32];
+    typedef typename T::raw raw;
+    constexpr int W = kUnitOf<kWide>, kTeams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1, kWarps = kBlock / 32;
+    __shared__ __align__(16) float part[2][32];
+    if (kLanes == 0 && threadIdx.x < 2 * 32)
+        part[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
+    __syncthreads();
     __shared__ __align__(16) float joined[kTeams][kTeams > 1 ? kLanes * kVecs * W : 4];
     const int lanes = kLanes ? kLanes : blockDim.x;
     const int lane = kLanes ? threadIdx.x % lanes : threadIdx.x, team = kLanes ? threadIdx.x / lanes : 0;
@@ -202,17 +240,20 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
     Words<T, W> next[kVecs];
     Kept<W> next_x[kVecs];
     float next_inv;
+    int r = blockIdx.x * kTeams + team;
+    const raw *from = static_cast<const raw *>(a.grad_y.data) + (int64_t)r * a.grad_y.stride + lane * W;
+    raw *to = static_cast<raw *>(a.grad.data) + (int64_t)r * a.grad.stride + lane * W;
     const auto fetch = [&](int r) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int u = lane + k * lanes;
             const Place p = row_place<W>(r, rows, u, units, width);
-            next[k] = load_unit<T, kWide>(a.grad_y, p);
+            next[k] = load<T, kWide>(a.grad_y, from + k * lanes * W, p);
             next_x[k] = load_kept<W>(a.kept, (uint32_t)r * units + u, p.row < 0 ? 0u : ~0u);
         }
         next_inv = r < rows ? __ldg(a.inv_rms + r) : 0.0f;
+        from += step * a.grad_y.stride;
     };
-    int r = blockIdx.x * kTeams + team;
     fetch(r);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
@@ -238,19 +279,20 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
         const float inv = next_inv;
         fetch(r + step);
         if (a.grad.data) {
-            const f2 mean = splat(-__fmul_rn(row_sum<kLanes>(both(dot), part[turn]), a.inv_width));
+            const f2 mean = splat(-__fmul_rn(row_sum<kLanes, kWarps>(both(dot), part[turn]), a.inv_width));
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j)
                     t[k][j] = mul2(fma2(h[k][j], mean, t[k][j]), splat(inv));
-                store_unit<T, kWide, (kLanes ? kLanes : 32)>(a.grad, row_place<W>(r, rows, lane + k * lanes, units, width), narrow_unit<T, W>(t[k]));
+                store<T, kWide, kLanes>(a.grad, to + k * lanes * W, row_place<W>(r, rows, lane + k * lanes, units, width), narrow_unit<T, W>(t[k]));
             }
+            to += step * a.grad.stride;
         }
     }
     if (!a.grad_weight)
         return;
-    float *const to = a.parts + (int64_t)blockIdx.x * a.groups * kGroup;
+    float *const sums = a.parts + (int64_t)blockIdx.x * a.groups * kGroup;
     if constexpr (kTeams > 1) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
@@ -263,7 +305,7 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
 #pragma unroll
             for (int i = 0; i < kTeams; ++i)
                 sum += joined[i][c];
-            to[c] = sum;
+            sums[c] = sum;
         }
     } else {
 #pragma unroll
@@ -272,7 +314,7 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
             if (u < units)
 #pragma unroll
                 for (int j = 0; j < W / 4; ++j)
-                    reinterpret_cast<ulonglong2 *>(to + u * W)[j] = make_ulonglong2(dw[k][2 * j], dw[k][2 * j + 1]);
+                    reinterpret_cast<ulonglong2 *>(sums + u * W)[j] = make_ulonglong2(dw[k][2 * j], dw[k][2 * j + 1]);
         }
     }
 }
@@ -481,7 +523,9 @@ int by_size(const NormGradArgs &a, cudaStream_t stream)
     if constexpr (!kWide) {
         if (block <= 576)
             return run<T, kWide, 0, 1, 576, 1>(a, block, stream);
-    } else if (block <= 576)
+    } else if (sizeof(typename T::raw) == 4 && block <= 512)
+        return run<T, kWide, 0, 1, 512, 2>(a, block, stream);
+    else if (block <= 576)
         return run<T, kWide, 0, 1, 576, 2>(a, block, stream);
     if constexpr (kWide)
         if (block > 1024)
