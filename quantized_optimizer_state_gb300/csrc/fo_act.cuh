@@ -464,7 +464,10 @@ __device__ __forceinline__ void keep_unit(const KeptOut &k, uint32_t unit, uint3
             codes.z = low_bytes(c[8], c[9], c[10], c[11]);
             codes.w = low_bytes(c[12], c[13], c[14], c[15]);
         }
-        __stcs(reinterpret_cast<typename CodeVec<W>::type *>(k.codes) + unit, codes);
+        // Without the streaming hint of the results: a backward pass that comes soon
+        // finds them in the L2 cache (norm of 16384 x 4096 BF16 57 us against 64); one
+        // that comes later loses nothing.
+        reinterpret_cast<typename CodeVec<W>::type *>(k.codes)[unit] = codes;
         if (unit % (32 / W) == 0)
             k.steps[unit / (32 / W)] = step_bits(step);
     }
