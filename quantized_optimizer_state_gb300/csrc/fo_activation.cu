@@ -6,9 +6,6 @@ namespace fo {
 namespace {
 
 constexpr int kThreads = 256;
-#ifndef UG
-#define UG 4
-#endif
 
 template <class T, int kKind, bool kGated, bool kWide, int kUnits>
 __global__ void __launch_bounds__(kThreads) activation_kernel(ActivationArgs a, UnitGrid g)
@@ -83,9 +80,11 @@ __global__ void __launch_bounds__(kThreads) activation_grad_kernel(ActivationGra
     }
 }
 
-// Units of a thread, all loaded before the first is used.
+// Units of a thread, all loaded before the first is used: 64 bytes of BF16 input
+// on their way (silu of 8192 x 14336 BF16, forward and backward: two units 206 us,
+// four 190), 32 where a unit has 16 elements and registers are short.
 template <bool kGated, bool kWide>
-constexpr int kUnits = kGated || !kWide ? (kWide ? 2 : 1) : UG;
+constexpr int kUnits = kWide ? (kGated ? 2 : 4) : 1;
 
 template <int N>
 unsigned ctas(const UnitGrid &g) { return (g.units + kThreads * N - 1) / (kThreads * N); }

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kTeamThreads, kCtas) policy_rows_kernel(Policy
         return;
     Sample next_sample = load_sample(a, r, true), later = load_sample(a, r + step < rows ? r + step : r, true);
     fetch(r, next_sample);
-    for (int turn = 0; r < rows; r += step, turn ^= 1) {
+    for (int turn = 0; r < rows; r += step) {
         const Row<T> row(a.in, r);
         const Sample s = next_sample;
         const bool there = s.token < row.vocab;
@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(kTeamThreads, kCtas) policy_rows_kernel(Policy
                     part[turn][threadIdx.x / 32] = z;
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(kTeam) : "memory");
                 z = warp_join<false>(part[turn][team * (kTeam / 32) + tid % (kTeam / 32)], a.in, kTeam / 32);
+                turn ^= 1;   // one barrier a sum is enough for two sets in turn, of rows that have one
             }
             const float sum = there ? z.z : kNan;
             mm = safe_max(z.m);
