@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_kernel(NormArgs a)
     typedef typename T::raw raw;
     constexpr int W = kUnitOf<kWide>, kWarps = kBlock / 32;
     __shared__ __align__(16) float part[4][32];
-    if (kLanes == 0 && threadIdx.x < 4 * 32)
-        part[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
+    for (int i = threadIdx.x; kLanes == 0 && i < 4 * 32; i += blockDim.x)
+        part[i / 32][i % 32] = 0.0f;
     __syncthreads();
     const int lanes = kLanes ? kLanes : blockDim.x, teams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1;
     const int lane = kLanes ? threadIdx.x % lanes : threadIdx.x;
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
     typedef typename T::raw raw;
     constexpr int W = kUnitOf<kWide>, kTeams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1, kWarps = kBlock / 32;
     __shared__ __align__(16) float part[2][32];
-    if (kLanes == 0 && threadIdx.x < 2 * 32)
-        part[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
+    for (int i = threadIdx.x; kLanes == 0 && i < 2 * 32; i += blockDim.x)
+        part[i / 32][i % 32] = 0.0f;
     __syncthreads();
     __shared__ __align__(16) float joined[kTeams][kTeams > 1 ? kLanes * kVecs * W : 4];
     const int lanes = kLanes ? kLanes : blockDim.x;
