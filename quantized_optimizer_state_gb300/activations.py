@@ -23,14 +23,14 @@ first order and in reverse mode; a tangent of forward mode is refused.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple, Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
 
 from . import fo
-from .losses import _on_device_of
+
+_native = fo.native
 
 KINDS = {"silu": (fo.FO_ACT_SILU, False), "gelu": (fo.FO_ACT_GELU, False),
          "swiglu": (fo.FO_ACT_SILU, True), "geglu": (fo.FO_ACT_GELU, True)}
@@ -92,179 +92,34 @@ def _check_tangent(*tensors: Optional[torch.Tensor]) -> None:
             raise NotImplementedError("operators on activations have no forward-mode derivative: an input carries a tangent")
 
 
-def _check_width(x: torch.Tensor) -> None:
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"a tensor [..., width] of at least one column is needed, not {tuple(x.shape)}")
-
-
-# The functions below hand the C calls the addresses of tensors that they have
-# just made themselves; what the caller passes is checked by fo's helpers. A call
-# is a few microseconds of host time, which is what small tensors take.
-
-_empty = torch.empty
-
-
-def _grad_rows(grad: torch.Tensor, shape, dtype, rows: int, dt: int) -> fo.FoRows:
-    """An incoming gradient of the result's shape and type (``rows`` and ``dt`` are theirs). One in a
-    layout that the kernels do not read (an expanded one, for example) is copied; the rows hold the copy."""
-    if grad.dtype is dtype and grad.shape == shape and grad.is_contiguous() and grad.get_device() == fo._current_device():
-        width = shape[-1]
-        return fo.FoRows(grad.data_ptr(), rows, width, width, dt, 0)
-    if grad.shape != shape or grad.dtype != dtype:
-        raise ValueError(f"grad_y must be {str(dtype).replace('torch.', '')} of shape {tuple(shape)}, not "
-                         f"{str(grad.dtype).replace('torch.', '')} of shape {tuple(grad.shape)}")
-    if fo._rows_of(grad) is None:
-        grad = grad.contiguous()
-    m = fo.matrix(grad, "grad_y")
-    m.keep = grad
-    return m
-
-
 def compress(x: torch.Tensor) -> Compressed:
     """The codes and steps of ``x``; groups of 32 run along the last dimension, the
     last one of a row may be partial. Not differentiable."""
     _check_tangent(x)
-    _check_width(x)
-    m = fo.matrix(x)
-    shape, dev = x.shape, x.device
-    g = -(-m.width // fo.GROUP)
-    lead = shape[:-1]
-    codes = _empty(lead + (g * fo.GROUP,), dtype=torch.int8, device=dev)
-    steps = _empty(lead + (g,), dtype=torch.bfloat16, device=dev)
-    status = fo.lib().fo_compress(ctypes.byref(m), codes.data_ptr(), steps.data_ptr(), fo._stream(None))
-    if status:
-        fo._check("fo_compress", status)
-    return Compressed(codes, steps, m.width, x.dtype)
+    codes, steps = _native().compress(x)
+    return Compressed(codes, steps, x.shape[-1], x.dtype)
 
 
 def expand(kept: Compressed, *, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The tensor that the codes stand for, rounded once to ``dtype`` (that of the
     compressed tensor where None). ``out``: where to write it."""
     codes, steps, width, own = kept
-    lead, g = codes.shape[:-1], -(-width // fo.GROUP)
-    if steps.shape != lead + (g,) or codes.shape[-1] != g * fo.GROUP:
-        raise ValueError(f"codes {tuple(codes.shape)} and steps {tuple(steps.shape)} are not those of {width} columns")
-    if out is not None:
-        if out.shape != lead + (width,) or (dtype is not None and out.dtype != dtype):
-            raise ValueError(f"out must be of shape {tuple(lead + (width,))}" + (f" and {dtype}" if dtype else "") +
-                             f", not {tuple(out.shape)} and {out.dtype}")
-        fo.fo_expand(codes, steps, out)
-        return out
-    x = _empty(lead + (width,), dtype=dtype or own, device=codes.device)
-    m = fo.matrix(x)
-    c, s = fo._kept(codes, steps, m, x.device.index)
-    status = fo.lib().fo_expand(c, s, ctypes.byref(m), fo._stream(None))
-    if status:
-        fo._check("fo_expand", status)
-    return x
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {dtype}, not {out.dtype}")
+    return _native().expand(codes, steps, width, dtype or own, out)
 
 
 # --- activation functions ------------------------------------------------------------------
 
-def _activation(x, kind, up, keep):
-    """(the result, the bytes that are kept or None, what :func:`_activation_grad` needs beside them)"""
+def _kind(kind: str, up: Optional[torch.Tensor]) -> Tuple[int, bool]:
+    """(fo_act_t, whether the kind is gated)"""
     try:
-        act, gated = KINDS[kind]
+        how = KINDS[kind]
     except (KeyError, TypeError):
         raise ValueError(f"kind must be one of {', '.join(KINDS)}, not {kind!r}") from None
-    _check_width(x)
-    if up is not None and not gated:
+    if up is not None and not how[1]:
         raise ValueError(f"{kind} takes no second input")
-    m, u, shape, dtype, dev = fo.matrix(x), None, x.shape, x.dtype, x.device
-    width, rows, dt = m.width, m.rows, m.dtype
-    if gated:
-        if up is None:
-            if width % 2:
-                raise ValueError(f"{kind} halves the last dimension, which must be even, not {width}")
-            width //= 2
-            shape = shape[:-1] + (width,)
-            m.width = width
-            u = ctypes.byref(fo.FoRows((m.data or 0) + width * x.element_size(), rows, width, m.row_stride, dt, 0))
-        else:
-            if up.shape != shape:
-                raise ValueError(f"up must have the gate's shape {tuple(shape)}, not {tuple(up.shape)}")
-            u = ctypes.byref(fo.matrix(up, "up", m))
-    y = _empty(shape, dtype=dtype, device=dev)
-    kept = c = s = uc = us = None
-    if keep:
-        n = rows * -(-width // fo.GROUP)          # groups
-        kept = _empty(n * (68 if gated else 34), dtype=torch.int8, device=dev)
-        c = kept.data_ptr()
-        s = c + n * fo.GROUP
-        if gated:
-            uc, s = s, s + n * fo.GROUP
-            us = s + 2 * n
-    status = fo.lib().fo_activation(act, ctypes.byref(m), u, ctypes.byref(fo.FoRows(y.data_ptr(), rows, width, width, dt, 0)),
-                                    c, s, uc, us, fo._stream(None))
-    if status:
-        fo._check("fo_activation", status)
-    return y, kept, (act, gated, gated and up is None, shape, dtype, rows, dt)
-
-
-def _activation_grad(kept, how, grad_y):
-    act, gated, halves, shape, dtype, rows, dt = how
-    m = _grad_rows(grad_y, shape, dtype, rows, dt)
-    width, dev = shape[-1], kept.device
-    n = rows * -(-width // fo.GROUP)
-    c = kept.data_ptr()
-    s = c + n * fo.GROUP
-    grad_up = uc = us = to_up = None
-    if halves:
-        stride = 2 * width
-        grad = _empty(shape[:-1] + (stride,), dtype=dtype, device=dev)
-    else:
-        stride = width
-        grad = _empty(shape, dtype=dtype, device=dev)
-    at = grad.data_ptr()
-    if gated:
-        uc, s = s, s + n * fo.GROUP
-        us = s + 2 * n
-        if not halves:
-            grad_up = torch.empty_like(grad)
-        to_up = ctypes.byref(fo.FoRows(at + width * grad.element_size() if halves else grad_up.data_ptr(), rows, width, stride, dt, 0))
-    status = fo.lib().fo_activation_grad(act, c, s, uc, us, ctypes.byref(m), ctypes.byref(fo.FoRows(at, rows, width, stride, dt, 0)),
-                                         to_up, fo._stream(None))
-    if status:
-        fo._check("fo_activation_grad", status)
-    return grad, grad_up
-
-
-def activation_forward(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, KeptActivation]:
-    """``(y, kept)``: :func:`activation` and what :func:`activation_backward` needs."""
-    _check_tangent(x, up)
-    y, kept, how = _activation(x, kind, up, True)
-    return y, KeptActivation(kind, kept, y.shape, y.dtype, how[2])
-
-
-def activation_backward(kept: KeptActivation, grad_y: torch.Tensor):
-    """The gradient of ``x`` (of ``(x, up)`` where ``up`` was given) for that of ``y``."""
-    kind, buffer, shape, dtype, halves = kept
-    act, gated = KINDS[kind]
-    rows = shape[:-1].numel()
-    fo._array(buffer, "kept", torch.int8, rows * -(-shape[-1] // fo.GROUP) * (68 if gated else 34), fo._current_device())
-    grad, grad_up = _activation_grad(buffer, (act, gated, halves, shape, dtype, rows, fo._logit_dtype(dtype, "kept")), grad_y)
-    return grad if grad_up is None else (grad, grad_up)
-
-
-class _Activation(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, up, kind):
-        y, kept, ctx.how = _activation(x, kind, up, True)
-        ctx.save_for_backward(kept)
-        return y
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_y):
-        kept, = ctx.saved_tensors
-        if kept.get_device() == fo._current_device():
-            return (*_activation_grad(kept, ctx.how, grad_y), None)
-        with torch.cuda.device(kept.device):
-            return (*_activation_grad(kept, ctx.how, grad_y), None)
-
-
-def _differentiable(*tensors) -> bool:
-    return torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in tensors])
+    return how
 
 
 def activation(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -273,93 +128,26 @@ def activation(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None)
     ``up`` are the halves of ``x`` along the last dimension, or ``x`` and ``up``.
     Differentiable; the input is kept in 8 bits where a gradient is asked for."""
     _check_tangent(x, up)
-    if _differentiable(x, up):
-        return _Activation.apply(x, up, kind)
-    return _activation(x, kind, up, False)[0]
+    return _native().activation(x, up, *_kind(kind, up))
+
+
+def activation_forward(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, KeptActivation]:
+    """``(y, kept)``: :func:`activation` and what :func:`activation_backward` needs."""
+    _check_tangent(x, up)
+    act, gated = _kind(kind, up)
+    y, kept = _native().activation_forward(x, up, act, gated)
+    return y, KeptActivation(kind, kept, y.shape, y.dtype, gated and up is None)
+
+
+def activation_backward(kept: KeptActivation, grad_y: torch.Tensor):
+    """The gradient of ``x`` (of ``(x, up)`` where ``up`` was given) for that of ``y``."""
+    kind, buffer, shape, dtype, halves = kept
+    act, gated = KINDS[kind]
+    grads = _native().activation_backward(buffer, act, gated, halves, shape, dtype, grad_y)
+    return grads if gated and not halves else grads[0]
 
 
 # --- norm ------------------------------------------------------------------------------------
-
-def _norm(x, weight, eps, keep):
-    """(the result, the bytes that are kept or None, what :func:`_norm_grad` needs beside them)"""
-    _check_width(x)
-    m, dev, shape = fo.matrix(x), x.device, x.shape
-    width, rows = m.width, m.rows
-    w, wt = None, 0
-    if weight is not None:
-        if weight.shape != shape[-1:]:
-            raise ValueError(f"weight must be of shape ({width},), not {tuple(weight.shape)}")
-        w, wt = fo._weight(weight, "weight", width, dev.index)
-    y = _empty(shape, dtype=x.dtype, device=dev)
-    kept = c = s = inv = None
-    if keep:
-        n = rows * -(-width // fo.GROUP)          # groups
-        kept = _empty(n * 34 + 4 * rows, dtype=torch.int8, device=dev)
-        c = kept.data_ptr()
-        inv = c + n * fo.GROUP
-        s = inv + 4 * rows
-    status = fo.lib().fo_rms_norm(ctypes.byref(m), w, wt, eps, ctypes.byref(fo.FoRows(y.data_ptr(), rows, width, width, m.dtype, 0)),
-                                  inv, c, s, fo._stream(None))
-    if status:
-        fo._check("fo_rms_norm", status)
-    return y, kept, (shape, x.dtype, rows, m.dtype, wt)
-
-
-def _norm_grad(kept, weight, how, grad_y, need_x, need_weight):
-    shape, dtype, rows, dt, wt = how
-    m = _grad_rows(grad_y, shape, dtype, rows, dt)
-    width, dev = shape[-1], kept.device
-    c = kept.data_ptr()
-    inv = c + rows * -(-width // fo.GROUP) * fo.GROUP
-    w = None if weight is None else weight.data_ptr()
-    grad = to = grad_weight = gw = parts = ws = None
-    if need_x:
-        grad = _empty(shape, dtype=dtype, device=dev)
-        to = ctypes.byref(fo.FoRows(grad.data_ptr(), rows, width, width, dt, 0))
-    if need_weight and weight is not None:
-        grad_weight = torch.empty_like(weight)
-        parts = _empty(fo.lib().fo_rms_norm_workspace(rows, width), dtype=torch.float32, device=dev)
-        gw, ws = grad_weight.data_ptr(), parts.data_ptr()
-    status = fo.lib().fo_rms_norm_grad(c, inv + 4 * rows, inv, w, wt, ctypes.byref(m), to, gw, ws, fo._stream(None))
-    if status:
-        fo._check("fo_rms_norm_grad", status)
-    return grad, grad_weight
-
-
-def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> Tuple[torch.Tensor, KeptNorm]:
-    """``(y, kept)``: :func:`rms_norm` and what :func:`rms_norm_backward` needs."""
-    _check_tangent(x, weight)
-    y, kept, _ = _norm(x, weight, eps, True)
-    return y, KeptNorm(kept, y.shape, y.dtype, weight)
-
-
-def rms_norm_backward(kept: KeptNorm, grad_y: torch.Tensor) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """``(grad_x, grad_weight)`` for the gradient of ``y``; ``grad_weight``, of the
-    weight's type, is None without one."""
-    buffer, shape, dtype, weight = kept
-    rows, cur = shape[:-1].numel(), fo._current_device()
-    fo._array(buffer, "kept", torch.int8, rows * (-(-shape[-1] // fo.GROUP) * 34 + 4), cur)
-    _, wt = fo._weight(weight, "weight", shape[-1], cur)
-    return _norm_grad(buffer, weight, (shape, dtype, rows, fo._logit_dtype(dtype, "kept"), wt), grad_y, True, True)
-
-
-class _Norm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, eps):
-        y, kept, ctx.how = _norm(x, weight, eps, True)
-        ctx.save_for_backward(kept, weight)
-        return y
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_y):
-        kept, weight = ctx.saved_tensors
-        need_x, need_weight, _ = ctx.needs_input_grad
-        if kept.get_device() == fo._current_device():
-            return (*_norm_grad(kept, weight, ctx.how, grad_y, need_x, need_weight), None)
-        with torch.cuda.device(kept.device):
-            return (*_norm_grad(kept, weight, ctx.how, grad_y, need_x, need_weight), None)
-
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> torch.Tensor:
     """``x / sqrt(mean(x^2) + eps) * weight`` over the last dimension, in ``x``'s type;
@@ -368,9 +156,21 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
     gradient of ``weight`` sums the rows in FP32, in an order that depends on their
     number and the device only."""
     _check_tangent(x, weight)
-    if _differentiable(x, weight):
-        return _Norm.apply(x, weight, eps)
-    return _norm(x, weight, eps, False)[0]
+    return _native().rms_norm(x, weight, eps)
+
+
+def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> Tuple[torch.Tensor, KeptNorm]:
+    """``(y, kept)``: :func:`rms_norm` and what :func:`rms_norm_backward` needs."""
+    _check_tangent(x, weight)
+    y, kept = _native().rms_norm_forward(x, weight, eps)
+    return y, KeptNorm(kept, y.shape, y.dtype, weight)
+
+
+def rms_norm_backward(kept: KeptNorm, grad_y: torch.Tensor) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``(grad_x, grad_weight)`` for the gradient of ``y``; ``grad_weight``, of the
+    weight's type, is None without one."""
+    buffer, shape, dtype, weight = kept
+    return _native().rms_norm_backward(buffer, shape, dtype, weight, grad_y)
 
 
 # --- matrix product ---------------------------------------------------------------------------
@@ -389,7 +189,7 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, grad_y):
         weight, *kept = ctx.saved_tensors
         grad_x = grad_weight = grad_bias = None
-        with _on_device_of(weight), torch.autocast("cuda", enabled=False):
+        with torch.cuda.device(weight.device), torch.autocast("cuda", enabled=False):
             rows = grad_y.reshape(-1, grad_y.shape[-1])
             if ctx.needs_input_grad[0]:
                 grad_x = grad_y @ weight
@@ -409,6 +209,6 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     if x.dtype != weight.dtype or (bias is not None and bias.dtype != x.dtype):
         raise TypeError(f"x, weight and bias must be of one type, not {x.dtype}, {weight.dtype}" +
                         (f" and {bias.dtype}" if bias is not None else ""))
-    if _differentiable(x, weight, bias):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         return _Linear.apply(x, weight, bias)
     return torch.nn.functional.linear(x, weight, bias)

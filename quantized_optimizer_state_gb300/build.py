@@ -4,6 +4,9 @@ The library is compiled from ``csrc/*.cu`` with IEEE-exact FP32 flags
 (no contraction, IEEE division and square root, no flush to zero) so that the
 kernels reproduce the arithmetic contract of ``include/fo.h`` bit for bit.
 Translation units compile in parallel; the result lands next to this file.
+Beside it comes ``_fo_torch.so``, a Python module in C++ (``csrc/fo_torch.cpp``)
+that makes the library's calls for PyTorch's tensors and their automatic
+differentiation; it is built against the installed PyTorch by the host compiler.
 """
 from __future__ import annotations
 
@@ -18,6 +21,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfo.so")
+TORCH_LIB = os.path.join(HERE, "_fo_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "fo_torch.cpp")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["fo_api.cu", "fo_step.cu", "fo_step_adamw.cu", "fo_step_adamw_dev.cu", "fo_step_sgd.cu",
            "fo_step_lion.cu", "fo_codecs.cu", "fo_verify.cu", "fo_loss_api.cu", "fo_logprobs.cu", "fo_distill.cu", "fo_policy.cu",
@@ -84,5 +89,70 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _torch_stamp() -> str:
+    """What the module was built against."""
+    import torch
+    return f"{torch.__version__} {os.path.dirname(torch.__file__)}"
+
+
+def torch_is_stale() -> bool:
+    stamp = os.path.join(BUILD_DIR, "torch_version")
+    if not os.path.exists(TORCH_LIB) or not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        if f.read() != _torch_stamp():
+            return True
+    t = os.path.getmtime(TORCH_LIB)
+    return any(os.path.getmtime(f) > t for f in (TORCH_SOURCE, os.path.join(INCLUDE, "fo.h"), __file__))
+
+
+def _compile_torch() -> str:
+    """Compile fo_torch.cpp; return the object."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    obj = os.path.join(BUILD_DIR, "fo_torch.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE]
+    for d in includes:
+        cmd += ["-isystem", d]
+    r = subprocess.run(cmd + ["-c", TORCH_SOURCE, "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fo_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", obj, "-o", tmp, "-L", HERE, "-l:libfo.so", "-Wl,-rpath,$ORIGIN", "-L", libs, f"-Wl,-rpath,{libs}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking _fo_torch.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    with open(os.path.join(BUILD_DIR, "torch_version"), "w") as f:
+        f.write(_torch_stamp())
+
+
+def build_torch() -> str:
+    """Build both, the module's compilation beside the library's; return the module's path."""
+    if not torch_is_stale():
+        build()
+        return TORCH_LIB
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        obj = ex.submit(_compile_torch)
+        build()
+        with _lock:
+            _link_torch(obj.result())
+    return TORCH_LIB
+
+
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
+    print(build_torch())

@@ -167,6 +167,30 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_torch_module = None
+
+
+def native():
+    """The module that makes the library's calls for PyTorch's tensors and their
+    automatic differentiation (csrc/fo_torch.cpp), built first if needed."""
+    global _torch_module
+    if _torch_module is None:
+        lib()
+        with _lock:
+            if _torch_module is None:
+                import importlib.util
+
+                import torch  # noqa: F401 - the module needs its libraries in the process
+                try:
+                    spec = importlib.util.spec_from_file_location(__package__ + "._fo_torch", _build.build_torch())
+                    module = importlib.util.module_from_spec(spec)
+                    spec.loader.exec_module(module)
+                except Exception as e:  # no silent fallback: the caller sees why
+                    raise RuntimeError(f"_fo_torch.so (the library's PyTorch module) is unavailable: {e}") from e
+                _torch_module = module
+    return _torch_module
+
+
 def _check(fn: str, status: int) -> None:
     if status != 0:
         msg = lib().fo_status_string(status).decode()

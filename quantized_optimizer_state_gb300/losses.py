@@ -268,69 +268,6 @@ class PolicyLossGrad(NamedTuple):
     grad: torch.Tensor       # of the logits
 
 
-def _policy(logits, tokens, old, advantages, ref, weight, how, with_stats, with_grad, out=None):
-    clip_low, clip_high, kl_weight, temperature = how
-    x = fo.logits_rows(logits, temperature)
-    dev, n = logits.device, x.rows
-    p = fo.policy(tokens, old, advantages, ref, n, clip_low, clip_high, kl_weight, dev.index)
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
-    logp = torch.empty_like(loss)
-    grad = to = stats = p_stats = None
-    if out is not None:
-        grad, to = out, fo._logits_grad(x, logits, out)
-    elif with_grad:
-        grad, to = _empty_grad(logits, x)
-    if with_stats:
-        stats = torch.empty((n, fo.FO_LOSS_STATS), dtype=torch.float32, device=dev)
-        p_stats = stats.data_ptr()
-    status = fo.lib().fo_policy_loss(ctypes.byref(x), ctypes.byref(p), fo._array(weight, "row_weight", torch.float32, n, dev.index),
-                                     loss.data_ptr(), logp.data_ptr(), p_stats, None if to is None else ctypes.byref(to),
-                                     fo._stream(None))
-    if status:
-        fo._check("fo_policy_loss", status)
-    if out is not None:
-        fo._modified(out)
-    return loss, logp, grad, stats
-
-
-class _Policy(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, tokens, old, advantages, ref, how):
-        loss, logp, _, stats = _policy(logits, tokens, old, advantages, ref, None, how, True, False)
-        ctx.save_for_backward(logits, tokens, stats)
-        ctx.temperature = how[3]
-        ctx.mark_non_differentiable(logp)
-        ctx.set_materialize_grads(False)
-        return loss, logp
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g_loss, _):
-        if g_loss is None:
-            return None, None, None, None, None, None
-        logits, tokens, stats = ctx.saved_tensors
-        with _on_device_of(logits):
-            x = fo.logits_rows(logits, ctx.temperature)
-            grad, to = _empty_grad(logits, x)
-            g_loss = g_loss.contiguous()
-            status = fo.lib().fo_policy_loss_grad(ctypes.byref(x), tokens.data_ptr(), stats.data_ptr(),
-                                                  fo._array(g_loss, "g_loss", torch.float32, x.rows, logits.device.index),
-                                                  ctypes.byref(to), fo._stream(None))
-            if status:
-                fo._check("fo_policy_loss_grad", status)
-        return grad, None, None, None, None, None
-
-
-def _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight):
-    _check_tangent(logits)
-    rows = logits.shape[:-1]
-    for name, x in (("tokens", tokens), ("old_logp", old_logp), ("advantages", advantages), ("ref_logp", ref_logp)):
-        _check_rows(name, x, rows)
-    if kl_weight and ref_logp is None:
-        raise ValueError("kl_weight needs ref_logp")
-    return tokens.contiguous(), old_logp.contiguous(), advantages.contiguous(), _dense(ref_logp if kl_weight else None)
-
-
 def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
                 clip_low: float = 0.2, clip_high: float = 0.2, ref_logp: Optional[torch.Tensor] = None,
                 kl_weight: float = 0.0, temperature: float = 1.0) -> PolicyLoss:
@@ -345,11 +282,10 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tens
     and ``ref_logp``: float32 of that shape, constants of the gradient. The loss is
     differentiable in ``logits``.
     """
-    tokens, old, advantages, ref = _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight)
-    how = (clip_low, clip_high, kl_weight, temperature)
-    if logits.requires_grad and torch.is_grad_enabled():
-        return PolicyLoss(*_Policy.apply(logits, tokens, old, advantages, ref, how))
-    return PolicyLoss(*_policy(logits, tokens, old, advantages, ref, None, how, False, False)[:2])
+    _check_tangent(logits)
+    if kl_weight and ref_logp is None:
+        raise ValueError("kl_weight needs ref_logp")
+    return PolicyLoss(*fo.native().policy_loss(logits, tokens, old_logp, advantages, ref_logp, clip_low, clip_high, kl_weight, temperature))
 
 
 def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
@@ -364,7 +300,8 @@ def policy_loss_grad(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch
     for padding, whose logits are not read. ``out``: where to write the gradient;
     it may be ``logits`` itself, which the gradient then replaces.
     """
-    tokens, old, advantages, ref = _check_policy(logits, tokens, old_logp, advantages, ref_logp, kl_weight)
-    _check_rows("row_weight", row_weight, logits.shape[:-1])
-    how = (clip_low, clip_high, kl_weight, temperature)
-    return PolicyLossGrad(*_policy(logits, tokens, old, advantages, ref, _dense(row_weight), how, False, True, out)[:3])
+    _check_tangent(logits)
+    if kl_weight and ref_logp is None:
+        raise ValueError("kl_weight needs ref_logp")
+    return PolicyLossGrad(*fo.native().policy_loss_grad(logits, tokens, old_logp, advantages, ref_logp, clip_low, clip_high, kl_weight,
+                                                        temperature, row_weight, out))

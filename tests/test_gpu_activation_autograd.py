@@ -276,6 +276,16 @@ def test_what_stands_around(n, w, cut, dtype):
     del kept
 
 
+def test_one_library_in_the_process():
+    """The PyTorch module and the ctypes binding call the same library: one counts the other's launches."""
+    x, before = make((4, 64), F32), fo.fo_kernel_launch_count()
+    c = A.compress(x)
+    assert fo.fo_kernel_launch_count() == before + 1
+    fo.fo_expand(c.codes, c.steps, x)
+    A.rms_norm_backward(A.rms_norm_forward(x, torch.ones(64, device="cuda"))[1], x)
+    assert fo.fo_kernel_launch_count() == before + 5
+
+
 def test_outputs_count_as_modified():
     x = make((4, 64), F32).requires_grad_(True)
     out = torch.empty(4, 64, device="cuda")
