@@ -1,5 +1,14 @@
 // fo_activation.cu -- activation functions, plain and gated, whose input is kept
 // as 8-bit codes for the backward pass.
+//   y = f(x) [u], dx = dy f'(x^) [u^], du = dy f(x^)
+//
+// One pass each way, codes made of the registers that hold the input. A pair of
+// gate and other half in BF16 is 8.125 bytes forward and as many backward, 26 and
+// 28 instructions an element (29 and 32 for gelu) of the 44 that the copy rate
+// leaves room for: bound by device memory, 8192 x 14336 BF16 swiglu 143 and 153 us
+// (0.98 and 0.92 of the measured copy rate), FP32 0.99 of it over both. In rows of
+// no alignment instructions bound it: 3001 x 2731 FP16 geglu 39 an element forward,
+// 18.8 us and 17.4 backward where the bytes alone take 9.8.
 #include "fo_act.cuh"
 
 namespace fo {

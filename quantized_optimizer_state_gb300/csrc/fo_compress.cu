@@ -1,11 +1,18 @@
 // fo_compress.cu -- activations to 8-bit codes and back.
+//
+// One pass: a group's largest magnitude in registers and one or two shuffles, its
+// codes at once. 2 + 1 + 1/16 bytes an element of BF16 either way, some 7
+// instructions, so device memory bounds it: 32768 x 14336 BF16 204 us to codes and
+// 203 back, 1.03 of the measured copy rate (the last codes written are still in
+// the L2 cache). In rows of no alignment the shifting adds about as many
+// instructions again: 8191 x 14337 BF16 60 and 65 us, 0.84.
 #include "fo_act.cuh"
 
 namespace fo {
 namespace {
 
 constexpr int kThreads = 256;
-// units of a thread, all loaded before the first is used
+// Units of a thread, all loaded before the first is used: 64 bytes of BF16.
 template <bool kWide>
 constexpr int kUnits = kWide ? 4 : 2;
 

@@ -2,6 +2,17 @@
 // backward pass.
 //   r = 1 / sqrt(mean x^2 + eps), y = x r w
 //   h = x^ r: dx = r (dy w - h mean(dy w h)), dw = sum over rows of dy h
+//
+// A row stays in registers between its sum and its result, so that every byte
+// crosses device memory once: 5.0625 bytes an element of BF16 either way. The
+// codes need no sum and come before it is waited for; the weight's gradient is
+// summed in registers over the rows that a team takes, and a second, small launch
+// adds up what the CTAs left (3 us). 16384 x 4096 BF16: 57 and 57 us, 0.88 of the
+// measured copy rate, 16 and 20 instructions an element; FP32 99 and 97, 0.91.
+// What is missing are the waits of a CTA for a row's sum: rows two ahead instead of
+// one change nothing (60 and 65 us then). Rows of 128 take 17 and 15 us for 131072, where
+// the bytes alone take 12.6. Rows of no alignment are bound by instructions and
+// occupancy: 8191 x 4099 BF16 50 and 65 us where the bytes take 25 each.
 #include <algorithm>
 
 #include "fo_act.cuh"
@@ -319,7 +330,8 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
     }
 }
 
-// The parts of 32 columns by a CTA: 32 chains a column, joined pairwise.
+// The parts of 32 columns by a CTA: 32 chains a column, joined pairwise. 608 parts
+// of 4096 columns 2.8 us (by 256 threads a CTA 8.5).
 constexpr int kJoin = 32;
 __global__ void __launch_bounds__(kJoin * 32) norm_weight_kernel(NormGradArgs a, int parts)
 {
@@ -337,7 +349,7 @@ __global__ void __launch_bounds__(kJoin * 32) norm_weight_kernel(NormGradArgs a,
         store_weight(a.grad_weight, a.weight_dtype, (int64_t)blockIdx.x * 32 + warp, sum);
 }
 
-// --- longer rows: read again from the L2 cache -----------------------------------------------
+// --- rows beyond kMaxWidth: an element a thread, read again from the L2 cache -----------------------------------------------
 
 // Element `c` of row `r`.
 template <class T>

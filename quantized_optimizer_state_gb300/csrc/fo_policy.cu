@@ -8,6 +8,10 @@
 namespace fo {
 namespace {
 
+// policy_kernel's shape is distill_kernel's, whose two passes it makes; the
+// measurements behind it stand there (fo_distill.cu). Clusters only where the cache
+// or few rows ask for them: loss alone, 1001 x 50257 FP32 by one CTA a row 40 us,
+// by two 51, by four 58.
 constexpr int kLong = 8, kShort = 2;              // warps that walk over a row: see launch
 constexpr int kStages = 4;                        // copies of four vectors a thread, in flight or in use
 constexpr int kCtasPerSm = 3, kShortPerSm = 8;    // of kLong and of kShort warps
@@ -108,7 +112,11 @@ struct Shared {
 // In each CTA a warp keeps bulk copies in flight into a ring of stages, running
 // ahead over the passes and rows; kWarps warps take the stages, sum, and write
 // the gradient; a warp joins the sums, forms the loss, and writes it and, last,
-// the token's own gradient.
+// the token's own gradient. 8192 x 128256 BF16, loss with gradient: 663 us, 0.90 of
+// the measured copy rate for one read and one write (1067 by a CTA a row without
+// the ring, with the row's two passes from its own loads); 8192 x 50257 261 us,
+// 0.93; loss alone, 4096 x 128256, 167 us, 0.93. Device memory gives 1.02 times
+// the logits.
 template <class T, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == kLong ? kCtasPerSm : kShortPerSm) policy_kernel(PolicyArgs a)
 {
