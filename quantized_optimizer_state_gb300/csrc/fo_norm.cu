@@ -523,7 +523,9 @@ int by_size(const NormArgs &a, cudaStream_t stream)
 // The gradient: a warp with two units a thread where they hold the row, one unit a
 // thread of more warps beyond (65536 x 512 FP32 49 us, by 64 threads 61; 65536 x
 // 768 BF16 by 64 threads 59, by 128 56; 16384 x 4096 BF16 64.6 and 63.6; 4096 x
-// 16384 BF16 by 512 threads of four units 125, by 1024 of two 96).
+// 16384 BF16 by 512 threads of four units 125, by 1024 of two 96). Two CTAs of 544
+// or 576 threads fit an SM at 56 registers; up to 512 threads have 64, without which
+// 16384 x 4096 takes 65 us instead of 57.
 template <class T, bool kWide>
 int by_size(const NormGradArgs &a, cudaStream_t stream)
 {
@@ -535,7 +537,7 @@ int by_size(const NormGradArgs &a, cudaStream_t stream)
     if constexpr (!kWide) {
         if (block <= 576)
             return run<T, kWide, 0, 1, 576, 1>(a, block, stream);
-    } else if (sizeof(typename T::raw) == 4 && block <= 512)
+    } else if (block <= 512)
         return run<T, kWide, 0, 1, 512, 2>(a, block, stream);
     else if (block <= 576)
         return run<T, kWide, 0, 1, 576, 2>(a, block, stream);
