@@ -447,9 +447,9 @@ typedef struct fo_policy {
     const int64_t *tokens;      /* [rows]                                   */
     const float *old_logp;      /* [rows]: of the policy that sampled       */
     const float *advantages;    /* [rows]                                   */
-    const float *ref_logp;      /* [rows], of a reference; NULL: no KL term */
-    double clip_low, clip_high; /* in [0, 1]; finite, not negative          */
-    double kl_weight;           /* finite, not negative                     */
+    const float *ref_logp;      /* [rows], of a reference; may be NULL where kl_weight is 0 */
+    double clip_low, clip_high; /* in [0, 1]; in [0, 2^100]                 */
+    double kl_weight;           /* in [0, 2^100]                            */
 } fo_policy_t;
 
 /*
@@ -487,12 +487,15 @@ fo_status_t fo_policy_loss_grad(const fo_logits_t *logits, const int64_t *tokens
  *
  * Matrices are rows of contiguous elements of BF16, FP16 or FP32 (fo_rows_t), all
  * of one call of one type, aligned to it. Rows that are only read may overlap;
- * rows that are written may not, and share no byte with another array. For a
+ * rows that are written may not, and what is written shares no byte with another
+ * array: from a matrix's first byte to its last, whatever lies between its rows (but
+ * grad_x and grad_up below may be side by side in the rows of one matrix). For a
  * matrix of `width` columns and G = ceil(width / 32), codes is [rows, 32 G] (0
- * beyond the width, beside a step that is a number), aligned to 16 bytes, and steps [rows, G]. All arithmetic is
+ * beyond the width, beside a step that is a number), aligned to 16 bytes, and
+ * steps [rows, G]. No byte beside the rows is read or written. All arithmetic is
  * FP32, results are rounded once, to the matrices' type. Every result is the
  * same bit for bit on every run of the same call on the same kind of device.
- * Rows beside others have no effect on them.
+ * What one row holds has no effect on another's results (grad_weight sums them all).
  */
 typedef struct fo_rows {
     void *data;             /* only read where the call names the matrix in, up or grad_y */
@@ -543,9 +546,10 @@ fo_status_t fo_activation_grad(fo_act_t kind, const int8_t *codes, const uint16_
  * or an infinity gives NaN.
  * fo_rms_norm_grad -- from the codes, with h = x^ r (r as it was):
  *   grad_x = r (grad_y w - h mean(grad_y w h)),  grad_weight = sum over rows of grad_y h.
- * grad_x or grad_weight may be NULL. workspace: FP32, fo_rms_norm_workspace(rows,
- * width) elements (NULL without grad_weight); its contents are of no use after
- * the call. With rows = 0, grad_weight is 0.
+ * grad_x or grad_weight may be NULL. workspace: FP32, aligned to 16 bytes,
+ * fo_rms_norm_workspace(rows, width) elements (NULL without grad_weight); its
+ * contents are of no use after the call. Calls that may run at the same time need
+ * one each. With rows = 0, grad_weight is 0.
  */
 fo_status_t fo_rms_norm(const fo_rows_t *in, const void *weight, int32_t weight_dtype, double eps, const fo_rows_t *y,
                         float *inv_rms, int8_t *codes, uint16_t *steps, fo_stream_t stream);
