@@ -5,10 +5,11 @@
 // One pass each way, codes made of the registers that hold the input. A pair of
 // gate and other half in BF16 is 8.125 bytes forward and as many backward, 26 and
 // 28 instructions an element (29 and 32 for gelu) of the 44 that the copy rate
-// leaves room for: bound by device memory, 8192 x 14336 BF16 swiglu 143 and 153 us
-// (0.98 and 0.92 of the measured copy rate), FP32 0.99 of it over both. In rows of
-// no alignment instructions bound it: 3001 x 2731 FP16 geglu 39 an element forward,
-// 18.8 us and 17.4 backward where the bytes alone take 9.8.
+// leaves room for: bound by device memory, 8192 x 14336 BF16 swiglu 142 and 148 us
+// (0.99 and 0.95 of the measured copy rate), FP32 1.02 of it over both (the last
+// codes are still in the L2 cache). In rows of no alignment instructions bound it:
+// 3001 x 2731 FP16 geglu 39 an element forward, 19.1 us and 16.9 backward where the
+// bytes alone take 9.8.
 #include "fo_act.cuh"
 
 namespace fo {
@@ -95,8 +96,8 @@ __global__ void __launch_bounds__((kThreads<kWide, true>)) activation_grad_kerne
 }
 
 // Units of a thread, all loaded before the first is used: 64 bytes of BF16 input
-// on their way (silu of 8192 x 14336 BF16, forward and backward: two units 206 us,
-// four 190), 32 where a unit has 16 elements and registers are short.
+// on their way (silu of 8192 x 14336 BF16, forward and backward, by CTAs of 256: two
+// units 206 us, four 190), 32 where a unit has 16 elements and registers are short.
 template <bool kGated, bool kWide>
 constexpr int kUnits = kWide ? (kGated ? 2 : 4) : 1;
 

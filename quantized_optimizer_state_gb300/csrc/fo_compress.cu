@@ -3,9 +3,9 @@
 // One pass: a group's largest magnitude in registers and one or two shuffles, its
 // codes at once. 2 + 1 + 1/16 bytes an element of BF16 either way, some 7
 // instructions, so device memory bounds it: 32768 x 14336 BF16 204 us to codes and
-// 203 back, 1.03 of the measured copy rate (the last codes written are still in
+// 205 back, 1.03 of the measured copy rate (the last codes written are still in
 // the L2 cache). In rows of no alignment the shifting adds about as many
-// instructions again: 8191 x 14337 BF16 60 and 65 us, 0.84.
+// instructions again: 8191 x 14337 BF16 57 and 65 us, 0.87.
 #include "fo_act.cuh"
 
 namespace fo {

@@ -7,10 +7,10 @@
 // crosses device memory once: 5.0625 bytes an element of BF16 either way. The
 // codes need no sum and come before it is waited for; the weight's gradient is
 // summed in registers over the rows that a team takes, and a second, small launch
-// adds up what the CTAs left (3 us). 16384 x 4096 BF16: 57 and 57 us, 0.88 of the
-// measured copy rate, 16 and 20 instructions an element; FP32 99 and 97, 0.91.
+// adds up what the CTAs left (3 us). 16384 x 4096 BF16: 56 and 56 us, 0.89 of the
+// measured copy rate, 16 and 20 instructions an element; FP32 98 and 105, 0.88.
 // What is missing are the waits of a CTA for a row's sum: rows two ahead instead of
-// one change nothing (60 and 65 us then). Rows of 128 take 17 and 15 us for 131072, where
+// one changed nothing. Rows of 128 take 16 and 15 us for 131072, where
 // the bytes alone take 12.6. Rows of no alignment are bound by instructions and
 // occupancy: 8191 x 4099 BF16 50 and 65 us where the bytes take 25 each.
 #include <algorithm>
