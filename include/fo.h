@@ -518,7 +518,7 @@ typedef enum fo_act {
 /*
  * fo_compress -- codes and steps of x. fo_expand -- x^, rounded to x's type,
  * into x. Errors of every call of this section: FO_ERR_NULL, FO_ERR_MISALIGNED,
- * FO_ERR_SIZE (rows < 0, width < 1, too many groups), FO_ERR_BAD_ARG (dtype,
+ * FO_ERR_SIZE (rows < 0, width < 1, too many groups, a span beyond 2^58 elements), FO_ERR_BAD_ARG (dtype,
  * stride, reserved, matrices of unlike sizes or types, eps), FO_ERR_ALIAS,
  * FO_ERR_CUDA. rows = 0 is a no-op.
  */

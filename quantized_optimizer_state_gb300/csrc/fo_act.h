@@ -79,11 +79,13 @@ struct NormGradArgs {
     bool weight_aligned;
 };
 
-// Rows of partial sums that the norm's gradient leaves at most: 1024, and more of
-// short rows, whose CTAs are small (up to 16 MB).
+// Rows of partial sums that the norm's gradient leaves at most: as many as CTAs fit
+// the device for rows held in registers (1024, and more of short rows, whose CTAs
+// are small), fewer of longer rows, whose columns fill the device by themselves.
 inline int64_t norm_parts(int64_t rows, int64_t groups)
 {
-    const int64_t most = groups < 4096 ? ((int64_t)1 << 17) / groups : 32, parts = most < 1024 ? 1024 : most;
+    const int64_t least = groups <= 512 ? 1024 : 64, most = ((int64_t)1 << (groups <= 512 ? 17 : 19)) / groups;
+    const int64_t parts = most < least ? least : most;
     return rows < parts ? rows : parts;
 }
 

@@ -30,6 +30,8 @@ fo_status_t check_rows(const fo_rows_t *x, bool written, const fo_rows_t *like =
         return FO_ERR_BAD_ARG;
     if (x->rows == 0)
         return FO_OK;
+    if ((double)x->rows * (double)x->row_stride > 0x1p58)   // offsets in bytes stay far inside 63 bits
+        return FO_ERR_SIZE;
     if (written && x->rows > 1 && x->row_stride < x->width)
         return FO_ERR_BAD_ARG;
     if (!x->data)

@@ -448,15 +448,15 @@ __global__ void __launch_bounds__(kThreads) norm_long_grad_kernel(NormGradArgs a
 template <class T>
 __global__ void __launch_bounds__(kThreads) norm_long_weight_kernel(NormGradArgs a)
 {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (c >= a.groups * kGroup)
         return;
     float sum = 0.0f;
-    for (int64_t r = blockIdx.x; c < a.width && r < a.rows; r += gridDim.x) {
+    for (int64_t r = blockIdx.y; c < a.width && r < a.rows; r += gridDim.y) {
         const float h = __fmul_rn(kept_at(a.kept, r * a.groups + c / kGroup, (int)(c % kGroup)), a.inv_rms[r]);
         sum = __fmaf_rn(load_at<T>(a.grad_y, r, c), h, sum);
     }
-    a.parts[blockIdx.x * a.groups * kGroup + c] = sum;
+    a.parts[blockIdx.y * a.groups * kGroup + c] = sum;
 }
 
 
@@ -577,7 +577,7 @@ cudaError_t launch(NormGradArgs a, cudaStream_t stream)
         }
         if (a.grad_weight) {
             parts = (int)norm_parts(a.rows, a.groups);
-            norm_long_weight_kernel<T><<<dim3((unsigned)parts, (unsigned)((a.groups * kGroup + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
+            norm_long_weight_kernel<T><<<dim3((unsigned)((a.groups * kGroup + kThreads - 1) / kThreads), (unsigned)parts), kThreads, 0, stream>>>(a);
             count_launch();
         }
     }

@@ -72,6 +72,7 @@ def test_matrices_are_checked_by_every_call(call):
     assert call(rows(dtype=3)) == BAD and call(rows(reserved=1)) == BAD
     assert call(rows(row_stride=-1)) == BAD and call(rows(row_stride=1 << 50)) == BAD
     assert call(rows(data=64 * MB + 1)) in (MISALIGNED, BAD)
+    assert call(rows(rows=1 << 27, width=100, row_stride=1 << 40)) in (SIZE, BAD)   # offsets beyond 63 bits; unlike y
 
 
 def test_empty_matrices_are_no_ops():
@@ -129,7 +130,8 @@ def test_norm_arguments():
     assert norm_grad(dy, dx, wtype=7) == BAD and norm_grad(dy, rows(128 * MB, width=99)) == BAD
     assert norm_grad(dy, None, gw=None) == 0                        # nothing asked for
     assert fo.fo_rms_norm_workspace(10, 64) == 640 and fo.fo_rms_norm_workspace(10, 65) == 960
-    assert fo.fo_rms_norm_workspace(10 ** 6, 64) == 1 << 22 and fo.fo_rms_norm_workspace(10 ** 6, 1 << 20) == 1 << 30
+    assert fo.fo_rms_norm_workspace(10 ** 6, 64) == 1 << 22 and fo.fo_rms_norm_workspace(10 ** 6, 1 << 20) == 1 << 26
+    assert fo.fo_rms_norm_workspace(10 ** 4, 16384) == 1 << 24 and fo.fo_rms_norm_workspace(10 ** 4, 32768) == 1 << 24
     assert fo.fo_rms_norm_workspace(0, 64) == 0
 
 

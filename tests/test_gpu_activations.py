@@ -326,6 +326,25 @@ def test_norm_of_no_rows():
     assert grad.shape == (0, 64) and torch.equal(gw, torch.zeros_like(weight))
 
 
+def test_norm_of_the_longest_rows():
+    """More columns than a grid has places in its second dimension times a CTA's threads."""
+    w = 20_000_011
+    x, dy = torch.zeros(2, w, dtype=BF, device="cuda"), torch.zeros(2, w, dtype=BF, device="cuda")
+    at = torch.tensor([0, 1, 16_777_215, 16_777_217, w - 1], device="cuda")
+    x[:, at] = make((2, 5), BF) + 3
+    dy[:, at] = make((2, 5), BF, seed=1)
+    weight = torch.ones(w, dtype=BF, device="cuda")
+    y, kept = A.rms_norm_forward(x, weight)
+    grad, gw = A.rms_norm_backward(kept, dy)
+    r = ref.inverse_rms(x, 1e-6)
+    ref.close(y[:, at], (x.double() * r)[:, at], 1e-5, "norm")
+    h = (ref.kept(x) * r)[:, at]
+    ref.close(gw[at], (dy[:, at].double() * h).sum(0), 1e-4 * (dy[:, at].double() * h).abs().sum(0), "weight's gradient")
+    assert int((gw != 0).sum()) == 5
+    mean = (dy[:, at].double() * h).sum(1, keepdim=True) / w
+    ref.close(grad[:, at], r * (dy[:, at].double() - h * mean), 1e-4 * r, "gradient")
+
+
 def test_norm_of_many_rows():
     n, w = 300000, 40
     x, weight = make((n, w), BF), torch.ones(w, device="cuda")
