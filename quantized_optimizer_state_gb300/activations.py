@@ -10,7 +10,8 @@ kernels: beside the optimizer state, what a training step holds in memory.
 The last three are differentiable. Their results are those of the input itself;
 what they keep of it for the backward pass are its codes (1.0625 bytes an element
 where bfloat16 takes 2), and the gradient is the formula's at the numbers that
-the codes stand for, within half a step (1/254 of a group's largest) of the input.
+the codes stand for, within half a step (at most 1/252 of a group's largest) of the
+input.
 Training loops that run the backward pass themselves have the calls in pairs:
 :func:`activation_forward` and :func:`activation_backward`, :func:`rms_norm_forward`
 and :func:`rms_norm_backward`.
@@ -18,8 +19,11 @@ and :func:`rms_norm_backward`.
 Tensors are bfloat16, float16 or float32 on the current CUDA device, ``[..., width]``
 with a contiguous last dimension and the rows one stride apart: ``x[:, :k]`` is
 read where it lies. The code, and the rules for infinities and NaN, stand in
-``include/fo.h``. Work is enqueued on the current stream. Derivatives are of the
-first order and in reverse mode; a tangent of forward mode is refused.
+``include/fo.h``. Work is enqueued on the current stream; calls can be captured in
+CUDA graphs, their temporaries are the graph's own (a backward pass by
+``torch.autograd.grad``, or with no eager graph of the same leaves alive, as PyTorch
+asks of every captured one). Derivatives are of the first order and in reverse mode;
+a tangent of forward mode is refused.
 """
 from __future__ import annotations
 
