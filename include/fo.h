@@ -483,7 +483,10 @@ fo_status_t fo_policy_loss_grad(const fo_logits_t *logits, const int64_t *tokens
  *          not rounded before
  *   x^   = code * step, exact in FP32
  * so |x^ - x| is at most (1 + 2^-15) step / 2. A NaN or an infinity in a group
- * makes its step NaN, and with it all that the group stands for.
+ * makes its step NaN, and with it all that the group stands for. As the step is
+ * rounded up, x^ of a number near the largest of a 16-bit type may lie beyond that:
+ * fo_expand gives the largest number then, and infinity only for an x^ more than a
+ * step beyond, which stands for no number of the type.
  *
  * Matrices are rows of contiguous elements of BF16, FP16 or FP32 (fo_rows_t), all
  * of one call of one type, aligned to it. Rows that are only read may overlap;
@@ -516,8 +519,9 @@ typedef enum fo_act {
 } fo_act_t;
 
 /*
- * fo_compress -- codes and steps of x. fo_expand -- x^, rounded to x's type,
- * into x. Errors of every call of this section: FO_ERR_NULL, FO_ERR_MISALIGNED,
+ * fo_compress -- codes and steps of x. fo_expand -- x^, rounded to x's type (that
+ * of the compressed matrix or another), into x.
+ * Errors of every call of this section: FO_ERR_NULL, FO_ERR_MISALIGNED,
  * FO_ERR_SIZE (rows < 0, width < 1, too many groups, a span beyond 2^58 elements), FO_ERR_BAD_ARG (dtype,
  * stride, reserved, matrices of unlike sizes or types, eps), FO_ERR_ALIAS,
  * FO_ERR_CUDA. rows = 0 is a no-op.

@@ -10,8 +10,8 @@ kernels: beside the optimizer state, what a training step holds in memory.
 The last three are differentiable. Their results are those of the input itself;
 what they keep of it for the backward pass are its codes (1.0625 bytes an element
 where bfloat16 takes 2), and the gradient is the formula's at the numbers that
-the codes stand for, within half a step (at most 1/252 of a group's largest) of the
-input.
+the codes stand for, within half a step (at most 1/252 of a group's largest, or
+2^-127) of the input.
 Training loops that run the backward pass themselves have the calls in pairs:
 :func:`activation_forward` and :func:`activation_backward`, :func:`rms_norm_forward`
 and :func:`rms_norm_backward`.
@@ -106,7 +106,9 @@ def compress(x: torch.Tensor) -> Compressed:
 
 def expand(kept: Compressed, *, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The tensor that the codes stand for, rounded once to ``dtype`` (that of the
-    compressed tensor where None). ``out``: where to write it."""
+    compressed tensor where None, in which numbers come back as numbers: next to the
+    type's largest a code may stand for more, and gives the largest). ``out``: where to
+    write it."""
     codes, steps, width, own = kept
     if out is not None and dtype is not None and out.dtype != dtype:
         raise ValueError(f"out must be {dtype}, not {out.dtype}")

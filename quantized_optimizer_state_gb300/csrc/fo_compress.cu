@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs a, UnitGrid
     for (int i = 0; i < N; ++i) {
         f2 x[W / 2];
         kept_unit<W>(k[i], x);
+        if constexpr (sizeof(typename T::raw) == 2)
+            last_number<T, W>(k[i], x);
         store_unit<T, kWide>(a.x, place<W>(first + i * kThreads, g.units, g.per_row, (int)a.width), narrow_unit<T, W>(x));
     }
 }
