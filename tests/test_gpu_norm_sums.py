@@ -1,0 +1,64 @@
+"""Sums of the norm: long rows of numbers of one sign, whose roundings add up.
+
+u = 2^-24. A sum of n positive terms added one by one is off by up to n u, and for like terms by a good part of it:
+they are all rounded the same way. Sums of parts that keep what their roundings lost are off by a few u, whatever n."""
+import pytest
+import torch
+
+from quantized_optimizer_state_gb300 import activations as A
+from quantized_optimizer_state_gb300 import fo
+from tests import act_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+u = 2.0 ** -24
+
+# 1 / rms: the squares' sum of long rows 2 u (of a thread) and 8 additions of threads and warps, the mean's product u, halved
+# by the root, and the root's own 2 u: below 8 u. A row in registers: up to 16 squares a lane pair one after another, 5
+# additions of lanes, 9 of warps, the mean: (16 + 14 + 1) / 2 + 2 below 18 u.
+SUM = {True: 8 * u, False: 18 * u}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    fo.lib()
+
+
+def rows(n, w, spread, seed=0):
+    """Positive numbers of one size."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (1.37 * (1 + spread * torch.rand((n, w), generator=g, device="cuda"))).contiguous()
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.01, 1.0])
+@pytest.mark.parametrize("n,w", [(2, 4096), (1, 16384), (3, 16385), (2, 131072), (2, 1 << 20), (1, 20_000_011)])
+def test_long_rows_of_one_sign(n, w, spread):
+    x = rows(n, w, spread)
+    y, kept = A.rms_norm_forward(x, eps=1e-6)
+    r = ref.inverse_rms(x, 1e-6)
+    err = SUM[w > 16384]
+    assert ((kept.inv_rms.double()[:, None] / r - 1).abs() <= err).all()
+    want = x.double() * r
+    assert ((y.double() - want).abs() <= want * (err + 2 * u)).all()
+    # the gradient's mean: dy of one sign, r as the call saw it
+    dy = rows(n, w, spread, seed=1)
+    grad, _ = A.rms_norm_backward(kept, dy)
+    r = kept.inv_rms.double()[:, None]
+    h = ref.kept(x) * r
+    mean = (dy.double() * h).mean(1, keepdim=True)
+    want = r * (dy.double() - h * mean)
+    # h's u, the products' and the sum's as above, twice (no root halves it), and the last three roundings
+    assert ((grad.double() - want).abs() <= r * (h * mean * (2 * err + 4 * u) + dy.double() * 4 * u)).all()
+
+
+@pytest.mark.parametrize("n,w", [(300, 16385), (3, 20000)])
+def test_infinities_of_long_rows(n, w):
+    """They go through the sums as infinities, not as NaN."""
+    x, dy = rows(n, w, 1.0), rows(n, w, 1.0, seed=1)
+    dy[1, 5] = float("inf")
+    _, kept = A.rms_norm_forward(x, torch.ones(w, device="cuda"))
+    grad, gw = A.rms_norm_backward(kept, dy)
+    assert torch.isinf(gw[5]) and torch.isfinite(gw[:5]).all() and torch.isfinite(gw[6:]).all()
+    assert torch.isnan(grad[1, 5]) and (grad[1, :5] == -float("inf")).all() and torch.isfinite(grad[0]).all()
