@@ -478,7 +478,8 @@ __device__ __forceinline__ void keep_unit(const KeptOut &k, uint32_t unit, uint3
 
 // A unit's codes and step as loaded, and the values x^ they stand for. A code
 // becomes the low byte of 2^23 + 128 + code, from which FP32 takes the rest away.
-// `factor` is multiplied into the step first.
+// `factor` is multiplied into the step first, or (kOnce) x^ by it, which rounds once
+// and takes an instruction a pair more.
 template <int W>
 struct Kept {
     typename CodeVec<W>::type codes;
@@ -494,10 +495,10 @@ __device__ __forceinline__ Kept<W> load_kept(const KeptIn &k, uint32_t unit, uin
     }
     return v;
 }
-template <int W>
+template <int W, bool kOnce = false>
 __device__ __forceinline__ void kept_unit(const Kept<W> &v, f2 (&x)[W / 2], float factor = 1.0f)
 {
-    const f2 base = splat(-(8388608.0f + 128.0f)), step = splat(__fmul_rn(step_value(v.step), factor));
+    const f2 base = splat(-(8388608.0f + 128.0f)), step = splat(kOnce ? step_value(v.step) : __fmul_rn(step_value(v.step), factor));
     uint32_t words[W / 4] = {v.codes.x, v.codes.y};
     if constexpr (W == 16) {
         words[2] = v.codes.z;
@@ -509,6 +510,8 @@ __device__ __forceinline__ void kept_unit(const Kept<W> &v, f2 (&x)[W / 2], floa
         const f2 n = pk(__uint_as_float(__byte_perm(w, 0x4b000000u, i % 2 ? 0x7442 : 0x7440)),
                         __uint_as_float(__byte_perm(w, 0x4b000000u, i % 2 ? 0x7443 : 0x7441)));
         x[i] = mul2(add2(n, base), step);
+        if (kOnce)
+            x[i] = mul2(x[i], splat(factor));
     }
 }
 

@@ -8,7 +8,7 @@
 // codes need no sum and come before it is waited for; the weight's gradient is
 // summed in registers over the rows that a team takes, and a second, small launch
 // adds up what the CTAs left (3 us). 16384 x 4096 BF16: 56 and 56 us, 0.89 of the
-// measured copy rate, 16 and 20 instructions an element; FP32 98 and 105, 0.88.
+// measured copy rate, 16 and 20 instructions an element; FP32 98 and 91, 0.95.
 // What is missing are the waits of a CTA for a row's sum: rows two ahead instead of
 // one changed nothing. Rows of 128 take 16 and 15 us for 131072, where
 // the bytes alone take 12.6. Rows of no alignment are bound by instructions and
@@ -238,6 +238,10 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
 {
     typedef typename T::raw raw;
     constexpr int W = kUnitOf<kWide>, kTeams = kLanes ? kBlock / (kLanes ? kLanes : 1) : 1, kWarps = kBlock / 32;
+    // h = x^ r with one rounding in FP32 (16384 x 4096 91 us, with two 103: a register less);
+    // in 16-bit types with two, of which neither reaches the results' own (4096 x 16384
+    // 115 us, with one 117).
+    constexpr bool kOnce = kExactType<T>;
     __shared__ __align__(16) float part[2][32];
     for (int i = threadIdx.x; kLanes == 0 && i < 2 * 32; i += blockDim.x)
         part[i / 32][i % 32] = 0.0f;
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             widen_unit<T, W>(next[k], t[k]);
-            kept_unit<W>(next_x[k], h[k], next_inv);
+            kept_unit<W, kOnce>(next_x[k], h[k], next_inv);
 #pragma unroll
             for (int j = 0; j < W / 2; ++j) {
                 dw[k][j] = fma2(t[k][j], h[k][j], dw[k][j]);

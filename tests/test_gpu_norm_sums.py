@@ -53,8 +53,8 @@ def test_long_rows_of_one_sign(n, w, spread):
     assert ((grad.double() - want).abs() <= r * (h * mean * (2 * err + 4 * u) + dy.double() * 4 * u)).all()
 
 
-@pytest.mark.parametrize("n,w", [(300, 16385), (3, 20000)])
-def test_infinities_of_long_rows(n, w):
+@pytest.mark.parametrize("n,w", [(300, 16385), (3, 20000), (300, 768), (4000, 128)])
+def test_infinities_in_sums(n, w):
     """They go through the sums as infinities, not as NaN."""
     x, dy = rows(n, w, 1.0), rows(n, w, 1.0, seed=1)
     dy[1, 5] = float("inf")
@@ -62,3 +62,13 @@ def test_infinities_of_long_rows(n, w):
     grad, gw = A.rms_norm_backward(kept, dy)
     assert torch.isinf(gw[5]) and torch.isfinite(gw[:5]).all() and torch.isfinite(gw[6:]).all()
     assert torch.isnan(grad[1, 5]) and (grad[1, :5] == -float("inf")).all() and torch.isfinite(grad[0]).all()
+
+
+@pytest.mark.parametrize("w", [64, 768, 5003, 20000])
+def test_normed_codes_are_rounded_once(w):
+    """FP32: with one row and dy = 1 the weight's gradient is h = x^ r itself."""
+    g = torch.Generator(device="cuda").manual_seed(w)
+    x = torch.randn((1, w), generator=g, device="cuda")
+    _, kept = A.rms_norm_forward(x, torch.ones(w, device="cuda"))
+    _, h = A.rms_norm_backward(kept, torch.ones_like(x))
+    assert torch.equal(h, (ref.kept(x) * kept.inv_rms.double()[:, None]).float()[0])
