@@ -22,6 +22,37 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
+// --- sums ------------------------------------------------------------------------------
+
+// A sum of products that keeps what its roundings lose (W. Kahan, "Further remarks on
+// reducing truncation errors", CACM 8(1), 1965): off by 2 roundings, whatever the
+// number of terms. One after another like terms are all rounded the same way:
+// 20 million equal squares, 78000 a thread, came out 9e-4 off.
+struct LongSum {
+    float sum = 0.0f, over = 0.0f;   // `over`: what is in the sum too much
+    __device__ __forceinline__ void add(float a, float b = 1.0f)
+    {
+        const float y = __fmaf_rn(a, b, -over), t = __fadd_rn(sum, y);
+        over = fabsf(t) < kInf ? __fsub_rn(__fsub_rn(t, sum), y) : 0.0f;   // infinities go on as such
+        sum = t;
+    }
+    // The sum of a warp's sums, in every lane: pairs with the rest of their addition,
+    // whichever is larger (D. Knuth, "The Art of Computer Programming", vol. 2, 4.2.2).
+    __device__ __forceinline__ float warp() const
+    {
+        float s = sum, rest = -over;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float b = __shfl_xor_sync(~0u, s, o), t = __fadd_rn(s, b), from_b = __fsub_rn(t, s);
+            const float lost = __fadd_rn(__fsub_rn(s, __fsub_rn(t, from_b)), __fsub_rn(b, from_b));
+            rest = __fadd_rn(rest, __shfl_xor_sync(~0u, rest, o));
+            rest = fabsf(t) < kInf ? __fadd_rn(rest, lost) : 0.0f;
+            s = t;
+        }
+        return __fadd_rn(s, rest);
+    }
+};
+
 // --- 1 / rms -----------------------------------------------------------------------
 
 // Squares of a row whose sum reaches 2^120 may lie outside FP32: such rows, which
@@ -316,11 +347,11 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
                 *reinterpret_cast<f2 *>(&joined[team][(lane + k * lanes) * W + 2 * j]) = dw[k][j];
         __syncthreads();
         for (int c = threadIdx.x; c < units * W; c += kBlock) {
-            float sum = 0.0f;
+            LongSum sum;
 #pragma unroll
             for (int i = 0; i < kTeams; ++i)
-                sum += joined[i][c];
-            sums[c] = sum;
+                sum.add(joined[i][c]);
+            sums[c] = sum.sum;
         }
     } else {
 #pragma unroll
@@ -334,23 +365,29 @@ __global__ void __launch_bounds__(kBlock, kCtas) norm_grad_kernel(NormGradArgs a
     }
 }
 
-// The parts of 32 columns by a CTA: 32 chains a column, joined pairwise. 608 parts
-// of 4096 columns 2.8 us (by 256 threads a CTA 8.5).
+// The parts of 32 columns by a CTA: 32 chains a column, joined pairwise, without what
+// roundings lose: each part has been rounded in its CTA, one after another by as many
+// rows as a thread takes (a 300th of them or fewer), and this adds one rounding to
+// that. 304 parts of 4096 columns 2.9 us (by 256 threads a CTA 8.5), the same as by
+// plain sums.
 constexpr int kJoin = 32;
 __global__ void __launch_bounds__(kJoin * 32) norm_weight_kernel(NormGradArgs a, int parts)
 {
-    __shared__ float part[kJoin][33];
+    __shared__ float part[2][kJoin][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane, pitch = a.groups * kGroup;
-    float sum = 0.0f;
+    LongSum sum;
 #pragma unroll 8
     for (int p = warp; p < parts; p += kJoin)
-        sum += a.parts[p * pitch + c];
-    part[warp][lane] = sum;
+        sum.add(a.parts[p * pitch + c]);
+    part[0][warp][lane] = sum.sum;
+    part[1][warp][lane] = sum.over;
     __syncthreads();
-    sum = warp_sum(part[lane][warp]);   // column `warp`, its chains across the lanes
+    sum.sum = part[0][lane][warp];   // column `warp`, its chains across the lanes
+    sum.over = part[1][lane][warp];
+    const float all = sum.warp();
     if (lane == 0 && (int64_t)blockIdx.x * 32 + warp < a.width)
-        store_weight(a.grad_weight, a.weight_dtype, (int64_t)blockIdx.x * 32 + warp, sum);
+        store_weight(a.grad_weight, a.weight_dtype, (int64_t)blockIdx.x * 32 + warp, all);
 }
 
 // --- rows beyond kMaxWidth --------------------------------------------------------------
@@ -402,20 +439,6 @@ __device__ __forceinline__ float block_sum(float v, float *part)
         v += __shfl_xor_sync(~0u, v, o);
     return v;
 }
-
-// A sum of products that keeps what its roundings lose (W. Kahan, "Further remarks on
-// reducing truncation errors", CACM 8(1), 1965): off by 2 roundings, whatever the
-// number of terms. One after another like terms are all rounded the same way:
-// 20 million equal squares, 78000 a thread, came out 9e-4 off.
-struct LongSum {
-    float sum = 0.0f, over = 0.0f;   // `over`: what is in the sum too much
-    __device__ __forceinline__ void add(float a, float b)
-    {
-        const float y = __fmaf_rn(a, b, -over), t = __fadd_rn(sum, y);
-        over = fabsf(t) < kInf ? __fsub_rn(__fsub_rn(t, sum), y) : 0.0f;   // infinities go on as such
-        sum = t;
-    }
-};
 
 // A row a CTA.
 template <class T>

@@ -1,4 +1,4 @@
-"""Sums of the norm: long rows of numbers of one sign, whose roundings add up.
+"""Sums of the norm: long rows of numbers of one sign, whose roundings add up, and the weight's gradient over rows.
 
 u = 2^-24. A sum of n positive terms added one by one is off by up to n u, and for like terms by a good part of it:
 they are all rounded the same way. Sums of parts that keep what their roundings lost are off by a few u, whatever n."""
@@ -72,3 +72,24 @@ def test_normed_codes_are_rounded_once(w):
     _, kept = A.rms_norm_forward(x, torch.ones(w, device="cuda"))
     _, h = A.rms_norm_backward(kept, torch.ones_like(x))
     assert torch.equal(h, (ref.kept(x) * kept.inv_rms.double()[:, None]).float()[0])
+
+
+@pytest.mark.parametrize("w", [768, 4096, 20000])
+def test_weights_gradient_keeps_small_terms_beside_large_ones(w):
+    """dy of +-2^30 in two of 128 rows, each of which a CTA sums by itself, and ones between them: the sum of the ones'
+    h is what is left."""
+    n = 128
+    x = torch.ones(n, w, device="cuda")
+    dy = torch.zeros(n, w, device="cuda")
+    dy[1:-1:7] = 1.0
+    weight = torch.ones(w, device="cuda")
+    _, kept = A.rms_norm_forward(x, weight)
+    r = kept.inv_rms.double()
+    assert (r == r[0]).all()
+    few = dy.clone()
+    dy[0], dy[n - 1] = 2.0 ** 30, -2.0 ** 30
+    _, got = A.rms_norm_backward(kept, dy)
+    _, want = A.rms_norm_backward(kept, few)
+    exact = (few.double() * (ref.kept(x) * r[:, None]).float().double()).sum(0)
+    assert ((want.double() - exact).abs() <= 2 * u * exact).all()
+    assert ((got.double() - exact).abs() <= 4 * u * exact).all()
