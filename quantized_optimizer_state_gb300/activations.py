@@ -159,7 +159,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
     """``x / sqrt(mean(x^2) + eps) * weight`` over the last dimension, in ``x``'s type;
     ``weight`` [width] may be of another one. ``eps`` in [2^-80, 2^20].
     Differentiable; ``x`` is kept in 8 bits where a gradient is asked for. The
-    gradient of ``weight`` sums the rows in FP32 (a 300th of them or fewer one after
+    gradient of ``weight`` sums the rows in FP32 (a 152th of them or fewer one after
     another), in an order that depends on their number and the device only."""
     _check_tangent(x, weight)
     return _native().rms_norm(x, weight, eps)
