@@ -1,4 +1,5 @@
-"""Activations at the ends of their types' ranges: codes of the largest finite numbers."""
+"""Activations at the ends of their types' ranges: codes of the largest finite numbers, and functions of 16-bit types
+where the exponential leaves FP32's normal numbers."""
 import pytest
 import torch
 
@@ -84,3 +85,22 @@ def test_norm_beside_the_largest_numbers(dtype, w):
     ref.close(grad, want, tol, "gradient")
     # r is a subnormal number of 21 bits here
     ref.close(gw, dw, dw_tol + 2.0 ** -21 * dw.abs(), "weight's gradient")
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_far_negative_side_of_bfloat16(kind):
+    """Results that are normal numbers keep their precision, to the last one (gelu's slope down to 2^-123: from 13.2 on,
+    where its exponential is below 2^-126, it is 0)."""
+    least, least_slope = (2.0 ** -133, 2.0 ** -133) if kind == "silu" else (2.0 ** -126, 2.0 ** -123)
+    x = torch.arange(0x4000, 0x4340, device="cuda", dtype=torch.int32)      # 2 to 192, negative
+    x = (x | 0x8000).to(torch.int16).view(BF)[:, None].contiguous()
+    value, _, _, rel = ref.act(kind, x)
+    y = A.activation(x, kind).double()
+    # the function's own error, a rounding to BF16, and (silu) of numbers below 2^-126 a place of them
+    assert ((y - value).abs() <= value.abs() * (rel + 2.0 ** -8 * (1 + 2.0 ** -8)) + least).all()
+    _, kept = A.activation_forward(x, kind)
+    got = A.activation_backward(kept, torch.ones_like(x)).double()
+    _, slope, size, rel = ref.act(kind, ref.kept(x), BF)
+    assert ((got - slope).abs() <= size * rel + slope.abs() * 2.0 ** -8 * (1 + 2.0 ** -8) + least_slope).all()
+    normal = value.abs() >= 2.0 ** -126
+    assert (y[normal] != 0).all() and normal.any()
