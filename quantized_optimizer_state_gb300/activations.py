@@ -191,11 +191,10 @@ class _Linear(torch.autograd.Function):
             return torch.nn.functional.linear(x, weight, bias)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_y):
         weight, *kept = ctx.saved_tensors
         grad_x = grad_weight = grad_bias = None
-        with torch.cuda.device(weight.device), torch.autocast("cuda", enabled=False):
+        with torch.cuda.device(weight.device), torch.autocast("cuda", enabled=False), torch.no_grad():
             rows = grad_y.reshape(-1, grad_y.shape[-1])
             if ctx.needs_input_grad[0]:
                 grad_x = grad_y @ weight
@@ -204,7 +203,9 @@ class _Linear(torch.autograd.Function):
                 grad_weight = rows.t() @ x.view(-1, x.shape[-1])
             if ctx.needs_input_grad[2]:
                 grad_bias = rows.sum(0)
-        return grad_x, grad_weight, grad_bias
+        if not torch.is_grad_enabled():
+            return grad_x, grad_weight, grad_bias
+        return tuple(_native().first_order([grad_x, grad_weight, grad_bias]))
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:

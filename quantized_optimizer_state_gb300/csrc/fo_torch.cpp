@@ -291,7 +291,9 @@ std::tuple<Tensor, Tensor> act_backward(const Tensor &kept, const Act &how, cons
 }
 
 // Derivatives are of the first order: a backward pass that is to be
-// differentiated gives gradients that refuse it.
+// differentiated gives gradients that refuse it, whether or not what reached it
+// asks for a gradient (its result depends on the operator's input too). They
+// are made to require one first: the refusing node passes by tensors that do not.
 variable_list first_order(variable_list grads)
 {
     if (!at::GradMode::is_enabled())
@@ -299,7 +301,7 @@ variable_list first_order(variable_list grads)
     variable_list made;
     for (const auto &g : grads)
         if (g.defined())
-            made.push_back(g);
+            made.push_back(g.detach().set_requires_grad(true));
     auto refuse = std::make_shared<torch::autograd::DelayedError>("the operators of this library have first derivatives only",
                                                                   (int64_t)made.size());
     made = (*refuse)(std::move(made));
@@ -308,6 +310,19 @@ variable_list first_order(variable_list grads)
         if (g.defined())
             g = made[at++];
     return grads;
+}
+
+// The same for a backward pass in Python; None for what has no gradient.
+std::vector<Maybe> first_order_of(const std::vector<Maybe> &grads)
+{
+    variable_list list;
+    for (const auto &g : grads)
+        list.push_back(defined(g) ? *g : Tensor());
+    list = first_order(std::move(list));
+    std::vector<Maybe> result;
+    for (const auto &g : list)
+        result.push_back(g.defined() ? Maybe(g) : Maybe());
+    return result;
 }
 
 struct ActFunction : torch::autograd::Function<ActFunction> {
@@ -657,4 +672,5 @@ PYBIND11_MODULE(_fo_torch, m)
     m.def("rms_norm_backward", &rms_norm_backward);
     m.def("policy_loss", &policy_loss);
     m.def("policy_loss_grad", &policy_loss_grad);
+    m.def("first_order", &first_order_of);
 }
