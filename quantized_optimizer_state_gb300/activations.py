@@ -211,11 +211,13 @@ class _Linear(torch.autograd.Function):
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``x @ weight.t() + bias`` with ``x`` kept in 8 bits for the gradient of
     ``weight``, which is a matrix product with the expanded copy (that of ``x``
-    needs the weight alone). One type for all."""
+    needs the weight alone). One type for all, that of the result too: autocast does
+    not reach the product, with a gradient or without."""
     _check_tangent(x, weight, bias)
     if x.dtype != weight.dtype or (bias is not None and bias.dtype != x.dtype):
         raise TypeError(f"x, weight and bias must be of one type, not {x.dtype}, {weight.dtype}" +
                         (f" and {bias.dtype}" if bias is not None else ""))
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         return _Linear.apply(x, weight, bias)
-    return torch.nn.functional.linear(x, weight, bias)
+    with torch.autocast("cuda", enabled=False):
+        return torch.nn.functional.linear(x, weight, bias)

@@ -22,6 +22,18 @@ def _cuda():
     fo.lib()
 
 
+@pytest.mark.parametrize("inside", [F32, BF])
+def test_linear_under_autocast_is_the_same_with_and_without_a_gradient(inside):
+    x, w, b = make((5, 64), inside), make((24, 64), inside, seed=1), make((24,), inside, seed=2)
+    with torch.autocast("cuda", dtype=torch.float16):
+        plain = A.linear(x, w, b)
+        with torch.no_grad():
+            quiet = A.linear(x, w.clone().requires_grad_(True), b)
+        trained = A.linear(x, w.clone().requires_grad_(True), b)
+    assert plain.dtype == quiet.dtype == trained.dtype == inside
+    assert torch.equal(plain, trained) and torch.equal(quiet, trained)
+
+
 def test_second_derivatives_are_refused_beside_other_terms():
     """A penalty on a gradient, added to a loss that has derivatives of its own: an error, not a gradient without the
     penalty's part."""
