@@ -660,17 +660,21 @@ std::tuple<Tensor, Tensor, Tensor> policy_loss_grad(const Tensor &logits, const 
 
 }  // namespace
 
+// Without the interpreter's lock: a launch waits where its stream's queue is full, and an
+// allocation may wait for the device, neither of which other Python threads should.
+// Arguments are C++ values by then; what calls Python takes the lock (check).
 PYBIND11_MODULE(_fo_torch, m)
 {
-    m.def("compress", &compress);
-    m.def("expand", &expand);
-    m.def("activation", &activation);
-    m.def("activation_forward", &activation_forward);
-    m.def("activation_backward", &activation_backward);
-    m.def("rms_norm", &rms_norm);
-    m.def("rms_norm_forward", &rms_norm_forward);
-    m.def("rms_norm_backward", &rms_norm_backward);
-    m.def("policy_loss", &policy_loss);
-    m.def("policy_loss_grad", &policy_loss_grad);
-    m.def("first_order", &first_order_of);
+    const py::call_guard<py::gil_scoped_release> unlocked;
+    m.def("compress", &compress, unlocked);
+    m.def("expand", &expand, unlocked);
+    m.def("activation", &activation, unlocked);
+    m.def("activation_forward", &activation_forward, unlocked);
+    m.def("activation_backward", &activation_backward, unlocked);
+    m.def("rms_norm", &rms_norm, unlocked);
+    m.def("rms_norm_forward", &rms_norm_forward, unlocked);
+    m.def("rms_norm_backward", &rms_norm_backward, unlocked);
+    m.def("policy_loss", &policy_loss, unlocked);
+    m.def("policy_loss_grad", &policy_loss_grad, unlocked);
+    m.def("first_order", &first_order_of, unlocked);
 }

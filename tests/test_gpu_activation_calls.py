@@ -45,3 +45,31 @@ def test_second_derivatives_are_refused_beside_other_terms():
         loss = (g ** 2).sum() + (x ** 2).sum() + (w ** 2).sum()
         with pytest.raises(RuntimeError, match="first derivatives|once_differentiable"):
             loss.backward()
+
+
+def test_other_threads_run_while_a_call_waits_for_the_queue():
+    """A launch waits where the stream's queue is full: other Python threads go on meanwhile."""
+    x = make((4, 64), BF)
+    kept = A.compress(x)
+    torch.cuda.synchronize()
+    stream, calls, done = torch.cuda.Stream(), 6000, []
+
+    def work():
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(2_000_000_000)           # about a second
+            begin = time.perf_counter()
+            for _ in range(calls):
+                A.expand(kept, out=x)
+            done.append(time.perf_counter() - begin)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    gap, last = 0.0, time.perf_counter()
+    while thread.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        gap, last = max(gap, now - last), now
+    thread.join()
+    torch.cuda.synchronize()
+    assert done and done[0] > 0.5, "the queue was never full"
+    assert gap < 0.5 * done[0], f"this thread stood still for {gap:.2f} of {done[0]:.2f} s"
