@@ -147,6 +147,7 @@ def activation_forward(x: torch.Tensor, kind: str, *, up: Optional[torch.Tensor]
 
 def activation_backward(kept: KeptActivation, grad_y: torch.Tensor):
     """The gradient of ``x`` (of ``(x, up)`` where ``up`` was given) for that of ``y``."""
+    _check_tangent(grad_y)
     kind, buffer, shape, dtype, halves = kept
     act, gated = KINDS[kind]
     grads = _native().activation_backward(buffer, act, gated, halves, shape, dtype, grad_y)
@@ -176,6 +177,7 @@ def rms_norm_backward(kept: KeptNorm, grad_y: torch.Tensor) -> Tuple[torch.Tenso
     """``(grad_x, grad_weight)`` for the gradient of ``y``; ``grad_weight``, of the
     weight's type, is None without one."""
     buffer, shape, dtype, weight = kept
+    _check_tangent(grad_y, weight)
     return _native().rms_norm_backward(buffer, shape, dtype, weight, grad_y)
 
 

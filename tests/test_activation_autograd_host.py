@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from quantized_optimizer_state_gb300 import activations as A
 from quantized_optimizer_state_gb300 import fo
 
 
@@ -30,3 +31,15 @@ def test_gradients_of_a_differentiated_backward_pass_refuse():
     x.grad = None
     Doubled.apply(x).sum().backward()
     assert torch.equal(x.grad, torch.full((3,), 2.0)) and not x.grad.requires_grad
+
+
+def test_tangents_of_incoming_gradients_are_refused():
+    x = torch.zeros(4, 64)
+    kept = A.KeptActivation("silu", torch.zeros(4 * 68, dtype=torch.int8), torch.Size((4, 64)), torch.float32, False)
+    norm = A.KeptNorm(torch.zeros(4 * 72, dtype=torch.int8), torch.Size((4, 64)), torch.float32, None)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, x)
+        for call in (lambda: A.activation_backward(kept, dual), lambda: A.rms_norm_backward(norm, dual),
+                     lambda: A.rms_norm_backward(norm._replace(weight=dual[0]), x)):
+            with pytest.raises(NotImplementedError, match="tangent"):
+                call()
