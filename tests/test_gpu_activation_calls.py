@@ -73,3 +73,31 @@ def test_other_threads_run_while_a_call_waits_for_the_queue():
     torch.cuda.synchronize()
     assert done and done[0] > 0.5, "the queue was never full"
     assert gap < 0.5 * done[0], f"this thread stood still for {gap:.2f} of {done[0]:.2f} s"
+
+
+def held(make_graph, expected, tensors):
+    """That what make_graph returns keeps the expected bytes allocated (the allocator rounds a tensor up by less than 1 MB)."""
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    keep = make_graph()
+    over = torch.cuda.memory_allocated() - before - expected
+    del keep
+    assert 0 <= over < tensors << 20, f"{over} bytes more than {expected}"
+
+
+def test_what_a_graph_holds():
+    """Of its input an operator keeps 1.0625 bytes an element (a norm 4 more a row), and each product a copy of its own."""
+    n, w = 8192, 4096
+    y, kept = n * w * 2, n * w * 34 // 32
+    wide = make((n, 2 * w), BF).requires_grad_(True)
+    x = wide.detach()[:, :w].contiguous().requires_grad_(True)
+    held(lambda: A.activation(x, "gelu"), y + kept, 2)
+    held(lambda: A.activation(wide, "swiglu"), y + 2 * kept, 2)
+    held(lambda: A.rms_norm(x), y + kept + 4 * n, 2)
+    held(lambda: A.activation(x.detach(), "gelu"), y, 1)
+    weights = [make((w, w), BF, seed=i, scale=0.01).requires_grad_(True) for i in (1, 2, 3)]
+    A.linear(x, weights[0])                            # the matrix library's workspace is there
+    held(lambda: A.linear(x, weights[0]), y + kept, 3)
+    held(lambda: [A.linear(x, m) for m in weights], 3 * (y + kept), 9)
+    with torch.no_grad():
+        held(lambda: A.linear(x, weights[0]), y, 1)
