@@ -4,11 +4,12 @@
 //
 // One pass each way, codes made of the registers that hold the input. A pair of
 // gate and other half in BF16 is 8.125 bytes forward and as many backward, 26 and
-// 28 instructions an element (29 and 32 for gelu) of the 44 that the copy rate
+// 28 instructions an element (30 and 31 for gelu) of the 44 that the copy rate
 // leaves room for: bound by device memory, 8192 x 14336 BF16 swiglu 142 and 148 us
 // (0.99 and 0.95 of the measured copy rate), FP32 1.02 of it over both (the last
-// codes are still in the L2 cache). In rows of no alignment instructions bound it:
-// 3001 x 2731 FP16 geglu 39 an element forward, 19.1 us and 16.9 backward where the
+// codes are still in the L2 cache; with other layers between, backward takes 152, and
+// FP32 4096 x 14336 125 instead of 118). In rows of no alignment instructions bound it:
+// 3001 x 2731 FP16 geglu 38 an element forward, 19.0 us and 16.9 backward where the
 // bytes alone take 9.8.
 #include "fo_act.cuh"
 

@@ -8,10 +8,12 @@
 // codes need no sum and come before it is waited for; the weight's gradient is
 // summed in registers over the rows that a team takes, and a second, small launch
 // adds up what the CTAs left (3 us). 16384 x 4096 BF16: 56 and 56 us, 0.89 of the
-// measured copy rate, 16 and 20 instructions an element; FP32 98 and 91, 0.95.
+// measured copy rate, 15 and 18 instructions an element; FP32 98 and 91, 0.95. The
+// backward passes are those right after their forward passes, which find the last
+// codes in the L2 cache: with other layers between they take 64 and 97.
 // What is missing are the waits of a CTA for a row's sum: rows two ahead instead of
-// one changed nothing. Rows of 128 take 16 and 15 us for 131072, where
-// the bytes alone take 12.6. Rows of no alignment are bound by instructions and
+// one changed nothing. Rows of 128 take 16.6 and 15.5 us (18.5 with other layers
+// between) for 131072, where the bytes alone take 12.6. Rows of no alignment are bound by instructions and
 // occupancy: 8191 x 4099 BF16 50 and 65 us where the bytes take 25 each.
 #include <algorithm>
 
