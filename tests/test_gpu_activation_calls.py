@@ -1,5 +1,6 @@
 """Operators on activations as calls of a program: under autocast, beside other Python threads, twice differentiated, and
 what a graph holds of them."""
+import gc
 import threading
 import time
 
@@ -77,7 +78,7 @@ def test_other_threads_run_while_a_call_waits_for_the_queue():
 
 def held(make_graph, expected, tensors):
     """That what make_graph returns keeps the expected bytes allocated (the allocator rounds a tensor up by less than 1 MB)."""
-    torch.cuda.synchronize()
+    gc.collect()                                       # what earlier tests left is not freed in between
     before = torch.cuda.memory_allocated()
     keep = make_graph()
     over = torch.cuda.memory_allocated() - before - expected
@@ -101,3 +102,23 @@ def test_what_a_graph_holds():
     held(lambda: [A.linear(x, m) for m in weights], 3 * (y + kept), 9)
     with torch.no_grad():
         held(lambda: A.linear(x, weights[0]), y, 1)
+
+
+def test_saved_tensors_go_through_hooks():
+    """What a graph keeps can be moved elsewhere meanwhile, by hooks in Python that the calls wait for."""
+    x, w, m = (make(s, BF, seed=i).requires_grad_(True) for i, s in enumerate([(6, 128), (128,), (16, 64)]))
+    t, zero = torch.arange(6, device="cuda"), torch.zeros(6, device="cuda")
+
+    def grads():
+        y = A.linear(A.activation(A.rms_norm(x, w), "swiglu"), m)
+        return torch.autograd.grad(policy_loss(y, t, zero - 3, zero + 1).loss.sum(), (x, w, m))
+
+    want, packed = grads(), []
+
+    def pack(a):
+        packed.append(a)
+        return a.cpu()
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda a: a.cuda()):
+        got = grads()
+    assert len(packed) >= 8 and all(torch.equal(p, q) for p, q in zip(got, want))
